@@ -110,6 +110,7 @@ extern "C" {
 #define FOS_STATUS_TILE_NONUNIFORM 1 /* 16x16 with a per-row amax that differs within a 16-row band */
 #define FOS_STATUS_BAD_OFFS 2        /* group offsets not monotone, not multiples of 16, or past M_alloc */
 #define FOS_STATUS_BARRIER_TIMEOUT 4 /* fused calls: the grid barrier did not complete in time (fos_set_barrier_poll_limit) */
+#define FOS_STATUS_BAD_INDEX 8       /* an expert index that is neither -1 nor below the number of experts */
 
 /* Bytes of the device workspace the fused calls (fos_quantize_fused,
  * fos_quantize_grouped_fused, fos_qdq_fused) need; the most groups the fused
@@ -359,6 +360,125 @@ int fos_quantize_grouped_fused_noalloc(const void* x, int dtype, int64_t M_alloc
                                        int G, const fos_config* cfg, uint8_t* codes, uint8_t* scales,
                                        float* group_amax_out, float* group_sdec_out, int32_t* d_status,
                                        void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the quantizer: the norm that makes 8-bit rows, the product
+ * that reads NVFP4 weights (dense and by expert), and the router's balance
+ * loss with the group offsets that the grouped calls take. They were added
+ * within ABI version 6: every earlier signature is unchanged. Their float
+ * results are not bitwise pinned: sums are binary32 or wider in an order that
+ * may depend on the shapes, but never on the order of execution, so a call
+ * repeated on the same inputs gives the same bits. NaN is not dropped here:
+ * it propagates by IEEE rules except where a call says otherwise. */
+
+/* fos_operand.type beyond the element types above */
+#define FOS_E4M3 3  /* 8-bit E4M3 values (fn variant) and a float32 scale */
+#define FOS_NVFP4 4 /* codes and block scales as fos_quantize writes them, and S_dec */
+
+/* fos_operand.gran: what one float32 scale covers; FOS_PER_TENSOR and
+ * FOS_PER_ROW as above */
+#define FOS_PER_GROUP 2 /* grouped call: scale[g] for the rows (of x) or the weight of group g */
+
+/* activations */
+#define FOS_ACT_NONE 0
+#define FOS_ACT_RELU 1
+#define FOS_ACT_GELU 2      /* v (1 + erf(v / sqrt 2)) / 2 */
+#define FOS_ACT_GELU_TANH 3 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+#define FOS_ACT_SILU 4      /* v / (1 + exp(-v)) */
+
+/* One operand of a product, rows of K values, contiguous.
+ *   FOS_BF16, FOS_FP16: data [rows, K], 16-byte aligned; scales and scale unused.
+ *   FOS_E4M3:           data uint8 [rows, K], 16-byte aligned; scale float32.
+ *   FOS_NVFP4:          data uint8 [rows, K/2], 8-byte aligned; block_scales
+ *                       uint8 [rows, K/16]; scale float32 (S_dec).
+ * scale holds 1 value (FOS_PER_TENSOR), one per row, or one per group. */
+typedef struct fos_operand {
+    const void* data;
+    const uint8_t* block_scales;
+    const float* scale;
+    int32_t type; /* FOS_BF16 | FOS_FP16 | FOS_E4M3 | FOS_NVFP4 */
+    int32_t gran; /* FOS_PER_TENSOR | FOS_PER_ROW | FOS_PER_GROUP */
+} fos_operand;
+
+/* What is done to a sum v before it is stored: v + bias, the activation,
+ * + residual, in binary32, then one rounding to the output type. */
+typedef struct fos_epilogue {
+    const void* bias;     /* nullable, [N] (grouped: [G, N]) of bias_dtype */
+    const void* residual; /* nullable, [M, N] of the output type; may be y itself */
+    int32_t bias_dtype;   /* FOS_BF16 | FOS_FP16 | FOS_FP32 */
+    int32_t activation;   /* FOS_ACT_* */
+} fos_epilogue;
+
+/* y[M, N] = act(x w^T + bias) + residual, x [M, K] of any operand type and w
+ * [N, K] in FOS_NVFP4 (per tensor or per row). This is the consumer of the
+ * codes and scales of fos_quantize, 1x16 and 16x16 alike, and (with
+ * fos_quantize_columnwise's output as w) of the transposed operand, which
+ * makes it the backward product dX = dY W too. y is bf16, fp16 or fp32,
+ * contiguous. Decoded values are exact in the 16-bit type of the matrix
+ * instruction, products exact and sums binary32, so the result differs from
+ * the exact one by the order of the sum and the rounding of the output.
+ *   work:       device memory of at least fos_linear_workspace() bytes,
+ *               16-byte aligned (NULL when that is 0). It needs no clearing
+ *               and carries nothing from call to call; calls that may overlap
+ *               need one each.
+ * epi may be NULL (no bias, no activation, no residual). */
+int fos_linear(const fos_operand* x, const fos_operand* w, int64_t M, int64_t N, int64_t K, const fos_epilogue* epi,
+               void* y, int out_dtype, void* work, int64_t work_bytes, void* stream);
+
+/* The bytes of work that fos_linear (G = 0) or fos_linear_grouped (G groups)
+ * needs for these sizes; -1 for sizes that the calls refuse. */
+int64_t fos_linear_workspace(int64_t M, int64_t N, int64_t K, int G);
+
+/* The same for G experts in one launch: rows [offs[g-1], offs[g]) of x (offs
+ * as for fos_quantize_grouped, but of any multiple, so unpadded groups are
+ * fine) times w[g], w [G, N, K] in FOS_NVFP4 with 1, G * N (FOS_PER_ROW) or G
+ * scales, bias [G, N]. Rows at or past offs[G-1] are not read and are written
+ * as zero (no bias, no residual). Offsets that decrease or leave [0, M] set
+ * FOS_STATUS_BAD_OFFS in the nullable d_status; each is then taken as if it
+ * were clamped to [the one before, M], and no access leaves the tensors. */
+int fos_linear_grouped(const fos_operand* x, const fos_operand* w, const int32_t* offs, int G, int64_t M, int64_t N,
+                       int64_t K, const fos_epilogue* epi, void* y, int out_dtype, void* work, int64_t work_bytes,
+                       int32_t* d_status, void* stream);
+
+/* Root-mean-square norm of a residual sum, with an 8-bit output: per row
+ *   h = x + residual (x without one), v = weight h / sqrt(mean(h^2) + eps),
+ *   s = max|v| / 448 (1 if every v is 0; at least 2^-126), q = E4M3(v / s).
+ * The norm takes h before its rounding. K is any positive number.
+ *   residual: nullable [M, K] of x's type.   weight: [K] of weight_dtype.
+ *   q: uint8 [M, K];  scale: float [M]: an FOS_E4M3 operand, FOS_PER_ROW.
+ *   h_out: nullable [M, K] of x's type, the new residual stream; may be x or
+ *          residual.   y_out: nullable [M, K] of x's type, v before the 8-bit
+ *          rounding (for a consumer of 16-bit values, such as a router).
+ * A row with a NaN or an infinity in h, or whose v overflows, has scale NaN
+ * and codes 0x7F (NaN). */
+int fos_rmsnorm_quantize(const void* x, int dtype, int64_t M, int64_t K, const void* residual, const void* weight,
+                         int weight_dtype, float eps, uint8_t* q, float* scale, void* h_out, void* y_out,
+                         void* stream);
+
+/* Load-balance loss of a router over E experts (1 <= E <= 1024), with what
+ * the grouped calls need. p = softmax(logits[t]) for each token t that the
+ * mask keeps, n such tokens, c_e their assignments to expert e:
+ *   slope_e = coef E c_e / (max(sum c, 1) max(n, 1)),
+ *   loss    = sum_e slope_e sum_t p_te   (= coef E sum_e f_e mean_t p_te).
+ *   logits: [T, E];  idx: int32 or int64 [T, k], -1 for an assignment that was
+ *           dropped; any other value outside [0, E) is ignored and sets
+ *           FOS_STATUS_BAD_INDEX in the nullable d_status.
+ *   mask:   nullable uint8 [T], 0 for a row that is not a token (not read).
+ *   loss:   float[1];  counts: int32[E], c;  slope: float[E], for the backward.
+ *   offs:   nullable int32[E]: the running sum of c_e rounded up to multiples
+ *           of `align` (>= 1), cumulative end offsets of padded groups.
+ *   work:   fos_balance_workspace() bytes, 8-byte aligned, as for fos_linear.
+ * A row of logits that are all -infinity has p = 0. */
+int fos_balance_loss(const void* logits, int dtype, int64_t T, int E, const void* idx, int idx_bytes, int k,
+                     const uint8_t* mask, float coef, int align, float* loss, int32_t* counts, int32_t* offs,
+                     float* slope, void* work, int64_t work_bytes, int32_t* d_status, void* stream);
+int64_t fos_balance_workspace(int64_t T, int E);
+
+/* Its gradient, dlogits_te = dloss p_te (slope_e - sum_j slope_j p_tj) in the
+ * logits' type, zero for masked rows; dloss: device float[1]; slope from the
+ * forward call (counts are piecewise constant and have no gradient). */
+int fos_balance_loss_backward(const float* dloss, const void* logits, int dtype, int64_t T, int E,
+                              const uint8_t* mask, const float* slope, void* dlogits, void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,10 +26,14 @@ METRICS = {"mae": 0, "mse": 1}
 PRECS = {"exact": 0, "fp16": 1}
 ORDERS = {"tree": 0, "seq": 1}
 AMAX_GRANS = {"tensor": 0, "row": 1, "band16": 2}
+OPERAND_GRANS = {"tensor": 0, "row": 1, "group": 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+OPERAND_E4M3, OPERAND_NVFP4 = 3, 4  # FOS_E4M3, FOS_NVFP4
 
 STATUS_TILE_NONUNIFORM = 1
 STATUS_BAD_OFFS = 2
 STATUS_BARRIER_TIMEOUT = 4
+STATUS_BAD_INDEX = 8
 FUSED_WORKSPACE_BYTES = 16384  # FOS_FUSED_WORKSPACE_BYTES
 FUSED_MAX_GROUPS = 256  # FOS_FUSED_MAX_GROUPS
 
@@ -51,7 +55,18 @@ class _Desc(ctypes.Structure):
                 ("M", ctypes.c_int64), ("K", ctypes.c_int64)]
 
 
+class _Operand(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_scales", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("type", ctypes.c_int32), ("gran", ctypes.c_int32)]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
+_F = ctypes.c_float
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SIGS = {
@@ -74,6 +89,13 @@ _SIGS = {
                                         _P]),
     "fos_quantize_grouped_fused_noalloc": (_I, [_P, _I, _I64, _I64, _P, _I, ctypes.POINTER(_Config), _P, _P, _P, _P,
                                                 _P, _P]),
+    "fos_linear_workspace": (_I64, [_I64, _I64, _I64, _I]),
+    "fos_linear": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _I, _P, _I64, _P]),
+    "fos_linear_grouped": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _I, _P, _I64, _P, _P]),
+    "fos_rmsnorm_quantize": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P]),
+    "fos_balance_workspace": (_I64, [_I64, _I]),
+    "fos_balance_loss": (_I, [_P, _I, _I64, _I, _P, _I, _I, _P, _F, _I, _P, _P, _P, _P, _P, _I64, _P, _P]),
+    "fos_balance_loss_backward": (_I, [_P, _P, _I, _I64, _I, _P, _P, _P, _P]),
 }
 EXPORTS = tuple(_SIGS)
 
@@ -474,3 +496,253 @@ def fos_quantize_grouped_fused_noalloc(x: torch.Tensor, offs: torch.Tensor, *, c
                                                                  _ptr(scales), _ptr(group_amax), _ptr(group_sdec),
                                                                  _ptr(status), _stream(dev)))
     return codes, scales, group_amax, group_sdec
+
+
+# ------------------------------------------------- operators around the quantizer
+
+
+def _match(t, name: str, device, shape=None, dtype=None):
+    """Check a tensor argument that the C call takes as a bare pointer."""
+    _need(t, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _float_type(t, name: str) -> int:
+    if t.dtype not in DTYPES:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def _scale_count(scale, gran: str, rows: int, groups: int | None, name: str, device):
+    if gran not in OPERAND_GRANS or (gran == "group" and groups is None):
+        raise ValueError(f"{name}: unknown scale granularity {gran!r}")
+    _match(scale, f"{name}'s scale", device, dtype=torch.float32)
+    want = {"tensor": 1, "row": rows, "group": groups}[gran]
+    if scale.numel() != want:
+        raise ValueError(f"{name}'s scale must hold {want} value(s) (per {gran}), got {scale.numel()}")
+
+
+def _activation_operand(x, gran, groups):
+    """(_Operand, M, K, device) of a bf16/fp16 tensor, an (E4M3 values,
+    scales) pair or a (codes, block scales, S_dec) triple."""
+    if isinstance(x, torch.Tensor):
+        _need(x, "x")
+        if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"x must be a bf16 or fp16 [M, K] tensor, got {x.dtype} {list(x.shape)}")
+        return _Operand(x.data_ptr(), None, None, DTYPES[x.dtype], 0), x.shape[0], x.shape[1], x.device
+    if not isinstance(x, (tuple, list)) or len(x) not in (2, 3):
+        raise ValueError("x must be a tensor, (q, scale) or (codes, scales, sdec)")
+    data = x[0]
+    _need(data, "x")
+    if data.dim() != 2:
+        raise ValueError(f"x must be rank 2, got {list(data.shape)}")
+    dev, M = data.device, data.shape[0]
+    if len(x) == 2:
+        if data.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError(f"x's values must be float8_e4m3fn, got {data.dtype}")
+        gran = gran or "row"
+        _scale_count(x[1], gran, M, groups, "x", dev)
+        return (_Operand(data.data_ptr(), None, x[1].data_ptr(), OPERAND_E4M3, OPERAND_GRANS[gran]), M,
+                data.shape[1], dev)
+    K = 2 * data.shape[1]
+    _match(data, "x's codes", dev, dtype=torch.uint8)
+    _match(x[1], "x's block scales", dev, (M, K // 16), torch.uint8)
+    gran = gran or "tensor"
+    _scale_count(x[2], gran, M, groups, "x", dev)
+    return (_Operand(data.data_ptr(), x[1].data_ptr(), x[2].data_ptr(), OPERAND_NVFP4, OPERAND_GRANS[gran]), M, K,
+            dev)
+
+
+def _linear(x, w, offs, bias, act, residual, out_dtype, out, x_gran, w_gran, workspace, status):
+    codes, scales, sdec = w
+    G = None if offs is None else offs.numel()
+    xo, M, K, dev = _activation_operand(x, x_gran, G)
+    lead = () if G is None else (G,)
+    if codes.dim() != 2 + len(lead):
+        raise ValueError(f"w's codes must have shape {[*lead, 'N', K // 2]}, got {list(codes.shape)}")
+    N = codes.shape[-2]
+    _match(codes, "w's codes", dev, (*lead, N, K // 2), torch.uint8)
+    _match(scales, "w's block scales", dev, (*lead, N, K // 16), torch.uint8)
+    _scale_count(sdec, w_gran, N * (G or 1), G, "w", dev)
+    wo = _Operand(codes.data_ptr(), scales.data_ptr(), sdec.data_ptr(), OPERAND_NVFP4, OPERAND_GRANS[w_gran])
+    if out is not None:
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = x.dtype if isinstance(x, torch.Tensor) else torch.bfloat16
+    if out_dtype not in DTYPES:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}")
+    if bias is not None:
+        _match(bias, "bias", dev, (*lead, N))
+        _float_type(bias, "bias")
+    if residual is not None:
+        _match(residual, "residual", dev, (M, N), out_dtype)
+    y = torch.empty(M, N, dtype=out_dtype, device=dev) if out is None else out
+    _match(y, "out", dev, (M, N))
+    epi = _Epilogue(None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
+                    0 if bias is None else DTYPES[bias.dtype], ACTIVATIONS[act])
+    lib = load_library()
+    need = lib.fos_linear_workspace(M, N, K, G or 0)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with torch.cuda.device(dev):
+        if G is None:
+            _check(lib.fos_linear(ctypes.byref(xo), ctypes.byref(wo), M, N, K, ctypes.byref(epi), _ptr(y),
+                                  DTYPES[out_dtype], _ptr(workspace), room, _stream(dev)))
+        else:
+            _match(offs, "offs", dev, (G,), torch.int32)
+            _check(lib.fos_linear_grouped(ctypes.byref(xo), ctypes.byref(wo), _ptr(offs), G, M, N, K,
+                                          ctypes.byref(epi), _ptr(y), DTYPES[out_dtype], _ptr(workspace), room,
+                                          _ptr(status), _stream(dev)))
+    return y
+
+
+def fos_linear(x, w, *, bias=None, act: str = "none", residual=None, out_dtype=None, out=None, x_gran=None,
+               w_gran: str = "tensor", workspace=None) -> torch.Tensor:
+    """act(x @ dequantize(w).T + bias) + residual, [M, N].
+
+    x: a bf16 or fp16 tensor [M, K]; (q, scale) of fos_rmsnorm_quantize (E4M3,
+    a scale per row); or (codes, scales, sdec) of fos_quantize. w: (codes,
+    scales, sdec) of fos_quantize for a weight [N, K], or of
+    fos_quantize_columnwise for the backward product. ``x_gran`` and ``w_gran``
+    say what one float32 scale covers ("tensor" or "row"; E4M3 rows default to
+    "row"). out_dtype defaults to x's, or bf16 for a quantized x. A workspace
+    (fos_linear_workspace bytes) is allocated when none is passed."""
+    return _linear(x, w, None, bias, act, residual, out_dtype, out, x_gran, w_gran, workspace, None)
+
+
+def fos_linear_grouped(x, w, offs: torch.Tensor, *, bias=None, act: str = "none", residual=None, out_dtype=None,
+                       out=None, x_gran=None, w_gran: str = "tensor", workspace=None, status=None) -> torch.Tensor:
+    """fos_linear of each group of rows with its own weight, in one launch:
+    rows [offs[g-1], offs[g]) of x take w[g] (codes [G, N, K/2], scales [G, N,
+    K/16], sdec [1], [G] with w_gran="group" or [G * N] with w_gran="row") and
+    bias[g]; rows at or past offs[-1] come out as zero."""
+    _need(offs, "offs")
+    return _linear(x, w, offs, bias, act, residual, out_dtype, out, x_gran, w_gran, workspace, status)
+
+
+def fos_linear_workspace(M: int, N: int, K: int, G: int = 0) -> int:
+    """Bytes of workspace of fos_linear (G = 0) or fos_linear_grouped."""
+    need = load_library().fos_linear_workspace(M, N, K, G)
+    if need < 0:
+        raise ValueError(f"unsupported sizes M={M} N={N} K={K} G={G}")
+    return need
+
+
+def fos_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, *, residual=None, eps: float = 1e-6, q=None,
+                         scale=None, h=None, y=None):
+    """RMS norm of x + residual, [M, K], with an 8-bit output. Returns (q
+    float8_e4m3fn[M, K], scale float32[M], h): q * scale is the normalised row
+    and h = x + residual in x's dtype (x itself without a residual). Pass
+    ``y`` (x's shape and dtype) to have the unquantized norm written too."""
+    _need(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be rank 2, got {list(x.shape)}")
+    M, K = x.shape
+    dev = x.device
+    _float_type(x, "x")
+    _match(weight, "weight", dev, (K,))
+    _float_type(weight, "weight")
+    if residual is not None:
+        _match(residual, "residual", dev, (M, K), x.dtype)
+        if h is None:
+            h = torch.empty_like(x)
+    for t, name in ((h, "h"), (y, "y")):
+        if t is not None:
+            _match(t, name, dev, (M, K), x.dtype)
+    if q is None:
+        q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=dev)
+    if scale is None:
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
+    _match(q, "q", dev, (M, K), torch.float8_e4m3fn)
+    _match(scale, "scale", dev, (M,), torch.float32)
+    with torch.cuda.device(dev):
+        _check(load_library().fos_rmsnorm_quantize(_ptr(x), DTYPES[x.dtype], M, K, _ptr(residual), _ptr(weight),
+                                                   DTYPES[weight.dtype], eps, _ptr(q), _ptr(scale), _ptr(h),
+                                                   _ptr(y), _stream(dev)))
+    return q, scale, x if h is None else h
+
+
+def _check_mask(mask, T, dev):
+    if mask is not None:
+        _match(mask, "mask", dev, (T,))
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
+
+
+def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0.01, mask=None, align: int = 16,
+                     loss=None, counts=None, offs=None, slope=None, workspace=None, status=None):
+    """Load-balance loss of router logits [T, E] and the chosen experts idx
+    [T, k] (int32 or int64, -1 for a dropped assignment). Returns (loss
+    float32[1], counts int32[E], offs int32[E], slope float32[E]): the
+    assignments per expert, the end offsets of groups padded to multiples of
+    ``align`` (what the grouped calls take), and what the backward call needs."""
+    _need(logits, "logits")
+    _need(idx, "idx")
+    if logits.dim() != 2 or idx.dim() != 2 or idx.shape[0] != logits.shape[0]:
+        raise ValueError(f"logits [T, E] and idx [T, k] expected, got {list(logits.shape)} and {list(idx.shape)}")
+    T, E = logits.shape
+    dev = logits.device
+    _float_type(logits, "logits")
+    _match(idx, "idx", dev)
+    if idx.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"idx must be int32 or int64, got {idx.dtype}")
+    _check_mask(mask, T, dev)
+    if loss is None:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+    if counts is None:
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+    if offs is None:
+        offs = torch.empty(E, dtype=torch.int32, device=dev)
+    if slope is None:
+        slope = torch.empty(E, dtype=torch.float32, device=dev)
+    for t, name, shape, dt in ((loss, "loss", (1,), torch.float32), (counts, "counts", (E,), torch.int32),
+                               (offs, "offs", (E,), torch.int32), (slope, "slope", (E,), torch.float32)):
+        _match(t, name, dev, shape, dt)
+    lib = load_library()
+    if workspace is None:
+        workspace = torch.empty(max(0, lib.fos_balance_workspace(T, E)), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.fos_balance_loss(_ptr(logits), DTYPES[logits.dtype], T, E, _ptr(idx), idx.element_size(),
+                                    idx.shape[1], _ptr(mask), coef, align, _ptr(loss), _ptr(counts), _ptr(offs),
+                                    _ptr(slope), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _ptr(status), _stream(dev)))
+    return loss, counts, offs, slope
+
+
+def fos_balance_workspace(T: int, E: int) -> int:
+    """Bytes of workspace of fos_balance_loss."""
+    need = load_library().fos_balance_workspace(T, E)
+    if need < 0:
+        raise ValueError(f"unsupported sizes T={T} E={E}")
+    return need
+
+
+def fos_balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, slope: torch.Tensor, *, mask=None,
+                              out=None) -> torch.Tensor:
+    """Gradient of fos_balance_loss with respect to its logits, times dloss
+    (float32[1]); ``slope`` and ``mask`` as in the forward call."""
+    _need(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be rank 2, got {list(logits.shape)}")
+    T, E = logits.shape
+    dev = logits.device
+    _float_type(logits, "logits")
+    _match(dloss, "dloss", dev, dtype=torch.float32)
+    if dloss.numel() != 1:
+        raise ValueError("dloss must hold one value")
+    _match(slope, "slope", dev, (E,), torch.float32)
+    _check_mask(mask, T, dev)
+    d = torch.empty_like(logits) if out is None else out
+    _match(d, "out", dev, (T, E), logits.dtype)
+    with torch.cuda.device(dev):
+        _check(load_library().fos_balance_loss_backward(_ptr(dloss), _ptr(logits), DTYPES[logits.dtype], T, E,
+                                                        _ptr(mask), _ptr(slope), _ptr(d), _stream(dev)))
+    return d

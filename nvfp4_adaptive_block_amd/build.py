@@ -10,13 +10,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfos.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fos_api.hip", "fos_kernels.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fos_api.hip", "fos_kernels.hip", "fos_linear.hip", "fos_norm.hip",
+                                            "fos_route.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
@@ -47,11 +49,24 @@ def build(out: str = LIB, extra: list[str] | None = None, quiet: bool = True, so
     """Compile `sources` (default: the library) into the shared object `out`
     with the library's flags and include paths. Other sources built this way
     (test kernels that call the device helpers) get the same numerics."""
+    srcs = list(sources or SOURCES)
+    flags = [*HIPCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC]
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, *(sources or SOURCES), "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    msgs = [ln for ln in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in ln]
-    if r.returncode != 0:
+    objs = [f"{tmp}.{i}.o" for i in range(len(srcs))]
+    # one compiler per source, side by side; then one link
+    compiles = [[hipcc(), *[f for f in flags if f != "-shared"], "-c", src, "-o", obj] for src, obj in zip(srcs, objs)]
+    link = [hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", tmp]
+    try:
+        with ThreadPoolExecutor(max_workers=max(1, min(4, len(srcs)))) as pool:
+            runs = list(pool.map(lambda c: subprocess.run(c, capture_output=True, text=True), compiles))
+        if all(r.returncode == 0 for r in runs):
+            runs.append(subprocess.run(link, capture_output=True, text=True))
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
+    msgs = [ln for r in runs for ln in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in ln]
+    if any(r.returncode != 0 for r in runs):
         sys.stderr.write("\n".join(msgs) + "\n")
         raise RuntimeError(f"hipcc failed building {os.path.basename(out)}")
     if msgs and not quiet:

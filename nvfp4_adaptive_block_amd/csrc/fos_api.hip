@@ -13,6 +13,7 @@
 
 #include "fos.h"
 #include "fos_kernels.h"
+#include "fos_ops.h"
 
 namespace {
 
@@ -634,3 +635,217 @@ int launch_grouped_fused(const void* x, int dtype, int64_t M_alloc, int64_t K, c
 }
 
 }  // namespace
+
+// ------------------------------------------------- operators around the quantizer
+
+namespace {
+
+int check_operand(const char* what, const fos_operand* o, int64_t rows, int64_t K, bool grouped) {
+  if (o->type != FOS_BF16 && o->type != FOS_FP16 && o->type != FOS_E4M3 && o->type != FOS_NVFP4)
+    return fail(FOS_ERR_DTYPE, "%s: unsupported operand type %d", what, o->type);
+  if (rows * K > 0 && !o->data) return fail(FOS_ERR_INVALID_ARG, "%s: data is NULL", what);
+  if (!aligned(o->data, o->type == FOS_NVFP4 ? 8 : 16))
+    return fail(FOS_ERR_ALIGN, "%s: data not %d-byte aligned", what, o->type == FOS_NVFP4 ? 8 : 16);
+  if (o->type == FOS_BF16 || o->type == FOS_FP16) return FOS_OK;
+  if (o->gran != FOS_PER_TENSOR && o->gran != FOS_PER_ROW && !(grouped && o->gran == FOS_PER_GROUP))
+    return fail(FOS_ERR_INVALID_ARG, "%s: bad scale granularity %d", what, o->gran);
+  if (!o->scale) return fail(FOS_ERR_INVALID_ARG, "%s: scale is NULL", what);
+  if (!aligned(o->scale, 4)) return fail(FOS_ERR_ALIGN, "%s: scale not 4-byte aligned", what);
+  if (o->type == FOS_NVFP4 && rows * K > 0 && !o->block_scales)
+    return fail(FOS_ERR_INVALID_ARG, "%s: block_scales is NULL", what);
+  return FOS_OK;
+}
+
+int check_linear_sizes(int64_t M, int64_t N, int64_t K, int64_t G) {
+  if (M < 0 || N < 0 || K < 0) return fail(FOS_ERR_INVALID_ARG, "negative size M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+  if (K % 16) return fail(FOS_ERR_SHAPE, "K=%lld is not a multiple of 16", (long long)K);
+  const int64_t most = int64_t(1) << 30;  // row and column numbers, and a row's bytes, fit 32 bits
+  if (M > most || N > most || K > most) return fail(FOS_ERR_SHAPE, "M, N and K are at most 2^30");
+  if (K > 0 && (M > kMaxElems / K || N > kMaxElems / K / (G > 0 ? G : 1))) return fail(FOS_ERR_SHAPE, "an operand exceeds 2^40 elements");
+  if (N > 0 && M > kMaxElems / N) return fail(FOS_ERR_SHAPE, "M*N exceeds 2^40 elements");
+  return FOS_OK;
+}
+
+int run_linear(const fos_operand* x, const fos_operand* w, const int32_t* offs, int G, int64_t M, int64_t N, int64_t K,
+               const fos_epilogue* epi, void* y, int out_dtype, void* work, int64_t work_bytes, int32_t* d_status,
+               void* stream) {
+  int rc;
+  const bool grouped = offs != nullptr;
+  if (!x || !w) return fail(FOS_ERR_INVALID_ARG, "x and w must be non-NULL");
+  if ((rc = check_dtype(out_dtype))) return rc;
+  if ((rc = check_linear_sizes(M, N, K, G))) return rc;
+  if ((rc = check_operand("x", x, M, K, grouped))) return rc;
+  if (w->type != FOS_NVFP4) return fail(FOS_ERR_DTYPE, "w: the weight must be FOS_NVFP4, got type %d", w->type);
+  if ((rc = check_operand("w", w, N * (grouped ? G : 1), K, grouped))) return rc;
+  if (M * N > 0 && !y) return fail(FOS_ERR_INVALID_ARG, "y is NULL");
+  if (!aligned(y, 16)) return fail(FOS_ERR_ALIGN, "y not 16-byte aligned");
+  if (epi) {
+    if (epi->activation < FOS_ACT_NONE || epi->activation > FOS_ACT_SILU) return fail(FOS_ERR_INVALID_ARG, "bad activation %d", epi->activation);
+    if (epi->bias && (rc = check_dtype(epi->bias_dtype))) return rc;
+    if (!aligned(epi->bias, 16) || !aligned(epi->residual, 16)) return fail(FOS_ERR_ALIGN, "bias/residual not 16-byte aligned");
+  }
+  if (!aligned(d_status, 4)) return fail(FOS_ERR_ALIGN, "status misaligned");
+  const int64_t need = fos::linear_workspace(M, N, K, grouped ? G : 0);
+  if (need > 0 && (!work || work_bytes < need))
+    return fail(FOS_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld needed", (long long)(work ? work_bytes : 0), (long long)need);
+  if (need > 0 && !aligned(work, 16)) return fail(FOS_ERR_ALIGN, "workspace not 16-byte aligned");
+  if ((rc = check_device())) return rc;
+  if (M * N == 0) return FOS_OK;
+  fos::LinearArgs a;
+  memset(&a, 0, sizeof a);
+  a.x = x->data;
+  a.xs = x->block_scales;
+  a.x_scale = x->scale;
+  a.x_type = x->type;
+  a.x_gran = x->type == FOS_BF16 || x->type == FOS_FP16 ? (int)fos::kScaleNone : x->gran;
+  a.w = static_cast<const uint8_t*>(w->data);
+  a.ws = w->block_scales;
+  a.w_scale = w->scale;
+  a.w_gran = w->gran;
+  if (epi) {
+    a.bias = epi->bias;
+    a.bias_dt = epi->bias_dtype;
+    a.res = epi->residual;
+    a.act = epi->activation;
+  }
+  a.y = y;
+  a.out_dt = out_dtype;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.offs = offs;
+  a.G = grouped ? G : 1;
+  a.status = d_status;
+  a.work = work;
+  const hipError_t e = fos::launch_linear(a, static_cast<hipStream_t>(stream));
+  if (e == hipErrorInvalidConfiguration) return fail(FOS_ERR_SHAPE, "too many tiles for one launch (M=%lld N=%lld)", (long long)M, (long long)N);
+  return launch_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fos_linear_workspace(int64_t M, int64_t N, int64_t K, int G) {
+  if (G < 0 || check_linear_sizes(M, N, K, G)) return -1;
+  return fos::linear_workspace(M, N, K, G);
+}
+
+int fos_linear(const fos_operand* x, const fos_operand* w, int64_t M, int64_t N, int64_t K, const fos_epilogue* epi,
+               void* y, int out_dtype, void* work, int64_t work_bytes, void* stream) {
+  return run_linear(x, w, nullptr, 0, M, N, K, epi, y, out_dtype, work, work_bytes, nullptr, stream);
+}
+
+int fos_linear_grouped(const fos_operand* x, const fos_operand* w, const int32_t* offs, int G, int64_t M, int64_t N,
+                       int64_t K, const fos_epilogue* epi, void* y, int out_dtype, void* work, int64_t work_bytes,
+                       int32_t* d_status, void* stream) {
+  if (G <= 0 || G > (1 << 20)) return fail(FOS_ERR_INVALID_ARG, "G must be in [1, 2^20], got %d", G);
+  if (!offs) return fail(FOS_ERR_INVALID_ARG, "offs is NULL");
+  if (!aligned(offs, 4)) return fail(FOS_ERR_ALIGN, "offs misaligned");
+  return run_linear(x, w, offs, G, M, N, K, epi, y, out_dtype, work, work_bytes, d_status, stream);
+}
+
+int fos_rmsnorm_quantize(const void* x, int dtype, int64_t M, int64_t K, const void* residual, const void* weight,
+                         int weight_dtype, float eps, uint8_t* q, float* scale, void* h_out, void* y_out,
+                         void* stream) {
+  int rc;
+  if ((rc = check_dtype(dtype)) || (rc = check_dtype(weight_dtype))) return rc;
+  if (M < 0 || K < 0) return fail(FOS_ERR_INVALID_ARG, "negative size M=%lld K=%lld", (long long)M, (long long)K);
+  if (K == 0) return fail(FOS_ERR_SHAPE, "K must be positive");
+  if (M > INT32_MAX || K > (int64_t(1) << 30) || M > kMaxElems / K)
+    return fail(FOS_ERR_SHAPE, "M < 2^31, K <= 2^30 and M*K <= 2^40, got M=%lld K=%lld", (long long)M, (long long)K);
+  if (!(eps >= 0.0f) || eps > 3e38f) return fail(FOS_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!weight) return fail(FOS_ERR_INVALID_ARG, "weight is NULL");
+  if (M > 0 && (!x || !q || !scale)) return fail(FOS_ERR_INVALID_ARG, "x, q and scale must be non-NULL");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(q, 16) || !aligned(h_out, 16) || !aligned(y_out, 16))
+    return fail(FOS_ERR_ALIGN, "a tensor is not 16-byte aligned");
+  if (!aligned(scale, 4)) return fail(FOS_ERR_ALIGN, "scale not 4-byte aligned");
+  if ((rc = check_device())) return rc;
+  if (M == 0) return FOS_OK;
+  fos::NormArgs a{x, residual, weight, weight_dtype, M, K, eps, q, scale, h_out, y_out};
+  return launch_status(fos::launch_norm(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_balance(int dtype, int64_t T, int E) {
+  int rc;
+  if ((rc = check_dtype(dtype))) return rc;
+  if (T < 0 || T > (int64_t(1) << 30)) return fail(FOS_ERR_SHAPE, "T must be in [0, 2^30], got %lld", (long long)T);
+  if (E < 1 || E > 1024) return fail(FOS_ERR_SHAPE, "E must be in [1, 1024], got %d", E);
+  return FOS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fos_balance_workspace(int64_t T, int E) {
+  if (check_balance(FOS_BF16, T, E)) return -1;
+  return fos::balance_workspace(T, E);
+}
+
+int fos_balance_loss(const void* logits, int dtype, int64_t T, int E, const void* idx, int idx_bytes, int k,
+                     const uint8_t* mask, float coef, int align, float* loss, int32_t* counts, int32_t* offs,
+                     float* slope, void* work, int64_t work_bytes, int32_t* d_status, void* stream) {
+  int rc;
+  if ((rc = check_balance(dtype, T, E))) return rc;
+  if (idx_bytes != 4 && idx_bytes != 8) return fail(FOS_ERR_DTYPE, "idx must be int32 or int64, got %d bytes", idx_bytes);
+  if (k < 1) return fail(FOS_ERR_INVALID_ARG, "k must be positive, got %d", k);
+  if (align < 1) return fail(FOS_ERR_INVALID_ARG, "align must be positive, got %d", align);
+  // the largest padded offset: all T k assignments, and a part of align in each group
+  if (T * k > INT32_MAX || T * k + (int64_t)E * (align - 1) > INT32_MAX)
+    return fail(FOS_ERR_SHAPE, "T*k rounded up per expert exceeds int32 (T=%lld k=%d align=%d)", (long long)T, k, align);
+  if (T > 0 && (!logits || !idx)) return fail(FOS_ERR_INVALID_ARG, "logits and idx must be non-NULL");
+  if (!loss || !counts || !slope || !work) return fail(FOS_ERR_INVALID_ARG, "loss, counts, slope and work must be non-NULL");
+  if (!aligned(logits, 16) || !aligned(idx, 8) || !aligned(work, 8)) return fail(FOS_ERR_ALIGN, "logits/idx/work misaligned");
+  if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(offs, 4) || !aligned(slope, 4) || !aligned(d_status, 4))
+    return fail(FOS_ERR_ALIGN, "loss/counts/offs/slope/status misaligned");
+  const int64_t need = fos::balance_workspace(T, E);
+  if (work_bytes < need) return fail(FOS_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld needed", (long long)work_bytes, (long long)need);
+  if ((rc = check_device())) return rc;
+  fos::BalanceArgs a;
+  memset(&a, 0, sizeof a);
+  a.logits = logits;
+  a.idx = idx;
+  a.idx64 = idx_bytes == 8;
+  a.mask = mask;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.align = align;
+  a.coef = coef;
+  a.loss = loss;
+  a.counts = counts;
+  a.offs = offs;
+  a.slope = slope;
+  a.work = work;
+  a.status = d_status;
+  return launch_status(fos::launch_balance(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+int fos_balance_loss_backward(const float* dloss, const void* logits, int dtype, int64_t T, int E,
+                              const uint8_t* mask, const float* slope, void* dlogits, void* stream) {
+  int rc;
+  if ((rc = check_balance(dtype, T, E))) return rc;
+  if (T > 0 && (!logits || !dlogits)) return fail(FOS_ERR_INVALID_ARG, "logits and dlogits must be non-NULL");
+  if (!dloss || !slope) return fail(FOS_ERR_INVALID_ARG, "dloss and slope must be non-NULL");
+  if (!aligned(logits, 16) || !aligned(dlogits, 16)) return fail(FOS_ERR_ALIGN, "logits/dlogits not 16-byte aligned");
+  if (!aligned(dloss, 4) || !aligned(slope, 4)) return fail(FOS_ERR_ALIGN, "dloss/slope misaligned");
+  if ((rc = check_device())) return rc;
+  if (T == 0) return FOS_OK;
+  fos::BalanceArgs a;
+  memset(&a, 0, sizeof a);
+  a.logits = logits;
+  a.mask = mask;
+  a.T = T;
+  a.E = E;
+  a.slope = const_cast<float*>(slope);
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  return launch_status(fos::launch_balance_backward(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
