@@ -212,38 +212,94 @@ __device__ __forceinline__ float to_f32(const void* p, int dt, int64_t i) {
   return dt == kBF16 ? __uint_as_float((uint32_t)v << 16) : (float)__builtin_bit_cast(_Float16, v);
 }
 
+// exp(v) by the base-2 instruction: off by about |v| half steps.
+__device__ __forceinline__ float exp_fast(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504088896341f); }
+
+// Activations of the epilogue. The reciprocal and exponential instructions are
+// good to a step of binary32; erfc is Abramowitz and Stegun's formula 7.1.26
+// (absolute error 1.5e-7), so gelu is off by at most 1e-7 |v| where the
+// library's erfc takes five times the instructions.
 __device__ __forceinline__ float activate(int act, float v) {
   switch (act) {
     case kActRelu: return v > 0.0f ? v : v != v ? v : 0.0f;
-    case kActGelu: return 0.5f * v * erfcf(v * -0.70710678118654752f);
-    case kActGeluTanh: {
-      // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u))
-      const float u = 0.79788456080286536f * __builtin_fmaf(0.044715f * v * v, v, v);
-      return v / (1.0f + expf(-2.0f * u));
+    case kActGelu: {
+      const float z = __builtin_fabsf(v) * 0.70710678118654752f;
+      const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, z, 1.0f));
+      float p = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+      p = __builtin_fmaf(t, p, 1.421413741f);
+      p = __builtin_fmaf(t, p, -0.284496736f);
+      p = __builtin_fmaf(t, p, 0.254829592f);
+      const float half_erfc = 0.5f * t * p * exp_fast(-z * z);  // of |v| / sqrt 2
+      return v * (v < 0.0f ? half_erfc : 1.0f - half_erfc);
     }
-    case kActSilu: return v / (1.0f + expf(-v));
+    case kActGeluTanh: {
+      // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
+      const float u = 0.79788456080286536f * __builtin_fmaf(0.044715f * v * v, v, v);
+      return v * __builtin_amdgcn_rcpf(1.0f + exp_fast(-2.0f * u));
+    }
+    case kActSilu: return v * __builtin_amdgcn_rcpf(1.0f + exp_fast(-v));
     default: return v;
   }
 }
 
+// Four neighbouring values of a tensor; `whole`: all four exist and the row
+// length is a multiple of 4, so that they lie on a 4-value boundary.
+__device__ __forceinline__ f32x4 load4(const void* p, int dt, int64_t i, bool whole, int have) {
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (!whole) {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if (j < have) v[j] = to_f32(p, dt, i + j);
+  } else if (dt == kFP32) {
+    v = *reinterpret_cast<const f32x4*>((const float*)p + i);
+  } else {
+    const uint2 t = *reinterpret_cast<const uint2*>((const uint16_t*)p + i);
+    v = dt == kBF16 ? f32x4{bf16_lo(t.x), bf16_hi(t.x), bf16_lo(t.y), bf16_hi(t.y)}
+                    : f32x4{f16_lo(t.x), f16_hi(t.x), f16_lo(t.y), f16_hi(t.y)};
+  }
+  return v;
+}
+
 // Finish columns n .. n + 3 of row m from their sums and store them. The sum
 // is rounded to the output type once, after the residual.
-__device__ __forceinline__ void finish4(const LinearArgs& a, int g, int64_t m, int64_t n, f32x4 acc) {
+__device__ __forceinline__ void finish4(const LinearArgs& a, int g, int64_t m, int64_t n, f32x4 v) {
+  const bool whole = a.N % 4 == 0;
+  const int have = a.N - n < 4 ? (int)(a.N - n) : 4;
   const float sx = a.x_gran == kScaleNone ? 1.0f : a.x_scale[a.x_gran == kScaleRow ? m : a.x_gran == kScaleGroup ? g : 0];
+  const int64_t at = m * a.N + n, wat = (int64_t)g * a.N + n;
+  if (a.w_gran == kScaleRow) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int64_t c = n + i;
-    if (c >= a.N) break;
-    const float sw = a.w_scale[a.w_gran == kScaleRow ? (int64_t)g * a.N + c : a.w_gran == kScaleGroup ? g : 0];
-    float v = acc[i] * (sx * sw);
-    if (a.bias) v += to_f32(a.bias, a.bias_dt, (int64_t)g * a.N + c);
-    v = activate(a.act, v);
-    const int64_t at = m * a.N + c;
-    if (a.res) v += to_f32(a.res, a.out_dt, at);
-    if (a.out_dt == kFP32)
-      ((float*)a.y)[at] = v;
-    else
-      ((uint16_t*)a.y)[at] = (uint16_t)(a.out_dt == kBF16 ? pack_bf16(v, 0.0f) : pack_f16(v, 0.0f));
+    for (int i = 0; i < 4; i++) v[i] *= sx * a.w_scale[i < have ? wat + i : wat];
+  } else {
+    v *= sx * a.w_scale[a.w_gran == kScaleGroup ? g : 0];
+  }
+  if (a.bias) v += load4(a.bias, a.bias_dt, wat, whole, have);
+  if (a.act != kActNone) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = activate(a.act, v[i]);
+  }
+  if (a.res) v += load4(a.res, a.out_dt, at, whole, have);
+  if (a.out_dt == kFP32) {
+    float* y = (float*)a.y + at;
+    if (whole) {
+      *reinterpret_cast<f32x4*>(y) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (i < have) y[i] = v[i];
+    }
+    return;
+  }
+  uint16_t* y = (uint16_t*)a.y + at;
+  const uint2 t = a.out_dt == kBF16 ? uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}
+                                    : uint2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
+  if (whole) {
+    *reinterpret_cast<uint2*>(y) = t;
+  } else {
+    y[0] = (uint16_t)t.x;
+    if (have > 1) y[1] = (uint16_t)(t.x >> 16);
+    if (have > 2) y[2] = (uint16_t)t.y;
+    if (have > 3) y[3] = (uint16_t)(t.y >> 16);
   }
 }
 
@@ -312,6 +368,280 @@ __global__ __launch_bounds__(64 * WAVES) void k_linear_stream(LinearArgs a, int 
   }
 }
 
+// The tile kernel: one workgroup of four waves takes BM rows and 256 columns,
+// each wave all BM rows and 64 columns. A 128-deep step of the activations is
+// staged in LDS as 16-bit values, twice (the next step's loads run while this
+// one is multiplied); the weights never pass through LDS: a wave decodes its own
+// 64 rows of them in registers, so each is decoded once per workgroup and the
+// LDS carries half of what two staged operands would (per step and wave 32 KiB
+// read for 128 matrix instructions of 16 cycles: half of the LDS's rate).
+//
+// LDS: row r of the tile is 16 chunks of 16 bytes (8 values), chunk c at slot
+// c ^ (r % 16). A fragment read takes, in 16 lanes, one chunk number of 16 rows:
+// 16 different slots, so no bank is hit twice.
+template <int XT, int BM>
+struct XStage {
+  static constexpr bool kDirect = XT == kBF16 || XT == kFP16;
+  static constexpr int kBlocks = BM * 8 / 256;  // 16-value blocks per thread and step
+  const uint8_t* base;   // first row of the tile
+  const uint8_t* sbase;  // NVFP4: its scales
+  uint32_t off[kDirect ? BM / 16 : kBlocks / 2];
+  uint32_t soff[XT == kXNVFP4 ? kBlocks / 2 : 1];
+  uint32_t regs[kBlocks / 2][XT == kXE4M3 ? 8 : XT == kXNVFP4 ? 4 : 16];
+  uint32_t sreg[kBlocks / 2];
+
+  // Byte offsets of what this thread loads in every step, from the tile's
+  // first row; rows past the end read the last one (their sums are dropped).
+  __device__ __forceinline__ void init(const LinearArgs& a, int64_t m0, int rows) {
+    const int64_t KB = a.K / 16;
+    if constexpr (kDirect) {
+      base = (const uint8_t*)a.x + m0 * a.K * 2;
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+      for (int i = 0; i < BM / 16; i++) {
+        const int r = (wave * (BM / 16) + i) * 4 + (lane >> 4);
+        const int c = (lane & 15) ^ (r & 15);
+        off[i] = (uint32_t)(r < rows ? r : rows - 1) * (uint32_t)(a.K * 2) + 16 * c;
+      }
+    } else {
+      base = (const uint8_t*)a.x + m0 * (XT == kXE4M3 ? a.K : a.K / 2);
+      sbase = XT == kXNVFP4 ? a.xs + m0 * KB : nullptr;
+#pragma unroll
+      for (int i = 0; i < kBlocks / 2; i++) {
+        const int r = i * 64 + (threadIdx.x >> 2), p = threadIdx.x & 3;  // blocks 2p, 2p + 1 of row r
+        const uint32_t row = r < rows ? r : rows - 1;
+        off[i] = row * (uint32_t)(XT == kXE4M3 ? a.K : a.K / 2) + p * (XT == kXE4M3 ? 32 : 16);
+        if constexpr (XT == kXNVFP4) soff[i] = row * (uint32_t)KB + 2 * p;
+      }
+    }
+  }
+
+  // Start the loads of the whole step that begins at block b: into LDS for
+  // 16-bit activations, into registers for those that are decoded first.
+  __device__ __forceinline__ void load(int64_t b, uint8_t* lds) {
+    if constexpr (kDirect) {
+      const uint8_t* p = base + b * 32;
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+      for (int i = 0; i < BM / 16; i++)
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(p + off[i]),
+                                         (__attribute__((address_space(3))) void*)(lds + (wave * (BM / 16) + i) * 1024),
+                                         16, 0, 0);
+    } else if constexpr (XT == kXE4M3) {
+      const uint8_t* p = base + b * 16;
+#pragma unroll
+      for (int i = 0; i < kBlocks / 2; i++) {
+        const uint4 t = *reinterpret_cast<const uint4*>(p + off[i]), u = *reinterpret_cast<const uint4*>(p + off[i] + 16);
+        regs[i][0] = t.x, regs[i][1] = t.y, regs[i][2] = t.z, regs[i][3] = t.w;
+        regs[i][4] = u.x, regs[i][5] = u.y, regs[i][6] = u.z, regs[i][7] = u.w;
+      }
+    } else {
+      const uint8_t *p = base + b * 8, *q = sbase + b;
+#pragma unroll
+      for (int i = 0; i < kBlocks / 2; i++) {
+        const Bytes16 t = *reinterpret_cast<const Bytes16*>(p + off[i]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) regs[i][j] = t.v[j];
+        sreg[i] = reinterpret_cast<const Bytes2*>(q + soff[i])->v;
+      }
+    }
+  }
+
+  // Decode what load() brought to registers and store it to LDS.
+  __device__ __forceinline__ void store(uint8_t* lds) {
+    if constexpr (!kDirect) {
+#pragma unroll
+      for (int i = 0; i < kBlocks / 2; i++) {
+        Frag f[4];
+        if constexpr (XT == kXE4M3) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            f[j / 2].u[2 * (j & 1)] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)regs[i][j], 1.0f, false));
+            f[j / 2].u[2 * (j & 1) + 1] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)regs[i][j], 1.0f, true));
+          }
+        } else {
+          decode_blocks<false>(regs[i], sreg[i], f);
+        }
+        put(lds, i * 64 + (threadIdx.x >> 2), 4 * (threadIdx.x & 3), f);
+      }
+    }
+  }
+
+  // Chunks c .. c + 3 of row r.
+  static __device__ __forceinline__ void put(uint8_t* lds, int r, int c, const Frag* f) {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      *reinterpret_cast<h8*>(lds + r * 256 + (((c + j) ^ (r & 15)) << 4)) = f[j].h;
+  }
+
+  // The last step when K ends inside it: blocks past the end are zero.
+  __device__ __forceinline__ void load_last(const LinearArgs& a, int64_t m0, int rows, int64_t b, uint8_t* lds) {
+#pragma unroll 1
+    for (int i = 0; i < BM / 64; i++) {
+      const int r = i * 64 + (threadIdx.x >> 2), p = threadIdx.x & 3;
+      Frag f[4];
+      load_x<XT>(a, m0 + (r < rows ? r : rows - 1), b + 2 * p, a.K / 16, f);
+      put(lds, r, 4 * p, f);
+    }
+  }
+};
+
+// The order of a launch's tiles. Consecutive workgroups go to the 8 XCDs in
+// turn, so each XCD gets a contiguous range of the tiles; along it, 8 row tiles
+// are taken per column tile, so that the workgroups that run on an XCD at a
+// time share their rows of both operands in its L2.
+__device__ __forceinline__ void tile_of(int64_t m_tiles, int64_t n_tiles, int64_t& tm, int64_t& tn) {
+  const int64_t total = m_tiles * n_tiles, id = blockIdx.x;
+  const int64_t x = id % 8, base = total / 8, more = total % 8;
+  const int64_t t = x * base + (x < more ? x : more) + id / 8;
+  const int64_t band = t / (8 * n_tiles), in = t % (8 * n_tiles);
+  const int64_t high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
+  tm = band * 8 + in % high;
+  tn = in / high;
+}
+
+template <int XT, int BM>
+__global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_tiles, int64_t n_tiles) {
+  constexpr bool BF16 = XT == kBF16;
+  constexpr int MT = BM / 16;
+  __shared__ __align__(16) uint8_t lds[2][BM * 256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 15, g4 = lane >> 4;
+  int64_t tm, tn;
+  tile_of(m_tiles, n_tiles, tm, tn);
+  RowTile rt{tm * BM, a.M, 0};
+  if (a.offs) {
+    if (a.status && blockIdx.x == 0 && wave == 0) check_offs(a);
+    rt = find_tile(a.offs, a.G, a.M, BM, tm);
+    if (rt.g < 0) return;
+  }
+  const int rows = rt.end - rt.m0 < BM ? (int)(rt.end - rt.m0) : BM;
+  const int64_t n0 = tn * 256 + wave * 64;
+  if (a.offs && rt.g == a.G) {
+    for (int r = col; r < rows; r += 16)
+      for (int i = 0; i < 4; i++) zero4(a, rt.m0 + r, n0 + 16 * i + 4 * g4);
+    return;
+  }
+  const int64_t KB = a.K / 16;
+  const int steps = (int)((KB + 7) / 8), whole = (int)(KB / 8);
+
+  const uint8_t* wc = a.w + ((int64_t)rt.g * a.N + (n0 < a.N ? n0 : a.N - 1)) * (a.K / 2);
+  const uint8_t* wsc = a.ws + ((int64_t)rt.g * a.N + (n0 < a.N ? n0 : a.N - 1)) * KB;
+  uint32_t woff[4], wsoff[4], codes[4][4], scales[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int64_t n = n0 + 16 * i + col;
+    const uint32_t r = n < a.N ? 16 * i + col : n0 < a.N ? (uint32_t)(a.N - 1 - n0) : 0;
+    woff[i] = r * (uint32_t)(a.K / 2) + 16 * g4;
+    wsoff[i] = r * (uint32_t)KB + 2 * g4;
+  }
+  auto load_w = [&](int step) {
+    if (step < whole) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const Bytes16 t = *reinterpret_cast<const Bytes16*>(wc + (int64_t)step * 64 + woff[i]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) codes[i][j] = t.v[j];
+        scales[i] = reinterpret_cast<const Bytes2*>(wsc + (int64_t)step * 8 + wsoff[i])->v;
+      }
+    } else {
+      const int64_t b = (int64_t)step * 8 + 2 * g4;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        uint2 t = {0, 0}, u = {0, 0};
+        scales[i] = 0;
+        if (b < KB) {
+          t = *reinterpret_cast<const uint2*>(wc + (int64_t)step * 64 + woff[i]);
+          scales[i] = wsc[(int64_t)step * 8 + wsoff[i]];
+        }
+        if (b + 1 < KB) {
+          u = *reinterpret_cast<const uint2*>(wc + (int64_t)step * 64 + woff[i] + 8);
+          scales[i] |= (uint32_t)wsc[(int64_t)step * 8 + wsoff[i] + 1] << 8;
+        }
+        codes[i][0] = t.x, codes[i][1] = t.y, codes[i][2] = u.x, codes[i][3] = u.y;
+      }
+    }
+  };
+
+  XStage<XT, BM> xs;
+  xs.init(a, rt.m0, rows);
+  auto load_x_step = [&](int step, uint8_t* to) {
+    if (step < whole)
+      xs.load((int64_t)step * 8, to);
+    else
+      xs.load_last(a, rt.m0, rows, (int64_t)step * 8, to);
+  };
+
+  f32x4 acc[4][MT];
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+#pragma unroll
+    for (int j = 0; j < MT; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  uint32_t roff[4];  // fragment c = 2 h + j of this lane: LDS byte offset in rows 0 .. 15
+#pragma unroll
+  for (int c = 0; c < 4; c++) roff[c] = col * 256 + (((4 * g4 + c) ^ col) << 4);
+
+  if (steps > 0) {
+    load_x_step(0, lds[0]);
+    if (0 < whole) xs.store(lds[0]);
+    load_w(0);
+  }
+  for (int step = 0; step < steps; step++) {
+    // this step's tile is in LDS (the wait covers the direct loads), and no
+    // wave reads the other one any more
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    const uint8_t* cur = lds[step & 1];
+    uint8_t* next = lds[(step & 1) ^ 1];
+    if (step + 1 < steps) load_x_step(step + 1, next);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      Frag w[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const f32x2 s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)scales[i], 1.0f, false);
+        const h2 s16 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales[i], 1.0f, false);
+        const h2 sh = h ? __builtin_shufflevector(s16, s16, 1, 1) : __builtin_shufflevector(s16, s16, 0, 0);
+        decode8<BF16>(codes[i][2 * h], h ? s.y : s.x, sh, w[i][0].u);
+        decode8<BF16>(codes[i][2 * h + 1], h ? s.y : s.x, sh, w[i][1].u);
+      }
+      // the registers of the codes are free again: half a step is left
+      if (h == 1 && step + 1 < steps) load_w(step + 1);
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          Frag x;
+          x.h = *reinterpret_cast<const h8*>(cur + roff[2 * h + j] + m * 4096);
+#pragma unroll
+          for (int i = 0; i < 4; i++) acc[i][m] = mfma<BF16>(w[i][j], x, acc[i][m]);
+        }
+      }
+    }
+    if (step + 1 < whole) xs.store(next);
+  }
+  // Each wave turns its sums by way of its quarter of the LDS, half of the rows
+  // at a time, so that 16 lanes store 64 neighbouring columns of a row.
+  __syncthreads();
+  uint8_t* mine = &lds[0][0] + wave * (BM * 128);
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+#pragma unroll
+    for (int m = 0; m < MT / 2; m++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<f32x4*>(mine + (16 * m + col) * 256 + (((4 * i + g4) ^ col) << 4)) = acc[i][half * (MT / 2) + m];
+#pragma unroll 1
+    for (int it = 0; it < BM / 8; it++) {
+      const int lr = 4 * it + g4, r = half * (BM / 2) + lr;
+      const f32x4 v = *reinterpret_cast<const f32x4*>(mine + lr * 256 + ((col ^ (lr & 15)) << 4));
+      const int64_t n = n0 + 4 * col;
+      if (r < rows && n < a.N) finish4(a, rt.g, rt.m0 + r, n, v);
+    }
+  }
+}
+
 constexpr int64_t kMaxGrid = INT32_MAX;
 
 // The most tiles of `rows` rows that M rows in G groups and a tail can need:
@@ -323,6 +653,17 @@ int64_t max_tiles(int64_t M, int64_t G, int64_t rows) {
 
 template <int XT>
 hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
+  // rows that share a weight, and whether the tile kernel's 32-bit offsets
+  // within a tile reach (256 rows of 2 K bytes)
+  const int64_t rows = a.offs ? (a.M + a.G - 1) / a.G : a.M;
+  if (rows > 64 && a.K <= (int64_t(1) << 22)) {
+    constexpr int BM = 128;
+    const int64_t nt = (a.N + 255) / 256;
+    const int64_t mt = a.offs ? max_tiles(a.M, a.G, BM) : (a.M + BM - 1) / BM;
+    if (mt > kMaxGrid / nt) return hipErrorInvalidConfiguration;
+    k_linear_tile<XT, BM><<<dim3((unsigned)(mt * nt)), dim3(256), 0, s>>>(a, mt, nt);
+    return hipGetLastError();
+  }
   constexpr int WAVES = 8;
   const int64_t nt = (a.N + 15) / 16;
   const int64_t mt = a.offs ? max_tiles(a.M, a.G, 16) : (a.M + 15) / 16;
