@@ -149,6 +149,12 @@ struct RowTile {
   int g;
 };
 
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // Tile `t` of the rows cut into groups and each group into tiles of `rows`
 // rows, in group order, the tail last. The wave holds 64 groups' offsets at a
 // time, one per lane, and finds the tile by a running sum of the groups' tile
@@ -183,9 +189,9 @@ __device__ RowTile find_tile(const int32_t* offs, int G, int64_t M, int64_t rows
       const int l = __ffsll(hit) - 1;
       const int64_t first = tiles + __shfl(sum - n, l, 64);
       RowTile r;
-      r.m0 = __shfl(start, l, 64) + (t - first) * rows;
-      r.end = __shfl(run, l, 64);
-      r.g = base + l;
+      r.m0 = uniform(__shfl(start, l, 64) + (t - first) * rows);
+      r.end = uniform(__shfl(run, l, 64));
+      r.g = __builtin_amdgcn_readfirstlane(base + l);
       return r;
     }
     tiles += __shfl(sum, 63, 64);
@@ -505,7 +511,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
   constexpr bool BF16 = XT == kBF16;
   constexpr int MT = BM / 16;
   __shared__ __align__(16) uint8_t lds[2][BM * 256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g4 = lane >> 4;
   int64_t tm, tn;
   tile_of(m_tiles, n_tiles, tm, tn);
@@ -523,53 +529,30 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
     return;
   }
   const int64_t KB = a.K / 16;
-  const int steps = (int)((KB + 7) / 8), whole = (int)(KB / 8);
+  const int whole = (int)(KB / 8);  // 128-deep steps; a part of one may follow
 
-  const uint8_t* wc = a.w + ((int64_t)rt.g * a.N + (n0 < a.N ? n0 : a.N - 1)) * (a.K / 2);
-  const uint8_t* wsc = a.ws + ((int64_t)rt.g * a.N + (n0 < a.N ? n0 : a.N - 1)) * KB;
+  // weight rows: uniform base, 32-bit lane offsets; columns past the end read
+  // the last row
+  const int64_t w0 = (int64_t)rt.g * a.N + (n0 < a.N ? n0 : a.N - 1);
+  const uint8_t* wc = a.w + w0 * (a.K / 2);
+  const uint8_t* wsc = a.ws + w0 * KB;
+  const int wrows = n0 < a.N ? (a.N - n0 < 64 ? (int)(a.N - n0) : 64) : 1;
   uint32_t woff[4], wsoff[4], codes[4][4], scales[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int64_t n = n0 + 16 * i + col;
-    const uint32_t r = n < a.N ? 16 * i + col : n0 < a.N ? (uint32_t)(a.N - 1 - n0) : 0;
+    const uint32_t r = 16 * i + col < wrows ? 16 * i + col : wrows - 1;
     woff[i] = r * (uint32_t)(a.K / 2) + 16 * g4;
     wsoff[i] = r * (uint32_t)KB + 2 * g4;
   }
   auto load_w = [&](int step) {
-    if (step < whole) {
+    const uint8_t *p = wc + (int64_t)step * 64, *q = wsc + (int64_t)step * 8;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const Bytes16 t = *reinterpret_cast<const Bytes16*>(wc + (int64_t)step * 64 + woff[i]);
+    for (int i = 0; i < 4; i++) {
+      const Bytes16 t = *reinterpret_cast<const Bytes16*>(p + woff[i]);
 #pragma unroll
-        for (int j = 0; j < 4; j++) codes[i][j] = t.v[j];
-        scales[i] = reinterpret_cast<const Bytes2*>(wsc + (int64_t)step * 8 + wsoff[i])->v;
-      }
-    } else {
-      const int64_t b = (int64_t)step * 8 + 2 * g4;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        uint2 t = {0, 0}, u = {0, 0};
-        scales[i] = 0;
-        if (b < KB) {
-          t = *reinterpret_cast<const uint2*>(wc + (int64_t)step * 64 + woff[i]);
-          scales[i] = wsc[(int64_t)step * 8 + wsoff[i]];
-        }
-        if (b + 1 < KB) {
-          u = *reinterpret_cast<const uint2*>(wc + (int64_t)step * 64 + woff[i] + 8);
-          scales[i] |= (uint32_t)wsc[(int64_t)step * 8 + wsoff[i] + 1] << 8;
-        }
-        codes[i][0] = t.x, codes[i][1] = t.y, codes[i][2] = u.x, codes[i][3] = u.y;
-      }
+      for (int j = 0; j < 4; j++) codes[i][j] = t.v[j];
+      scales[i] = reinterpret_cast<const Bytes2*>(q + wsoff[i])->v;
     }
-  };
-
-  XStage<XT, BM> xs;
-  xs.init(a, rt.m0, rows);
-  auto load_x_step = [&](int step, uint8_t* to) {
-    if (step < whole)
-      xs.load((int64_t)step * 8, to);
-    else
-      xs.load_last(a, rt.m0, rows, (int64_t)step * 8, to);
   };
 
   f32x4 acc[4][MT];
@@ -582,21 +565,14 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
 #pragma unroll
   for (int c = 0; c < 4; c++) roff[c] = col * 256 + (((4 * g4 + c) ^ col) << 4);
 
-  if (steps > 0) {
-    load_x_step(0, lds[0]);
-    if (0 < whole) xs.store(lds[0]);
-    load_w(0);
-  }
-  for (int step = 0; step < steps; step++) {
-    // this step's tile is in LDS (the wait covers the direct loads), and no
-    // wave reads the other one any more
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    const uint8_t* cur = lds[step & 1];
-    uint8_t* next = lds[(step & 1) ^ 1];
-    if (step + 1 < steps) load_x_step(step + 1, next);
+  // Multiply the staged step by the codes in registers; `refill` runs once
+  // the codes have been decoded and leaves half a step for its loads.
+  auto multiply = [&](const uint8_t* cur, auto refill) {
 #pragma unroll
     for (int h = 0; h < 2; h++) {
+      Frag x[2][2];
+#pragma unroll
+      for (int j = 0; j < 2; j++) x[0][j].h = *reinterpret_cast<const h8*>(cur + roff[2 * h + j]);
       Frag w[4][2];
 #pragma unroll
       for (int i = 0; i < 4; i++) {
@@ -606,20 +582,63 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
         decode8<BF16>(codes[i][2 * h], h ? s.y : s.x, sh, w[i][0].u);
         decode8<BF16>(codes[i][2 * h + 1], h ? s.y : s.x, sh, w[i][1].u);
       }
-      // the registers of the codes are free again: half a step is left
-      if (h == 1 && step + 1 < steps) load_w(step + 1);
+      if (h == 1) refill();
 #pragma unroll
       for (int m = 0; m < MT; m++) {
+        if (m + 1 < MT) {
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-          Frag x;
-          x.h = *reinterpret_cast<const h8*>(cur + roff[2 * h + j] + m * 4096);
-#pragma unroll
-          for (int i = 0; i < 4; i++) acc[i][m] = mfma<BF16>(w[i][j], x, acc[i][m]);
+          for (int j = 0; j < 2; j++)
+            x[(m + 1) & 1][j].h = *reinterpret_cast<const h8*>(cur + roff[2 * h + j] + (m + 1) * 4096);
         }
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) acc[i][m] = mfma<BF16>(w[i][j], x[m & 1][j], acc[i][m]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (step + 1 < whole) xs.store(next);
+  };
+
+  XStage<XT, BM> xs;
+  xs.init(a, rt.m0, rows);
+  if (whole > 0) {
+    xs.load(0, lds[0]);
+    load_w(0);
+    xs.store(lds[0]);
+  }
+  for (int step = 0; step < whole; step++) {
+    // this step's tile is in LDS (the wait covers the direct loads), and no
+    // wave reads the other one any more
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    uint8_t* next = lds[(step & 1) ^ 1];
+    const bool more = step + 1 < whole;
+    if (more) xs.load((int64_t)(step + 1) * 8, next);
+    multiply(lds[step & 1], [&] {
+      if (more) load_w(step + 1);
+    });
+    if (more) xs.store(next);
+  }
+  if (KB % 8) {  // the part of a step that is left: zeros past the end
+    uint8_t* last = lds[whole & 1];  // not the tile that a wave may still read
+    xs.load_last(a, rt.m0, rows, (int64_t)whole * 8, last);
+    const int64_t b = (int64_t)whole * 8 + 2 * g4;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      uint2 t = {0, 0}, u = {0, 0};
+      scales[i] = 0;
+      if (b < KB) {
+        t = *reinterpret_cast<const uint2*>(wc + (int64_t)whole * 64 + woff[i]);
+        scales[i] = wsc[(int64_t)whole * 8 + wsoff[i]];
+      }
+      if (b + 1 < KB) {
+        u = *reinterpret_cast<const uint2*>(wc + (int64_t)whole * 64 + woff[i] + 8);
+        scales[i] |= (uint32_t)wsc[(int64_t)whole * 8 + wsoff[i] + 1] << 8;
+      }
+      codes[i][0] = t.x, codes[i][1] = t.y, codes[i][2] = u.x, codes[i][3] = u.y;
+    }
+    __syncthreads();
+    multiply(last, [] {});
   }
   // Each wave turns its sums by way of its quarter of the LDS, half of the rows
   // at a time, so that 16 lanes store 64 neighbouring columns of a row.
