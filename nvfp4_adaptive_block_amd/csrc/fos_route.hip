@@ -21,8 +21,9 @@
 namespace fos {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;  // forward
 constexpr int kWaves = kThreads / 64;
+constexpr int kMaxExperts = 1024;
 
 template <int DT>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -40,173 +41,381 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
     ((uint16_t*)p)[i] = (uint16_t)(DT == kBF16 ? pack_bf16(v, 0.0f) : pack_f16(v, 0.0f));
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) { return (a != a) ? a : (b != b) ? b : a > b ? a : b; }
+// Four values from element i on, at the elements' own alignment.
+struct __attribute__((packed, aligned(2))) Quad16 {
+  uint32_t v[2];
+};
+struct __attribute__((packed, aligned(4))) Quad32 {
+  float v[4];
+};
 
-// softmax of row t in lane-strided columns: p[i] is column lane + 64 i.
-template <int DT, int EPL>
-__device__ __forceinline__ void softmax_row(const void* logits, int64_t t, int E, float* p) {
-  const int lane = threadIdx.x & 63;
-  float top = -__builtin_huge_valf();
+template <int DT>
+__device__ __forceinline__ void load4(const void* p, int64_t i, float* v) {
+  if constexpr (DT == kFP32) {
+    const Quad32 t = *reinterpret_cast<const Quad32*>((const float*)p + i);
 #pragma unroll
-  for (int i = 0; i < EPL; i++) {
-    const int e = lane + 64 * i;
-    p[i] = e < E ? load1<DT>(logits, t * E + e) : -__builtin_huge_valf();
-    top = max_nan(top, p[i]);
+    for (int j = 0; j < 4; j++) v[j] = t.v[j];
+  } else {
+    const Quad16 t = *reinterpret_cast<const Quad16*>((const uint16_t*)p + i);
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      v[2 * j] = DT == kBF16 ? bf16_lo(t.v[j]) : f16_lo(t.v[j]);
+      v[2 * j + 1] = DT == kBF16 ? bf16_hi(t.v[j]) : f16_hi(t.v[j]);
+    }
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor(top, d, 64));
-  const bool none = top == -__builtin_huge_valf();
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < EPL; i++) {
-    p[i] = none ? 0.0f : expf(p[i] - top);
-    sum += p[i];
-  }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-  const float inv = none ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int i = 0; i < EPL; i++) p[i] *= inv;
 }
 
-// Each workgroup takes a contiguous range of rows and leaves E column sums, E
-// counts and its number of live rows in the workspace.
-template <int DT, int EPL>
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
+  if constexpr (DT == kFP32) {
+    *reinterpret_cast<Quad32*>((float*)p + i) = Quad32{{v[0], v[1], v[2], v[3]}};
+  } else {
+    Quad16 t;
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+      t.v[j] = DT == kBF16 ? pack_bf16(v[2 * j], v[2 * j + 1]) : pack_f16(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<Quad16*>((uint16_t*)p + i) = t;
+  }
+}
+
+// Reductions over the 16 lanes of a row, by rotations within a DPP row: each
+// level adds the same pair in either lane, so all lanes get the same bits.
+constexpr int kRor = 0x120;
+__device__ __forceinline__ float sum16(float v) {
+  v += dpp<kRor + 8>(v);
+  v += dpp<kRor + 4>(v);
+  v += dpp<kRor + 2>(v);
+  v += dpp<kRor + 1>(v);
+  return v;
+}
+__device__ __forceinline__ float max16(float v) {  // a NaN is dropped
+  v = __builtin_fmaxf(v, dpp<kRor + 8>(v));
+  v = __builtin_fmaxf(v, dpp<kRor + 4>(v));
+  v = __builtin_fmaxf(v, dpp<kRor + 2>(v));
+  v = __builtin_fmaxf(v, dpp<kRor + 1>(v));
+  return v;
+}
+
+// A row of logits takes 16 lanes, so that a wave works on four and a row's
+// reductions are four register rotations each. Lane l owns, in piece i, the
+// four columns from 64 i + 4 l on. The lane in which E ends reads the row's
+// last four instead and drops those that its neighbour has; every slot's column
+// is `at(i) + j`, and it is the lane's own where mine() says so. (E below 4:
+// every lane reads by element.)
+template <int P>
+struct Columns {
+  int E, first;
+  __device__ __forceinline__ Columns(int e) : E(e), first(4 * (threadIdx.x & 15)) {}
+  __device__ __forceinline__ int begin(int i) const { return 64 * i + first; }
+  __device__ __forceinline__ int at(int i) const {
+    const int b = begin(i);
+    return E < 4 ? b : b + 4 <= E ? b : E - 4;
+  }
+  __device__ __forceinline__ bool mine(int i, int j) const { return at(i) + j >= begin(i) && at(i) + j < E; }
+};
+
+template <int DT, int P>
+__device__ __forceinline__ void load_row(const void* logits, int64_t t, const Columns<P>& c, float (*v)[4]) {
+#pragma unroll
+  for (int i = 0; i < P; i++) {
+    if (c.E < 4) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[i][j] = c.mine(i, j) ? load1<DT>(logits, t * c.E + c.at(i) + j) : 0.0f;
+    } else {
+      load4<DT>(logits, t * c.E + c.at(i), v[i]);
+    }
+  }
+}
+
+// v becomes its softmax; slots that are not the lane's own and rows that are
+// not live become 0. exp is the base-2 instruction: relative error about
+// |v - max| half steps. A NaN goes through exp into the sum and the whole row.
+template <int P>
+__device__ __forceinline__ void softmax(const Columns<P>& c, bool live, float (*v)[4]) {
+  const float low = -__builtin_huge_valf();
+  float top = low;
+#pragma unroll
+  for (int i = 0; i < P; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      v[i][j] = live && c.mine(i, j) ? v[i][j] : low;
+      top = __builtin_fmaxf(top, v[i][j]);
+    }
+  top = max16(top);
+  const float shift = top == low ? 0.0f : top;  // every logit -inf: each exp is 0
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      v[i][j] = __builtin_amdgcn_exp2f((v[i][j] - shift) * 1.44269504088896341f);
+      sum += v[i][j];
+    }
+  sum = sum16(sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < P; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[i][j] *= inv;
+}
+
+// The workspace: per workgroup E column sums and E counts, live rows, then the
+// joined columns and the counter of the second launch.
+struct Work {
+  float* sums;
+  int32_t* counts;
+  int32_t* live;
+  double* col;
+  int32_t* cnt;
+  int32_t* done;
+  __host__ __device__ static int64_t bytes(int64_t blocks, int64_t E) {
+    return (blocks * E * 8 + blocks * 4 + 7) / 8 * 8 + E * 12 + 4;
+  }
+  __device__ Work(void* p, int64_t blocks, int64_t E) {
+    sums = (float*)p;
+    counts = (int32_t*)(sums + blocks * E);
+    live = counts + blocks * E;
+    col = (double*)((uint8_t*)p + (blocks * E * 8 + blocks * 4 + 7) / 8 * 8);
+    cnt = (int32_t*)(col + E);
+    done = cnt + E;
+  }
+};
+
+// The results from each expert's column sum and count (LDS, E of each), by all
+// threads of a workgroup; thread t takes `per` neighbouring experts.
+__device__ void finish(const BalanceArgs& a, const double* col, const int32_t* cnt, int32_t live) {
+  __shared__ int32_t wave_cnt[16], wave_pad[16];
+  __shared__ double wave_loss[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x / 64;
+  const int per = (a.E + blockDim.x - 1) / blockDim.x;
+  const int e0 = threadIdx.x * per, e1 = e0 + per < a.E ? e0 + per : a.E;
+  int32_t c = 0, pad = 0;
+  for (int e = e0; e < e1; e++) {
+    c += cnt[e];
+    pad += (int32_t)(((int64_t)cnt[e] + a.align - 1) / a.align * a.align);
+  }
+  int32_t sum = c, run = pad;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    sum += __shfl_xor(sum, d, 64);
+    const int32_t o = __shfl_up(run, d, 64);
+    if (lane >= d) run += o;
+  }
+  if (lane == 63) {
+    wave_cnt[wave] = sum;
+    wave_pad[wave] = run;
+  }
+  __syncthreads();
+  int32_t all = 0, before = run - pad;
+  for (int w = 0; w < waves; w++) {
+    all += wave_cnt[w];
+    if (w < wave) before += wave_pad[w];
+  }
+  const double scale = (double)a.coef * a.E / ((double)(all > 1 ? all : 1) * (double)(live > 1 ? live : 1));
+  double loss = 0.0;
+  for (int e = e0; e < e1; e++) {
+    const double slope = scale * cnt[e];
+    loss += slope * col[e];
+    before += (int32_t)(((int64_t)cnt[e] + a.align - 1) / a.align * a.align);
+    a.counts[e] = cnt[e];
+    a.slope[e] = (float)slope;
+    if (a.offs) a.offs[e] = before;
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) loss += __shfl_xor(loss, d, 64);
+  if (lane == 0) wave_loss[wave] = loss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < waves; w++) loss += wave_loss[w];
+    *a.loss = (float)loss;
+  }
+}
+
+// Each workgroup takes a contiguous range of rows, its waves four at a time
+// (the next four are loaded while these are worked on), and leaves E column
+// sums, E counts and its number of live rows in the workspace; a workgroup that
+// is alone finishes.
+template <int DT, int P>
 __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t per = (a.T + gridDim.x - 1) / gridDim.x;
-  const int64_t t0 = per * blockIdx.x, t1 = t0 + per < a.T ? t0 + per : a.T;
-  extern __shared__ float lds[];
-  float* sums = lds;                              // [kWaves][E]
-  int32_t* hist = (int32_t*)(lds + kWaves * a.E);  // [E]
+  const int64_t t0 = per * blockIdx.x < a.T ? per * blockIdx.x : a.T, t1 = t0 + per < a.T ? t0 + per : a.T;
+  __shared__ int32_t hist[64 * P];
+  __shared__ float sums[kWaves][64 * P];
   __shared__ int32_t live_rows;
   for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
   if (threadIdx.x == 0) live_rows = 0;
   __syncthreads();
-  float acc[EPL] = {};
+  const Columns<P> c(a.E);
+  float acc[P][4] = {}, next[P][4];
   int32_t live = 0;
-  for (int64_t t = t0 + wave; t < t1; t += kWaves) {
-    if (a.mask && !a.mask[t]) continue;
-    live++;
-    float p[EPL];
-    softmax_row<DT, EPL>(a.logits, t, a.E, p);
+  int64_t t = t0 + wave * 4 + (lane >> 4);
+  bool have = t < t1 && (!a.mask || a.mask[t]);
+  if (have) load_row<DT, P>(a.logits, t, c, next);
+  for (int64_t base = t0 + wave * 4; base < t1; base += 4 * kWaves) {
+    float v[P][4];
 #pragma unroll
-    for (int i = 0; i < EPL; i++) acc[i] += p[i];
+    for (int i = 0; i < P; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[i][j] = next[i][j];
+    const bool now = have;
+    t += 4 * kWaves;
+    have = t < t1 && (!a.mask || a.mask[t]);
+    if (have) load_row<DT, P>(a.logits, t, c, next);
+    softmax(c, now, v);
+    live += now;
+#pragma unroll
+    for (int i = 0; i < P; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) acc[i][j] += v[i][j];
   }
-  if (lane == 0) atomicAdd(&live_rows, live);
-#pragma unroll
-  for (int i = 0; i < EPL; i++)
-    if (lane + 64 * i < a.E) sums[wave * a.E + lane + 64 * i] = acc[i];
+  // assignments: a thread takes a row's k indices
   bool bad = false;
-  for (int64_t j = t0 * a.k + threadIdx.x; j < t1 * a.k; j += kThreads) {
-    if (a.mask && !a.mask[j / a.k]) continue;
-    const int64_t e = a.idx64 ? ((const int64_t*)a.idx)[j] : (int64_t)((const int32_t*)a.idx)[j];
-    if (e >= 0 && e < a.E)
-      atomicAdd(&hist[e], 1);
-    else
-      bad |= e != -1;
+  for (int64_t r = t0 + threadIdx.x; r < t1; r += kThreads) {
+    if (a.mask && !a.mask[r]) continue;
+    for (int j = 0; j < a.k; j++) {
+      const int64_t at = r * a.k + j;
+      const int64_t e = a.idx64 ? ((const int64_t*)a.idx)[at] : (int64_t)((const int32_t*)a.idx)[at];
+      if (e >= 0 && e < a.E)
+        atomicAdd(&hist[e], 1);
+      else
+        bad |= e != -1;
+    }
   }
   if (bad && a.status) atomicOr(a.status, kStatusBadIndex);
-  __syncthreads();
-  double* psum = (double*)a.work;                                   // [blocks][E]
-  int32_t* pcount = (int32_t*)(psum + (int64_t)gridDim.x * a.E);    // [blocks][E]
-  int32_t* plive = pcount + (int64_t)gridDim.x * a.E;               // [blocks]
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    double s = 0.0;
-    for (int w = 0; w < kWaves; w++) s += (double)sums[w * a.E + e];
-    psum[(int64_t)blockIdx.x * a.E + e] = s;
-    pcount[(int64_t)blockIdx.x * a.E + e] = hist[e];
-  }
-  if (threadIdx.x == 0) plive[blockIdx.x] = live_rows;
-}
-
-// One workgroup joins the partial rows.
-__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, int blocks) {
-  const double* psum = (const double*)a.work;
-  const int32_t* pcount = (const int32_t*)(psum + (int64_t)blocks * a.E);
-  const int32_t* plive = pcount + (int64_t)blocks * a.E;
-  __shared__ double col[1024];
-  __shared__ int32_t cnt[1024];
-  __shared__ int64_t total;
-  __shared__ int32_t live;
-  if (threadIdx.x == 0) {
-    total = 0;
-    live = 0;
-  }
-  __syncthreads();
-  const int e = threadIdx.x;
-  double s = 0.0;
-  int32_t c = 0;
-  if (e < a.E)
-    for (int b = 0; b < blocks; b++) {
-      s += psum[(int64_t)b * a.E + e];
-      c += pcount[(int64_t)b * a.E + e];
+  // the wave's four rows of lanes, then the waves in order
+#pragma unroll
+  for (int i = 0; i < P; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      acc[i][j] += __shfl_xor(acc[i][j], 16, 64);
+      acc[i][j] += __shfl_xor(acc[i][j], 32, 64);
+      if (lane < 16 && c.mine(i, j)) sums[wave][c.at(i) + j] = acc[i][j];
     }
-  int32_t n = 0;
-  for (int b = threadIdx.x; b < blocks; b += 1024) n += plive[b];
-  atomicAdd(&live, n);
-  atomicAdd((unsigned long long*)&total, (unsigned long long)c);
+  if ((lane & 15) == 0 && live) atomicAdd(&live_rows, live);
   __syncthreads();
-  const double C = total > 1 ? (double)total : 1.0, N = live > 1 ? (double)live : 1.0;
-  const double slope = (double)a.coef * a.E * c / (C * N);
-  if (e < a.E) {
-    a.counts[e] = c;
-    a.slope[e] = (float)slope;
-  }
-  col[e] = e < a.E ? slope * s : 0.0;
-  cnt[e] = e < a.E ? (c + a.align - 1) / a.align * a.align : 0;
-  __syncthreads();
-  for (int d = 512; d >= 1; d >>= 1) {
-    if (e < d) col[e] += col[e + d];
+  if (gridDim.x == 1) {
+    __shared__ double col[64 * P];
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+      double s = 0.0;
+      for (int w = 0; w < kWaves; w++) s += (double)sums[w][e];
+      col[e] = s;
+    }
     __syncthreads();
+    finish(a, col, hist, live_rows);
+    return;
   }
-  for (int d = 1; d < 1024; d <<= 1) {
-    const int32_t v = e >= d ? cnt[e - d] : 0;
-    __syncthreads();
-    cnt[e] += v;
-    __syncthreads();
+  const Work w(a.work, gridDim.x, a.E);
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    float s = sums[0][e];
+    for (int v = 1; v < kWaves; v++) s += sums[v][e];
+    w.sums[(int64_t)blockIdx.x * a.E + e] = s;
+    w.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
   }
-  if (e == 0) *a.loss = (float)col[0];
-  if (a.offs && e < a.E) a.offs[e] = cnt[e];
+  if (threadIdx.x == 0) {
+    w.live[blockIdx.x] = live_rows;
+    if (blockIdx.x == 0) *w.done = 0;
+  }
 }
 
-template <int DT, int EPL>
-__global__ __launch_bounds__(kThreads) void k_balance_backward(BalanceArgs a) {
+// Joins the workgroups' rows: each workgroup takes 32 columns, and the one that
+// ends last (a counter that the first launch cleared) finishes.
+__global__ __launch_bounds__(256) void k_balance_join(BalanceArgs a, int blocks) {
+  const Work w(a.work, blocks, a.E);
+  const int c = threadIdx.x & 31, part = threadIdx.x >> 5, e = blockIdx.x * 32 + c;
+  __shared__ double part_sum[8][32];
+  __shared__ int32_t part_cnt[8][32];
+  __shared__ double col[kMaxExperts];
+  __shared__ int32_t cnt[kMaxExperts];
+  __shared__ int32_t live, last;
+  double s = 0.0;
+  int32_t n = 0;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int b = part; b < blocks; b += 8) {
+      s += (double)w.sums[(int64_t)b * a.E + e];
+      n += w.counts[(int64_t)b * a.E + e];
+    }
+  }
+  part_sum[part][c] = s;
+  part_cnt[part][c] = n;
+  if (threadIdx.x == 0) live = 0;
+  __syncthreads();
+  if (part == 0 && e < a.E) {
+    for (int p = 1; p < 8; p++) {
+      s += part_sum[p][c];
+      n += part_cnt[p][c];
+    }
+    __hip_atomic_store(&w.col[e], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(&w.cnt[e], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(w.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int i = threadIdx.x; i < a.E; i += 256) {
+    col[i] = __hip_atomic_load(&w.col[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    cnt[i] = __hip_atomic_load(&w.cnt[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  int32_t rows = 0;
+  for (int b = threadIdx.x; b < blocks; b += 256) rows += w.live[b];
+  if (rows) atomicAdd(&live, rows);
+  __syncthreads();
+  finish(a, col, cnt, live);
+}
+
+template <int DT, int P>
+__global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a) {
   const int lane = threadIdx.x & 63;
   const float g = *a.dloss;
-  float slope[EPL];
+  const Columns<P> c(a.E);
+  float slope[P][4];
 #pragma unroll
-  for (int i = 0; i < EPL; i++) slope[i] = lane + 64 * i < a.E ? a.slope[lane + 64 * i] : 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); t < a.T; t += (int64_t)gridDim.x * kWaves) {
-    float p[EPL];
-    float dot = 0.0f;
+  for (int i = 0; i < P; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) slope[i][j] = c.mine(i, j) ? a.slope[c.at(i) + j] : 0.0f;
+  for (int64_t base = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4; base < a.T; base += (int64_t)gridDim.x * 16) {
+    const int64_t t = base + (lane >> 4);
+    if (t >= a.T) break;
     const bool live = !a.mask || a.mask[t];
-    if (live) {
-      softmax_row<DT, EPL>(a.logits, t, a.E, p);
+    float v[P][4], dot = 0.0f;
+    if (live) load_row<DT, P>(a.logits, t, c, v);
+    softmax(c, live, v);
 #pragma unroll
-      for (int i = 0; i < EPL; i++) dot += p[i] * slope[i];
+    for (int i = 0; i < P; i++)
 #pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d, 64);
+      for (int j = 0; j < 4; j++) dot += v[i][j] * slope[i][j];
+    dot = sum16(dot);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[i][j] = live ? g * (v[i][j] * (slope[i][j] - dot)) : 0.0f;
+      if (c.E >= 4 && c.at(i) == c.begin(i)) {
+        store4<DT>(a.dlogits, t * a.E + c.at(i), v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          if (c.mine(i, j)) store1<DT>(a.dlogits, t * a.E + c.at(i) + j, v[i][j]);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < EPL; i++)
-      if (lane + 64 * i < a.E)
-        store1<DT>(a.dlogits, t * a.E + lane + 64 * i, live ? g * (p[i] * (slope[i] - dot)) : 0.0f);
   }
 }
 
-template <int DT, int EPL>
+template <int DT, int P>
 hipError_t run(const BalanceArgs& a, bool backward, hipStream_t s) {
   if (backward) {
-    const int64_t g = (a.T + kWaves - 1) / kWaves;
-    k_balance_backward<DT, EPL><<<dim3((unsigned)(g < 2048 ? g : 2048)), dim3(kThreads), 0, s>>>(a);
+    const int64_t g = (a.T + 15) / 16;
+    k_balance_backward<DT, P><<<dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s>>>(a);
     return hipGetLastError();
   }
   const int blocks = balance_blocks(a.T, a.E);
-  k_balance<DT, EPL><<<dim3(blocks), dim3(kThreads), (kWaves + 1) * a.E * 4, s>>>(a);
+  k_balance<DT, P><<<dim3(blocks), dim3(kThreads), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  k_balance_finish<<<dim3(1), dim3(1024), 0, s>>>(a, blocks);
+  if (e != hipSuccess || blocks == 1) return e;
+  k_balance_join<<<dim3((a.E + 31) / 32), dim3(256), 0, s>>>(a, blocks);
   return hipGetLastError();
 }
 
@@ -230,14 +439,11 @@ hipError_t by_type(int dt, const BalanceArgs& a, bool backward, hipStream_t s) {
 }  // namespace
 
 int balance_blocks(int64_t T, int) {
-  const int64_t b = (T + 31) / 32;
-  return b < 1 ? 1 : b > 256 ? 256 : (int)b;
+  const int64_t b = (T + 63) / 64;
+  return b < 1 ? 1 : b > 512 ? 512 : (int)b;
 }
 
-int64_t balance_workspace(int64_t T, int E) {
-  const int64_t b = balance_blocks(T, E);
-  return b * E * 12 + b * 4;
-}
+int64_t balance_workspace(int64_t T, int E) { return Work::bytes(balance_blocks(T, E), E); }
 
 hipError_t launch_balance(int dt, const BalanceArgs& a, hipStream_t s) { return by_type(dt, a, false, s); }
 hipError_t launch_balance_backward(int dt, const BalanceArgs& a, hipStream_t s) { return by_type(dt, a, true, s); }
