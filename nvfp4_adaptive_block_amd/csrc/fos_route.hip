@@ -100,22 +100,26 @@ __device__ __forceinline__ float max16(float v) {  // a NaN is dropped
 // reductions are four register rotations each. Lane l owns, in piece i, the
 // four columns from 64 i + 4 l on. The lane in which E ends reads the row's
 // last four instead and drops those that its neighbour has; every slot's column
-// is `at(i) + j`, and it is the lane's own where mine() says so. (E below 4:
-// every lane reads by element.)
-template <int P>
+// is at(i) + j, and it is the lane's own where mine() says so. (E below 4: every
+// lane reads by element.) FULL: E is 64 P and every slot is its lane's own, which
+// the compiler then knows: the comparisons are a fifth of the instructions, and
+// these kernels are near the vector units' limit.
+template <int P, bool FULL>
 struct Columns {
   int E, first;
-  __device__ __forceinline__ Columns(int e) : E(e), first(4 * (threadIdx.x & 15)) {}
+  __device__ __forceinline__ Columns(int e) : E(FULL ? 64 * P : e), first(4 * (threadIdx.x & 15)) {}
   __device__ __forceinline__ int begin(int i) const { return 64 * i + first; }
   __device__ __forceinline__ int at(int i) const {
     const int b = begin(i);
-    return E < 4 ? b : b + 4 <= E ? b : E - 4;
+    return FULL || E < 4 ? b : b + 4 <= E ? b : E - 4;
   }
-  __device__ __forceinline__ bool mine(int i, int j) const { return at(i) + j >= begin(i) && at(i) + j < E; }
+  __device__ __forceinline__ bool mine(int i, int j) const {
+    return FULL || (at(i) + j >= begin(i) && at(i) + j < E);
+  }
 };
 
-template <int DT, int P>
-__device__ __forceinline__ void load_row(const void* logits, int64_t t, const Columns<P>& c, float (*v)[4]) {
+template <int DT, int P, bool FULL>
+__device__ __forceinline__ void load_row(const void* logits, int64_t t, const Columns<P, FULL>& c, float (*v)[4]) {
 #pragma unroll
   for (int i = 0; i < P; i++) {
     if (c.E < 4) {
@@ -130,8 +134,8 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t t, const Co
 // v becomes its softmax; slots that are not the lane's own and rows that are
 // not live become 0. exp is the base-2 instruction: relative error about
 // |v - max| half steps. A NaN goes through exp into the sum and the whole row.
-template <int P>
-__device__ __forceinline__ void softmax(const Columns<P>& c, bool live, float (*v)[4]) {
+template <int P, bool FULL>
+__device__ __forceinline__ void softmax(const Columns<P, FULL>& c, bool live, float (*v)[4]) {
   const float low = -__builtin_huge_valf();
   float top = low;
 #pragma unroll
@@ -189,10 +193,13 @@ __device__ void finish(const BalanceArgs& a, const double* col, const int32_t* c
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x / 64;
   const int per = (a.E + blockDim.x - 1) / blockDim.x;
   const int e0 = threadIdx.x * per, e1 = e0 + per < a.E ? e0 + per : a.E;
+  // the host has checked that no padded count or sum of them exceeds int32
+  const uint32_t align = a.align;
+  auto padded = [&](int e) { return (int32_t)(((uint32_t)cnt[e] + align - 1) / align * align); };
   int32_t c = 0, pad = 0;
   for (int e = e0; e < e1; e++) {
     c += cnt[e];
-    pad += (int32_t)(((int64_t)cnt[e] + a.align - 1) / a.align * a.align);
+    pad += padded(e);
   }
   int32_t sum = c, run = pad;
 #pragma unroll
@@ -216,7 +223,7 @@ __device__ void finish(const BalanceArgs& a, const double* col, const int32_t* c
   for (int e = e0; e < e1; e++) {
     const double slope = scale * cnt[e];
     loss += slope * col[e];
-    before += (int32_t)(((int64_t)cnt[e] + a.align - 1) / a.align * a.align);
+    before += per == 1 ? pad : padded(e);
     a.counts[e] = cnt[e];
     a.slope[e] = (float)slope;
     if (a.offs) a.offs[e] = before;
@@ -235,7 +242,7 @@ __device__ void finish(const BalanceArgs& a, const double* col, const int32_t* c
 // (the next four are loaded while these are worked on), and leaves E column
 // sums, E counts and its number of live rows in the workspace; a workgroup that
 // is alone finishes.
-template <int DT, int P>
+template <int DT, int P, bool FULL>
 __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t per = (a.T + gridDim.x - 1) / gridDim.x;
@@ -246,12 +253,12 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
   if (threadIdx.x == 0) live_rows = 0;
   __syncthreads();
-  const Columns<P> c(a.E);
+  const Columns<P, FULL> c(a.E);
   float acc[P][4] = {}, next[P][4];
   int32_t live = 0;
   int64_t t = t0 + wave * 4 + (lane >> 4);
   bool have = t < t1 && (!a.mask || a.mask[t]);
-  if (have) load_row<DT, P>(a.logits, t, c, next);
+  if (have) load_row<DT, P, FULL>(a.logits, t, c, next);
   for (int64_t base = t0 + wave * 4; base < t1; base += 4 * kWaves) {
     float v[P][4];
 #pragma unroll
@@ -261,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
     const bool now = have;
     t += 4 * kWaves;
     have = t < t1 && (!a.mask || a.mask[t]);
-    if (have) load_row<DT, P>(a.logits, t, c, next);
+    if (have) load_row<DT, P, FULL>(a.logits, t, c, next);
     softmax(c, now, v);
     live += now;
 #pragma unroll
@@ -319,59 +326,66 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
 }
 
 // Joins the workgroups' rows: each workgroup takes 32 columns, and the one that
-// ends last (a counter that the first launch cleared) finishes.
-__global__ __launch_bounds__(256) void k_balance_join(BalanceArgs a, int blocks) {
+// ends last (a counter that the first launch cleared) finishes. Bound by
+// latency: a chain of five trips to memory, 9 us whatever T is.
+__global__ __launch_bounds__(1024) void k_balance_join(BalanceArgs a, int blocks) {
   const Work w(a.work, blocks, a.E);
   const int c = threadIdx.x & 31, part = threadIdx.x >> 5, e = blockIdx.x * 32 + c;
-  __shared__ double part_sum[8][32];
-  __shared__ int32_t part_cnt[8][32];
+  __shared__ double part_sum[16][32];
+  __shared__ int32_t part_cnt[16][32];
   __shared__ double col[kMaxExperts];
   __shared__ int32_t cnt[kMaxExperts];
   __shared__ int32_t live, last;
   double s = 0.0;
-  int32_t n = 0;
+  int32_t n = 0, rows = 0;
+  for (int b = threadIdx.x; b < blocks; b += 1024) rows += w.live[b];
   if (e < a.E) {
 #pragma unroll 8
-    for (int b = part; b < blocks; b += 8) {
+    for (int b = part; b < blocks; b += 32) {
       s += (double)w.sums[(int64_t)b * a.E + e];
       n += w.counts[(int64_t)b * a.E + e];
     }
   }
-  part_sum[part][c] = s;
-  part_cnt[part][c] = n;
+  s += __shfl_xor(s, 32, 64);
+  n += __shfl_xor(n, 32, 64);
+  if (!(part & 1)) {
+    part_sum[part >> 1][c] = s;
+    part_cnt[part >> 1][c] = n;
+  }
   if (threadIdx.x == 0) live = 0;
   __syncthreads();
   if (part == 0 && e < a.E) {
-    for (int p = 1; p < 8; p++) {
+#pragma unroll
+    for (int p = 1; p < 16; p++) {
       s += part_sum[p][c];
       n += part_cnt[p][c];
     }
     __hip_atomic_store(&w.col[e], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_store(&w.cnt[e], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __threadfence();
+  // The joined columns pass between workgroups as device-scope atomics only,
+  // which go to the point that all XCDs share; waiting for the stores before
+  // the count orders them without a fence, whose cache write-back took 8 us.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0)
-    last = __hip_atomic_fetch_add(w.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+    last = __hip_atomic_fetch_add(w.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  for (int i = threadIdx.x; i < a.E; i += 256) {
+  for (int i = threadIdx.x; i < a.E; i += 1024) {
     col[i] = __hip_atomic_load(&w.col[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     cnt[i] = __hip_atomic_load(&w.cnt[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  int32_t rows = 0;
-  for (int b = threadIdx.x; b < blocks; b += 256) rows += w.live[b];
   if (rows) atomicAdd(&live, rows);
   __syncthreads();
   finish(a, col, cnt, live);
 }
 
-template <int DT, int P>
+template <int DT, int P, bool FULL>
 __global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a) {
   const int lane = threadIdx.x & 63;
   const float g = *a.dloss;
-  const Columns<P> c(a.E);
+  const Columns<P, FULL> c(a.E);
   float slope[P][4];
 #pragma unroll
   for (int i = 0; i < P; i++)
@@ -382,7 +396,7 @@ __global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a) {
     if (t >= a.T) break;
     const bool live = !a.mask || a.mask[t];
     float v[P][4], dot = 0.0f;
-    if (live) load_row<DT, P>(a.logits, t, c, v);
+    if (live) load_row<DT, P, FULL>(a.logits, t, c, v);
     softmax(c, live, v);
 #pragma unroll
     for (int i = 0; i < P; i++)
@@ -404,28 +418,33 @@ __global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a) {
   }
 }
 
-template <int DT, int P>
+template <int DT, int P, bool FULL>
 hipError_t run(const BalanceArgs& a, bool backward, hipStream_t s) {
   if (backward) {
     const int64_t g = (a.T + 15) / 16;
-    k_balance_backward<DT, P><<<dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s>>>(a);
+    k_balance_backward<DT, P, FULL><<<dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s>>>(a);
     return hipGetLastError();
   }
   const int blocks = balance_blocks(a.T, a.E);
-  k_balance<DT, P><<<dim3(blocks), dim3(kThreads), 0, s>>>(a);
+  k_balance<DT, P, FULL><<<dim3(blocks), dim3(kThreads), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || blocks == 1) return e;
-  k_balance_join<<<dim3((a.E + 31) / 32), dim3(256), 0, s>>>(a, blocks);
+  k_balance_join<<<dim3((a.E + 31) / 32), dim3(1024), 0, s>>>(a, blocks);
   return hipGetLastError();
+}
+
+template <int DT, int P>
+hipError_t by_fill(const BalanceArgs& a, bool backward, hipStream_t s) {
+  return a.E == 64 * P ? run<DT, P, true>(a, backward, s) : run<DT, P, false>(a, backward, s);
 }
 
 template <int DT>
 hipError_t by_width(const BalanceArgs& a, bool backward, hipStream_t s) {
-  if (a.E <= 64) return run<DT, 1>(a, backward, s);
-  if (a.E <= 128) return run<DT, 2>(a, backward, s);
-  if (a.E <= 256) return run<DT, 4>(a, backward, s);
-  if (a.E <= 512) return run<DT, 8>(a, backward, s);
-  return run<DT, 16>(a, backward, s);
+  if (a.E <= 64) return by_fill<DT, 1>(a, backward, s);
+  if (a.E <= 128) return by_fill<DT, 2>(a, backward, s);
+  if (a.E <= 256) return by_fill<DT, 4>(a, backward, s);
+  if (a.E <= 512) return by_fill<DT, 8>(a, backward, s);
+  return by_fill<DT, 16>(a, backward, s);
 }
 
 hipError_t by_type(int dt, const BalanceArgs& a, bool backward, hipStream_t s) {
