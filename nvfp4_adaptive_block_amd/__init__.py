@@ -499,32 +499,63 @@ def fos_quantize_grouped_fused_noalloc(x: torch.Tensor, offs: torch.Tensor, *, c
 
 
 # ------------------------------------------------- operators around the quantizer
+#
+# A call on one token takes the GPU a few microseconds, less than careless
+# argument handling takes the host: these bindings pass plain integers to
+# ctypes, compare each tensor's properties once and switch devices only where
+# the current one is another.
 
 
-def _match(t, name: str, device, shape=None, dtype=None):
-    """Check a tensor argument that the C call takes as a bare pointer."""
+def _mismatch(t, name, device, shape, dtype):
     _need(t, name)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _match(t, name: str, device, shape=None, dtype=None) -> int:
+    """Address of a tensor that the C call takes as a bare pointer, checked."""
+    if (t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape)
+            or (dtype is not None and t.dtype != dtype)):
+        _mismatch(t, name, device, shape, dtype)
+    return t.data_ptr()
+
+
+# The current stream's handle without a Stream object (2 us less a call) where
+# this torch has the function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(dev, fn, *args):
+    """fn(*args, current stream of dev) with dev current; raises on an error code."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        _check(rc)
+
+
 def _float_type(t, name: str) -> int:
-    if t.dtype not in DTYPES:
+    code = DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-    return DTYPES[t.dtype]
+    return code
 
 
-def _scale_count(scale, gran: str, rows: int, groups: int | None, name: str, device):
+def _scale_pointer(scale, gran: str, rows: int, groups: int | None, name: str, device) -> int:
     if gran not in OPERAND_GRANS or (gran == "group" and groups is None):
         raise ValueError(f"{name}: unknown scale granularity {gran!r}")
-    _match(scale, f"{name}'s scale", device, dtype=torch.float32)
-    want = {"tensor": 1, "row": rows, "group": groups}[gran]
+    want = 1 if gran == "tensor" else rows if gran == "row" else groups
     if scale.numel() != want:
         raise ValueError(f"{name}'s scale must hold {want} value(s) (per {gran}), got {scale.numel()}")
+    return _match(scale, f"{name}'s scale", device, None, torch.float32)
 
 
 def _activation_operand(x, gran, groups):
@@ -534,73 +565,70 @@ def _activation_operand(x, gran, groups):
         _need(x, "x")
         if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError(f"x must be a bf16 or fp16 [M, K] tensor, got {x.dtype} {list(x.shape)}")
-        return _Operand(x.data_ptr(), None, None, DTYPES[x.dtype], 0), x.shape[0], x.shape[1], x.device
+        M, K = x.shape
+        return _Operand(x.data_ptr(), None, None, DTYPES[x.dtype], 0), M, K, x.device
     if not isinstance(x, (tuple, list)) or len(x) not in (2, 3):
         raise ValueError("x must be a tensor, (q, scale) or (codes, scales, sdec)")
     data = x[0]
     _need(data, "x")
     if data.dim() != 2:
         raise ValueError(f"x must be rank 2, got {list(data.shape)}")
-    dev, M = data.device, data.shape[0]
+    dev = data.device
+    M, width = data.shape
     if len(x) == 2:
         if data.dtype not in (torch.float8_e4m3fn, torch.uint8):
             raise ValueError(f"x's values must be float8_e4m3fn, got {data.dtype}")
         gran = gran or "row"
-        _scale_count(x[1], gran, M, groups, "x", dev)
-        return (_Operand(data.data_ptr(), None, x[1].data_ptr(), OPERAND_E4M3, OPERAND_GRANS[gran]), M,
-                data.shape[1], dev)
-    K = 2 * data.shape[1]
-    _match(data, "x's codes", dev, dtype=torch.uint8)
-    _match(x[1], "x's block scales", dev, (M, K // 16), torch.uint8)
+        scale = _scale_pointer(x[1], gran, M, groups, "x", dev)
+        return _Operand(data.data_ptr(), None, scale, OPERAND_E4M3, OPERAND_GRANS[gran]), M, width, dev
+    K = 2 * width
     gran = gran or "tensor"
-    _scale_count(x[2], gran, M, groups, "x", dev)
-    return (_Operand(data.data_ptr(), x[1].data_ptr(), x[2].data_ptr(), OPERAND_NVFP4, OPERAND_GRANS[gran]), M, K,
-            dev)
+    return (_Operand(_match(data, "x's codes", dev, None, torch.uint8),
+                     _match(x[1], "x's block scales", dev, (M, K // 16), torch.uint8),
+                     _scale_pointer(x[2], gran, M, groups, "x", dev), OPERAND_NVFP4, OPERAND_GRANS[gran]), M, K, dev)
 
 
 def _linear(x, w, offs, bias, act, residual, out_dtype, out, x_gran, w_gran, workspace, status):
     codes, scales, sdec = w
     G = None if offs is None else offs.numel()
     xo, M, K, dev = _activation_operand(x, x_gran, G)
-    lead = () if G is None else (G,)
-    if codes.dim() != 2 + len(lead):
-        raise ValueError(f"w's codes must have shape {[*lead, 'N', K // 2]}, got {list(codes.shape)}")
+    if codes.dim() != (2 if G is None else 3):
+        raise ValueError(f"w's codes must have shape {['N', K // 2] if G is None else [G, 'N', K // 2]}, "
+                         f"got {list(codes.shape)}")
     N = codes.shape[-2]
-    _match(codes, "w's codes", dev, (*lead, N, K // 2), torch.uint8)
-    _match(scales, "w's block scales", dev, (*lead, N, K // 16), torch.uint8)
-    _scale_count(sdec, w_gran, N * (G or 1), G, "w", dev)
-    wo = _Operand(codes.data_ptr(), scales.data_ptr(), sdec.data_ptr(), OPERAND_NVFP4, OPERAND_GRANS[w_gran])
+    lead = (N,) if G is None else (G, N)
+    wo = _Operand(_match(codes, "w's codes", dev, (*lead, K // 2), torch.uint8),
+                  _match(scales, "w's block scales", dev, (*lead, K // 16), torch.uint8),
+                  _scale_pointer(sdec, w_gran, N * (G or 1), G, "w", dev), OPERAND_NVFP4, OPERAND_GRANS[w_gran])
     if out is not None:
         out_dtype = out.dtype
     elif out_dtype is None:
         out_dtype = x.dtype if isinstance(x, torch.Tensor) else torch.bfloat16
-    if out_dtype not in DTYPES:
+    out_code = DTYPES.get(out_dtype)
+    if out_code is None:
         raise ValueError(f"unsupported output dtype {out_dtype}")
     if act not in ACTIVATIONS:
         raise ValueError(f"unknown activation {act!r}")
-    if bias is not None:
-        _match(bias, "bias", dev, (*lead, N))
-        _float_type(bias, "bias")
-    if residual is not None:
-        _match(residual, "residual", dev, (M, N), out_dtype)
+    epi = None
+    if bias is not None or residual is not None or act != "none":
+        epi = ctypes.byref(_Epilogue(None if bias is None else _match(bias, "bias", dev, lead),
+                                     None if residual is None else _match(residual, "residual", dev, (M, N),
+                                                                          out_dtype),
+                                     0 if bias is None else _float_type(bias, "bias"), ACTIVATIONS[act]))
     y = torch.empty(M, N, dtype=out_dtype, device=dev) if out is None else out
-    _match(y, "out", dev, (M, N))
-    epi = _Epilogue(None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
-                    0 if bias is None else DTYPES[bias.dtype], ACTIVATIONS[act])
+    yp = y.data_ptr() if out is None else _match(out, "out", dev, (M, N))
     lib = load_library()
     need = lib.fos_linear_workspace(M, N, K, G or 0)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(dev):
-        if G is None:
-            _check(lib.fos_linear(ctypes.byref(xo), ctypes.byref(wo), M, N, K, ctypes.byref(epi), _ptr(y),
-                                  DTYPES[out_dtype], _ptr(workspace), room, _stream(dev)))
-        else:
-            _match(offs, "offs", dev, (G,), torch.int32)
-            _check(lib.fos_linear_grouped(ctypes.byref(xo), ctypes.byref(wo), _ptr(offs), G, M, N, K,
-                                          ctypes.byref(epi), _ptr(y), DTYPES[out_dtype], _ptr(workspace), room,
-                                          _ptr(status), _stream(dev)))
+    work, room = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                      workspace.numel() * workspace.element_size())
+    if G is None:
+        _call(dev, lib.fos_linear, ctypes.byref(xo), ctypes.byref(wo), M, N, K, epi, yp, out_code, work, room)
+    else:
+        _call(dev, lib.fos_linear_grouped, ctypes.byref(xo), ctypes.byref(wo),
+              _match(offs, "offs", dev, (G,), torch.int32), G, M, N, K, epi, yp, out_code, work, room,
+              None if status is None else status.data_ptr())
     return y
 
 
@@ -645,36 +673,32 @@ def fos_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, *, residual=None
     _need(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must be rank 2, got {list(x.shape)}")
-    M, K = x.shape
-    dev = x.device
-    _float_type(x, "x")
-    _match(weight, "weight", dev, (K,))
-    _float_type(weight, "weight")
+    shape = x.shape
+    M, K = shape
+    dev, dtype = x.device, x.dtype
+    code, wp, rp = _float_type(x, "x"), _match(weight, "weight", dev, (K,)), None
     if residual is not None:
-        _match(residual, "residual", dev, (M, K), x.dtype)
+        rp = _match(residual, "residual", dev, shape, dtype)
         if h is None:
             h = torch.empty_like(x)
-    for t, name in ((h, "h"), (y, "y")):
-        if t is not None:
-            _match(t, name, dev, (M, K), x.dtype)
+    hp = None if h is None else _match(h, "h", dev, shape, dtype)
+    yp = None if y is None else _match(y, "y", dev, shape, dtype)
     if q is None:
         q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=dev)
     if scale is None:
         scale = torch.empty(M, dtype=torch.float32, device=dev)
-    _match(q, "q", dev, (M, K), torch.float8_e4m3fn)
-    _match(scale, "scale", dev, (M,), torch.float32)
-    with torch.cuda.device(dev):
-        _check(load_library().fos_rmsnorm_quantize(_ptr(x), DTYPES[x.dtype], M, K, _ptr(residual), _ptr(weight),
-                                                   DTYPES[weight.dtype], eps, _ptr(q), _ptr(scale), _ptr(h),
-                                                   _ptr(y), _stream(dev)))
+    _call(dev, load_library().fos_rmsnorm_quantize, x.data_ptr(), code, M, K, rp, wp, _float_type(weight, "weight"),
+          eps, _match(q, "q", dev, shape, torch.float8_e4m3fn), _match(scale, "scale", dev, (M,), torch.float32), hp,
+          yp)
     return q, scale, x if h is None else h
 
 
-def _check_mask(mask, T, dev):
-    if mask is not None:
-        _match(mask, "mask", dev, (T,))
-        if mask.dtype not in (torch.bool, torch.uint8):
-            raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
+def _mask_pointer(mask, T, dev):
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
+    return _match(mask, "mask", dev, (T,))
 
 
 def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0.01, mask=None, align: int = 16,
@@ -690,11 +714,9 @@ def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0
         raise ValueError(f"logits [T, E] and idx [T, k] expected, got {list(logits.shape)} and {list(idx.shape)}")
     T, E = logits.shape
     dev = logits.device
-    _float_type(logits, "logits")
-    _match(idx, "idx", dev)
+    code = _float_type(logits, "logits")
     if idx.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"idx must be int32 or int64, got {idx.dtype}")
-    _check_mask(mask, T, dev)
     if loss is None:
         loss = torch.empty(1, dtype=torch.float32, device=dev)
     if counts is None:
@@ -703,17 +725,15 @@ def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0
         offs = torch.empty(E, dtype=torch.int32, device=dev)
     if slope is None:
         slope = torch.empty(E, dtype=torch.float32, device=dev)
-    for t, name, shape, dt in ((loss, "loss", (1,), torch.float32), (counts, "counts", (E,), torch.int32),
-                               (offs, "offs", (E,), torch.int32), (slope, "slope", (E,), torch.float32)):
-        _match(t, name, dev, shape, dt)
     lib = load_library()
     if workspace is None:
         workspace = torch.empty(max(0, lib.fos_balance_workspace(T, E)), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.fos_balance_loss(_ptr(logits), DTYPES[logits.dtype], T, E, _ptr(idx), idx.element_size(),
-                                    idx.shape[1], _ptr(mask), coef, align, _ptr(loss), _ptr(counts), _ptr(offs),
-                                    _ptr(slope), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _ptr(status), _stream(dev)))
+    _call(dev, lib.fos_balance_loss, logits.data_ptr(), code, T, E, _match(idx, "idx", dev),
+          8 if idx.dtype == torch.int64 else 4, idx.shape[1], _mask_pointer(mask, T, dev), coef, align,
+          _match(loss, "loss", dev, (1,), torch.float32), _match(counts, "counts", dev, (E,), torch.int32),
+          _match(offs, "offs", dev, (E,), torch.int32), _match(slope, "slope", dev, (E,), torch.float32),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          None if status is None else status.data_ptr())
     return loss, counts, offs, slope
 
 
@@ -734,15 +754,11 @@ def fos_balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, slope: 
         raise ValueError(f"logits must be rank 2, got {list(logits.shape)}")
     T, E = logits.shape
     dev = logits.device
-    _float_type(logits, "logits")
-    _match(dloss, "dloss", dev, dtype=torch.float32)
+    code = _float_type(logits, "logits")
     if dloss.numel() != 1:
         raise ValueError("dloss must hold one value")
-    _match(slope, "slope", dev, (E,), torch.float32)
-    _check_mask(mask, T, dev)
     d = torch.empty_like(logits) if out is None else out
-    _match(d, "out", dev, (T, E), logits.dtype)
-    with torch.cuda.device(dev):
-        _check(load_library().fos_balance_loss_backward(_ptr(dloss), _ptr(logits), DTYPES[logits.dtype], T, E,
-                                                        _ptr(mask), _ptr(slope), _ptr(d), _stream(dev)))
+    _call(dev, load_library().fos_balance_loss_backward, _match(dloss, "dloss", dev, None, torch.float32),
+          logits.data_ptr(), code, T, E, _mask_pointer(mask, T, dev),
+          _match(slope, "slope", dev, (E,), torch.float32), _match(d, "out", dev, (T, E), logits.dtype))
     return d

@@ -320,14 +320,71 @@ __device__ __forceinline__ void zero4(const LinearArgs& a, int64_t m, int64_t n)
 
 // ---------------------------------------------------------------- kernels
 
-// One workgroup: 16 columns of y and 16 * MT rows. Its waves take the 128-deep
-// steps of k in turn and their sums are joined through LDS in wave order.
-template <int XT, int MT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_linear_stream(LinearArgs a, int n_tiles) {
+// What one lane holds of a row of activations for a 128-deep step (its blocks
+// 2g and 2g + 1), as it lies in memory.
+template <int XT>
+struct XRaw {
+  static constexpr int kWords = XT == kXE4M3 ? 8 : XT == kXNVFP4 ? 4 : 16;
+  uint32_t v[kWords];
+  uint32_t s;
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; i++) v[i] = 0;
+    s = 0;
+  }
+  // p: the lane's first block of a whole step; q: its scale bytes
+  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* q) {
+    if constexpr (XT == kXNVFP4) {
+      const Bytes16 t = *reinterpret_cast<const Bytes16*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[i] = t.v[i];
+      s = reinterpret_cast<const Bytes2*>(q)->v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; i++) {
+        const uint4 t = reinterpret_cast<const uint4*>(p)[i];
+        v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void decode(Frag* f) const {
+    if constexpr (XT == kXNVFP4) {
+      decode_blocks<false>(v, s, f);
+    } else if constexpr (XT == kXE4M3) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        f[j / 2].u[2 * (j & 1)] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)v[j], 1.0f, false));
+        f[j / 2].u[2 * (j & 1) + 1] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)v[j], 1.0f, true));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) f[i].u[j] = v[4 * i + j];
+    }
+  }
+};
+
+// Bytes of one 16-value block of a row of activations.
+template <int XT>
+constexpr int x_block_bytes() {
+  return XT == kXE4M3 ? 16 : XT == kXNVFP4 ? 8 : 32;
+}
+
+// The stream kernel, for few rows per weight: one workgroup takes 16 NT columns
+// of y and 16 MT rows, and its eight waves take the 128-deep steps of k in turn,
+// so that the weight is read once, straight to registers, by as many waves as
+// the chip has. A wave keeps DEPTH steps of loads in flight (4 KiB of codes).
+// Rows of the activations that do not exist are not loaded. The waves' sums are
+// joined through LDS in wave order.
+template <int XT, int MT, int NT>
+__global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int WAVES = 8, DEPTH = MT == 4 && NT == 1 ? 2 : 4 / NT;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x / n_tiles;
-  const int64_t n0 = 16 * (int64_t)(blockIdx.x % n_tiles);
+  const int64_t n0 = 16 * NT * (int64_t)(blockIdx.x % n_tiles);
   RowTile rt{t * 16 * MT, a.M, 0};
   if (a.offs) {
     if (a.status && blockIdx.x == 0 && wave == 0) check_offs(a);
@@ -335,41 +392,114 @@ __global__ __launch_bounds__(64 * WAVES) void k_linear_stream(LinearArgs a, int 
     if (rt.g < 0) return;
   }
   const int col = lane & 15, g4 = lane >> 4;
-  const bool tail = a.offs && rt.g == a.G;
+  if (a.offs && rt.g == a.G) {
+    for (int i = wave; i < MT * NT; i += WAVES) {
+      const int64_t m = rt.m0 + 16 * (i % MT) + col, n = n0 + 16 * (i / MT) + 4 * g4;
+      if (m < rt.end) zero4(a, m, n);
+    }
+    return;
+  }
   const int64_t KB = a.K / 16;
-  f32x4 acc[MT] = {};
-  if (!tail) {
-    const int64_t n = n0 + col < a.N ? n0 + col : a.N - 1;
-    const int64_t row = (int64_t)rt.g * a.N + n;
-    const uint8_t* wc = a.w + row * (a.K / 2);
-    const uint8_t* wsc = a.ws + row * KB;
-    for (int64_t b = 8 * wave; b < KB; b += 8 * WAVES) {
+  const int whole = (int)(KB / 8);  // 128-deep steps; a part of one may follow
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; i++)
+#pragma unroll
+    for (int j = 0; j < MT; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const uint8_t *wp[NT], *wq[NT], *xp[MT], *xq[MT];  // at the lane's first block
+  bool have[MT];
+#pragma unroll
+  for (int i = 0; i < NT; i++) {
+    const int64_t n = n0 + 16 * i + col;
+    const int64_t row = (int64_t)rt.g * a.N + (n < a.N ? n : a.N - 1);
+    wp[i] = a.w + row * (a.K / 2) + 16 * g4;
+    wq[i] = a.ws + row * KB + 2 * g4;
+  }
+#pragma unroll
+  for (int j = 0; j < MT; j++) {
+    const int64_t m = rt.m0 + 16 * j + col;
+    have[j] = m < rt.end;
+    const int64_t row = have[j] ? m : rt.m0;
+    xp[j] = (const uint8_t*)a.x + (row * KB + 2 * g4) * x_block_bytes<XT>();
+    xq[j] = XT == kXNVFP4 ? a.xs + row * KB + 2 * g4 : nullptr;
+  }
+
+  uint32_t codes[DEPTH][NT][4], scales[DEPTH][NT];
+  XRaw<XT> xr[DEPTH][MT];
+#pragma unroll
+  for (int d = 0; d < DEPTH; d++)
+#pragma unroll
+    for (int j = 0; j < MT; j++) xr[d][j].clear();
+  auto load = [&](int d, int64_t step) {
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+      const Bytes16 v = *reinterpret_cast<const Bytes16*>(wp[i] + step * 64);
+#pragma unroll
+      for (int j = 0; j < 4; j++) codes[d][i][j] = v.v[j];
+      scales[d][i] = reinterpret_cast<const Bytes2*>(wq[i] + step * 8)->v;
+    }
+#pragma unroll
+    for (int j = 0; j < MT; j++)
+      if (have[j]) xr[d][j].load(xp[j] + step * 8 * x_block_bytes<XT>(), xq[j] + step * 8);
+  };
+  auto multiply = [&](int d) {
+    Frag x[MT][4];
+#pragma unroll
+    for (int j = 0; j < MT; j++) xr[d][j].decode(x[j]);
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
       Frag w[4];
-      load_nvfp4<BF16>(wc, wsc, b + 2 * g4, KB, w);
+      decode_blocks<BF16>(codes[d][i], scales[d][i], w);
 #pragma unroll
-      for (int i = 0; i < MT; i++) {
-        int64_t m = rt.m0 + 16 * i + col;
-        if (m >= rt.end) m = rt.end - 1;
-        Frag x[4];
-        load_x<XT>(a, m, b + 2 * g4, KB, x);
+      for (int k = 0; k < 4; k++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i] = mfma<BF16>(w[j], x[j], acc[i]);
+        for (int j = 0; j < MT; j++) acc[i][j] = mfma<BF16>(w[k], x[j][k], acc[i][j]);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; d++)
+    if (wave + d * WAVES < whole) load(d, wave + d * WAVES);
+  for (int step = wave; step < whole; step += WAVES * DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++) {
+      if (step + d * WAVES < whole) {
+        multiply(d);
+        if (step + (d + DEPTH) * WAVES < whole) load(d, step + (d + DEPTH) * WAVES);
       }
     }
   }
-  __shared__ f32x4 part[WAVES][MT][64];
+  if (KB % 8 && wave == whole % WAVES) {  // the part of a step that is left
+    const int64_t b = (int64_t)whole * 8 + 2 * g4;
+    Frag x[MT][4];
 #pragma unroll
-  for (int i = 0; i < MT; i++) part[wave][i][lane] = acc[i];
-  __syncthreads();
-  for (int i = wave; i < MT; i += WAVES) {
-    f32x4 s = part[0][i][lane];
-    for (int v = 1; v < WAVES; v++) s += part[v][i][lane];
-    const int64_t m = rt.m0 + 16 * i + col, n = n0 + 4 * g4;
-    if (m < rt.end && n < a.N) {
-      if (tail)
-        zero4(a, m, n);
-      else
-        finish4(a, rt.g, m, n, s);
+    for (int j = 0; j < MT; j++) load_x<XT>(a, have[j] ? rt.m0 + 16 * j + col : rt.m0, b, KB, x[j]);
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+      const int64_t n = n0 + 16 * i + col;
+      const int64_t row = (int64_t)rt.g * a.N + (n < a.N ? n : a.N - 1);
+      Frag w[4];
+      load_nvfp4<BF16>(a.w + row * (a.K / 2), a.ws + row * KB, b, KB, w);
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int j = 0; j < MT; j++) acc[i][j] = mfma<BF16>(w[k], x[j][k], acc[i][j]);
+    }
+  }
+  // one column tile at a time, in two halves of the LDS in turn
+  __shared__ f32x4 part[NT > 1 ? 2 : 1][WAVES][MT][64];
+#pragma unroll
+  for (int i = 0; i < NT; i++) {
+#pragma unroll
+    for (int j = 0; j < MT; j++) part[i & 1][wave][j][lane] = acc[i][j];
+    __syncthreads();
+    const int j = (wave + WAVES - (i * MT) % WAVES) % WAVES;  // row tile of this wave
+    const int64_t m = rt.m0 + 16 * j + col, n = n0 + 16 * i + 4 * g4;
+    if (j < MT && m < rt.end && n < a.N) {
+      f32x4 s = part[i & 1][0][j][lane];
+#pragma unroll
+      for (int v = 1; v < WAVES; v++) s += part[i & 1][v][j][lane];
+      finish4(a, rt.g, m, n, s);
     }
   }
 }
@@ -670,6 +800,28 @@ int64_t max_tiles(int64_t M, int64_t G, int64_t rows) {
   return (M + parts * (rows - 1)) / rows;
 }
 
+template <int XT, int MT, int NT>
+hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
+  const int64_t n_tiles = (a.N + 16 * NT - 1) / (16 * NT);
+  if (m_tiles > kMaxGrid / n_tiles) return hipErrorInvalidConfiguration;
+  k_linear_stream<XT, MT, NT><<<dim3((unsigned)(m_tiles * n_tiles)), dim3(512), 0, s>>>(a, (int)n_tiles);
+  return hipGetLastError();
+}
+
+template <int XT, int MT>
+hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
+  const int64_t m_tiles = a.offs ? max_tiles(a.M, a.G, 16 * MT) : (a.M + 16 * MT - 1) / (16 * MT);
+  const int64_t n16 = (a.N + 15) / 16;
+#ifdef FOS_NT
+  if (FOS_NT == 4) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
+  if (FOS_NT == 2) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
+  return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
+#endif
+  if (n16 / 4 * m_tiles >= 224) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
+  if (n16 / 2 * m_tiles >= 224) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
+  return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
+}
+
 template <int XT>
 hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
   // rows that share a weight, and whether the tile kernel's 32-bit offsets
@@ -683,12 +835,7 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
     k_linear_tile<XT, BM><<<dim3((unsigned)(mt * nt)), dim3(256), 0, s>>>(a, mt, nt);
     return hipGetLastError();
   }
-  constexpr int WAVES = 8;
-  const int64_t nt = (a.N + 15) / 16;
-  const int64_t mt = a.offs ? max_tiles(a.M, a.G, 16) : (a.M + 15) / 16;
-  if (mt > kMaxGrid / nt) return hipErrorInvalidConfiguration;
-  k_linear_stream<XT, 1, WAVES><<<dim3((unsigned)(mt * nt)), dim3(64 * WAVES), 0, s>>>(a, (int)nt);
-  return hipGetLastError();
+  return rows <= 16 ? launch_stream<XT, 1>(a, s) : rows <= 32 ? launch_stream<XT, 2>(a, s) : launch_stream<XT, 4>(a, s);
 }
 
 }  // namespace
