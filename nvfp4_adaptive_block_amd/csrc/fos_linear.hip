@@ -24,6 +24,13 @@
 #include "fos_device.h"
 #include "fos_ops.h"
 
+#ifndef FOS_STREAM_MAX
+#define FOS_STREAM_MAX 64
+#endif
+#ifndef FOS_BM
+#define FOS_BM 0
+#define FOS_SPLIT 0
+#endif
 namespace fos {
 namespace {
 
@@ -504,6 +511,27 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
   }
 }
 
+// Loads of the tile kernel's loop: a uniform address in scalar registers plus a
+// 32-bit lane offset. (Left to itself the compiler carries a 64-bit address per
+// lane and load through the loop: 24 registers that spill.) The alignments are
+// those that K % 16 == 0 gives.
+#define FOS_GLOBAL __attribute__((address_space(1)))
+typedef const FOS_GLOBAL uint8_t* GlobalBytes;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
+
+__device__ __forceinline__ uint32_t lane_offset(uint32_t v) {  // stays 32 bits wide in the loop
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ GlobalBytes scalar(const uint8_t* p) {
+  GlobalBytes g = (GlobalBytes)p;
+  asm volatile("" : "+s"(g));
+  return g;
+}
+
 // The tile kernel: one workgroup of four waves takes BM rows and 256 columns,
 // each wave all BM rows and 64 columns. A 128-deep step of the activations is
 // staged in LDS as 16-bit values, twice (the next step's loads run while this
@@ -556,29 +584,31 @@ struct XStage {
   // 16-bit activations, into registers for those that are decoded first.
   __device__ __forceinline__ void load(int64_t b, uint8_t* lds) {
     if constexpr (kDirect) {
-      const uint8_t* p = base + b * 32;
+      const GlobalBytes p = scalar(base + b * 32);
       const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
       for (int i = 0; i < BM / 16; i++)
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(p + off[i]),
+        __builtin_amdgcn_global_load_lds((const FOS_GLOBAL void*)(p + lane_offset(off[i])),
                                          (__attribute__((address_space(3))) void*)(lds + (wave * (BM / 16) + i) * 1024),
                                          16, 0, 0);
     } else if constexpr (XT == kXE4M3) {
-      const uint8_t* p = base + b * 16;
+      const GlobalBytes p = scalar(base + b * 16);
 #pragma unroll
-      for (int i = 0; i < kBlocks / 2; i++) {
-        const uint4 t = *reinterpret_cast<const uint4*>(p + off[i]), u = *reinterpret_cast<const uint4*>(p + off[i] + 16);
-        regs[i][0] = t.x, regs[i][1] = t.y, regs[i][2] = t.z, regs[i][3] = t.w;
-        regs[i][4] = u.x, regs[i][5] = u.y, regs[i][6] = u.z, regs[i][7] = u.w;
-      }
+      for (int i = 0; i < kBlocks / 2; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const u32x4 t = *(const FOS_GLOBAL u32x4*)(p + lane_offset(off[i]) + 16 * j);
+#pragma unroll
+          for (int k = 0; k < 4; k++) regs[i][4 * j + k] = t[k];
+        }
     } else {
-      const uint8_t *p = base + b * 8, *q = sbase + b;
+      const GlobalBytes p = scalar(base + b * 8), q = scalar(sbase + b);
 #pragma unroll
       for (int i = 0; i < kBlocks / 2; i++) {
-        const Bytes16 t = *reinterpret_cast<const Bytes16*>(p + off[i]);
+        const u32x4 t = *(const FOS_GLOBAL u32x4_a8*)(p + lane_offset(off[i]));
 #pragma unroll
-        for (int j = 0; j < 4; j++) regs[i][j] = t.v[j];
-        sreg[i] = reinterpret_cast<const Bytes2*>(q + soff[i])->v;
+        for (int j = 0; j < 4; j++) regs[i][j] = t[j];
+        sreg[i] = *(const FOS_GLOBAL u16_a1*)(q + lane_offset(soff[i]));
       }
     }
   }
@@ -626,8 +656,8 @@ struct XStage {
 // turn, so each XCD gets a contiguous range of the tiles; along it, 8 row tiles
 // are taken per column tile, so that the workgroups that run on an XCD at a
 // time share their rows of both operands in its L2.
-__device__ __forceinline__ void tile_of(int64_t m_tiles, int64_t n_tiles, int64_t& tm, int64_t& tn) {
-  const int64_t total = m_tiles * n_tiles, id = blockIdx.x;
+__device__ __forceinline__ void tile_of(int64_t m_tiles, int64_t n_tiles, int64_t id, int64_t& tm, int64_t& tn) {
+  const int64_t total = m_tiles * n_tiles;
   const int64_t x = id % 8, base = total / 8, more = total % 8;
   const int64_t t = x * base + (x < more ? x : more) + id / 8;
   const int64_t band = t / (8 * n_tiles), in = t % (8 * n_tiles);
@@ -636,15 +666,33 @@ __device__ __forceinline__ void tile_of(int64_t m_tiles, int64_t n_tiles, int64_
   tn = in / high;
 }
 
+// Waits that the compiler's own wait insertion knows of: at most N vector
+// memory operations still on their way.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N < 16, "");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | N);
+  asm volatile("" ::: "memory");
+}
+
+// A workgroup barrier for LDS alone: outstanding loads of registers stay on
+// their way (__syncthreads would wait for them).
+__device__ __forceinline__ void block_sync() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <int XT, int BM>
-__global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_tiles, int64_t n_tiles) {
+__global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArgs a, int64_t m_tiles, int64_t n_tiles,
+                                                                       int splits) {
   constexpr bool BF16 = XT == kBF16;
   constexpr int MT = BM / 16;
   __shared__ __align__(16) uint8_t lds[2][BM * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g4 = lane >> 4;
   int64_t tm, tn;
-  tile_of(m_tiles, n_tiles, tm, tn);
+  tile_of(m_tiles, n_tiles, blockIdx.x % (m_tiles * n_tiles), tm, tn);
   RowTile rt{tm * BM, a.M, 0};
   if (a.offs) {
     if (a.status && blockIdx.x == 0 && wave == 0) check_offs(a);
@@ -659,7 +707,11 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
     return;
   }
   const int64_t KB = a.K / 16;
-  const int whole = (int)(KB / 8);  // 128-deep steps; a part of one may follow
+  // 128-deep steps of this workgroup's part of K; the last part may end inside one
+  const int part = (int)(blockIdx.x / (m_tiles * n_tiles)), all = (int)(KB / 8), per = (all + splits - 1) / splits;
+  const int first = per * part < all ? per * part : all;
+  const int whole = part == splits - 1 ? all : first + per < all ? first + per : all;
+  const bool remainder = KB % 8 && part == splits - 1;
 
   // weight rows: uniform base, 32-bit lane offsets; columns past the end read
   // the last row
@@ -667,21 +719,23 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
   const uint8_t* wc = a.w + w0 * (a.K / 2);
   const uint8_t* wsc = a.ws + w0 * KB;
   const int wrows = n0 < a.N ? (a.N - n0 < 64 ? (int)(a.N - n0) : 64) : 1;
-  uint32_t woff[4], wsoff[4], codes[4][4], scales[4];
+  uint32_t woff[4], wsoff[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const uint32_t r = 16 * i + col < wrows ? 16 * i + col : wrows - 1;
     woff[i] = r * (uint32_t)(a.K / 2) + 16 * g4;
     wsoff[i] = r * (uint32_t)KB + 2 * g4;
   }
+  struct Weights {
+    u32x4 codes[4];
+    uint32_t scales[4];
+  } w_now, w_next;
   auto load_w = [&](int step) {
-    const uint8_t *p = wc + (int64_t)step * 64, *q = wsc + (int64_t)step * 8;
+    const GlobalBytes p = scalar(wc + (int64_t)step * 64), q = scalar(wsc + (int64_t)step * 8);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const Bytes16 t = *reinterpret_cast<const Bytes16*>(p + woff[i]);
-#pragma unroll
-      for (int j = 0; j < 4; j++) codes[i][j] = t.v[j];
-      scales[i] = reinterpret_cast<const Bytes2*>(q + wsoff[i])->v;
+      w_next.codes[i] = *(const FOS_GLOBAL u32x4_a8*)(p + lane_offset(woff[i]));
+      w_next.scales[i] = *(const FOS_GLOBAL u16_a1*)(q + lane_offset(wsoff[i]));
     }
   };
 
@@ -695,9 +749,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
 #pragma unroll
   for (int c = 0; c < 4; c++) roff[c] = col * 256 + (((4 * g4 + c) ^ col) << 4);
 
-  // Multiply the staged step by the codes in registers; `refill` runs once
-  // the codes have been decoded and leaves half a step for its loads.
-  auto multiply = [&](const uint8_t* cur, auto refill) {
+  // Multiply the staged step by the weights in registers.
+  auto multiply = [&](const uint8_t* cur) {
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       Frag x[2][2];
@@ -706,13 +759,12 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
       Frag w[4][2];
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const f32x2 s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)scales[i], 1.0f, false);
-        const h2 s16 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales[i], 1.0f, false);
+        const f32x2 s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w_now.scales[i], 1.0f, false);
+        const h2 s16 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w_now.scales[i], 1.0f, false);
         const h2 sh = h ? __builtin_shufflevector(s16, s16, 1, 1) : __builtin_shufflevector(s16, s16, 0, 0);
-        decode8<BF16>(codes[i][2 * h], h ? s.y : s.x, sh, w[i][0].u);
-        decode8<BF16>(codes[i][2 * h + 1], h ? s.y : s.x, sh, w[i][1].u);
+        decode8<BF16>(w_now.codes[i][2 * h], h ? s.y : s.x, sh, w[i][0].u);
+        decode8<BF16>(w_now.codes[i][2 * h + 1], h ? s.y : s.x, sh, w[i][1].u);
       }
-      if (h == 1) refill();
 #pragma unroll
       for (int m = 0; m < MT; m++) {
         if (m + 1 < MT) {
@@ -731,44 +783,47 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
 
   XStage<XT, BM> xs;
   xs.init(a, rt.m0, rows);
-  if (whole > 0) {
-    xs.load(0, lds[0]);
-    load_w(0);
-    xs.store(lds[0]);
+  if (whole > first) {
+    xs.load((int64_t)first * 8, lds[first & 1]);
+    load_w(first);
+    xs.store(lds[first & 1]);
   }
-  for (int step = 0; step < whole; step++) {
-    // this step's tile is in LDS (the wait covers the direct loads), and no
-    // wave reads the other one any more
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+  for (int step = first; step < whole; step++) {
+    // This step's tile is in LDS and its weights are in registers, and no wave
+    // reads the other tile any more. All of the next step's loads start here
+    // and have this step's time. (The last step loads itself again: a load that
+    // may not happen would make the compiler wait where the paths meet.)
+    wait_vm<0>();
+    block_sync();
+    w_now = w_next;
     uint8_t* next = lds[(step & 1) ^ 1];
-    const bool more = step + 1 < whole;
-    if (more) xs.load((int64_t)(step + 1) * 8, next);
-    multiply(lds[step & 1], [&] {
-      if (more) load_w(step + 1);
-    });
-    if (more) xs.store(next);
+    const int after = step + 1 < whole ? step + 1 : step;
+    load_w(after);
+    xs.load((int64_t)after * 8, next);
+    multiply(lds[step & 1]);
+    xs.store(next);
   }
-  if (KB % 8) {  // the part of a step that is left: zeros past the end
-    uint8_t* last = lds[whole & 1];  // not the tile that a wave may still read
+  wait_vm<0>();
+  __syncthreads();
+  if (remainder) {  // the part of a step that is left: zeros past the end
+    uint8_t* last = lds[whole & 1];
     xs.load_last(a, rt.m0, rows, (int64_t)whole * 8, last);
     const int64_t b = (int64_t)whole * 8 + 2 * g4;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      uint2 t = {0, 0}, u = {0, 0};
-      scales[i] = 0;
-      if (b < KB) {
-        t = *reinterpret_cast<const uint2*>(wc + (int64_t)whole * 64 + woff[i]);
-        scales[i] = wsc[(int64_t)whole * 8 + wsoff[i]];
+      w_now.scales[i] = 0;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        uint2 t = {0, 0};
+        if (b + h < KB) {
+          t = *reinterpret_cast<const uint2*>(wc + (int64_t)whole * 64 + woff[i] + 8 * h);
+          w_now.scales[i] |= (uint32_t)wsc[(int64_t)whole * 8 + wsoff[i] + h] << (8 * h);
+        }
+        w_now.codes[i][2 * h] = t.x, w_now.codes[i][2 * h + 1] = t.y;
       }
-      if (b + 1 < KB) {
-        u = *reinterpret_cast<const uint2*>(wc + (int64_t)whole * 64 + woff[i] + 8);
-        scales[i] |= (uint32_t)wsc[(int64_t)whole * 8 + wsoff[i] + 1] << 8;
-      }
-      codes[i][0] = t.x, codes[i][1] = t.y, codes[i][2] = u.x, codes[i][3] = u.y;
     }
     __syncthreads();
-    multiply(last, [] {});
+    multiply(last);
   }
   // Each wave turns its sums by way of its quarter of the LDS, half of the rows
   // at a time, so that 16 lanes store 64 neighbouring columns of a row.
@@ -786,8 +841,23 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int64_t m_
       const int lr = 4 * it + g4, r = half * (BM / 2) + lr;
       const f32x4 v = *reinterpret_cast<const f32x4*>(mine + lr * 256 + ((col ^ (lr & 15)) << 4));
       const int64_t n = n0 + 4 * col;
-      if (r < rows && n < a.N) finish4(a, rt.g, rt.m0 + r, n, v);
+      if (r >= rows || n >= a.N) continue;
+      if (splits == 1)
+        finish4(a, rt.g, rt.m0 + r, n, v);
+      else  // rows of the workspace are padded to a multiple of 4 columns
+        *reinterpret_cast<f32x4*>((float*)a.work + (part * a.M + rt.m0 + r) * ((a.N + 3) / 4 * 4) + n) = v;
     }
+  }
+}
+
+// Joins the parts of K in order and finishes: four columns per thread.
+__global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, int splits) {
+  const int64_t quads = (a.N + 3) / 4, total = a.M * quads;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const f32x4* p = (const f32x4*)a.work + i;
+    f32x4 v = p[0];
+    for (int s = 1; s < splits; s++) v += p[s * total];
+    finish4(a, 0, i / quads, i % quads * 4, v);
   }
 }
 
@@ -800,6 +870,31 @@ int64_t max_tiles(int64_t M, int64_t G, int64_t rows) {
   return (M + parts * (rows - 1)) / rows;
 }
 
+// How a product is cut, from its sizes alone (G = 0: dense).
+struct Plan {
+  bool stream;    // the stream kernel; else the tile kernel
+  int bm;         // rows of a tile
+  int splits;     // parts of K
+  int64_t m_tiles;
+};
+
+Plan plan(int64_t M, int64_t N, int64_t K, int64_t G) {
+  Plan p{true, 16, 1, 0};
+  const int64_t rows = G ? (M + G - 1) / G : M;  // rows that share a weight
+  // 2^22: the tile kernel's 32-bit offsets within a tile reach
+  if (rows > FOS_STREAM_MAX && K <= (int64_t(1) << 22)) {
+    p.stream = false;
+    auto tiles = [&](int bm) { return G ? max_tiles(M, G, bm) : (M + bm - 1) / bm; };
+    p.bm = FOS_BM ? FOS_BM : 128;
+    p.m_tiles = tiles(p.bm);
+    if (FOS_SPLIT) p.splits = FOS_SPLIT;
+  } else {
+    p.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.m_tiles = G ? max_tiles(M, G, p.bm) : (M + p.bm - 1) / p.bm;
+  }
+  return p;
+}
+
 template <int XT, int MT, int NT>
 hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
   const int64_t n_tiles = (a.N + 16 * NT - 1) / (16 * NT);
@@ -809,14 +904,8 @@ hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) 
 }
 
 template <int XT, int MT>
-hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
-  const int64_t m_tiles = a.offs ? max_tiles(a.M, a.G, 16 * MT) : (a.M + 16 * MT - 1) / (16 * MT);
+hipError_t launch_stream(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
   const int64_t n16 = (a.N + 15) / 16;
-#ifdef FOS_NT
-  if (FOS_NT == 4) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
-  if (FOS_NT == 2) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
-  return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
-#endif
   if (n16 / 4 * m_tiles >= 224) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
   if (n16 / 2 * m_tiles >= 224) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
   return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
@@ -824,23 +913,32 @@ hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
 
 template <int XT>
 hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
-  // rows that share a weight, and whether the tile kernel's 32-bit offsets
-  // within a tile reach (256 rows of 2 K bytes)
-  const int64_t rows = a.offs ? (a.M + a.G - 1) / a.G : a.M;
-  if (rows > 64 && a.K <= (int64_t(1) << 22)) {
-    constexpr int BM = 128;
-    const int64_t nt = (a.N + 255) / 256;
-    const int64_t mt = a.offs ? max_tiles(a.M, a.G, BM) : (a.M + BM - 1) / BM;
-    if (mt > kMaxGrid / nt) return hipErrorInvalidConfiguration;
-    k_linear_tile<XT, BM><<<dim3((unsigned)(mt * nt)), dim3(256), 0, s>>>(a, mt, nt);
-    return hipGetLastError();
+  const Plan p = plan(a.M, a.N, a.K, a.offs ? a.G : 0);
+  if (p.stream) {
+    if (p.bm == 16) return launch_stream<XT, 1>(a, p.m_tiles, s);
+    if (p.bm == 32) return launch_stream<XT, 2>(a, p.m_tiles, s);
+    return launch_stream<XT, 4>(a, p.m_tiles, s);
   }
-  return rows <= 16 ? launch_stream<XT, 1>(a, s) : rows <= 32 ? launch_stream<XT, 2>(a, s) : launch_stream<XT, 4>(a, s);
+  const int64_t n_tiles = (a.N + 255) / 256;
+  if (p.m_tiles > kMaxGrid / n_tiles / p.splits) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(p.m_tiles * n_tiles * p.splits));
+  if (p.bm == 64)
+    k_linear_tile<XT, 64><<<grid, dim3(256), 0, s>>>(a, p.m_tiles, n_tiles, p.splits);
+  else
+    k_linear_tile<XT, 128><<<grid, dim3(256), 0, s>>>(a, p.m_tiles, n_tiles, p.splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t blocks = (a.M * ((a.N + 3) / 4) + 255) / 256;
+  k_linear_join<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s>>>(a, p.splits);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t linear_workspace(int64_t, int64_t, int64_t, int) { return 0; }
+int64_t linear_workspace(int64_t M, int64_t N, int64_t K, int G) {
+  const Plan p = plan(M, N, K, G);
+  return p.splits == 1 ? 0 : p.splits * M * ((N + 3) / 4 * 4) * 4;
+}
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   switch (a.x_type) {
