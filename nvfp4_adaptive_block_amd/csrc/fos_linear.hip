@@ -273,46 +273,77 @@ __device__ __forceinline__ f32x4 load4(const void* p, int dt, int64_t i, bool wh
   return v;
 }
 
-// Finish columns n .. n + 3 of row m from their sums and store them. The sum
-// is rounded to the output type once, after the residual.
-__device__ __forceinline__ void finish4(const LinearArgs& a, int g, int64_t m, int64_t n, f32x4 v) {
-  const bool whole = a.N % 4 == 0;
-  const int have = a.N - n < 4 ? (int)(a.N - n) : 4;
-  const float sx = a.x_gran == kScaleNone ? 1.0f : a.x_scale[a.x_gran == kScaleRow ? m : a.x_gran == kScaleGroup ? g : 0];
-  const int64_t at = m * a.N + n, wat = (int64_t)g * a.N + n;
-  if (a.w_gran == kScaleRow) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) v[i] *= sx * a.w_scale[i < have ? wat + i : wat];
-  } else {
-    v *= sx * a.w_scale[a.w_gran == kScaleGroup ? g : 0];
+// Which of columns n .. n + 3 exist, and whether they can be accessed together.
+struct Quad {
+  int64_t n;
+  bool whole;
+  int have;
+  __device__ __forceinline__ Quad(const LinearArgs& a, int64_t col) {
+    n = col;
+    whole = a.N % 4 == 0;
+    have = col >= a.N ? 0 : a.N - col < 4 ? (int)(a.N - col) : 4;
   }
-  if (a.bias) v += load4(a.bias, a.bias_dt, wat, whole, have);
+};
+
+// What the epilogue needs of four columns of weight g, and of a row: loaded
+// apart from their use, so that the loads of several run together.
+struct ColumnTail {
+  f32x4 scale, bias;
+  __device__ __forceinline__ void load(const LinearArgs& a, int g, const Quad& q) {
+    scale = bias = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (q.have == 0) return;
+    const int64_t at = (int64_t)g * a.N + q.n;
+    if (a.w_gran == kScaleRow)
+      scale = load4(a.w_scale, kFP32, at, false, q.have);
+    else
+      scale = f32x4{1.0f, 1.0f, 1.0f, 1.0f} * a.w_scale[a.w_gran == kScaleGroup ? g : 0];
+    if (a.bias) bias = load4(a.bias, a.bias_dt, at, q.whole, q.have);
+  }
+};
+struct RowTail {
+  float scale;
+  f32x4 res;
+  __device__ __forceinline__ void load(const LinearArgs& a, int g, int64_t m, const Quad& q) {
+    scale = a.x_gran == kScaleNone ? 1.0f : a.x_scale[a.x_gran == kScaleRow ? m : a.x_gran == kScaleGroup ? g : 0];
+    res = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.res) res = load4(a.res, a.out_dt, m * a.N + q.n, q.whole, q.have);
+  }
+};
+
+// Finish four columns of row m from their sums and store them. The sum is
+// rounded to the output type once, after the residual.
+__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, const Quad& q, const ColumnTail& ct,
+                                        const RowTail& rt, f32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] *= rt.scale * ct.scale[i];
+  if (a.bias) v += ct.bias;
   if (a.act != kActNone) {
 #pragma unroll
     for (int i = 0; i < 4; i++) v[i] = activate(a.act, v[i]);
   }
-  if (a.res) v += load4(a.res, a.out_dt, at, whole, have);
+  if (a.res) v += rt.res;
+  const int64_t at = m * a.N + q.n;
   if (a.out_dt == kFP32) {
     float* y = (float*)a.y + at;
-    if (whole) {
+    if (q.whole) {
       *reinterpret_cast<f32x4*>(y) = v;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        if (i < have) y[i] = v[i];
+        if (i < q.have) y[i] = v[i];
     }
     return;
   }
   uint16_t* y = (uint16_t*)a.y + at;
   const uint2 t = a.out_dt == kBF16 ? uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}
                                     : uint2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
-  if (whole) {
+  if (q.whole) {
     *reinterpret_cast<uint2*>(y) = t;
   } else {
     y[0] = (uint16_t)t.x;
-    if (have > 1) y[1] = (uint16_t)(t.x >> 16);
-    if (have > 2) y[2] = (uint16_t)t.y;
-    if (have > 3) y[3] = (uint16_t)(t.y >> 16);
+    if (q.have > 1) y[1] = (uint16_t)(t.x >> 16);
+    if (q.have > 2) y[2] = (uint16_t)t.y;
+    if (q.have > 3) y[3] = (uint16_t)(t.y >> 16);
   }
 }
 
@@ -432,6 +463,27 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
     xq[j] = XT == kXNVFP4 ? a.xs + row * KB + 2 * g4 : nullptr;
   }
 
+  // The tiles of y that this wave will finish (row tile turn(i) of column tile
+  // i, where that is below MT: one in eight), and what that takes.
+  auto turn = [&](int i) { return (wave + WAVES - (i * MT) % WAVES) % WAVES; };
+  constexpr int TURNS = (NT * MT + WAVES - 1) / WAVES;
+  ColumnTail columns[TURNS];
+  RowTail row[TURNS];
+  bool live[TURNS] = {};
+#pragma unroll
+  for (int i = 0; i < NT; i++) {
+    if (const int j = turn(i); j < MT) {
+      const int k = i * MT / WAVES;
+      const Quad q(a, n0 + 16 * i + 4 * g4);
+      const int64_t m = rt.m0 + 16 * j + col;
+      live[k] = m < rt.end && q.have;
+      if (live[k]) {
+        columns[k].load(a, rt.g, q);
+        row[k].load(a, rt.g, m, q);
+      }
+    }
+  }
+
   uint32_t codes[DEPTH][NT][4], scales[DEPTH][NT];
   XRaw<XT> xr[DEPTH][MT];
 #pragma unroll
@@ -500,13 +552,12 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
 #pragma unroll
     for (int j = 0; j < MT; j++) part[i & 1][wave][j][lane] = acc[i][j];
     __syncthreads();
-    const int j = (wave + WAVES - (i * MT) % WAVES) % WAVES;  // row tile of this wave
-    const int64_t m = rt.m0 + 16 * j + col, n = n0 + 16 * i + 4 * g4;
-    if (j < MT && m < rt.end && n < a.N) {
+    if (const int j = turn(i); j < MT) {
+      const int k = i * MT / WAVES;  // the wave's first or second tile
       f32x4 s = part[i & 1][0][j][lane];
 #pragma unroll
       for (int v = 1; v < WAVES; v++) s += part[i & 1][v][j][lane];
-      finish4(a, rt.g, m, n, s);
+      if (live[k]) finish4(a, rt.m0 + 16 * j + col, Quad(a, n0 + 16 * i + 4 * g4), columns[k], row[k], s);
     }
   }
 }
@@ -520,6 +571,7 @@ typedef const FOS_GLOBAL uint8_t* GlobalBytes;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
 __device__ __forceinline__ uint32_t lane_offset(uint32_t v) {  // stays 32 bits wide in the loop
@@ -656,12 +708,12 @@ struct XStage {
 // turn, so each XCD gets a contiguous range of the tiles; along it, 8 row tiles
 // are taken per column tile, so that the workgroups that run on an XCD at a
 // time share their rows of both operands in its L2.
-__device__ __forceinline__ void tile_of(int64_t m_tiles, int64_t n_tiles, int64_t id, int64_t& tm, int64_t& tn) {
-  const int64_t total = m_tiles * n_tiles;
-  const int64_t x = id % 8, base = total / 8, more = total % 8;
-  const int64_t t = x * base + (x < more ? x : more) + id / 8;
-  const int64_t band = t / (8 * n_tiles), in = t % (8 * n_tiles);
-  const int64_t high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
+__device__ __forceinline__ void tile_of(uint32_t m_tiles, uint32_t n_tiles, uint32_t id, int64_t& tm, int64_t& tn) {
+  const uint32_t total = m_tiles * n_tiles;  // a grid: below 2^31
+  const uint32_t x = id % 8, base = total / 8, more = total % 8;
+  const uint32_t t = x * base + (x < more ? x : more) + id / 8;
+  const uint32_t band = t / (8 * n_tiles), in = t % (8 * n_tiles);
+  const uint32_t high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
   tm = band * 8 + in % high;
   tn = in / high;
 }
@@ -684,7 +736,7 @@ __device__ __forceinline__ void block_sync() {
 }
 
 template <int XT, int BM>
-__global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArgs a, int64_t m_tiles, int64_t n_tiles,
+__global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles,
                                                                        int splits) {
   constexpr bool BF16 = XT == kBF16;
   constexpr int MT = BM / 16;
@@ -719,23 +771,37 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
   const uint8_t* wc = a.w + w0 * (a.K / 2);
   const uint8_t* wsc = a.ws + w0 * KB;
   const int wrows = n0 < a.N ? (a.N - n0 < 64 ? (int)(a.N - n0) : 64) : 1;
-  uint32_t woff[4], wsoff[4];
+  //
+  // A load instruction costs a cycle for every 64 bytes or row that four
+  // consecutive lanes touch, and the matrix instruction wants consecutive lanes
+  // in different rows. So four neighbouring lanes load the 64 bytes of a row,
+  // and one lane the 8 scale bytes of each of the wave's 64 rows, and the lanes
+  // swap them when the step begins: 20 exchanges against 1500 cycles of loads.
+  uint32_t woff[4], wsoff;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const uint32_t r = 16 * i + col < wrows ? 16 * i + col : wrows - 1;
-    woff[i] = r * (uint32_t)(a.K / 2) + 16 * g4;
-    wsoff[i] = r * (uint32_t)KB + 2 * g4;
+    const int r = 16 * i + (lane >> 2);
+    woff[i] = (uint32_t)(r < wrows ? r : wrows - 1) * (uint32_t)(a.K / 2) + 16 * (lane & 3);
   }
-  struct Weights {
-    u32x4 codes[4];
-    uint32_t scales[4];
-  } w_now, w_next;
+  wsoff = (uint32_t)(lane < wrows ? lane : wrows - 1) * (uint32_t)KB;
+  u32x4 w_load[4];
+  u32x2 s_load;
+  uint32_t codes[4][4], scales[4];
   auto load_w = [&](int step) {
     const GlobalBytes p = scalar(wc + (int64_t)step * 64), q = scalar(wsc + (int64_t)step * 8);
 #pragma unroll
+    for (int i = 0; i < 4; i++) w_load[i] = *(const FOS_GLOBAL u32x4_a8*)(p + lane_offset(woff[i]));
+    s_load = *(const FOS_GLOBAL u32x2_a1*)(q + lane_offset(wsoff));
+  };
+  auto take_w = [&] {
+#pragma unroll
     for (int i = 0; i < 4; i++) {
-      w_next.codes[i] = *(const FOS_GLOBAL u32x4_a8*)(p + lane_offset(woff[i]));
-      w_next.scales[i] = *(const FOS_GLOBAL u16_a1*)(q + lane_offset(wsoff[i]));
+#pragma unroll
+      for (int j = 0; j < 4; j++) codes[i][j] = __builtin_amdgcn_ds_bpermute(16 * col + 4 * g4, w_load[i][j]);
+      // bytes 2 g and 2 g + 1 of the row's eight
+      const uint32_t lo = __builtin_amdgcn_ds_bpermute(64 * i + 4 * col, s_load[0]);
+      const uint32_t hi = __builtin_amdgcn_ds_bpermute(64 * i + 4 * col, s_load[1]);
+      scales[i] = (g4 < 2 ? lo : hi) >> (16 * (g4 & 1));
     }
   };
 
@@ -759,11 +825,11 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
       Frag w[4][2];
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const f32x2 s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w_now.scales[i], 1.0f, false);
-        const h2 s16 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w_now.scales[i], 1.0f, false);
+        const f32x2 s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)scales[i], 1.0f, false);
+        const h2 s16 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales[i], 1.0f, false);
         const h2 sh = h ? __builtin_shufflevector(s16, s16, 1, 1) : __builtin_shufflevector(s16, s16, 0, 0);
-        decode8<BF16>(w_now.codes[i][2 * h], h ? s.y : s.x, sh, w[i][0].u);
-        decode8<BF16>(w_now.codes[i][2 * h + 1], h ? s.y : s.x, sh, w[i][1].u);
+        decode8<BF16>(codes[i][2 * h], h ? s.y : s.x, sh, w[i][0].u);
+        decode8<BF16>(codes[i][2 * h + 1], h ? s.y : s.x, sh, w[i][1].u);
       }
 #pragma unroll
       for (int m = 0; m < MT; m++) {
@@ -795,7 +861,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
     // may not happen would make the compiler wait where the paths meet.)
     wait_vm<0>();
     block_sync();
-    w_now = w_next;
+    take_w();
     uint8_t* next = lds[(step & 1) ^ 1];
     const int after = step + 1 < whole ? step + 1 : step;
     load_w(after);
@@ -811,15 +877,16 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
     const int64_t b = (int64_t)whole * 8 + 2 * g4;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      w_now.scales[i] = 0;
+      const int64_t r = 16 * i + col < wrows ? 16 * i + col : wrows - 1;
+      scales[i] = 0;
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         uint2 t = {0, 0};
         if (b + h < KB) {
-          t = *reinterpret_cast<const uint2*>(wc + (int64_t)whole * 64 + woff[i] + 8 * h);
-          w_now.scales[i] |= (uint32_t)wsc[(int64_t)whole * 8 + wsoff[i] + h] << (8 * h);
+          t = *reinterpret_cast<const uint2*>(wc + r * (a.K / 2) + 8 * (b + h));
+          scales[i] |= (uint32_t)wsc[r * KB + b + h] << (8 * h);
         }
-        w_now.codes[i][2 * h] = t.x, w_now.codes[i][2 * h + 1] = t.y;
+        codes[i][2 * h] = t.x, codes[i][2 * h + 1] = t.y;
       }
     }
     __syncthreads();
@@ -827,6 +894,9 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
   }
   // Each wave turns its sums by way of its quarter of the LDS, half of the rows
   // at a time, so that 16 lanes store 64 neighbouring columns of a row.
+  const Quad q(a, n0 + 4 * col);
+  ColumnTail columns;
+  if (splits == 1) columns.load(a, rt.g, q);
   __syncthreads();
   uint8_t* mine = &lds[0][0] + wave * (BM * 128);
 #pragma unroll
@@ -836,29 +906,47 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
 #pragma unroll
       for (int i = 0; i < 4; i++)
         *reinterpret_cast<f32x4*>(mine + (16 * m + col) * 256 + (((4 * i + g4) ^ col) << 4)) = acc[i][half * (MT / 2) + m];
+    // four rows of lanes at a time, eight steps' loads together
 #pragma unroll 1
-    for (int it = 0; it < BM / 8; it++) {
-      const int lr = 4 * it + g4, r = half * (BM / 2) + lr;
-      const f32x4 v = *reinterpret_cast<const f32x4*>(mine + lr * 256 + ((col ^ (lr & 15)) << 4));
-      const int64_t n = n0 + 4 * col;
-      if (r >= rows || n >= a.N) continue;
-      if (splits == 1)
-        finish4(a, rt.g, rt.m0 + r, n, v);
-      else  // rows of the workspace are padded to a multiple of 4 columns
-        *reinterpret_cast<f32x4*>((float*)a.work + (part * a.M + rt.m0 + r) * ((a.N + 3) / 4 * 4) + n) = v;
+    for (int it = 0; it < BM / 8; it += 8) {
+      RowTail row[8];
+      if (splits == 1) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const int r = half * (BM / 2) + 4 * (it + k) + g4;
+          if (r < rows && q.have) row[k].load(a, rt.g, rt.m0 + r, q);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const int lr = 4 * (it + k) + g4, r = half * (BM / 2) + lr;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(mine + lr * 256 + ((col ^ (lr & 15)) << 4));
+        if (r >= rows || !q.have) continue;
+        if (splits == 1)
+          finish4(a, rt.m0 + r, q, columns, row[k], v);
+        else  // rows of the workspace are padded to a multiple of 4 columns
+          *reinterpret_cast<f32x4*>((float*)a.work + (part * a.M + rt.m0 + r) * ((a.N + 3) / 4 * 4) + q.n) = v;
+      }
     }
   }
 }
 
 // Joins the parts of K in order and finishes: four columns per thread.
 __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, int splits) {
-  const int64_t quads = (a.N + 3) / 4, total = a.M * quads;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const f32x4* p = (const f32x4*)a.work + i;
-    f32x4 v = p[0];
-    for (int s = 1; s < splits; s++) v += p[s * total];
-    finish4(a, 0, i / quads, i % quads * 4, v);
-  }
+  const uint32_t quads = (uint32_t)((a.N + 3) / 4), blocks = (quads + 255) / 256;  // workgroups per row
+  const int64_t m = blockIdx.x / blocks, total = a.M * quads;
+  const uint32_t c = blockIdx.x % blocks * 256 + threadIdx.x;
+  if (c >= quads) return;
+  const Quad q(a, (int64_t)c * 4);
+  ColumnTail columns;
+  RowTail row;
+  columns.load(a, 0, q);
+  row.load(a, 0, m, q);
+  const f32x4* p = (const f32x4*)a.work + m * quads + c;
+  f32x4 v = p[0];
+#pragma unroll 4
+  for (int s = 1; s < splits; s++) v += p[s * total];
+  finish4(a, m, q, columns, row, v);
 }
 
 constexpr int64_t kMaxGrid = INT32_MAX;
@@ -923,13 +1011,13 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
   if (p.m_tiles > kMaxGrid / n_tiles / p.splits) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(p.m_tiles * n_tiles * p.splits));
   if (p.bm == 64)
-    k_linear_tile<XT, 64><<<grid, dim3(256), 0, s>>>(a, p.m_tiles, n_tiles, p.splits);
+    k_linear_tile<XT, 64><<<grid, dim3(256), 0, s>>>(a, (uint32_t)p.m_tiles, (uint32_t)n_tiles, p.splits);
   else
-    k_linear_tile<XT, 128><<<grid, dim3(256), 0, s>>>(a, p.m_tiles, n_tiles, p.splits);
+    k_linear_tile<XT, 128><<<grid, dim3(256), 0, s>>>(a, (uint32_t)p.m_tiles, (uint32_t)n_tiles, p.splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t blocks = (a.M * ((a.N + 3) / 4) + 255) / 256;
-  k_linear_join<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s>>>(a, p.splits);
+  const int64_t blocks = a.M * (((a.N + 3) / 4 + 255) / 256);
+  k_linear_join<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a, p.splits);
   return hipGetLastError();
 }
 
