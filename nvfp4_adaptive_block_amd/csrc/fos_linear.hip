@@ -39,6 +39,14 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// the same at the alignment that a tensor's rows give
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
 // Eight 16-bit values along k of one row.
 union Frag {
@@ -255,32 +263,31 @@ __device__ __forceinline__ float activate(int act, float v) {
   }
 }
 
-// Four neighbouring values of a tensor; `whole`: all four exist and the row
-// length is a multiple of 4, so that they lie on a 4-value boundary.
-__device__ __forceinline__ f32x4 load4(const void* p, int dt, int64_t i, bool whole, int have) {
+// Four neighbouring values of a tensor, `have` of which exist. Rows of any
+// length: the accesses need no more than the elements' own alignment.
+
+__device__ __forceinline__ f32x4 load4(const void* p, int dt, int64_t i, int have) {
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (!whole) {
+  if (have < 4) {
 #pragma unroll
     for (int j = 0; j < 4; j++)
       if (j < have) v[j] = to_f32(p, dt, i + j);
   } else if (dt == kFP32) {
-    v = *reinterpret_cast<const f32x4*>((const float*)p + i);
+    v = *reinterpret_cast<const f32x4_a4*>((const float*)p + i);
   } else {
-    const uint2 t = *reinterpret_cast<const uint2*>((const uint16_t*)p + i);
+    const u32x2 t = *reinterpret_cast<const u32x2_a2*>((const uint16_t*)p + i);
     v = dt == kBF16 ? f32x4{bf16_lo(t.x), bf16_hi(t.x), bf16_lo(t.y), bf16_hi(t.y)}
                     : f32x4{f16_lo(t.x), f16_hi(t.x), f16_lo(t.y), f16_hi(t.y)};
   }
   return v;
 }
 
-// Which of columns n .. n + 3 exist, and whether they can be accessed together.
+// Columns n .. n + 3 and how many of them exist.
 struct Quad {
   int64_t n;
-  bool whole;
   int have;
   __device__ __forceinline__ Quad(const LinearArgs& a, int64_t col) {
     n = col;
-    whole = a.N % 4 == 0;
     have = col >= a.N ? 0 : a.N - col < 4 ? (int)(a.N - col) : 4;
   }
 };
@@ -294,10 +301,10 @@ struct ColumnTail {
     if (q.have == 0) return;
     const int64_t at = (int64_t)g * a.N + q.n;
     if (a.w_gran == kScaleRow)
-      scale = load4(a.w_scale, kFP32, at, false, q.have);
+      scale = load4(a.w_scale, kFP32, at, q.have);
     else
       scale = f32x4{1.0f, 1.0f, 1.0f, 1.0f} * a.w_scale[a.w_gran == kScaleGroup ? g : 0];
-    if (a.bias) bias = load4(a.bias, a.bias_dt, at, q.whole, q.have);
+    if (a.bias) bias = load4(a.bias, a.bias_dt, at, q.have);
   }
 };
 struct RowTail {
@@ -306,7 +313,7 @@ struct RowTail {
   __device__ __forceinline__ void load(const LinearArgs& a, int g, int64_t m, const Quad& q) {
     scale = a.x_gran == kScaleNone ? 1.0f : a.x_scale[a.x_gran == kScaleRow ? m : a.x_gran == kScaleGroup ? g : 0];
     res = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.res) res = load4(a.res, a.out_dt, m * a.N + q.n, q.whole, q.have);
+    if (a.res) res = load4(a.res, a.out_dt, m * a.N + q.n, q.have);
   }
 };
 
@@ -325,8 +332,8 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, const Qu
   const int64_t at = m * a.N + q.n;
   if (a.out_dt == kFP32) {
     float* y = (float*)a.y + at;
-    if (q.whole) {
-      *reinterpret_cast<f32x4*>(y) = v;
+    if (q.have == 4) {
+      *reinterpret_cast<f32x4_a4*>(y) = v;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; i++)
@@ -335,10 +342,10 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, const Qu
     return;
   }
   uint16_t* y = (uint16_t*)a.y + at;
-  const uint2 t = a.out_dt == kBF16 ? uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}
-                                    : uint2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
-  if (q.whole) {
-    *reinterpret_cast<uint2*>(y) = t;
+  const u32x2 t = a.out_dt == kBF16 ? u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}
+                                    : u32x2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
+  if (q.have == 4) {
+    *reinterpret_cast<u32x2_a2*>(y) = t;
   } else {
     y[0] = (uint16_t)t.x;
     if (q.have > 1) y[1] = (uint16_t)(t.x >> 16);
@@ -358,71 +365,101 @@ __device__ __forceinline__ void zero4(const LinearArgs& a, int64_t m, int64_t n)
 
 // ---------------------------------------------------------------- kernels
 
-// What one lane holds of a row of activations for a 128-deep step (its blocks
-// 2g and 2g + 1), as it lies in memory.
+// A 128-deep step of 16 rows of activations on its way through one wave: loaded
+// with neighbouring lanes in the same row (16 lanes to a row of 16-bit values, 8
+// of E4M3, 4 of NVFP4 codes), put into the wave's own piece of LDS as it is, and
+// read back as the matrix instruction wants it, lane l the 32 values of its
+// blocks 2g and 2g + 1 of row l % 16. LDS operations of one wave run in order, so
+// no barrier is needed. Chunks of 16 bytes are swizzled so that the 16 rows that
+// are read together lie in 16 different places of the 256 bytes that LDS serves
+// at a time.
 template <int XT>
-struct XRaw {
-  static constexpr int kWords = XT == kXE4M3 ? 8 : XT == kXNVFP4 ? 4 : 16;
-  uint32_t v[kWords];
-  uint32_t s;
+struct XTile {
+  static constexpr int kLanes = XT == kXE4M3 ? 8 : XT == kXNVFP4 ? 4 : 16;  // per row
+  static constexpr int kLoads = kLanes / 4;                                  // of 64 / kLanes rows
+  static constexpr int kBytes = 16 * 16 * kLanes;
+  u32x4 v[kLoads];
+  u32x2 s;
 
+  static __device__ __forceinline__ int slot(int row, int chunk) {
+    return row * 16 * kLanes + ((chunk ^ (kLanes == 16 ? row : kLanes == 8 ? row >> 1 : row >> 2)) << 4);
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < kWords; i++) v[i] = 0;
-    s = 0;
+    for (int i = 0; i < kLoads; i++) v[i] = u32x4{0, 0, 0, 0};
+    s = u32x2{0, 0};
   }
-  // p: the lane's first block of a whole step; q: its scale bytes
-  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* q) {
+  // rows: how many exist; p: row 0 of the tile at the step; q: its scales.
+  // Rows that do not exist keep what clear() put there.
+  __device__ __forceinline__ void load(const LinearArgs& a, const uint8_t* p, const uint8_t* q, int rows) {
+    const int lane = threadIdx.x & 63;
+    const int64_t stride = a.K / 16 * (2 * kLanes);
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int row = i * (64 / kLanes) + lane / kLanes;
+      if (row < rows) v[i] = *reinterpret_cast<const u32x4_a8*>(p + row * stride + 16 * (lane % kLanes));
+    }
     if constexpr (XT == kXNVFP4) {
-      const Bytes16 t = *reinterpret_cast<const Bytes16*>(p);
-#pragma unroll
-      for (int i = 0; i < 4; i++) v[i] = t.v[i];
-      s = reinterpret_cast<const Bytes2*>(q)->v;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords / 4; i++) {
-        const uint4 t = reinterpret_cast<const uint4*>(p)[i];
-        v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
-      }
+      const int row = lane & 15;
+      if (row < rows) s = *reinterpret_cast<const u32x2_a1*>(q + row * (a.K / 16));
     }
   }
-  __device__ __forceinline__ void decode(Frag* f) const {
+  __device__ __forceinline__ void put(uint8_t* lds) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kLoads; i++)
+      *reinterpret_cast<u32x4*>(lds + slot(i * (64 / kLanes) + lane / kLanes, lane % kLanes)) = v[i];
+  }
+  // (scales: this lane's two bytes, from row_scales of s)
+  static __device__ __forceinline__ void get(const uint8_t* lds, uint32_t scales, Frag* f) {
+    const int lane = threadIdx.x & 63, col = lane & 15, g4 = lane >> 4;
+    u32x4 t[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) t[i] = *reinterpret_cast<const u32x4*>(lds + slot(col, kLoads * g4 + i));
     if constexpr (XT == kXNVFP4) {
-      decode_blocks<false>(v, s, f);
+      const uint32_t c[4] = {t[0][0], t[0][1], t[0][2], t[0][3]};
+      decode_blocks<false>(c, scales, f);
     } else if constexpr (XT == kXE4M3) {
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        f[j / 2].u[2 * (j & 1)] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)v[j], 1.0f, false));
-        f[j / 2].u[2 * (j & 1) + 1] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)v[j], 1.0f, true));
+        const int w = (int)t[j / 4][j % 4];
+        f[j / 2].u[2 * (j & 1)] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+        f[j / 2].u[2 * (j & 1) + 1] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) f[i].u[j] = v[4 * i + j];
+        for (int j = 0; j < 4; j++) f[i].u[j] = t[i][j];
     }
   }
 };
 
-// Bytes of one 16-value block of a row of activations.
-template <int XT>
-constexpr int x_block_bytes() {
-  return XT == kXE4M3 ? 16 : XT == kXNVFP4 ? 8 : 32;
+// Scale bytes 2 g and 2 g + 1 of row l % 16, where lane `from + row` holds the
+// eight bytes of a row.
+__device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
+  const int lane = threadIdx.x & 63, g4 = lane >> 4;
+  const uint32_t lo = __builtin_amdgcn_ds_bpermute(4 * (from + (lane & 15)), s[0]);
+  const uint32_t hi = __builtin_amdgcn_ds_bpermute(4 * (from + (lane & 15)), s[1]);
+  return (g4 < 2 ? lo : hi) >> (16 * (g4 & 1));
 }
 
 // The stream kernel, for few rows per weight: one workgroup takes 16 NT columns
 // of y and 16 MT rows, and its eight waves take the 128-deep steps of k in turn,
-// so that the weight is read once, straight to registers, by as many waves as
-// the chip has. A wave keeps DEPTH steps of loads in flight (4 KiB of codes).
-// Rows of the activations that do not exist are not loaded. The waves' sums are
-// joined through LDS in wave order.
+// so that the weight is read once by as many waves as the chip has. A wave keeps
+// DEPTH steps of loads in flight (4 KiB of codes). Like the activations, the
+// weights are loaded four lanes to a row and turned through the wave's own LDS.
+// The waves' sums are joined through LDS in wave order.
 template <int XT, int MT, int NT>
 __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16;
-  constexpr int WAVES = 8, DEPTH = MT == 4 && NT == 1 ? 2 : 4 / NT;
+  constexpr int WAVES = 8, DEPTH = MT == 4 ? 1 : 4 / NT;
+  constexpr int kWaveBytes = NT * 1024 + XTile<XT>::kBytes;
+  constexpr int kPartBytes = (NT > 1 ? 2 : 1) * WAVES * MT * 1024;
+  __shared__ __align__(16) uint8_t lds[kPartBytes > WAVES * kWaveBytes ? kPartBytes : WAVES * kWaveBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = blockIdx.x / n_tiles;
-  const int64_t n0 = 16 * NT * (int64_t)(blockIdx.x % n_tiles);
+  const int64_t t = blockIdx.x / (uint32_t)n_tiles;
+  const int64_t n0 = 16 * NT * (int64_t)(blockIdx.x % (uint32_t)n_tiles);
   RowTile rt{t * 16 * MT, a.M, 0};
   if (a.offs) {
     if (a.status && blockIdx.x == 0 && wave == 0) check_offs(a);
@@ -445,23 +482,19 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
 #pragma unroll
     for (int j = 0; j < MT; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const uint8_t *wp[NT], *wq[NT], *xp[MT], *xq[MT];  // at the lane's first block
-  bool have[MT];
+  // columns past the end read the last row of the weight
+  const int wrows = a.N - n0 < 16 * NT ? (int)(a.N - n0) : 16 * NT;
+  const int64_t w0 = (int64_t)rt.g * a.N + n0;
+  const uint8_t* wp[NT];
+  const uint8_t* wq = a.ws + (w0 + (lane < wrows ? lane : wrows - 1)) * KB;
 #pragma unroll
   for (int i = 0; i < NT; i++) {
-    const int64_t n = n0 + 16 * i + col;
-    const int64_t row = (int64_t)rt.g * a.N + (n < a.N ? n : a.N - 1);
-    wp[i] = a.w + row * (a.K / 2) + 16 * g4;
-    wq[i] = a.ws + row * KB + 2 * g4;
+    const int r = 16 * i + (lane >> 2);
+    wp[i] = a.w + (w0 + (r < wrows ? r : wrows - 1)) * (a.K / 2) + 16 * (lane & 3);
   }
-#pragma unroll
-  for (int j = 0; j < MT; j++) {
-    const int64_t m = rt.m0 + 16 * j + col;
-    have[j] = m < rt.end;
-    const int64_t row = have[j] ? m : rt.m0;
-    xp[j] = (const uint8_t*)a.x + (row * KB + 2 * g4) * x_block_bytes<XT>();
-    xq[j] = XT == kXNVFP4 ? a.xs + row * KB + 2 * g4 : nullptr;
-  }
+  const int xrows = rt.end - rt.m0 < 16 * MT ? (int)(rt.end - rt.m0) : 16 * MT;
+  const uint8_t* xp = (const uint8_t*)a.x + rt.m0 * KB * (2 * XTile<XT>::kLanes);
+  const uint8_t* xq = XT == kXNVFP4 ? a.xs + rt.m0 * KB : nullptr;
 
   // The tiles of y that this wave will finish (row tile turn(i) of column tile
   // i, where that is below MT: one in eight), and what that takes.
@@ -484,69 +517,85 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
     }
   }
 
-  uint32_t codes[DEPTH][NT][4], scales[DEPTH][NT];
-  XRaw<XT> xr[DEPTH][MT];
+  u32x4 codes[DEPTH][NT];
+  u32x2 scales[DEPTH];
+  XTile<XT> x[DEPTH][MT];
 #pragma unroll
   for (int d = 0; d < DEPTH; d++)
 #pragma unroll
-    for (int j = 0; j < MT; j++) xr[d][j].clear();
-  auto load = [&](int d, int64_t step) {
+    for (int j = 0; j < MT; j++) x[d][j].clear();
+  auto load_w = [&](int d, int64_t step) {
+#pragma unroll
+    for (int i = 0; i < NT; i++) codes[d][i] = *reinterpret_cast<const u32x4_a8*>(wp[i] + step * 64);
+    if (NT == 4 || lane < 16 * NT) scales[d] = *reinterpret_cast<const u32x2_a1*>(wq + step * 8);
+  };
+  auto load_rows = [&](int d, int j, int64_t step) {
+    x[d][j].load(a, xp + 16 * j * KB * (2 * XTile<XT>::kLanes) + step * (16 * XTile<XT>::kLanes),
+                 xq + 16 * j * KB + step * 8, xrows - 16 * j);
+  };
+  uint8_t* wl = lds + wave * kWaveBytes;
+  uint8_t* xl = wl + NT * 1024;
+  // One step from the registers of stage d, which are loaded again for `after`
+  // (below `whole`, or not at all) as soon as their contents are in LDS.
+  auto multiply = [&](int d, int after) {
+    uint32_t ws[NT];
 #pragma unroll
     for (int i = 0; i < NT; i++) {
-      const Bytes16 v = *reinterpret_cast<const Bytes16*>(wp[i] + step * 64);
+      *reinterpret_cast<u32x4*>(wl + i * 1024 + XTile<kXNVFP4>::slot(lane >> 2, lane & 3)) = codes[d][i];
+      ws[i] = row_scales(scales[d], 16 * i);
+    }
+    if (after < whole) load_w(d, after);
+    Frag w[NT][4];
 #pragma unroll
-      for (int j = 0; j < 4; j++) codes[d][i][j] = v.v[j];
-      scales[d][i] = reinterpret_cast<const Bytes2*>(wq[i] + step * 8)->v;
+    for (int i = 0; i < NT; i++) {
+      const u32x4 t = *reinterpret_cast<const u32x4*>(wl + i * 1024 + XTile<kXNVFP4>::slot(col, g4));
+      const uint32_t c[4] = {t[0], t[1], t[2], t[3]};
+      decode_blocks<BF16>(c, ws[i], w[i]);
     }
 #pragma unroll
-    for (int j = 0; j < MT; j++)
-      if (have[j]) xr[d][j].load(xp[j] + step * 8 * x_block_bytes<XT>(), xq[j] + step * 8);
-  };
-  auto multiply = [&](int d) {
-    Frag x[MT][4];
-#pragma unroll
-    for (int j = 0; j < MT; j++) xr[d][j].decode(x[j]);
-#pragma unroll
-    for (int i = 0; i < NT; i++) {
-      Frag w[4];
-      decode_blocks<BF16>(codes[d][i], scales[d][i], w);
+    for (int j = 0; j < MT; j++) {
+      x[d][j].put(xl);
+      const uint32_t sc = XT == kXNVFP4 ? row_scales(x[d][j].s, 0) : 0;
+      if (after < whole) load_rows(d, j, after);
+      Frag f[4];
+      XTile<XT>::get(xl, sc, f);
 #pragma unroll
       for (int k = 0; k < 4; k++)
 #pragma unroll
-        for (int j = 0; j < MT; j++) acc[i][j] = mfma<BF16>(w[k], x[j][k], acc[i][j]);
+        for (int i = 0; i < NT; i++) acc[i][j] = mfma<BF16>(w[i][k], f[k], acc[i][j]);
     }
   };
 #pragma unroll
   for (int d = 0; d < DEPTH; d++)
-    if (wave + d * WAVES < whole) load(d, wave + d * WAVES);
+    if (wave + d * WAVES < whole) {
+      load_w(d, wave + d * WAVES);
+#pragma unroll
+      for (int j = 0; j < MT; j++) load_rows(d, j, wave + d * WAVES);
+    }
   for (int step = wave; step < whole; step += WAVES * DEPTH) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; d++) {
-      if (step + d * WAVES < whole) {
-        multiply(d);
-        if (step + (d + DEPTH) * WAVES < whole) load(d, step + (d + DEPTH) * WAVES);
-      }
-    }
+    for (int d = 0; d < DEPTH; d++)
+      if (step + d * WAVES < whole) multiply(d, step + (d + DEPTH) * WAVES);
   }
   if (KB % 8 && wave == whole % WAVES) {  // the part of a step that is left
     const int64_t b = (int64_t)whole * 8 + 2 * g4;
-    Frag x[MT][4];
+    Frag f[MT][4];
 #pragma unroll
-    for (int j = 0; j < MT; j++) load_x<XT>(a, have[j] ? rt.m0 + 16 * j + col : rt.m0, b, KB, x[j]);
+    for (int j = 0; j < MT; j++) load_x<XT>(a, rt.m0 + (16 * j + col < xrows ? 16 * j + col : 0), b, KB, f[j]);
 #pragma unroll
     for (int i = 0; i < NT; i++) {
-      const int64_t n = n0 + 16 * i + col;
-      const int64_t row = (int64_t)rt.g * a.N + (n < a.N ? n : a.N - 1);
+      const int64_t row = w0 + (16 * i + col < wrows ? 16 * i + col : wrows - 1);
       Frag w[4];
       load_nvfp4<BF16>(a.w + row * (a.K / 2), a.ws + row * KB, b, KB, w);
 #pragma unroll
       for (int k = 0; k < 4; k++)
 #pragma unroll
-        for (int j = 0; j < MT; j++) acc[i][j] = mfma<BF16>(w[k], x[j][k], acc[i][j]);
+        for (int j = 0; j < MT; j++) acc[i][j] = mfma<BF16>(w[k], f[j][k], acc[i][j]);
     }
   }
   // one column tile at a time, in two halves of the LDS in turn
-  __shared__ f32x4 part[NT > 1 ? 2 : 1][WAVES][MT][64];
+  f32x4(*part)[WAVES][MT][64] = reinterpret_cast<f32x4(*)[WAVES][MT][64]>(lds);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < NT; i++) {
 #pragma unroll
@@ -568,11 +617,6 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
 // those that K % 16 == 0 gives.
 #define FOS_GLOBAL __attribute__((address_space(1)))
 typedef const FOS_GLOBAL uint8_t* GlobalBytes;
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
-typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
-typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
 __device__ __forceinline__ uint32_t lane_offset(uint32_t v) {  // stays 32 bits wide in the loop
   asm volatile("" : "+v"(v));
@@ -831,6 +875,8 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
         decode8<BF16>(codes[i][2 * h], h ? s.y : s.x, sh, w[i][0].u);
         decode8<BF16>(codes[i][2 * h + 1], h ? s.y : s.x, sh, w[i][1].u);
       }
+      // the other workgroup's wave on this SIMD decodes meanwhile
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int m = 0; m < MT; m++) {
         if (m + 1 < MT) {
@@ -844,6 +890,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
           for (int i = 0; i < 4; i++) acc[i][m] = mfma<BF16>(w[i][j], x[m & 1][j], acc[i][m]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_s_setprio(0);
     }
   };
 
@@ -994,7 +1041,14 @@ hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) 
 template <int XT, int MT>
 hipError_t launch_stream(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
   const int64_t n16 = (a.N + 15) / 16;
-  if (n16 / 4 * m_tiles >= 224) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
+#ifdef FOS_NT
+  if (FOS_NT == 4) { if constexpr (MT < 4 || XT > kFP16) return launch_stream_n<XT, MT, 4>(a, m_tiles, s); }
+  if (FOS_NT >= 2) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
+  if (FOS_NT == 1) return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
+#endif
+  if constexpr (MT < 4 || XT > kFP16) {
+    if (n16 / 4 * m_tiles >= 224) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
+  }
   if (n16 / 2 * m_tiles >= 224) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
   return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
 }
