@@ -365,6 +365,22 @@ __device__ __forceinline__ void zero4(const LinearArgs& a, int64_t m, int64_t n)
 
 // ---------------------------------------------------------------- kernels
 
+// Where the LDS tiles keep a row's 16-byte chunks. LDS serves a 16-byte read of
+// 16 lanes at a time, but not of 16 neighbours: lanes 0-3 and 12-15 go with
+// 20-27, and 4-11 with 16-19 and 28-31 (the same in the upper half). With lane l
+// reading row l % 16 that is every row once, half of them one group of 16 lanes
+// further on, at another chunk. Chunk c of row r stands at c ^ swizzle(r), where
+// the two halves of the rows get different values of the bit that the chunk
+// numbers of the two groups do not differ in; then all 16 places differ. (Plain
+// c ^ r met every place twice: 41% of the tile kernel's LDS cycles.)
+// BITS: log2 of the chunks in a row; with fewer than 16 the rows that share the
+// 256 bytes count too.
+template <int BITS>
+__device__ __forceinline__ int swizzle(int r) {
+  const int v = (r & 15) >> (4 - BITS);
+  return v ^ ((v & (1 << (BITS - 2))) << 1);
+}
+
 // A 128-deep step of 16 rows of activations on its way through one wave: loaded
 // with neighbouring lanes in the same row (16 lanes to a row of 16-bit values, 8
 // of E4M3, 4 of NVFP4 codes), put into the wave's own piece of LDS as it is, and
@@ -382,7 +398,7 @@ struct XTile {
   u32x2 s;
 
   static __device__ __forceinline__ int slot(int row, int chunk) {
-    return row * 16 * kLanes + ((chunk ^ (kLanes == 16 ? row : kLanes == 8 ? row >> 1 : row >> 2)) << 4);
+    return row * 16 * kLanes + ((chunk ^ swizzle<kLanes == 16 ? 4 : kLanes == 8 ? 3 : 2>(row)) << 4);
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -636,9 +652,7 @@ __device__ __forceinline__ GlobalBytes scalar(const uint8_t* p) {
 // LDS carries half of what two staged operands would (per step and wave 32 KiB
 // read for 128 matrix instructions of 16 cycles: half of the LDS's rate).
 //
-// LDS: row r of the tile is 16 chunks of 16 bytes (8 values), chunk c at slot
-// c ^ (r % 16). A fragment read takes, in 16 lanes, one chunk number of 16 rows:
-// 16 different slots, so no bank is hit twice.
+// LDS: row r of the tile is 16 chunks of 16 bytes (8 values), swizzled as above.
 template <int XT, int BM>
 struct XStage {
   static constexpr bool kDirect = XT == kBF16 || XT == kFP16;
@@ -660,7 +674,7 @@ struct XStage {
 #pragma unroll
       for (int i = 0; i < BM / 16; i++) {
         const int r = (wave * (BM / 16) + i) * 4 + (lane >> 4);
-        const int c = (lane & 15) ^ (r & 15);
+        const int c = (lane & 15) ^ swizzle<4>(r);
         off[i] = (uint32_t)(r < rows ? r : rows - 1) * (uint32_t)(a.K * 2) + 16 * c;
       }
     } else {
@@ -733,7 +747,7 @@ struct XStage {
   static __device__ __forceinline__ void put(uint8_t* lds, int r, int c, const Frag* f) {
 #pragma unroll
     for (int j = 0; j < 4; j++)
-      *reinterpret_cast<h8*>(lds + r * 256 + (((c + j) ^ (r & 15)) << 4)) = f[j].h;
+      *reinterpret_cast<h8*>(lds + r * 256 + (((c + j) ^ swizzle<4>(r)) << 4)) = f[j].h;
   }
 
   // The last step when K ends inside it: blocks past the end are zero.
@@ -857,7 +871,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
 
   uint32_t roff[4];  // fragment c = 2 h + j of this lane: LDS byte offset in rows 0 .. 15
 #pragma unroll
-  for (int c = 0; c < 4; c++) roff[c] = col * 256 + (((4 * g4 + c) ^ col) << 4);
+  for (int c = 0; c < 4; c++) roff[c] = col * 256 + (((4 * g4 + c) ^ swizzle<4>(col)) << 4);
 
   // Multiply the staged step by the weights in registers.
   auto multiply = [&](const uint8_t* cur) {
@@ -952,7 +966,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
     for (int m = 0; m < MT / 2; m++)
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        *reinterpret_cast<f32x4*>(mine + (16 * m + col) * 256 + (((4 * i + g4) ^ col) << 4)) = acc[i][half * (MT / 2) + m];
+        *reinterpret_cast<f32x4*>(mine + (16 * m + col) * 256 + (((4 * i + g4) ^ swizzle<4>(col)) << 4)) = acc[i][half * (MT / 2) + m];
     // four rows of lanes at a time, eight steps' loads together
 #pragma unroll 1
     for (int it = 0; it < BM / 8; it += 8) {
@@ -967,7 +981,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         const int lr = 4 * (it + k) + g4, r = half * (BM / 2) + lr;
-        const f32x4 v = *reinterpret_cast<const f32x4*>(mine + lr * 256 + ((col ^ (lr & 15)) << 4));
+        const f32x4 v = *reinterpret_cast<const f32x4*>(mine + lr * 256 + ((col ^ swizzle<4>(lr)) << 4));
         if (r >= rows || !q.have) continue;
         if (splits == 1)
           finish4(a, rt.m0 + r, q, columns, row[k], v);
