@@ -24,13 +24,6 @@
 #include "fos_device.h"
 #include "fos_ops.h"
 
-#ifndef FOS_STREAM_MAX
-#define FOS_STREAM_MAX 64
-#endif
-#ifndef FOS_BM
-#define FOS_BM 0
-#define FOS_SPLIT 0
-#endif
 namespace fos {
 namespace {
 
@@ -164,53 +157,58 @@ struct RowTile {
   int g;
 };
 
-// A value that is the same in every lane, in scalar registers.
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
+// Inclusive sum over the wave's lanes in lane order, by shifts within rows of
+// 16 lanes and two broadcasts of a row's last lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15, into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);  // row_bcast:31, into rows 2 and 3
 }
 
 // Tile `t` of the rows cut into groups and each group into tiles of `rows`
 // rows, in group order, the tail last. The wave holds 64 groups' offsets at a
 // time, one per lane, and finds the tile by a running sum of the groups' tile
-// counts. Offsets are clamped to [previous, M], so a bad one sends no access
-// out of bounds.
-__device__ RowTile find_tile(const int32_t* offs, int G, int64_t M, int64_t rows, int64_t t) {
+// counts. Offsets are clamped to [previous, M], so a bad one sends no access out
+// of bounds. M is at most 2^30, so row and tile counts fit an int.
+__device__ RowTile find_tile(const int32_t* offs, int G, int M, int rows, int t) {
   const int lane = threadIdx.x & 63;
-  int64_t prev = 0, tiles = 0;  // of the groups before this batch
+  int prev = 0, tiles = 0;  // of the groups before this batch
   for (int base = 0; base <= G; base += 64) {
     const int g = base + lane;
     const bool have = g <= G;
-    // running maximum of the ends, clamped
-    int64_t run = g < G ? (int64_t)offs[g] : g == G ? M : 0;
-    if (run > M) run = M;
-    if (run < prev) run = prev;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up(run, d, 64);
-      if (lane >= d && o > run) run = o;
+    int end = g < G ? offs[g] : M;
+    int start = g == 0 ? 0 : g <= G ? offs[g - 1] : M;
+    if (__ballot(have && (start < prev || end < start || end > M))) {
+      // offsets that break the contract: running maximum of the clamped ends
+      end = end > M ? M : end < prev ? prev : end;
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(end, d, 64);
+        if (lane >= d && o > end) end = o;
+      }
+      start = __shfl_up(end, 1, 64);
+      if (lane == 0) start = prev;
     }
-    int64_t start = __shfl_up(run, 1, 64);
-    if (lane == 0) start = prev;
-    const int64_t n = have ? (run - start + rows - 1) / rows : 0;
-    int64_t sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += o;
-    }
+    const int n = have ? (int)((uint32_t)(end - start + rows - 1) / (uint32_t)rows) : 0;
+    const int sum = wave_scan(n);
     const unsigned long long hit = __ballot(tiles + sum > t);
     if (hit) {
       const int l = __ffsll(hit) - 1;
-      const int64_t first = tiles + __shfl(sum - n, l, 64);
+      const int first = tiles + __builtin_amdgcn_readlane(sum - n, l);
       RowTile r;
-      r.m0 = uniform(__shfl(start, l, 64) + (t - first) * rows);
-      r.end = uniform(__shfl(run, l, 64));
-      r.g = __builtin_amdgcn_readfirstlane(base + l);
+      r.m0 = (int64_t)__builtin_amdgcn_readlane(start, l) + (int64_t)(t - first) * rows;
+      r.end = __builtin_amdgcn_readlane(end, l);
+      r.g = base + l;
       return r;
     }
-    tiles += __shfl(sum, 63, 64);
-    prev = __shfl(run, 63, 64);
+    tiles += __builtin_amdgcn_readlane(sum, 63);
+    prev = __builtin_amdgcn_readlane(end, 63);
   }
   return RowTile{0, 0, -1};
 }
@@ -469,6 +467,7 @@ __device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
 template <int XT, int MT, int NT>
 __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16;
+  // (64 rows of activations leave the registers for one stage)
   constexpr int WAVES = 8, DEPTH = MT == 4 ? 1 : 4 / NT;
   constexpr int kWaveBytes = NT * 1024 + XTile<XT>::kBytes;
   constexpr int kPartBytes = (NT > 1 ? 2 : 1) * WAVES * MT * 1024;
@@ -479,7 +478,7 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
   RowTile rt{t * 16 * MT, a.M, 0};
   if (a.offs) {
     if (a.status && blockIdx.x == 0 && wave == 0) check_offs(a);
-    rt = find_tile(a.offs, a.G, a.M, 16 * MT, t);
+    rt = find_tile(a.offs, a.G, (int)a.M, 16 * MT, (int)t);
     if (rt.g < 0) return;
   }
   const int col = lane & 15, g4 = lane >> 4;
@@ -806,7 +805,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
   RowTile rt{tm * BM, a.M, 0};
   if (a.offs) {
     if (a.status && blockIdx.x == 0 && wave == 0) check_offs(a);
-    rt = find_tile(a.offs, a.G, a.M, BM, tm);
+    rt = find_tile(a.offs, a.G, (int)a.M, BM, (int)tm);
     if (rt.g < 0) return;
   }
   const int rows = rt.end - rt.m0 < BM ? (int)(rt.end - rt.m0) : BM;
@@ -1021,27 +1020,74 @@ int64_t max_tiles(int64_t M, int64_t G, int64_t rows) {
 
 // How a product is cut, from its sizes alone (G = 0: dense).
 struct Plan {
-  bool stream;    // the stream kernel; else the tile kernel
-  int bm;         // rows of a tile
-  int splits;     // parts of K
-  int64_t m_tiles;
+  bool stream;      // the stream kernel; else the tile kernel
+  int bm;           // rows of a tile
+  int splits;       // parts of K
+  int64_t m_tiles;  // an upper bound for groups
 };
 
+// Column tiles of a stream workgroup: as many as leave the chip nearly full,
+// since each reads the activations once. (Four with 64 rows of 16-bit values
+// would not fit the registers.)
+int stream_columns(int64_t m_tiles, int64_t N, int bm, bool narrow) {
+  const int64_t n16 = (N + 15) / 16;
+  if ((bm < 64 || narrow) && n16 / 4 * m_tiles >= 224) return 4;
+  return n16 / 2 * m_tiles >= 224 ? 2 : 1;
+}
+
+// Estimated microseconds, fitted to what the kernels take on 256 CUs (fp16, N =
+// 640 ... 14336, K = 2048 ... 14336); they only have to rank the choices.
+//
+// Stream kernel, 64 rows: one workgroup per CU at a time; its waves take K / 1024
+// steps each. 64 x 4096 x 4096: 11 us (tile kernel at best 19), 256 x 4096 x
+// 4096: 23 (25), 1024 x 4096 x 4096: 83 (50).
+double stream_us(int64_t m_tiles, int64_t N, int64_t K) {
+  const int columns = stream_columns(m_tiles, N, 64, false);
+  const int64_t wgs = m_tiles * ((N + 16 * columns - 1) / (16 * columns));
+  return 4.0 + (double)((wgs + 255) / 256) * ((double)K / 1024.0) * (columns == 1 ? 1.75 : 2.4);
+}
+
+// Tile kernel: a 128-deep step takes 2.15 us with one workgroup of 128 rows on a
+// CU and 3.6 with two (1.4, 2.2 and 3.1 with one to three of 64 rows); parts of K
+// cost a second launch and their sums' way through memory. 2048 x 4096 x 4096:
+// 128 rows 79 us, 64 rows 76; 256 x 4096 x 4096 in 64-row tiles: one part 49 us,
+// four 25; 128 x 4096 x 14336: one part 154 us, eight 32.
+double tile_us(double tiles, int64_t M, int64_t N, int64_t K, int bm, int splits) {
+  const int n = (int)((tiles * splits + 255.0) / 256.0), most = bm == 64 ? 3 : 2;
+  const double one = bm == 64 ? 1.4 : 2.15, full = bm == 64 ? 3.1 : 3.6;
+  const double step = n >= most ? full * n / most : n == 2 ? 2.2 : one;
+  const double steps = (double)((K + 127) / 128) / splits;
+  const double join = splits > 1 ? 3.0 + (double)splits * (double)M * (double)N * 8.0 / 8e6 : 0.0;
+  return 6.0 + step * steps + join;
+}
+
 Plan plan(int64_t M, int64_t N, int64_t K, int64_t G) {
-  Plan p{true, 16, 1, 0};
   const int64_t rows = G ? (M + G - 1) / G : M;  // rows that share a weight
-  // 2^22: the tile kernel's 32-bit offsets within a tile reach
-  if (rows > FOS_STREAM_MAX && K <= (int64_t(1) << 22)) {
-    p.stream = false;
-    auto tiles = [&](int bm) { return G ? max_tiles(M, G, bm) : (M + bm - 1) / bm; };
-    p.bm = FOS_BM ? FOS_BM : 128;
-    p.m_tiles = tiles(p.bm);
-    if (FOS_SPLIT) p.splits = FOS_SPLIT;
-  } else {
-    p.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.m_tiles = G ? max_tiles(M, G, p.bm) : (M + p.bm - 1) / p.bm;
+  auto tiles = [&](int bm) { return G ? max_tiles(M, G, bm) : (M + bm - 1) / bm; };
+  const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  Plan best{true, bm, 1, tiles(bm)};
+  // few rows: the weights' way from memory is what counts (64 experts of
+  // 2048 x 7168: 32 rows each 248 us, 292 with tiles; 64 rows 429 and 353).
+  // 2^22: the tile kernel's 32-bit offsets within a tile reach.
+  if (rows <= (G ? 40 : 64) || K > (int64_t(1) << 22)) return best;
+  const int64_t n_tiles = (N + 255) / 256;
+  double least = G ? 1e30 : stream_us(best.m_tiles, N, K);
+  for (int b = 64; b <= 128; b *= 2) {
+    // a group ends inside a tile, on average at its middle
+    const double t = (G ? (double)M / b + 0.5 * (double)G : (double)tiles(b)) * (double)n_tiles;
+    for (int s = 1; s <= (G ? 1 : 8); s++) {
+      if (s > 1 && (K / 128 < 2 * s || t * s > 768.0)) break;
+      const double us = tile_us(t, M, N, K, b, s);
+      if (us < least) {
+        least = us;
+        best = Plan{false, b, s, tiles(b)};
+      }
+    }
   }
-  return p;
+#ifdef FOS_BM
+  if (FOS_BM) best = Plan{false, FOS_BM, FOS_SPLIT ? FOS_SPLIT : 1, tiles(FOS_BM)};
+#endif
+  return best;
 }
 
 template <int XT, int MT, int NT>
@@ -1054,17 +1100,12 @@ hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) 
 
 template <int XT, int MT>
 hipError_t launch_stream(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
-  const int64_t n16 = (a.N + 15) / 16;
-#ifdef FOS_NT
-  if (FOS_NT == 4) { if constexpr (MT < 4 || XT > kFP16) return launch_stream_n<XT, MT, 4>(a, m_tiles, s); }
-  if (FOS_NT >= 2) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
-  if (FOS_NT == 1) return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
-#endif
-  if constexpr (MT < 4 || XT > kFP16) {
-    if (n16 / 4 * m_tiles >= 224) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
+  constexpr bool narrow = XT > kFP16;
+  const int columns = stream_columns(m_tiles, a.N, 16 * MT, narrow);
+  if constexpr (MT < 4 || narrow) {
+    if (columns == 4) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
   }
-  if (n16 / 2 * m_tiles >= 224) return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
-  return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
+  return columns == 2 ? launch_stream_n<XT, MT, 2>(a, m_tiles, s) : launch_stream_n<XT, MT, 1>(a, m_tiles, s);
 }
 
 template <int XT>
