@@ -414,7 +414,8 @@ typedef struct fos_epilogue {
  * codes and scales of fos_quantize, 1x16 and 16x16 alike, and (with
  * fos_quantize_columnwise's output as w) of the transposed operand, which
  * makes it the backward product dX = dY W too. y is bf16, fp16 or fp32,
- * contiguous. Decoded values are exact in the 16-bit type of the matrix
+ * contiguous. M and N are at most 2^30, K at most 2^22 and a multiple of 16.
+ * Decoded values are exact in the 16-bit type of the matrix
  * instruction, products exact and sums binary32, so the result differs from
  * the exact one by the order of the sum and the rounding of the output.
  *   work:       device memory of at least fos_linear_workspace() bytes,

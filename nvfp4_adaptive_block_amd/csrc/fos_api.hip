@@ -659,8 +659,9 @@ int check_operand(const char* what, const fos_operand* o, int64_t rows, int64_t 
 int check_linear_sizes(int64_t M, int64_t N, int64_t K, int64_t G) {
   if (M < 0 || N < 0 || K < 0) return fail(FOS_ERR_INVALID_ARG, "negative size M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
   if (K % 16) return fail(FOS_ERR_SHAPE, "K=%lld is not a multiple of 16", (long long)K);
-  const int64_t most = int64_t(1) << 30;  // row and column numbers, and a row's bytes, fit 32 bits
-  if (M > most || N > most || K > most) return fail(FOS_ERR_SHAPE, "M, N and K are at most 2^30");
+  // row and column numbers fit 32 bits, and so do offsets within 256 rows
+  if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 22))
+    return fail(FOS_ERR_SHAPE, "M and N are at most 2^30 and K 2^22, got M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
   if (K > 0 && (M > kMaxElems / K || N > kMaxElems / K / (G > 0 ? G : 1))) return fail(FOS_ERR_SHAPE, "an operand exceeds 2^40 elements");
   if (N > 0 && M > kMaxElems / N) return fail(FOS_ERR_SHAPE, "M*N exceeds 2^40 elements");
   return FOS_OK;

@@ -363,6 +363,23 @@ __device__ __forceinline__ void zero4(const LinearArgs& a, int64_t m, int64_t n)
 
 // ---------------------------------------------------------------- kernels
 
+// Loads of the kernels' loops: a uniform address in scalar registers plus a
+// 32-bit lane offset (K is at most 2^22, so 256 rows are within reach). (Left to itself the compiler carries a 64-bit address per
+// lane and load through the loop: 24 registers that spill.) The alignments are
+// those that K % 16 == 0 gives.
+#define FOS_GLOBAL __attribute__((address_space(1)))
+typedef const FOS_GLOBAL uint8_t* GlobalBytes;
+
+__device__ __forceinline__ uint32_t lane_offset(uint32_t v) {  // stays 32 bits wide in the loop
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ GlobalBytes scalar(const uint8_t* p) {
+  GlobalBytes g = (GlobalBytes)p;
+  asm volatile("" : "+s"(g));
+  return g;
+}
+
 // Where the LDS tiles keep a row's 16-byte chunks. LDS serves a 16-byte read of
 // 16 lanes at a time, but not of 16 neighbours: lanes 0-3 and 12-15 go with
 // 20-27, and 4-11 with 16-19 and 28-31 (the same in the upper half). With lane l
@@ -403,19 +420,24 @@ struct XTile {
     for (int i = 0; i < kLoads; i++) v[i] = u32x4{0, 0, 0, 0};
     s = u32x2{0, 0};
   }
-  // rows: how many exist; p: row 0 of the tile at the step; q: its scales.
-  // Rows that do not exist keep what clear() put there.
-  __device__ __forceinline__ void load(const LinearArgs& a, const uint8_t* p, const uint8_t* q, int rows) {
+  // Lane offsets of the first load and of the scales, from row 0.
+  static __device__ __forceinline__ uint32_t offset(int64_t KB) {
     const int lane = threadIdx.x & 63;
-    const int64_t stride = a.K / 16 * (2 * kLanes);
+    return (uint32_t)(lane / kLanes) * (uint32_t)(KB * 2 * kLanes) + 16 * (lane % kLanes);
+  }
+  static __device__ __forceinline__ uint32_t scale_offset(int64_t KB) { return (threadIdx.x & 15) * (uint32_t)KB; }
+  // p: row 0 of the tile at the step; q: its scales; rows: how many exist. Rows
+  // that do not keep what clear() put there.
+  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* q, uint32_t off, uint32_t soff, int64_t KB, int rows) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
-      const int row = i * (64 / kLanes) + lane / kLanes;
-      if (row < rows) v[i] = *reinterpret_cast<const u32x4_a8*>(p + row * stride + 16 * (lane % kLanes));
+      const GlobalBytes g = scalar(p + i * (64 / kLanes) * (KB * 2 * kLanes));
+      if (i * (64 / kLanes) + lane / kLanes < rows) v[i] = *(const FOS_GLOBAL u32x4_a8*)(g + lane_offset(off));
     }
     if constexpr (XT == kXNVFP4) {
-      const int row = lane & 15;
-      if (row < rows) s = *reinterpret_cast<const u32x2_a1*>(q + row * (a.K / 16));
+      const GlobalBytes g = scalar(q);
+      if ((lane & 15) < rows) s = *(const FOS_GLOBAL u32x2_a1*)(g + lane_offset(soff));
     }
   }
   __device__ __forceinline__ void put(uint8_t* lds) const {
@@ -465,10 +487,10 @@ __device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
 // weights are loaded four lanes to a row and turned through the wave's own LDS.
 // The waves' sums are joined through LDS in wave order.
 template <int XT, int MT, int NT>
-__global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles) {
+__global__ __launch_bounds__(512, MT == 1 && NT == 4 ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16;
-  // (64 rows of activations leave the registers for one stage)
-  constexpr int WAVES = 8, DEPTH = MT == 4 ? 1 : 4 / NT;
+  // (more than 32 rows of activations leave the registers for one stage)
+  constexpr int WAVES = 8, DEPTH = MT >= 3 ? 1 : 4 / NT;
   constexpr int kWaveBytes = NT * 1024 + XTile<XT>::kBytes;
   constexpr int kPartBytes = (NT > 1 ? 2 : 1) * WAVES * MT * 1024;
   __shared__ __align__(16) uint8_t lds[kPartBytes > WAVES * kWaveBytes ? kPartBytes : WAVES * kWaveBytes];
@@ -500,28 +522,31 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
   // columns past the end read the last row of the weight
   const int wrows = a.N - n0 < 16 * NT ? (int)(a.N - n0) : 16 * NT;
   const int64_t w0 = (int64_t)rt.g * a.N + n0;
-  const uint8_t* wp[NT];
-  const uint8_t* wq = a.ws + (w0 + (lane < wrows ? lane : wrows - 1)) * KB;
+  const uint8_t *wc = a.w + w0 * (a.K / 2), *wsc = a.ws + w0 * KB;
+  uint32_t woff[NT];
 #pragma unroll
   for (int i = 0; i < NT; i++) {
     const int r = 16 * i + (lane >> 2);
-    wp[i] = a.w + (w0 + (r < wrows ? r : wrows - 1)) * (a.K / 2) + 16 * (lane & 3);
+    woff[i] = (uint32_t)(r < wrows ? r : wrows - 1) * (uint32_t)(a.K / 2) + 16 * (lane & 3);
   }
+  const uint32_t wsoff = (uint32_t)(lane < wrows ? lane : wrows - 1) * (uint32_t)KB;
   const int xrows = rt.end - rt.m0 < 16 * MT ? (int)(rt.end - rt.m0) : 16 * MT;
-  const uint8_t* xp = (const uint8_t*)a.x + rt.m0 * KB * (2 * XTile<XT>::kLanes);
-  const uint8_t* xq = XT == kXNVFP4 ? a.xs + rt.m0 * KB : nullptr;
+  const uint8_t* xc = (const uint8_t*)a.x + rt.m0 * KB * (2 * XTile<XT>::kLanes);
+  const uint8_t* xsc = XT == kXNVFP4 ? a.xs + rt.m0 * KB : nullptr;
+  const uint32_t xoff = XTile<XT>::offset(KB), xsoff = XTile<XT>::scale_offset(KB);
 
   // The tiles of y that this wave will finish (row tile turn(i) of column tile
   // i, where that is below MT: one in eight), and what that takes.
-  auto turn = [&](int i) { return (wave + WAVES - (i * MT) % WAVES) % WAVES; };
-  constexpr int TURNS = (NT * MT + WAVES - 1) / WAVES;
+  constexpr int MP = MT == 3 ? 4 : MT;  // a divisor of the waves
+  auto turn = [&](int i) { return (wave + WAVES - (i * MP) % WAVES) % WAVES; };
+  constexpr int TURNS = (NT * MP + WAVES - 1) / WAVES;
   ColumnTail columns[TURNS];
   RowTail row[TURNS];
   bool live[TURNS] = {};
 #pragma unroll
   for (int i = 0; i < NT; i++) {
     if (const int j = turn(i); j < MT) {
-      const int k = i * MT / WAVES;
+      const int k = i * MP / WAVES;
       const Quad q(a, n0 + 16 * i + 4 * g4);
       const int64_t m = rt.m0 + 16 * j + col;
       live[k] = m < rt.end && q.have;
@@ -540,13 +565,14 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
 #pragma unroll
     for (int j = 0; j < MT; j++) x[d][j].clear();
   auto load_w = [&](int d, int64_t step) {
+    const GlobalBytes p = scalar(wc + step * 64), q = scalar(wsc + step * 8);
 #pragma unroll
-    for (int i = 0; i < NT; i++) codes[d][i] = *reinterpret_cast<const u32x4_a8*>(wp[i] + step * 64);
-    if (NT == 4 || lane < 16 * NT) scales[d] = *reinterpret_cast<const u32x2_a1*>(wq + step * 8);
+    for (int i = 0; i < NT; i++) codes[d][i] = *(const FOS_GLOBAL u32x4_a8*)(p + lane_offset(woff[i]));
+    if (NT == 4 || lane < 16 * NT) scales[d] = *(const FOS_GLOBAL u32x2_a1*)(q + lane_offset(wsoff));
   };
   auto load_rows = [&](int d, int j, int64_t step) {
-    x[d][j].load(a, xp + 16 * j * KB * (2 * XTile<XT>::kLanes) + step * (16 * XTile<XT>::kLanes),
-                 xq + 16 * j * KB + step * 8, xrows - 16 * j);
+    x[d][j].load(xc + 16 * j * KB * (2 * XTile<XT>::kLanes) + step * (16 * XTile<XT>::kLanes),
+                 XT == kXNVFP4 ? xsc + 16 * j * KB + step * 8 : nullptr, xoff, xsoff, KB, xrows - 16 * j);
   };
   uint8_t* wl = lds + wave * kWaveBytes;
   uint8_t* xl = wl + NT * 1024;
@@ -560,24 +586,41 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
       ws[i] = row_scales(scales[d], 16 * i);
     }
     if (after < whole) load_w(d, after);
-    Frag w[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; i++) {
+    auto take_w = [&](int i, Frag* w) {
       const u32x4 t = *reinterpret_cast<const u32x4*>(wl + i * 1024 + XTile<kXNVFP4>::slot(col, g4));
       const uint32_t c[4] = {t[0], t[1], t[2], t[3]};
-      decode_blocks<BF16>(c, ws[i], w[i]);
-    }
-#pragma unroll
-    for (int j = 0; j < MT; j++) {
+      decode_blocks<BF16>(c, ws[i], w);
+    };
+    auto take_x = [&](int j, Frag* f) {
       x[d][j].put(xl);
       const uint32_t sc = XT == kXNVFP4 ? row_scales(x[d][j].s, 0) : 0;
       if (after < whole) load_rows(d, j, after);
-      Frag f[4];
       XTile<XT>::get(xl, sc, f);
+    };
+    if constexpr (MT == 1) {  // hold the activations, not the weights
+      Frag f[4];
+      take_x(0, f);
 #pragma unroll
-      for (int k = 0; k < 4; k++)
+      for (int i = 0; i < NT; i++) {
+        Frag w[4];
+        take_w(i, w);
 #pragma unroll
-        for (int i = 0; i < NT; i++) acc[i][j] = mfma<BF16>(w[i][k], f[k], acc[i][j]);
+        for (int k = 0; k < 4; k++) acc[i][0] = mfma<BF16>(w[k], f[k], acc[i][0]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      Frag w[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; i++) take_w(i, w[i]);
+#pragma unroll
+      for (int j = 0; j < MT; j++) {
+        Frag f[4];
+        take_x(j, f);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+#pragma unroll
+          for (int i = 0; i < NT; i++) acc[i][j] = mfma<BF16>(w[i][k], f[k], acc[i][j]);
+      }
     }
   };
 #pragma unroll
@@ -617,30 +660,13 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int n_tiles
     for (int j = 0; j < MT; j++) part[i & 1][wave][j][lane] = acc[i][j];
     __syncthreads();
     if (const int j = turn(i); j < MT) {
-      const int k = i * MT / WAVES;  // the wave's first or second tile
+      const int k = i * MP / WAVES;  // the wave's first or second tile
       f32x4 s = part[i & 1][0][j][lane];
 #pragma unroll
       for (int v = 1; v < WAVES; v++) s += part[i & 1][v][j][lane];
       if (live[k]) finish4(a, rt.m0 + 16 * j + col, Quad(a, n0 + 16 * i + 4 * g4), columns[k], row[k], s);
     }
   }
-}
-
-// Loads of the tile kernel's loop: a uniform address in scalar registers plus a
-// 32-bit lane offset. (Left to itself the compiler carries a 64-bit address per
-// lane and load through the loop: 24 registers that spill.) The alignments are
-// those that K % 16 == 0 gives.
-#define FOS_GLOBAL __attribute__((address_space(1)))
-typedef const FOS_GLOBAL uint8_t* GlobalBytes;
-
-__device__ __forceinline__ uint32_t lane_offset(uint32_t v) {  // stays 32 bits wide in the loop
-  asm volatile("" : "+v"(v));
-  return v;
-}
-__device__ __forceinline__ GlobalBytes scalar(const uint8_t* p) {
-  GlobalBytes g = (GlobalBytes)p;
-  asm volatile("" : "+s"(g));
-  return g;
 }
 
 // The tile kernel: one workgroup of four waves takes BM rows and 256 columns,
@@ -792,8 +818,9 @@ __device__ __forceinline__ void block_sync() {
   asm volatile("" ::: "memory");
 }
 
+// (three workgroups of 64 rows fit a CU without spills for fp16 only)
 template <int XT, int BM>
-__global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles,
+__global__ __launch_bounds__(256, BM == 64 && XT == kFP16 ? 3 : 2) void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles,
                                                                        int splits) {
   constexpr bool BF16 = XT == kBF16;
   constexpr int MT = BM / 16;
@@ -872,7 +899,9 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_linear_tile(LinearArg
 #pragma unroll
   for (int c = 0; c < 4; c++) roff[c] = col * 256 + (((4 * g4 + c) ^ swizzle<4>(col)) << 4);
 
-  // Multiply the staged step by the weights in registers.
+  // Multiply the staged step by the weights in registers. (Leaving out the row
+  // tiles past a group's end made the loop slower by more than it saved: 64
+  // experts of 240 rows 593 us, 584 without.)
   auto multiply = [&](const uint8_t* cur) {
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -1027,11 +1056,11 @@ struct Plan {
 };
 
 // Column tiles of a stream workgroup: as many as leave the chip nearly full,
-// since each reads the activations once. (Four with 64 rows of 16-bit values
-// would not fit the registers.)
+// since each reads the activations once. (Four with more than 32 rows of 16-bit
+// values would not fit the registers.)
 int stream_columns(int64_t m_tiles, int64_t N, int bm, bool narrow) {
   const int64_t n16 = (N + 15) / 16;
-  if ((bm < 64 || narrow) && n16 / 4 * m_tiles >= 224) return 4;
+  if ((bm < 48 || narrow) && n16 / 4 * m_tiles >= 224) return 4;
   return n16 / 2 * m_tiles >= 224 ? 2 : 1;
 }
 
@@ -1048,28 +1077,26 @@ double stream_us(int64_t m_tiles, int64_t N, int64_t K) {
 }
 
 // Tile kernel: a 128-deep step takes 2.15 us with one workgroup of 128 rows on a
-// CU and 3.6 with two (1.4, 2.2 and 3.1 with one to three of 64 rows); parts of K
-// cost a second launch and their sums' way through memory. 2048 x 4096 x 4096:
-// 128 rows 79 us, 64 rows 76; 256 x 4096 x 4096 in 64-row tiles: one part 49 us,
-// four 25; 128 x 4096 x 14336: one part 154 us, eight 32.
+// CU and 3.6 with two (64 rows: 1.4 and 2.25); parts of K cost a second launch
+// and their sums' way through memory. 2048 x 4096 x 4096: 128 rows 79 us, 64 rows
+// 76; 256 x 4096 x 4096 in 64-row tiles: one part 49 us, four 25; 128 x 4096 x
+// 14336: one part 154 us, eight 32.
 double tile_us(double tiles, int64_t M, int64_t N, int64_t K, int bm, int splits) {
-  const int n = (int)((tiles * splits + 255.0) / 256.0), most = bm == 64 ? 3 : 2;
-  const double one = bm == 64 ? 1.4 : 2.15, full = bm == 64 ? 3.1 : 3.6;
-  const double step = n >= most ? full * n / most : n == 2 ? 2.2 : one;
+  const int n = (int)((tiles * splits + 255.0) / 256.0);
+  const double step = bm == 64 ? (n == 1 ? 1.4 : 1.125 * n) : (n == 1 ? 2.15 : 1.8 * n);
   const double steps = (double)((K + 127) / 128) / splits;
   const double join = splits > 1 ? 3.0 + (double)splits * (double)M * (double)N * 8.0 / 8e6 : 0.0;
-  return 6.0 + step * steps + join;
+  return (bm == 64 ? 5.0 : 9.0) + step * steps + join;
 }
 
 Plan plan(int64_t M, int64_t N, int64_t K, int64_t G) {
   const int64_t rows = G ? (M + G - 1) / G : M;  // rows that share a weight
   auto tiles = [&](int bm) { return G ? max_tiles(M, G, bm) : (M + bm - 1) / bm; };
-  const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   Plan best{true, bm, 1, tiles(bm)};
   // few rows: the weights' way from memory is what counts (64 experts of
-  // 2048 x 7168: 32 rows each 248 us, 292 with tiles; 64 rows 429 and 353).
-  // 2^22: the tile kernel's 32-bit offsets within a tile reach.
-  if (rows <= (G ? 40 : 64) || K > (int64_t(1) << 22)) return best;
+  // 2048 x 7168: 32 rows each 248 us, 292 with tiles; 64 rows 429 and 353)
+  if (rows <= (G ? 40 : 64)) return best;
   const int64_t n_tiles = (N + 255) / 256;
   double least = G ? 1e30 : stream_us(best.m_tiles, N, K);
   for (int b = 64; b <= 128; b *= 2) {
@@ -1102,7 +1129,7 @@ template <int XT, int MT>
 hipError_t launch_stream(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
   constexpr bool narrow = XT > kFP16;
   const int columns = stream_columns(m_tiles, a.N, 16 * MT, narrow);
-  if constexpr (MT < 4 || narrow) {
+  if constexpr (MT < 3 || narrow) {
     if (columns == 4) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
   }
   return columns == 2 ? launch_stream_n<XT, MT, 2>(a, m_tiles, s) : launch_stream_n<XT, MT, 1>(a, m_tiles, s);
@@ -1114,6 +1141,7 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
   if (p.stream) {
     if (p.bm == 16) return launch_stream<XT, 1>(a, p.m_tiles, s);
     if (p.bm == 32) return launch_stream<XT, 2>(a, p.m_tiles, s);
+    if (p.bm == 48) return launch_stream<XT, 3>(a, p.m_tiles, s);
     return launch_stream<XT, 4>(a, p.m_tiles, s);
   }
   const int64_t n_tiles = (a.N + 255) / 256;

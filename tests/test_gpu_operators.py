@@ -62,7 +62,7 @@ def make_w(N, K, seed, gran="tensor", G=None):
 
 
 SIZES = [(1, 1, 16), (1, 16, 16), (2, 3, 32), (3, 5, 48), (5, 17, 112), (15, 16, 128), (16, 64, 144), (17, 33, 256),
-         (31, 64, 272), (48, 96, 512), (63, 65, 528), (64, 128, 1024), (65, 130, 1040), (100, 256, 384),
+         (31, 64, 272), (48, 96, 512), (40, 4128, 160), (33, 70, 1104), (63, 65, 528), (64, 128, 1024), (65, 130, 1040), (100, 256, 384),
          (128, 257, 640), (129, 64, 1936), (200, 511, 256), (257, 300, 2064), (384, 512, 1024), (1, 64, 14336),
          (7, 40, 7168)]
 KINDS = ["bf16", "fp16", "e4m3", "nvfp4", "nvfp4_row"]
