@@ -481,16 +481,15 @@ __device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
 }
 
 // The stream kernel, for few rows per weight: one workgroup takes 16 NT columns
-// of y and 16 MT rows, and its eight waves take the 128-deep steps of k in turn,
-// so that the weight is read once by as many waves as the chip has. A wave keeps
+// of y and 16 MT rows, and its waves take the 128-deep steps of k in turn, so that the weight is read once by as many waves as the chip has. A wave keeps
 // DEPTH steps of loads in flight (4 KiB of codes). Like the activations, the
 // weights are loaded four lanes to a row and turned through the wave's own LDS.
 // The waves' sums are joined through LDS in wave order.
-template <int XT, int MT, int NT>
-__global__ __launch_bounds__(512, MT == 1 && NT == 4 ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
+template <int XT, int MT, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, MT == 1 && (NT == 4 || WAVES == 16) ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16;
   // (more than 32 rows of activations leave the registers for one stage)
-  constexpr int WAVES = 8, DEPTH = MT >= 3 ? 1 : 4 / NT;
+  constexpr int DEPTH = MT >= 3 ? 1 : WAVES == 16 ? 2 : 4 / NT;
   constexpr int kWaveBytes = NT * 1024 + XTile<XT>::kBytes;
   constexpr int kPartBytes = (NT > 1 ? 2 : 1) * WAVES * MT * 1024;
   __shared__ __align__(16) uint8_t lds[kPartBytes > WAVES * kWaveBytes ? kPartBytes : WAVES * kWaveBytes];
@@ -1121,7 +1120,10 @@ template <int XT, int MT, int NT>
 hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
   const int64_t n_tiles = (a.N + 16 * NT - 1) / (16 * NT);
   if (m_tiles > kMaxGrid / n_tiles) return hipErrorInvalidConfiguration;
-  k_linear_stream<XT, MT, NT><<<dim3((unsigned)(m_tiles * n_tiles)), dim3(512), 0, s>>>(a, (int)n_tiles);
+  // Eight waves; sixteen with half the steps in flight where a workgroup has one
+  // column tile and the chain of a wave's steps is what takes the time.
+  constexpr int WAVES = MT == 1 && NT == 1 ? 16 : 8;
+  k_linear_stream<XT, MT, NT, WAVES><<<dim3((unsigned)(m_tiles * n_tiles)), dim3(64 * WAVES), 0, s>>>(a, (int)n_tiles);
   return hipGetLastError();
 }
 
