@@ -62,7 +62,9 @@ def make_w(N, K, seed, gran="tensor", G=None):
 
 
 SIZES = [(1, 1, 16), (1, 16, 16), (2, 3, 32), (3, 5, 48), (5, 17, 112), (15, 16, 128), (16, 64, 144), (17, 33, 256),
-         (31, 64, 272), (48, 96, 512), (40, 4128, 160), (33, 70, 1104), (63, 65, 528), (64, 128, 1024), (65, 130, 1040), (100, 256, 384),
+         (31, 64, 272), (48, 96, 512), (40, 4128, 160), (33, 70, 1104), (20, 14400, 64),
+         (40, 14400, 64), (64, 14388, 80), (2, 14403, 144), (150, 1030, 2128), (90, 520, 4096), (300, 4100, 400),
+         (63, 65, 528), (64, 128, 1024), (65, 130, 1040), (100, 256, 384),
          (128, 257, 640), (129, 64, 1936), (200, 511, 256), (257, 300, 2064), (384, 512, 1024), (1, 64, 14336),
          (7, 40, 7168)]
 KINDS = ["bf16", "fp16", "e4m3", "nvfp4", "nvfp4_row"]
@@ -603,3 +605,34 @@ def test_python_refusals():
         fos.fos_linear(flat.view(4, 32), w)
     with pytest.raises(fos.FosError):
         fos.fos_linear(x, w, workspace=None, out=torch.zeros(40, device="cuda")[2:34].view(4, 8))
+
+
+# ------------------------------------------------------------------ together
+
+
+@pytest.mark.parametrize("tokens,width,hidden,experts,top", [(1, 256, 320, 4, 2), (200, 256, 320, 6, 2),
+                                                             (700, 512, 1024, 16, 4)])
+def test_example_block(tokens, width, hidden, experts, top):
+    """examples/moe_feed_forward.py against the block on unquantized values:
+    two NVFP4 operands in a row are each off by about a tenth, E4M3 by a
+    thirtieth, and errors of different elements are independent."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_feed_forward.py")
+    spec = importlib.util.spec_from_file_location("moe_feed_forward", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    w = ex.make_weights(width, hidden, experts)
+    x = torch.randn(tokens, width, generator=gen(1)).bfloat16().cuda()
+    r = torch.randn(tokens, width, generator=gen(2)).bfloat16().cuda()
+    out, loss, saved = ex.forward(x, r, ex.quantize_weights(w), top)
+    want = ex.reference(x, r, w, top)
+    h = x.float() + r.float()
+    assert float((out.float() - want).norm() / (want - h).norm()) < 0.25
+    y, logits, slope = saved
+    idx = torch.softmax(logits, 1).topk(top, 1).indices.cpu()
+    wl, *_, wg, _ = balance_reference(logits.cpu(), idx, None, 0.01, 16, 1.0)
+    assert abs(float(loss) - float(wl)) < 1e-5 * float(wl)
+    grad = ex.router_gradient(saved, torch.ones(1, device="cuda")).cpu().double()
+    ref_grad = wg.t() @ y.cpu().double()
+    assert float((grad - ref_grad).norm()) <= 1e-4 * float(ref_grad.norm()) + 1e-9
