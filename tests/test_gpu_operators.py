@@ -112,6 +112,32 @@ def test_linear_epilogue(act, out, bias_dt, M, N, K):
     assert_within(y, want, bound, act + " in place")
 
 
+# sizes that are cut into tiles of 64 and of 128 rows, in one part of K and in several
+TILED = [(2050, 1500, 528, False), (3000, 4099, 528, False), (150, 2051, 4208, True), (130, 1500, 3088, True),
+         (4100, 515, 4112, True)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3", "nvfp4_row"])
+@pytest.mark.parametrize("M,N,K,parts", TILED)
+def test_linear_tiles(kind, M, N, K, parts):
+    assert (fos.fos_linear_workspace(M, N, K) > 0) == parts
+    x, xv, xg = make_x(kind, M, K, M + N)
+    w, wv = make_w(N, K, M + K, "row")
+    bias = torch.randn(N, generator=gen(9))
+    out_dtype = torch.float32 if kind != "bf16" else torch.bfloat16
+    res = torch.randn(M, N, generator=gen(10)).to(out_dtype)
+    y, raw = guarded((M, N), out_dtype)
+    ws = torch.full((fos.fos_linear_workspace(M, N, K) + 16,), 255, dtype=torch.uint8, device="cuda")
+    fos.fos_linear(x, w, out=y, bias=cuda(bias), residual=cuda(res), act="relu", x_gran=xg, w_gran="row", workspace=ws)
+    want, bound = ref.linear(xv, wv, bias, "relu", res, out_dtype)
+    assert_within(y, want, bound, f"{kind} {M}x{N}x{K}")
+    assert_guard(raw)
+    assert (ws[-16:] == 255).all(), "wrote past the workspace"
+    z = cuda(res)  # in place of the residual, on a workspace that the last call left
+    fos.fos_linear(x, w, out=z, bias=cuda(bias), residual=z, act="relu", x_gran=xg, w_gran="row", workspace=ws)
+    assert torch.equal(z.view(torch.uint8), y.view(torch.uint8))
+
+
 @pytest.mark.parametrize("M,N,K", [(0, 8, 32), (8, 0, 32), (5, 9, 0)])
 def test_linear_empty(M, N, K):
     x = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
@@ -238,6 +264,9 @@ GROUPS = [
     (30, 16, 64, list(range(0, 26, 1)) * 5),   # not monotone: see the test of bad offsets
     (16, 24, 64, [0] * 70 + [3] * 60 + [16]),  # more groups than a wave has lanes
     (5, 20, 128, [0, 0, 0]),                   # every row in the tail
+    (300, 300, 400, [100, 100, 290]),          # tiles of 64 rows
+    (8200, 1030, 272, [4101, 8100]),
+    (8200, 4099, 528, [4101, 8100]),           # tiles of 128 rows
 ]
 
 
