@@ -1055,12 +1055,10 @@ struct Plan {
 };
 
 // Column tiles of a stream workgroup: as many as leave the chip nearly full,
-// since each reads the activations once. (Four with more than 32 rows of 16-bit
-// values would not fit the registers.)
-int stream_columns(int64_t m_tiles, int64_t N, int bm, bool narrow) {
+// since each reads the activations once (64 x 14336 x 4096: four 21 us, two 25).
+int stream_columns(int64_t m_tiles, int64_t N) {
   const int64_t n16 = (N + 15) / 16;
-  if ((bm < 48 || narrow) && n16 / 4 * m_tiles >= 224) return 4;
-  return n16 / 2 * m_tiles >= 224 ? 2 : 1;
+  return n16 / 4 * m_tiles >= 224 ? 4 : n16 / 2 * m_tiles >= 224 ? 2 : 1;
 }
 
 // Estimated microseconds, fitted to what the kernels take on 256 CUs (fp16, N =
@@ -1068,11 +1066,12 @@ int stream_columns(int64_t m_tiles, int64_t N, int bm, bool narrow) {
 //
 // Stream kernel, 64 rows: one workgroup per CU at a time; its waves take K / 1024
 // steps each. 64 x 4096 x 4096: 11 us (tile kernel at best 19), 256 x 4096 x
-// 4096: 23 (25), 1024 x 4096 x 4096: 83 (50).
+// 4096: 21 (25), 1024 x 4096 x 4096: 83 (50).
 double stream_us(int64_t m_tiles, int64_t N, int64_t K) {
-  const int columns = stream_columns(m_tiles, N, 64, false);
+  const int columns = stream_columns(m_tiles, N);
   const int64_t wgs = m_tiles * ((N + 16 * columns - 1) / (16 * columns));
-  return 4.0 + (double)((wgs + 255) / 256) * ((double)K / 1024.0) * (columns == 1 ? 1.75 : 2.4);
+  const double step = columns == 1 ? 1.75 : columns == 2 ? 2.4 : 4.3;
+  return 4.0 + (double)((wgs + 255) / 256) * ((double)K / 1024.0) * step;
 }
 
 // Tile kernel: a 128-deep step takes 2.15 us with one workgroup of 128 rows on a
@@ -1129,12 +1128,11 @@ hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) 
 
 template <int XT, int MT>
 hipError_t launch_stream(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
-  constexpr bool narrow = XT > kFP16;
-  const int columns = stream_columns(m_tiles, a.N, 16 * MT, narrow);
-  if constexpr (MT < 3 || narrow) {
-    if (columns == 4) return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
+  switch (stream_columns(m_tiles, a.N)) {
+    case 4: return launch_stream_n<XT, MT, 4>(a, m_tiles, s);
+    case 2: return launch_stream_n<XT, MT, 2>(a, m_tiles, s);
+    default: return launch_stream_n<XT, MT, 1>(a, m_tiles, s);
   }
-  return columns == 2 ? launch_stream_n<XT, MT, 2>(a, m_tiles, s) : launch_stream_n<XT, MT, 1>(a, m_tiles, s);
 }
 
 template <int XT>
