@@ -486,7 +486,7 @@ __device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
 // weights are loaded four lanes to a row and turned through the wave's own LDS.
 // The waves' sums are joined through LDS in wave order.
 template <int XT, int MT, int NT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, MT == 1 && (NT == 4 || WAVES == 16) ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
+__global__ __launch_bounds__(64 * WAVES, MT == 1 ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16;
   // (more than 32 rows of activations leave the registers for one stage)
   constexpr int DEPTH = MT >= 3 ? 1 : WAVES == 16 ? 2 : 4 / NT;
@@ -558,26 +558,25 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 && (NT == 4 || WAVES == 16) ? 4
 
   u32x4 codes[DEPTH][NT];
   u32x2 scales[DEPTH];
-  XTile<XT> x[DEPTH][MT];
+  XTile<XT> x[MT];  // the activations come from L2: one step ahead is enough
 #pragma unroll
-  for (int d = 0; d < DEPTH; d++)
-#pragma unroll
-    for (int j = 0; j < MT; j++) x[d][j].clear();
+  for (int j = 0; j < MT; j++) x[j].clear();
   auto load_w = [&](int d, int64_t step) {
     const GlobalBytes p = scalar(wc + step * 64), q = scalar(wsc + step * 8);
 #pragma unroll
     for (int i = 0; i < NT; i++) codes[d][i] = *(const FOS_GLOBAL u32x4_a8*)(p + lane_offset(woff[i]));
     if (NT == 4 || lane < 16 * NT) scales[d] = *(const FOS_GLOBAL u32x2_a1*)(q + lane_offset(wsoff));
   };
-  auto load_rows = [&](int d, int j, int64_t step) {
-    x[d][j].load(xc + 16 * j * KB * (2 * XTile<XT>::kLanes) + step * (16 * XTile<XT>::kLanes),
+  auto load_rows = [&](int j, int64_t step) {
+    x[j].load(xc + 16 * j * KB * (2 * XTile<XT>::kLanes) + step * (16 * XTile<XT>::kLanes),
                  XT == kXNVFP4 ? xsc + 16 * j * KB + step * 8 : nullptr, xoff, xsoff, KB, xrows - 16 * j);
   };
   uint8_t* wl = lds + wave * kWaveBytes;
   uint8_t* xl = wl + NT * 1024;
-  // One step from the registers of stage d, which are loaded again for `after`
-  // (below `whole`, or not at all) as soon as their contents are in LDS.
-  auto multiply = [&](int d, int after) {
+  // One step from the registers of stage d, which are loaded again for the step
+  // that they serve next as soon as their contents are in LDS.
+  auto multiply = [&](int d, int step) {
+    const int after = step + DEPTH * WAVES, after_x = step + WAVES;
     uint32_t ws[NT];
 #pragma unroll
     for (int i = 0; i < NT; i++) {
@@ -591,9 +590,9 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 && (NT == 4 || WAVES == 16) ? 4
       decode_blocks<BF16>(c, ws[i], w);
     };
     auto take_x = [&](int j, Frag* f) {
-      x[d][j].put(xl);
-      const uint32_t sc = XT == kXNVFP4 ? row_scales(x[d][j].s, 0) : 0;
-      if (after < whole) load_rows(d, j, after);
+      x[j].put(xl);
+      const uint32_t sc = XT == kXNVFP4 ? row_scales(x[j].s, 0) : 0;
+      if (after_x < whole) load_rows(j, after_x);
       XTile<XT>::get(xl, sc, f);
     };
     if constexpr (MT == 1) {  // hold the activations, not the weights
@@ -624,15 +623,15 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 && (NT == 4 || WAVES == 16) ? 4
   };
 #pragma unroll
   for (int d = 0; d < DEPTH; d++)
-    if (wave + d * WAVES < whole) {
-      load_w(d, wave + d * WAVES);
+    if (wave + d * WAVES < whole) load_w(d, wave + d * WAVES);
+  if (wave < whole) {
 #pragma unroll
-      for (int j = 0; j < MT; j++) load_rows(d, j, wave + d * WAVES);
-    }
+    for (int j = 0; j < MT; j++) load_rows(j, wave);
+  }
   for (int step = wave; step < whole; step += WAVES * DEPTH) {
 #pragma unroll
     for (int d = 0; d < DEPTH; d++)
-      if (step + d * WAVES < whole) multiply(d, step + (d + DEPTH) * WAVES);
+      if (step + d * WAVES < whole) multiply(d, step + d * WAVES);
   }
   if (KB % 8 && wave == whole % WAVES) {  // the part of a step that is left
     const int64_t b = (int64_t)whole * 8 + 2 * g4;
