@@ -15,9 +15,15 @@
 // The matrix instruction 16x16x32 takes, from lane l, eight values along k of
 // row l % 16 of each operand, and any assignment of k to (lane, element) will
 // do as long as both operands use the same. Here lane l owns the 16-value
-// blocks 2g and 2g + 1 (g = l / 16) of a 128-deep step: one 16-byte load of
-// codes, one 2-byte load of scales, four instructions. The weight is the first
-// operand, so a lane's four sums are four neighbouring columns of one row of y.
+// blocks 2g and 2g + 1 (g = l / 16) of a 128-deep step: 16 bytes of codes, two
+// scale bytes, four instructions. The weight is the first operand, so a lane's
+// four sums are four neighbouring columns of one row of y.
+//
+// What bounds it: few rows, the weights' way from memory (64 experts of 2048 x
+// 7168 at decode: 297 MB in 79 us, 3.8 TB/s where a copy reaches 5.0); many
+// rows, the matrix units at the clock that the power limit leaves (8192 x 4096 x
+// 14336: 1.20 to 1.30 PFLOP/s; a loop of matrix instructions alone reaches 1.88,
+// the library's 16-bit product 1.45 to 1.53 without the decode).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -263,7 +269,6 @@ __device__ __forceinline__ float activate(int act, float v) {
 
 // Four neighbouring values of a tensor, `have` of which exist. Rows of any
 // length: the accesses need no more than the elements' own alignment.
-
 __device__ __forceinline__ f32x4 load4(const void* p, int dt, int64_t i, int have) {
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (have < 4) {
@@ -364,9 +369,9 @@ __device__ __forceinline__ void zero4(const LinearArgs& a, int64_t m, int64_t n)
 // ---------------------------------------------------------------- kernels
 
 // Loads of the kernels' loops: a uniform address in scalar registers plus a
-// 32-bit lane offset (K is at most 2^22, so 256 rows are within reach). (Left to itself the compiler carries a 64-bit address per
-// lane and load through the loop: 24 registers that spill.) The alignments are
-// those that K % 16 == 0 gives.
+// 32-bit lane offset (K is at most 2^22, so 256 rows are within reach). Left to
+// itself the compiler carries a 64-bit address per lane and load through the
+// loop: 24 registers that spill. The alignments are those that K % 16 == 0 gives.
 #define FOS_GLOBAL __attribute__((address_space(1)))
 typedef const FOS_GLOBAL uint8_t* GlobalBytes;
 
@@ -481,10 +486,14 @@ __device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
 }
 
 // The stream kernel, for few rows per weight: one workgroup takes 16 NT columns
-// of y and 16 MT rows, and its waves take the 128-deep steps of k in turn, so that the weight is read once by as many waves as the chip has. A wave keeps
-// DEPTH steps of loads in flight (4 KiB of codes). Like the activations, the
-// weights are loaded four lanes to a row and turned through the wave's own LDS.
-// The waves' sums are joined through LDS in wave order.
+// of y and 16 MT rows, and its waves take the 128-deep steps of k in turn, so
+// that the weight is read once by as many waves as the chip has. A wave keeps
+// DEPTH steps of the weight's loads in flight. Like the activations, the weights
+// are loaded four lanes to a row and turned through the wave's own LDS: a load
+// costs a cycle for every row that four consecutive lanes touch (16 x 4096 x
+// 14336: 21 us with a row per lane, 14 so). The waves' sums are joined through
+// LDS in wave order. 1 x 4096 x 14336 bf16: 10.5 us, 3.1 TB/s; 64 x 14336 x 4096:
+// 22 us.
 template <int XT, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16;
@@ -569,7 +578,7 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 4 : 2) void k_linear_stream(L
   };
   auto load_rows = [&](int j, int64_t step) {
     x[j].load(xc + 16 * j * KB * (2 * XTile<XT>::kLanes) + step * (16 * XTile<XT>::kLanes),
-                 XT == kXNVFP4 ? xsc + 16 * j * KB + step * 8 : nullptr, xoff, xsoff, KB, xrows - 16 * j);
+              XT == kXNVFP4 ? xsc + 16 * j * KB + step * 8 : nullptr, xoff, xsoff, KB, xrows - 16 * j);
   };
   uint8_t* wl = lds + wave * kWaveBytes;
   uint8_t* xl = wl + NT * 1024;
@@ -799,27 +808,18 @@ __device__ __forceinline__ void tile_of(uint32_t m_tiles, uint32_t n_tiles, uint
   tn = in / high;
 }
 
-// Waits that the compiler's own wait insertion knows of: at most N vector
-// memory operations still on their way.
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(N < 16, "");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | N);
-  asm volatile("" ::: "memory");
-}
-
-// A workgroup barrier for LDS alone: outstanding loads of registers stay on
-// their way (__syncthreads would wait for them).
-__device__ __forceinline__ void block_sync() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
+// Every load of this wave has arrived, the direct ones to LDS among them: the
+// compiler does not wait for those by itself. (vmcnt = 0, the other counters at
+// their maximum.)
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);
   asm volatile("" ::: "memory");
 }
 
 // (three workgroups of 64 rows fit a CU without spills for fp16 only)
 template <int XT, int BM>
-__global__ __launch_bounds__(256, BM == 64 && XT == kFP16 ? 3 : 2) void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles,
-                                                                       int splits) {
+__global__ __launch_bounds__(256, BM == 64 && XT == kFP16 ? 3 : 2)
+void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles, int splits) {
   constexpr bool BF16 = XT == kBF16;
   constexpr int MT = BM / 16;
   __shared__ __align__(16) uint8_t lds[2][BM * 256];
@@ -853,12 +853,12 @@ __global__ __launch_bounds__(256, BM == 64 && XT == kFP16 ? 3 : 2) void k_linear
   const uint8_t* wc = a.w + w0 * (a.K / 2);
   const uint8_t* wsc = a.ws + w0 * KB;
   const int wrows = n0 < a.N ? (a.N - n0 < 64 ? (int)(a.N - n0) : 64) : 1;
-  //
+
   // A load instruction costs a cycle for every 64 bytes or row that four
   // consecutive lanes touch, and the matrix instruction wants consecutive lanes
   // in different rows. So four neighbouring lanes load the 64 bytes of a row,
   // and one lane the 8 scale bytes of each of the wave's 64 rows, and the lanes
-  // swap them when the step begins: 20 exchanges against 1500 cycles of loads.
+  // swap them when the step begins: 24 exchanges against 1500 cycles of loads.
   uint32_t woff[4], wsoff;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -946,8 +946,8 @@ __global__ __launch_bounds__(256, BM == 64 && XT == kFP16 ? 3 : 2) void k_linear
     // reads the other tile any more. All of the next step's loads start here
     // and have this step's time. (The last step loads itself again: a load that
     // may not happen would make the compiler wait where the paths meet.)
-    wait_vm<0>();
-    block_sync();
+    wait_loads();
+    __syncthreads();
     take_w();
     uint8_t* next = lds[(step & 1) ^ 1];
     const int after = step + 1 < whole ? step + 1 : step;
@@ -956,7 +956,7 @@ __global__ __launch_bounds__(256, BM == 64 && XT == kFP16 ? 3 : 2) void k_linear
     multiply(lds[step & 1]);
     xs.store(next);
   }
-  wait_vm<0>();
+  wait_loads();
   __syncthreads();
   if (remainder) {  // the part of a step that is left: zeros past the end
     uint8_t* last = lds[whole & 1];
@@ -1108,9 +1108,6 @@ Plan plan(int64_t M, int64_t N, int64_t K, int64_t G) {
       }
     }
   }
-#ifdef FOS_BM
-  if (FOS_BM) best = Plan{false, FOS_BM, FOS_SPLIT ? FOS_SPLIT : 1, tiles(FOS_BM)};
-#endif
   return best;
 }
 

@@ -287,8 +287,8 @@ hipError_t rows(const NormArgs& a, hipStream_t s) {
 // (seven waves of four chunks took 116 us where sixteen of two take 89, 4096 x
 // 14336 bf16), and the fewest registers that leaves (8192 x 4096: two chunks in
 // four waves 51 us, one in eight 59; 4096 x 8192: two in eight 49, four in four
-// 56). Bound by HBM: 8192 x 4096 bf16 with a residual moves 235 MB in 51 us,
-// 4.6 TB/s where a copy reaches 5.0.
+// 56). Bound by HBM: 8192 x 4096 bf16 with a residual moves 235 MB in 48 us,
+// 4.9 TB/s where a copy reaches 5.0.
 template <int DT, int WT>
 hipError_t by_width(const NormArgs& a, hipStream_t s) {
   const int64_t chunks = (a.K + 7) / 8;

@@ -460,6 +460,8 @@ hipError_t by_type(int dt, const BalanceArgs& a, bool backward, hipStream_t s) {
 
 // Up to 256 rows one workgroup does it all (128 x 64: 7 us, 10 with a second
 // launch; 512 x 256: 19 and 13); then 64 rows each, up to two workgroups per CU.
+// 65536 x 256 bf16, top 8: the forward pass reads 36 MB in 13 us and joins in 10
+// (latency), the backward pass moves 67 MB in 13 us, 5.2 TB/s, the rate of a copy.
 int balance_blocks(int64_t T, int) {
   const int64_t b = T <= 256 ? 1 : (T + 63) / 64;
   return b < 1 ? 1 : b > 512 ? 512 : (int)b;
