@@ -621,14 +621,14 @@ def _linear(x, w, offs, bias, act, residual, out_dtype, out, x_gran, w_gran, wor
     need = lib.fos_linear_workspace(M, N, K, G or 0)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    work, room = (None, 0) if workspace is None else (workspace.data_ptr(),
+    work, room = (None, 0) if workspace is None else (_match(workspace, "workspace", dev),
                                                       workspace.numel() * workspace.element_size())
     if G is None:
         _call(dev, lib.fos_linear, ctypes.byref(xo), ctypes.byref(wo), M, N, K, epi, yp, out_code, work, room)
     else:
         _call(dev, lib.fos_linear_grouped, ctypes.byref(xo), ctypes.byref(wo),
               _match(offs, "offs", dev, (G,), torch.int32), G, M, N, K, epi, yp, out_code, work, room,
-              None if status is None else status.data_ptr())
+              None if status is None else _match(status, "status", dev, None, torch.int32))
     return y
 
 
@@ -732,8 +732,8 @@ def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0
           8 if idx.dtype == torch.int64 else 4, idx.shape[1], _mask_pointer(mask, T, dev), coef, align,
           _match(loss, "loss", dev, (1,), torch.float32), _match(counts, "counts", dev, (E,), torch.int32),
           _match(offs, "offs", dev, (E,), torch.int32), _match(slope, "slope", dev, (E,), torch.float32),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          None if status is None else status.data_ptr())
+          _match(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
+          None if status is None else _match(status, "status", dev, None, torch.int32))
     return loss, counts, offs, slope
 
 

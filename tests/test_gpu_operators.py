@@ -636,6 +636,37 @@ def test_python_refusals():
         fos.fos_linear(x, w, workspace=None, out=torch.zeros(40, device="cuda")[2:34].view(4, 8))
 
 
+def test_workspace_and_status_are_checked():
+    """Memory that the kernels write besides their outputs: on the host, with
+    gaps or of another type it is refused before a launch."""
+    M, N, K = 130, 1500, 3088  # in several parts of K
+    need = fos.fos_linear_workspace(M, N, K)
+    assert need > 0
+    x = torch.randn(M, K, generator=gen(3)).bfloat16().cuda()
+    w = make_w(N, K, 4)[0]
+    offs = torch.tensor([M], dtype=torch.int32, device="cuda")
+    w3 = (w[0][None], w[1][None], w[2])
+    logits = torch.randn(8, 16, generator=gen(5)).cuda()
+    idx = torch.zeros(8, 2, dtype=torch.int64, device="cuda")
+    room = fos.fos_balance_workspace(8, 16)
+    for bad in (lambda n: torch.empty(n, dtype=torch.uint8),
+                lambda n: torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            fos.fos_linear(x, w, workspace=bad(need))
+        with pytest.raises(ValueError):
+            fos.fos_balance_loss(logits, idx, workspace=bad(room))
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.uint8, device="cuda"),
+                torch.zeros(1, dtype=torch.int64, device="cuda")):
+        with pytest.raises(ValueError):
+            fos.fos_linear_grouped(x, w3, offs, status=bad)
+        with pytest.raises(ValueError):
+            fos.fos_balance_loss(logits, idx, status=bad)
+    with pytest.raises(fos.FosError):
+        fos.fos_linear(x, w, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    y = fos.fos_linear(x, w, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(y, fos.fos_linear(x, w))
+
+
 # ------------------------------------------------------------------ together
 
 
