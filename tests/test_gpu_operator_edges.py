@@ -1,0 +1,42 @@
+"""The operators around the quantizer at the edges of their ranges: values
+beside a rounding's border, scales and rows near the ends of binary32, sizes
+past a single launch. GPU only."""
+import pytest
+import torch
+
+import nvfp4_adaptive_block_amd as fos
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- norm
+
+
+def e4m3_middles():
+    """The values halfway between two neighbouring E4M3 magnitudes."""
+    codes = torch.arange(0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    return (codes[1:] + codes[:-1]) / 2
+
+
+@pytest.mark.parametrize("form", ["packed", "row", "wide"])
+def test_norm_codes_at_the_middle_of_two(form):
+    """q is E4M3 of v / s, the quotient rounded once. Rows of ones have rms 1,
+    so v is the weight: multiples of the row's scale that lie on the middle of
+    two codes, or one step of binary32 beside it, and the row's maximum."""
+    for seed in range(12):
+        # (the last rows of scales near the least and the largest that binary32 has)
+        size = {9: 2.0 ** -116, 10: 2.0 ** -80, 11: 2.0 ** 127}.get(seed, 1.0)
+        top = (torch.rand(1, generator=torch.Generator().manual_seed(seed)) + 0.5) * size
+        v = (e4m3_middles() * (top / 448).double()).float()
+        v = torch.cat([top, v, torch.nextafter(v, torch.zeros(())), torch.nextafter(v, top.expand_as(v)), -v])
+        w = v.repeat({"packed": 1, "row": 3, "wide": 70}[form])
+        w = torch.cat([w, torch.zeros(-len(w) % 8)]) if seed % 2 else w
+        K = len(w)
+        assert (8 <= K <= 512, 512 < K <= 32768, K > 32768)[["packed", "row", "wide"].index(form)]
+        x = torch.ones(5, K, device="cuda")
+        y = torch.empty_like(x)
+        q, s, _ = fos.fos_rmsnorm_quantize(x, w.cuda(), eps=0.0, y=y)
+        y, s = y.cpu(), s.cpu()
+        assert torch.equal(y, w.expand(5, K)) and torch.equal(s, (top / 448).expand(5))
+        want = (y / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8)), seed
