@@ -38,11 +38,24 @@ __device__ __forceinline__ float load_weight(const NormArgs& a, int64_t i) {
                               : a.weight_dt == kBF16 ? load1<kBF16>(a.weight, i) : load1<kFP16>(a.weight, i);
 }
 
-// 1 / sqrt(mean + eps) from the sum of squares, NaN if the sum is not finite.
-__device__ __forceinline__ float inv_rms(double sum, int64_t K, float eps) {
-  const double r = 1.0 / sqrt(sum / (double)K + (double)eps);
-  return sum < __builtin_huge_val() ? (float)r : __builtin_nanf("");
-}
+// 1 / sqrt(mean + eps) from a row's sum of squares, as r times a power of two;
+// NaN if the sum is not finite. The power is 1 but where the reciprocal nears the
+// ends of binary32's range (eps 0 and a row of subnormals; a row of the largest
+// values): h takes it before r then, and neither is lost.
+struct InverseRms {
+  float r, up;
+  bool far;  // the same in all lanes; up is 1 where it is not set
+  __device__ __forceinline__ InverseRms(double sum, int64_t K, float eps) {
+    const double w = sum < __builtin_huge_val() ? 1.0 / sqrt(sum / (double)K + (double)eps) : __builtin_nan("");
+    r = (float)w;
+    up = 1.0f;
+    far = __builtin_amdgcn_readfirstlane(!(r >= 0x1p-100f && r <= 0x1p100f));
+    if (far) {
+      up = w > 1.0 ? 0x1p64f : 0x1p-64f;
+      r = (float)(w * (w > 1.0 ? 0x1p-64 : 0x1p64));
+    }
+  }
+};
 
 // The row's scale from max|y|: NaN unless the maximum is finite.
 __device__ __forceinline__ float row_scale(float top) {
@@ -116,13 +129,13 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
   __syncthreads();
   ss = sums[0];
   for (int i = 1; i < waves; i++) ss += sums[i];
-  const float r = inv_rms(ss, a.K, a.eps);
+  const InverseRms inv(ss, a.K, a.eps);
   float top = 0.0f;
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < a.K; i += threads) {
     float h = load1<DT>(a.x, base + i);
     if (a.res) h += load1<DT>(a.res, base + i);
-    top = max_nan(top, __builtin_fabsf(load_weight(a, i) * (h * r)));
+    top = max_nan(top, __builtin_fabsf(load_weight(a, i) * (h * inv.up * inv.r)));
   }
   top = wave_max(top);
   if ((threadIdx.x & 63) == 0) tops[wave] = top;
@@ -135,7 +148,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
   for (int64_t i = threadIdx.x; i < a.K; i += threads) {
     float h = load1<DT>(a.x, base + i);
     if (a.res) h += load1<DT>(a.res, base + i);
-    const float y = load_weight(a, i) * (h * r);
+    const float y = load_weight(a, i) * (h * inv.up * inv.r);
     float t;
     divide.operator()<1>(&y, &t);
     a.q[base + i] = s != s ? 0x7F : (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, 0.0f, 0, false);
@@ -256,14 +269,20 @@ __global__ __launch_bounds__(64 * WAVES) void k_norm_rows(NormArgs a) {
     ss = sums[0];
     for (int i = 1; i < WAVES; i++) ss += sums[i];
   }
-  const float r = inv_rms(ss, a.K, a.eps);
+  const InverseRms inv(ss, a.K, a.eps);
+  if (inv.far) {
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) h[c][j] *= inv.up;
+  }
   float top = 0.0f;
 #pragma unroll
   for (int c = 0; c < C; c++)
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      h[c][j] = w[c][j] * (h[c][j] * r);
-      // padding has h = w = 0 and adds nothing (it is NaN exactly when r is)
+      h[c][j] = w[c][j] * (h[c][j] * inv.r);
+      // padding has h = w = 0 and adds nothing (it is NaN exactly where the row is)
       top = max_nan(top, __builtin_fabsf(h[c][j]));
     }
   top = wave_max(top);

@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import nvfp4_adaptive_block_amd as fos
+from operator_reference import DTYPES, gen
+from test_gpu_operators import check_norm, cuda
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +42,24 @@ def test_norm_codes_at_the_middle_of_two(form):
         assert torch.equal(y, w.expand(5, K)) and torch.equal(s, (top / 448).expand(5))
         want = (y / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
         assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8)), seed
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [40, 999, 40000])
+def test_norm_rows_whose_rms_is_near_the_ends_of_binary32(dt, K):
+    """With eps = 0 a row of subnormals has a reciprocal rms past binary32's
+    largest value, and a row of the largest values one among its subnormals:
+    the result is of order 1 in both."""
+    x = torch.randn(6, K, generator=gen(K)).clamp(-3, 3)
+    x[0] *= 2.0 ** -129
+    x[1] *= 2.0 ** -131
+    x[2, 1:] = 0             # one subnormal in a row of zeros
+    x[2, 0] = 2.0 ** -131
+    x[3] *= 2.0 ** 126
+    x[4] = 3.38e38
+    x = x.to(DTYPES[dt])
+    w = 1 + 0.3 * torch.randn(K, generator=gen(1))
+    y = torch.empty(6, K, dtype=DTYPES[dt], device="cuda")
+    q, s, h = fos.fos_rmsnorm_quantize(cuda(x), cuda(w), eps=0.0, y=y)
+    assert torch.isfinite(s).all()
+    check_norm(x, None, w, 0.0, q.cpu(), s, x, y)
