@@ -366,12 +366,25 @@ hipError_t by_weight(const NormArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// A launch has fewer than 2^32 threads, up to 1024 of them for a row, so that
+// calls of more rows are several launches.
 hipError_t launch_norm(int dt, const NormArgs& a, hipStream_t s) {
-  switch (dt) {
-    case kBF16: return by_weight<kBF16>(a, s);
-    case kFP16: return by_weight<kFP16>(a, s);
-    default: return by_weight<kFP32>(a, s);
+  constexpr int64_t kRows = int64_t(1) << 21;
+  const int64_t size = dt == kFP32 ? 4 : 2;
+  for (int64_t row = 0; row < a.M; row += kRows) {
+    NormArgs part = a;
+    part.M = a.M - row < kRows ? a.M - row : kRows;
+    part.x = (const uint8_t*)a.x + row * a.K * size;
+    if (a.res) part.res = (const uint8_t*)a.res + row * a.K * size;
+    part.q = a.q + row * a.K;
+    part.scale = a.scale + row;
+    if (a.h) part.h = (uint8_t*)a.h + row * a.K * size;
+    if (a.y) part.y = (uint8_t*)a.y + row * a.K * size;
+    const hipError_t e = dt == kBF16 ? by_weight<kBF16>(part, s)
+                         : dt == kFP16 ? by_weight<kFP16>(part, s) : by_weight<kFP32>(part, s);
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 }  // namespace fos

@@ -63,3 +63,21 @@ def test_norm_rows_whose_rms_is_near_the_ends_of_binary32(dt, K):
     q, s, h = fos.fos_rmsnorm_quantize(cuda(x), cuda(w), eps=0.0, y=y)
     assert torch.isfinite(s).all()
     check_norm(x, None, w, 0.0, q.cpu(), s, x, y)
+
+
+@pytest.mark.parametrize("M,K", [(2 ** 21 + 5, 9), (3 * 2 ** 21, 3), (2 ** 26 + 3, 4)])
+def test_norm_of_more_rows_than_a_launch_has(M, K):
+    """Rows on both sides of every 2^21 against the reference, and no row left out."""
+    g = torch.Generator("cuda")
+    g.manual_seed(K)
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    res = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16) if K == 9 else None
+    w = 1 + 0.3 * torch.randn(K, generator=gen(2))
+    s = torch.full((M,), float("nan"), device="cuda")
+    y = torch.full_like(x, float("nan"))
+    q, s, h = fos.fos_rmsnorm_quantize(x, w.cuda(), residual=res, eps=1e-5, scale=s, y=y)
+    assert torch.isfinite(s).all() and torch.isfinite(y).all()
+    near = torch.cat([torch.arange(max(0, at - 20), min(M, at + 20)) for at in [*range(0, M, 2 ** 21), M]]).cuda()
+    pick = lambda t: None if t is None else t[near].cpu()
+    check_norm(pick(x), pick(res), w, 1e-5, q.view(torch.uint8)[near].cpu().view(torch.float8_e4m3fn), pick(s), pick(h),
+               pick(y))
