@@ -414,7 +414,9 @@ typedef struct fos_epilogue {
  * codes and scales of fos_quantize, 1x16 and 16x16 alike, and (with
  * fos_quantize_columnwise's output as w) of the transposed operand, which
  * makes it the backward product dX = dY W too. y is bf16, fp16 or fp32,
- * contiguous. M and N are at most 2^30, K at most 2^22 and a multiple of 16.
+ * contiguous. M and N are at most 2^30, K at most 2^22 and a multiple of 16;
+ * sizes whose tiles need 2^32 threads or more (16 rows by 2^29 columns, say)
+ * do not fit a launch and are FOS_ERR_SHAPE too.
  * Decoded values are exact in the 16-bit type of the matrix
  * instruction, products exact and sums binary32, so the result differs from
  * the exact one by the order of the sum and the rounding of the output.

@@ -664,6 +664,8 @@ int check_linear_sizes(int64_t M, int64_t N, int64_t K, int64_t G) {
     return fail(FOS_ERR_SHAPE, "M and N are at most 2^30 and K 2^22, got M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
   if (K > 0 && (M > kMaxElems / K || N > kMaxElems / K / (G > 0 ? G : 1))) return fail(FOS_ERR_SHAPE, "an operand exceeds 2^40 elements");
   if (N > 0 && M > kMaxElems / N) return fail(FOS_ERR_SHAPE, "M*N exceeds 2^40 elements");
+  if (M > 0 && N > 0 && !fos::linear_fits(M, N, K, (int)G))
+    return fail(FOS_ERR_SHAPE, "too many tiles for one launch (M=%lld N=%lld G=%lld)", (long long)M, (long long)N, (long long)G);
   return FOS_OK;
 }
 
@@ -718,9 +720,7 @@ int run_linear(const fos_operand* x, const fos_operand* w, const int32_t* offs, 
   a.G = grouped ? G : 1;
   a.status = d_status;
   a.work = work;
-  const hipError_t e = fos::launch_linear(a, static_cast<hipStream_t>(stream));
-  if (e == hipErrorInvalidConfiguration) return fail(FOS_ERR_SHAPE, "too many tiles for one launch (M=%lld N=%lld)", (long long)M, (long long)N);
-  return launch_status(e);
+  return launch_status(fos::launch_linear(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

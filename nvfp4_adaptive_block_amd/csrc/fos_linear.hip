@@ -1098,8 +1098,6 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, int splits) {
   finish(a, (int)m, 0, (int)m, q, columns, row, v);
 }
 
-constexpr int64_t kMaxGrid = INT32_MAX;
-
 // The most tiles of `rows` rows that M rows in G groups and a tail can need:
 // each non-empty group may end inside a tile.
 int64_t max_tiles(int64_t M, int64_t G, int64_t rows) {
@@ -1120,6 +1118,18 @@ struct Plan {
 int stream_columns(int64_t m_tiles, int64_t N) {
   const int64_t n16 = (N + 15) / 16;
   return n16 / 4 * m_tiles >= 224 ? 4 : n16 / 2 * m_tiles >= 224 ? 2 : 1;
+}
+
+// Eight waves; sixteen with half the steps in flight where a workgroup has one
+// column tile and the chain of a wave's steps is what takes the time.
+constexpr int stream_waves(int mt, int nt) { return mt == 1 && nt == 1 ? 16 : 8; }
+
+// A launch has fewer than 2^32 threads. (The join of parts of K comes nowhere
+// near: parts are for at most 768 tiles.)
+bool fits(const Plan& p, int64_t N) {
+  const int nt = p.stream ? stream_columns(p.m_tiles, N) : 16;
+  const int64_t threads = p.stream ? 64 * stream_waves(p.bm / 16, nt) : 256;
+  return p.m_tiles * p.splits <= UINT32_MAX / threads / ((N + 16 * nt - 1) / (16 * nt));
 }
 
 // Estimated microseconds, fitted to what the kernels take on 256 CUs (fp16, N =
@@ -1157,7 +1167,7 @@ Plan plan(int64_t M, int64_t N, int64_t K, int64_t G) {
   // 2048 x 7168: 32 rows each 248 us, 292 with tiles; 64 rows 429 and 353)
   if (rows <= (G ? 40 : 64)) return best;
   const int64_t n_tiles = (N + 255) / 256;
-  double least = G ? 1e30 : stream_us(best.m_tiles, N, K);
+  double least = G || !fits(best, N) ? 1e30 : stream_us(best.m_tiles, N, K);
   for (int b = 64; b <= 128; b *= 2) {
     // a group ends inside a tile, on average at its middle
     const double t = (G ? (double)M / b + 0.5 * (double)G : (double)tiles(b)) * (double)n_tiles;
@@ -1176,10 +1186,7 @@ Plan plan(int64_t M, int64_t N, int64_t K, int64_t G) {
 template <int XT, int MT, int NT>
 hipError_t launch_stream_n(const LinearArgs& a, int64_t m_tiles, hipStream_t s) {
   const int64_t n_tiles = (a.N + 16 * NT - 1) / (16 * NT);
-  if (m_tiles > kMaxGrid / n_tiles) return hipErrorInvalidConfiguration;
-  // Eight waves; sixteen with half the steps in flight where a workgroup has one
-  // column tile and the chain of a wave's steps is what takes the time.
-  constexpr int WAVES = MT == 1 && NT == 1 ? 16 : 8;
+  constexpr int WAVES = stream_waves(MT, NT);
   k_linear_stream<XT, MT, NT, WAVES><<<dim3((unsigned)(m_tiles * n_tiles)), dim3(64 * WAVES), 0, s>>>(a, (int)n_tiles);
   return hipGetLastError();
 }
@@ -1203,7 +1210,6 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
     return launch_stream<XT, 4>(a, p.m_tiles, s);
   }
   const int64_t n_tiles = (a.N + 255) / 256;
-  if (p.m_tiles > kMaxGrid / n_tiles / p.splits) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(p.m_tiles * n_tiles * p.splits));
   if (p.bm == 64)
     k_linear_tile<XT, 64><<<grid, dim3(256), 0, s>>>(a, (uint32_t)p.m_tiles, (uint32_t)n_tiles, p.splits);
@@ -1222,6 +1228,8 @@ int64_t linear_workspace(int64_t M, int64_t N, int64_t K, int G) {
   const Plan p = plan(M, N, K, G);
   return p.splits == 1 ? 0 : p.splits * M * ((N + 3) / 4 * 4) * 4;
 }
+
+bool linear_fits(int64_t M, int64_t N, int64_t K, int G) { return fits(plan(M, N, K, G), N); }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   switch (a.x_type) {

@@ -40,7 +40,8 @@ struct LinearArgs {
 
 // Bytes of workspace of a launch (G = 0: dense).
 int64_t linear_workspace(int64_t M, int64_t N, int64_t K, int G);
-// hipErrorInvalidConfiguration: more tiles than a grid holds.
+// Whether a grid holds the tiles of a product with M, N > 0.
+bool linear_fits(int64_t M, int64_t N, int64_t K, int G);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 
 struct NormArgs {
