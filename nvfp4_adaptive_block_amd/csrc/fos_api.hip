@@ -649,7 +649,7 @@ int check_operand(const char* what, const fos_operand* o, int64_t rows, int64_t 
   if (o->type == FOS_BF16 || o->type == FOS_FP16) return FOS_OK;
   if (o->gran != FOS_PER_TENSOR && o->gran != FOS_PER_ROW && !(grouped && o->gran == FOS_PER_GROUP))
     return fail(FOS_ERR_INVALID_ARG, "%s: bad scale granularity %d", what, o->gran);
-  if (!o->scale) return fail(FOS_ERR_INVALID_ARG, "%s: scale is NULL", what);
+  if (!o->scale && (rows > 0 || o->gran != FOS_PER_ROW)) return fail(FOS_ERR_INVALID_ARG, "%s: scale is NULL", what);
   if (!aligned(o->scale, 4)) return fail(FOS_ERR_ALIGN, "%s: scale not 4-byte aligned", what);
   if (o->type == FOS_NVFP4 && rows * K > 0 && !o->block_scales)
     return fail(FOS_ERR_INVALID_ARG, "%s: block_scales is NULL", what);

@@ -6,7 +6,7 @@ import torch
 
 import nvfp4_adaptive_block_amd as fos
 from operator_reference import DTYPES, gen
-from test_gpu_operators import check_norm, cuda
+from test_gpu_operators import check_norm, cuda, make_w
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,32 @@ def test_norm_of_more_rows_than_a_launch_has(M, K):
     pick = lambda t: None if t is None else t[near].cpu()
     check_norm(pick(x), pick(res), w, 1e-5, q.view(torch.uint8)[near].cpu().view(torch.float8_e4m3fn), pick(s), pick(h),
                pick(y))
+
+
+# ---------------------------------------------------------------- product
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_product_of_no_rows(grouped):
+    """What the norm and the quantizer return for no tokens goes into the
+    product as for some."""
+    K, N = 64, 24
+    offs = torch.zeros(2, dtype=torch.int32, device="cuda")
+    w = make_w(N, K, 1, "tensor", 2 if grouped else None)[0]
+    for rows in (0, 5):
+        x = torch.ones(rows, K, dtype=torch.bfloat16, device="cuda")
+        q, s, _ = fos.fos_rmsnorm_quantize(x, torch.ones(K, device="cuda"))
+        codes = (torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda"),
+                 torch.zeros(rows, K // 16, dtype=torch.uint8, device="cuda"), torch.ones(rows, device="cuda"))
+        for operand, gran in (((q, s), None), (codes, "row")):
+            if grouped:
+                y = fos.fos_linear_grouped(operand, w, offs, x_gran=gran)
+            else:
+                y = fos.fos_linear(operand, w, x_gran=gran)
+            assert y.shape == (rows, N)
+
+
+def test_product_with_no_columns():
+    x = torch.ones(3, 64, dtype=torch.bfloat16, device="cuda")
+    w = make_w(0, 64, 1, "row")[0]
+    assert fos.fos_linear(x, w, w_gran="row").shape == (3, 0)

@@ -3,7 +3,9 @@ take, on the host: every check runs before a device is touched."""
 import pytest
 
 import nvfp4_adaptive_block_amd as fos
-from test_operators_host import O, P, SHAPE, linear
+from test_operators_host import C, INVALID, O, P, SHAPE, linear, operand
+
+DEVICE = 6  # where there is no GPU, what a call that passes every check ends with
 
 
 @pytest.mark.parametrize("G,M,N,K,fits", [
@@ -16,3 +18,20 @@ def test_products_past_a_launch_are_refused_for_their_shape(G, M, N, K, fits):
     assert (fos.load_library().fos_linear_workspace(M, N, K, G) >= 0) == fits
     if not fits:
         assert linear(M=M, N=N, K=K, **(dict(G=G, offs=P(O)) if G else {})) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=operand(0, type=3, gran=1, scale=0), M=0, y=0), dict(x=operand(0, 0, 0, 4, 1), M=0, y=0),
+    dict(x=operand(0, type=3, gran=1, scale=0), M=0, y=0, G=2, offs=P(O)),
+    dict(w=operand(0, 0, 0, 4, 1), N=0, y=0), dict(w=operand(0, 0, 0, 4, 1), N=0, y=0, G=2, offs=P(O)),
+])
+def test_operands_without_rows_need_no_row_scales(kw):
+    """A tensor without elements has no address."""
+    assert linear(**kw) in (0, DEVICE)
+
+
+@pytest.mark.parametrize("kw", [dict(x=operand(type=3, gran=1, scale=0)), dict(x=operand(0, 0, 0, 4, 0), M=0, y=0),
+                                dict(x=operand(0, type=3, scale=0), M=0, y=0), dict(w=operand(C, scale=0, gran=1)),
+                                dict(w=operand(0, 0, 0, 4, 2), N=0, y=0, G=2, offs=P(O))])
+def test_scales_that_there_are_are_needed(kw):
+    assert linear(**kw) == INVALID
