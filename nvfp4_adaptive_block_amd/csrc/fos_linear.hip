@@ -327,8 +327,9 @@ struct ColumnTail {
     if (a.bias) bias = load4(a.bias, a.bias_dt, at, q.have);
   }
 };
-// R rows m, m + step ...; those past `last` take the last one's.
-template <int R>
+// R rows m, m + step ...; those past `last` take the last one's. SX: whether x
+// may have a scale.
+template <bool SX, int R>
 struct RowTails {
   float scale[R];
   u32x4 res[R];
@@ -338,9 +339,9 @@ struct RowTails {
       for (int k = 0; k < R; k++) f(k, (int64_t)min(m + k * step, last));
     };
     each([&](int k, int64_t) { scale[k] = 1.0f, res[k] = u32x4{0, 0, 0, 0}; });
-    if (a.x_gran == kScaleRow) {
+    if (SX && a.x_gran == kScaleRow) {
       each([&](int k, int64_t r) { scale[k] = a.x_scale[r]; });
-    } else if (a.x_gran != kScaleNone) {
+    } else if (SX && a.x_gran != kScaleNone) {
       const float s = a.x_scale[a.x_gran == kScaleGroup ? g : 0];
       each([&](int k, int64_t) { scale[k] = s; });
     }
@@ -356,14 +357,32 @@ struct RowTails {
 
 // Finish four columns of rows m, m + step ... up to `last` from their sums and
 // store them. The sum is rounded to the output type once, after the residual.
-template <int R>
+template <bool SX, int R>
 __device__ __forceinline__ void finish(const LinearArgs& a, int m, int step, int last, const Quad& q,
-                                       const ColumnTail& ct, const RowTails<R>& rt, f32x4 (&v)[R]) {
+                                       const ColumnTail& ct, const RowTails<SX, R>& rt, f32x4 (&v)[R]) {
   auto each = [&](auto f) {
 #pragma unroll
     for (int k = 0; k < R; k++) f(k);
   };
-  each([&](int k) { v[k] *= rt.scale[k] * ct.scale; });
+  if (!SX || a.x_gran == kScaleNone) {
+    each([&](int k) { v[k] *= ct.scale; });
+  } else {
+    // The product of two scales may leave binary32's range though the result does
+    // not. A sum of decoded values is 0 or between 2^-20 and 2^45: it takes both
+    // mantissas, then the exponents at once. (The columns' parts are taken anew for
+    // each row: kept, they spill. 64 experts of 240 rows: 576 us, 570 with the
+    // scales' product in binary32.)
+    each([&](int k) {
+      const int e = __builtin_amdgcn_frexp_expf(rt.scale[k]);
+      const float m = __builtin_amdgcn_frexp_mantf(rt.scale[k]);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        float c = ct.scale[i];
+        asm volatile("" : "+v"(c));
+        v[k][i] = __builtin_ldexpf(v[k][i] * (m * __builtin_amdgcn_frexp_mantf(c)), e + __builtin_amdgcn_frexp_expf(c));
+      }
+    });
+  }
   if (a.bias) {
     const f32x4 bias = widen4(ct.bias, a.bias_dt);
     each([&](int k) { v[k] += bias; });
@@ -544,7 +563,7 @@ __device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
 // 22 us.
 template <int XT, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
-  constexpr bool BF16 = XT == kBF16;
+  constexpr bool BF16 = XT == kBF16, SX = XT == kXE4M3 || XT == kXNVFP4;
   // (more than 32 rows of activations leave the registers for one stage)
   constexpr int DEPTH = MT >= 3 ? 1 : WAVES == 16 ? 2 : 4 / NT;
   constexpr int kWaveBytes = NT * 1024 + XTile<XT>::kBytes;
@@ -597,7 +616,7 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 4 : 2) void k_linear_stream(L
   auto turn = [&](int i) { return (wave + WAVES - (i * MP) % WAVES) % WAVES; };
   constexpr int TURNS = (NT * MP + WAVES - 1) / WAVES;
   ColumnTail columns[TURNS];
-  RowTails<1> row[TURNS];
+  RowTails<SX, 1> row[TURNS];
   bool live[TURNS] = {};
 #pragma unroll
   for (int i = 0; i < NT; i++) {
@@ -871,7 +890,7 @@ __device__ __forceinline__ void wait_loads() {
 template <int XT, int BM>
 __global__ __launch_bounds__(256, BM == 64 && XT == kFP16 ? 3 : 2)
 void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles, int splits) {
-  constexpr bool BF16 = XT == kBF16;
+  constexpr bool BF16 = XT == kBF16, SX = XT == kXE4M3 || XT == kXNVFP4;
   constexpr int MT = BM / 16;
   __shared__ __align__(16) uint8_t lds[2][BM * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1039,7 +1058,7 @@ void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles, int splits)
   constexpr int R = BM == 64 && XT == kFP16 ? 4 : 8;
   const Quad q(a, n0 + 4 * col);
   ColumnTail columns;
-  RowTails<R> next;
+  RowTails<SX, R> next;
   const int last = (int)rt.m0 + rows - 1;
   const bool finishes = splits == 1 && q.have;
   if (finishes) {
@@ -1060,7 +1079,7 @@ void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles, int splits)
     for (int it = 0; it < BM / 8 / R; it++) {
       const int b = half * (BM / 8 / R) + it;
       const int m = (int)rt.m0 + 4 * R * b + g4;
-      const RowTails<R> row = next;
+      const RowTails<SX, R> row = next;
       if (finishes && b + 1 < BM / 4 / R) next.load(a, rt.g, m + 4 * R, 4, last, q);
       f32x4 v[R];
 #pragma unroll
@@ -1088,7 +1107,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, int splits) {
   if (c >= quads) return;
   const Quad q(a, (int64_t)c * 4);
   ColumnTail columns;
-  RowTails<1> row;
+  RowTails<true, 1> row;
   columns.load(a, 0, q);
   row.load(a, 0, (int)m, 0, (int)m, q);
   const f32x4* p = (const f32x4*)a.work + m * quads + c;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import nvfp4_adaptive_block_amd as fos
-from operator_reference import DTYPES, gen
+from operator_reference import DTYPES, decode_nvfp4, gen, random_nvfp4
 from test_gpu_operators import check_norm, cuda, make_w
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +110,75 @@ def test_product_with_no_columns():
     x = torch.ones(3, 64, dtype=torch.bfloat16, device="cuda")
     w = make_w(0, 64, 1, "row")[0]
     assert fos.fos_linear(x, w, w_gran="row").shape == (3, 0)
+
+
+def scaled_rows(kind, M, K, seed):
+    """Quantized rows whose scales are near the ends of binary32's range: (operand, unscaled
+    values, scales). Every sixth row is zero, and every sixth holds one small value."""
+    g = gen(seed)
+    s = torch.tensor([1e-25, 1e-23, 1e25, 1e19, 1.0, 1e25]).repeat(M // 6 + 1)[:M].contiguous()
+    if kind == "e4m3":
+        q = (torch.randn(M, K, generator=g) * 60).clamp(-448, 448)
+        q[2::6] = 0
+        q[3::6] = 0
+        q[3::6, 1] = 2.0 ** -9
+        q = q.to(torch.float8_e4m3fn)
+        return (q, s), q.double(), s.double()
+    codes, scales = random_nvfp4(M, K, seed)
+    scales[2::6] = 0
+    scales[3::6] = 0
+    scales[3::6, 0] = 1
+    codes[3::6, :8] = 0
+    codes[3::6, 0] = 0x10  # the second value is the smallest
+    return (codes, scales, s), decode_nvfp4(codes, scales), s.double()
+
+
+def assert_scaled(y, x, sx, w, sw):
+    """y = (x w^T) sx sw in float32: the sum in any order (as in operator_reference),
+    the product of the scales applied to it, one rounding; past the range, an infinity."""
+    y = y.cpu().double()
+    v = x @ w.T
+    S = (x.abs() @ w.abs().T) * sx[:, None] * sw
+    v = v * sx[:, None] * sw
+    bound = (4 * x.shape[1] ** 0.5 + 8) * 2.0 ** -24 * S + 2.0 ** -23 * v.abs() + 2.0 ** -149
+    top = torch.finfo(torch.float32).max
+    over, fits = v.abs() - bound > top, v.abs() + bound < top
+    assert not torch.isnan(y).any()
+    assert torch.equal(y[over], v[over].sign() * float("inf"))
+    off = (y - v).abs() > bound
+    assert not (off & fits).any(), (int((off & fits).sum()), y[off & fits][0], v[off & fits][0])
+
+
+# few rows, tiles of 64 and of 128 rows, and K in several parts
+@pytest.mark.parametrize("kind", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("gran", ["tensor", "row"])
+@pytest.mark.parametrize("M,N,K", [(20, 33, 256), (50, 700, 1104), (2050, 1500, 528), (3000, 4099, 272), (150, 2051, 4208)])
+def test_product_of_scales_past_binary32(kind, gran, M, N, K):
+    """Each scale, the sum and (mostly) the result are in binary32's range; the
+    product of the two scales is not."""
+    x, xv, sx = scaled_rows(kind, M, K, M)
+    codes, scales = random_nvfp4(N, K, N)
+    wv = decode_nvfp4(codes, scales)
+    for s in (1e-20, 1e20):
+        sw = torch.full((N,) if gran == "row" else (1,), s)
+        if gran == "row":
+            sw[::3] = 1 / s
+        y = fos.fos_linear(cuda(x), cuda((codes, scales, sw)), out_dtype=torch.float32, x_gran="row", w_gran=gran)
+        assert_scaled(y, xv, sx, wv, sw.double())
+
+
+@pytest.mark.parametrize("M", [12, 150])
+def test_product_by_group_of_scales_past_binary32(M):
+    N, K = 40, 272
+    x, xv, _ = scaled_rows("e4m3", M, K, 3)
+    codes, scales = random_nvfp4(3 * N, K, 4)
+    wv = decode_nvfp4(codes, scales)
+    sx, sw = torch.tensor([1e-25, 1e25, 1e19]), torch.tensor([1e-19, 1e20, 1e20])
+    ends = [0, M // 3, 2 * M // 3, M]
+    y = fos.fos_linear_grouped(cuda((x[0], sx)), cuda((codes.view(3, N, -1), scales.view(3, N, -1), sw)),
+                               torch.tensor(ends[1:], dtype=torch.int32).cuda(), out_dtype=torch.float32,
+                               x_gran="group", w_gran="group")
+    for g in range(3):
+        rows = slice(ends[g], ends[g + 1])
+        assert_scaled(y[rows], xv[rows], sx[g].double().expand(ends[g + 1] - ends[g]), wv[g * N:(g + 1) * N],
+                      sw[g].double())
