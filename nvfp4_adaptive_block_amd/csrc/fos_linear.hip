@@ -453,6 +453,16 @@ __device__ __forceinline__ GlobalBytes scalar(const uint8_t* p) {
   return g;
 }
 
+// Between LDS accesses of one wave that different lanes make to the same place.
+// The hardware runs a wave's LDS operations in order; the compiler, which sees
+// one lane at a time, moves no memory access past this, and it is no instruction.
+// (A pair of wavefront fences in place of the asm made the forms of 16-bit
+// activations spill: 64 x 14336 x 4096 bf16 60 us, 21 with this.)
+__device__ __forceinline__ void wave_lds_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Where the LDS tiles keep a row's 16-byte chunks. LDS serves a 16-byte read of
 // 16 lanes at a time, but not of 16 neighbours: lanes 0-3 and 12-15 go with
 // 20-27, and 4-11 with 16-19 and 28-31 (the same in the upper half). With lane l
@@ -473,8 +483,7 @@ __device__ __forceinline__ int swizzle(int r) {
 // with neighbouring lanes in the same row (16 lanes to a row of 16-bit values, 8
 // of E4M3, 4 of NVFP4 codes), put into the wave's own piece of LDS as it is, and
 // read back as the matrix instruction wants it, lane l the 32 values of its
-// blocks 2g and 2g + 1 of row l % 16. LDS operations of one wave run in order, so
-// no barrier is needed. Chunks of 16 bytes are swizzled so that the 16 rows that
+// blocks 2g and 2g + 1 of row l % 16. Chunks of 16 bytes are swizzled so that the 16 rows that
 // are read together lie in 16 different places of the 256 bytes that LDS serves
 // at a time.
 template <int XT>
@@ -515,9 +524,11 @@ struct XTile {
   }
   __device__ __forceinline__ void put(uint8_t* lds) const {
     const int lane = threadIdx.x & 63;
+    wave_lds_order();
 #pragma unroll
     for (int i = 0; i < kLoads; i++)
       *reinterpret_cast<u32x4*>(lds + slot(i * (64 / kLanes) + lane / kLanes, lane % kLanes)) = v[i];
+    wave_lds_order();
   }
   // (scales: this lane's two bytes, from row_scales of s)
   static __device__ __forceinline__ void get(const uint8_t* lds, uint32_t scales, Frag* f) {
@@ -655,11 +666,13 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 4 : 2) void k_linear_stream(L
   auto multiply = [&](int d, int step) {
     const int after = step + DEPTH * WAVES, after_x = step + WAVES;
     uint32_t ws[NT];
+    wave_lds_order();
 #pragma unroll
     for (int i = 0; i < NT; i++) {
       *reinterpret_cast<u32x4*>(wl + i * 1024 + XTile<kXNVFP4>::slot(lane >> 2, lane & 3)) = codes[d][i];
       ws[i] = row_scales(scales[d], 16 * i);
     }
+    wave_lds_order();
     if (after < whole) load_w(d, after);
     auto take_w = [&](int i, Frag* w) {
       const u32x4 t = *reinterpret_cast<const u32x4*>(wl + i * 1024 + XTile<kXNVFP4>::slot(col, g4));
@@ -1070,12 +1083,14 @@ void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles, int splits)
   uint8_t* mine = &lds[0][0] + wave * (BM * 128);
 #pragma unroll
   for (int half = 0; half < 2; half++) {
+    wave_lds_order();
 #pragma unroll
     for (int m = 0; m < MT / 2; m++)
 #pragma unroll
       for (int i = 0; i < 4; i++)
         *reinterpret_cast<f32x4*>(mine + (16 * m + col) * 256 + (((4 * i + g4) ^ swizzle<4>(col)) << 4)) =
             acc[i][half * (MT / 2) + m];
+    wave_lds_order();
 #pragma unroll 1
     for (int it = 0; it < BM / 8 / R; it++) {
       const int b = half * (BM / 8 / R) + it;
