@@ -361,21 +361,19 @@ __global__ __launch_bounds__(1024) void k_balance_join(BalanceArgs a, int blocks
       s += part_sum[p][c];
       n += part_cnt[p][c];
     }
-    __hip_atomic_store(&w.col[e], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(&w.cnt[e], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    w.col[e] = s;
+    w.cnt[e] = n;
   }
-  // The joined columns pass between workgroups as device-scope atomics only,
-  // which go to the point that all XCDs share; waiting for the stores before
-  // the count orders them without a fence, whose cache write-back took 8 us.
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // the workgroup's columns are released by one thread after the barrier, and
+  // acquired by the one that counts last
   __syncthreads();
   if (threadIdx.x == 0)
-    last = __hip_atomic_fetch_add(w.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+    last = __hip_atomic_fetch_add(w.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
   __syncthreads();
   if (!last) return;
   for (int i = threadIdx.x; i < a.E; i += 1024) {
-    col[i] = __hip_atomic_load(&w.col[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    cnt[i] = __hip_atomic_load(&w.cnt[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    col[i] = w.col[i];
+    cnt[i] = w.cnt[i];
   }
   if (rows) atomicAdd(&live, rows);
   __syncthreads();

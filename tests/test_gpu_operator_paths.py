@@ -143,3 +143,19 @@ def test_balance_of_many_tokens_and_experts(T, E, k, dt):
     check_balance(logits, idx, None, align=1)
     mask = torch.rand(T, generator=gen(E)) < 0.9
     check_balance(logits, idx.int(), mask)
+
+
+@pytest.mark.parametrize("T,E", [(3000, 1000), (40000, 33)])
+def test_balance_joins_the_same_columns_every_time(T, E):
+    """The second launch's workgroups hand their columns to the one that ends
+    last: two hundred calls on one workspace, other launches between them."""
+    logits = torch.randn(2, T, E, generator=gen(T)).cuda()
+    idx = logits.topk(2, 2).indices
+    ws = torch.empty(fos.fos_balance_workspace(T, E), dtype=torch.uint8, device="cuda")
+    want = [fos.fos_balance_loss(logits[i], idx[i]) for i in range(2)]
+    for i in range(2):
+        check_balance(logits[i].cpu(), idx[i].cpu(), None)
+    got = [fos.fos_balance_loss(logits[k % 2], idx[k % 2], workspace=ws) for k in range(200)]
+    for k, outs in enumerate(got):
+        for a, b in zip(outs, want[k % 2]):
+            assert torch.equal(a, b), k
