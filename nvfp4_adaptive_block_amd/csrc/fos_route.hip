@@ -9,9 +9,10 @@
 //
 // A live row without a finite or +infinite logit (all -infinity) has p = 0: it
 // counts as a token and neither adds to the loss nor gets a gradient. Masked
-// rows are not read. Counts are integers; column sums of p are binary32 within
-// a wave's rows and binary64 from there on, joined in a fixed order, so that
-// results do not depend on the order of execution.
+// rows are not read. Counts are integers; column sums of p are binary32 over at
+// most 256 rows (64 of each of four lanes) and binary64 from there on, but that a
+// workgroup's sum is rounded to binary32 once on its way to the join; the order is
+// fixed, so that results do not depend on that of execution.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -23,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 512;  // forward
 constexpr int kWaves = kThreads / 64;
+constexpr int kRows = 64;  // that a lane adds up in binary32
 constexpr int kMaxExperts = 1024;
 
 template <int DT>
@@ -248,34 +250,55 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   const int64_t per = (a.T + gridDim.x - 1) / gridDim.x;
   const int64_t t0 = per * blockIdx.x < a.T ? per * blockIdx.x : a.T, t1 = t0 + per < a.T ? t0 + per : a.T;
   __shared__ int32_t hist[64 * P];
-  __shared__ float sums[kWaves][64 * P];
+  __shared__ double sums[kWaves][64 * P];
   __shared__ int32_t live_rows;
   for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
   if (threadIdx.x == 0) live_rows = 0;
   __syncthreads();
   const Columns<P, FULL> c(a.E);
-  float acc[P][4] = {}, next[P][4];
+  float next[P][4];
   int32_t live = 0;
   int64_t t = t0 + wave * 4 + (lane >> 4);
   bool have = t < t1 && (!a.mask || a.mask[t]);
   if (have) load_row<DT, P, FULL>(a.logits, t, c, next);
-  for (int64_t base = t0 + wave * 4; base < t1; base += 4 * kWaves) {
-    float v[P][4];
+  int64_t base = t0 + wave * 4;
+  bool more = false;
+  do {
+    float acc[P][4] = {};
+    for (int n = 0; n < kRows && base < t1; n++, base += 4 * kWaves) {
+      float v[P][4];
 #pragma unroll
-    for (int i = 0; i < P; i++)
+      for (int i = 0; i < P; i++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) v[i][j] = next[i][j];
-    const bool now = have;
-    t += 4 * kWaves;
-    have = t < t1 && (!a.mask || a.mask[t]);
-    if (have) load_row<DT, P, FULL>(a.logits, t, c, next);
-    softmax(c, now, v);
-    live += now;
+        for (int j = 0; j < 4; j++) v[i][j] = next[i][j];
+      const bool now = have;
+      t += 4 * kWaves;
+      have = t < t1 && (!a.mask || a.mask[t]);
+      if (have) load_row<DT, P, FULL>(a.logits, t, c, next);
+      softmax(c, now, v);
+      live += now;
 #pragma unroll
-    for (int i = 0; i < P; i++)
+      for (int i = 0; i < P; i++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) acc[i][j] += v[i][j];
-  }
+        for (int j = 0; j < 4; j++) acc[i][j] += v[i][j];
+    }
+    // the wave's four rows of lanes; the first 16 lanes own the columns
+    auto add_up = [&](auto add) {
+#pragma unroll
+      for (int i = 0; i < P; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          acc[i][j] += __shfl_xor(acc[i][j], 16, 64);
+          acc[i][j] += __shfl_xor(acc[i][j], 32, 64);
+          if (lane < 16 && c.mine(i, j)) add(sums[wave][c.at(i) + j], (double)acc[i][j]);
+        }
+    };
+    if (more)
+      add_up([](double& to, double d) { to += d; });
+    else
+      add_up([](double& to, double d) { to = d; });
+    more = true;
+  } while (base < t1);
   // assignments: a thread takes a row's k indices
   bool bad = false;
   for (int64_t r = t0 + threadIdx.x; r < t1; r += kThreads) {
@@ -290,22 +313,13 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
     }
   }
   if (bad && a.status) atomicOr(a.status, kStatusBadIndex);
-  // the wave's four rows of lanes, then the waves in order
-#pragma unroll
-  for (int i = 0; i < P; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      acc[i][j] += __shfl_xor(acc[i][j], 16, 64);
-      acc[i][j] += __shfl_xor(acc[i][j], 32, 64);
-      if (lane < 16 && c.mine(i, j)) sums[wave][c.at(i) + j] = acc[i][j];
-    }
   if ((lane & 15) == 0 && live) atomicAdd(&live_rows, live);
   __syncthreads();
   if (gridDim.x == 1) {
     __shared__ double col[64 * P];
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
       double s = 0.0;
-      for (int w = 0; w < kWaves; w++) s += (double)sums[w][e];
+      for (int w = 0; w < kWaves; w++) s += sums[w][e];
       col[e] = s;
     }
     __syncthreads();
@@ -314,9 +328,9 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   }
   const Work w(a.work, gridDim.x, a.E);
   for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    float s = sums[0][e];
+    double s = sums[0][e];
     for (int v = 1; v < kWaves; v++) s += sums[v][e];
-    w.sums[(int64_t)blockIdx.x * a.E + e] = s;
+    w.sums[(int64_t)blockIdx.x * a.E + e] = (float)s;
     w.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
   }
   if (threadIdx.x == 0) {

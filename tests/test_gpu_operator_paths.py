@@ -4,6 +4,7 @@ has in flight, and to the join of parts of K (test_operator_paths_host.py
 asserts that they go there). GPU only."""
 from functools import lru_cache
 
+import numpy as np
 import pytest
 import torch
 
@@ -159,3 +160,17 @@ def test_balance_joins_the_same_columns_every_time(T, E):
     for k, outs in enumerate(got):
         for a, b in zip(outs, want[k % 2]):
             assert torch.equal(a, b), k
+
+
+def test_balance_sums_long_columns_in_64_bits():
+    """2^24 rows of the same two logits, all sent to the first expert: the loss is
+    2 coef p. p is off by the exponential's argument (half a step of |v|), exp, a
+    sum and a division; in binary32 are 64 additions of rows, two of lanes, and the
+    roundings of a workgroup's sum and of the loss, half a step each."""
+    T, v = 2 ** 24, 2.9
+    logits = torch.tensor([v, 0.0]).expand(T, 2).contiguous().cuda()
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    loss, counts, *_ = fos.fos_balance_loss(logits, idx, coef=0.5, align=1)
+    assert counts.tolist() == [T, 0]
+    p = 1 / (1 + np.exp(-float(np.float32(v))))
+    assert abs(float(loss) / p - 1) <= (2 * v + 8 + 2 + 64 + 2 + 2) * 2.0 ** -24
