@@ -401,7 +401,11 @@ typedef struct fos_operand {
 } fos_operand;
 
 /* What is done to a sum v before it is stored: v + bias, the activation,
- * + residual, in binary32, then one rounding to the output type. */
+ * + residual, in binary32, then one rounding to the output type. An activation
+ * is good to a few half steps of binary32 relative to its result, and as many
+ * more as its exponential's argument is large: 16 + 1.5 v^2 for gelu, 6 + 1.5 |v|
+ * for silu, 6 + 10.4 (|v| + 0.045 |v|^3) for gelu_tanh (results below 1e-36 may
+ * be 0). */
 typedef struct fos_epilogue {
     const void* bias;     /* nullable, [N] (grouped: [G, N]) of bias_dtype */
     const void* residual; /* nullable, [M, N] of the output type; may be y itself */

@@ -1,11 +1,12 @@
 """The operators around the quantizer at the edges of their ranges: values
 beside a rounding's border, scales and rows near the ends of binary32, sizes
 past a single launch. GPU only."""
+import numpy as np
 import pytest
 import torch
 
 import nvfp4_adaptive_block_amd as fos
-from operator_reference import DTYPES, decode_nvfp4, gen, random_nvfp4
+from operator_reference import DTYPES, activate, decode_nvfp4, gen, half_step, random_nvfp4
 from test_gpu_operators import check_norm, cuda, make_w
 
 pytestmark = pytest.mark.gpu
@@ -182,3 +183,32 @@ def test_product_by_group_of_scales_past_binary32(M):
         rows = slice(ends[g], ends[g + 1])
         assert_scaled(y[rows], xv[rows], sx[g].double().expand(ends[g + 1] - ends[g]), wv[g * N:(g + 1) * N],
                       sw[g].double())
+
+
+# how far an activation of v may be off, in half steps of binary32: what its
+# instructions round, and the rounding of the exponential's argument (1.5 half
+# steps of the argument, for gelu_tanh 5 more in u)
+ACTIVATION_STEPS = {"none": lambda v: 0 * v, "relu": lambda v: 0 * v, "silu": lambda v: 6 + 1.5 * v.abs(),
+                    "gelu": lambda v: 16 + 1.5 * v * v,
+                    "gelu_tanh": lambda v: 6 + 6.5 * 1.6 * (v.abs() + 0.045 * v.abs() ** 3)}
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("M,N,K", [(3, 4100, 32), (2050, 1500, 528), (150, 2051, 4208)])
+def test_activations_of_exact_values(M, N, K, out):
+    """The product of zeros and a bias: the activation of a known value, relative
+    to the result, for small results too (past 1e-36 they may be zero)."""
+    x = torch.zeros(M, K, dtype=torch.float16, device="cuda")
+    w = make_w(N, K, 1)[0]
+    v = torch.cat([torch.linspace(-12, 8, N - 60), torch.logspace(-30, 2, 30), -torch.logspace(-30, 2, 30)])
+    for act, steps in ACTIVATION_STEPS.items():
+        y = fos.fos_linear(x, w, bias=cuda(v), act=act, out_dtype=DTYPES[out]).cpu()
+        assert torch.equal(y, y[:1].expand(M, N))
+        want = activate(act, v.double())
+        if act == "gelu_tanh":  # (1 + tanh u) / 2 without its cancellation
+            want = v.double() * torch.sigmoid(2 * (2 / np.pi) ** 0.5 * (v.double() + 0.044715 * v.double() ** 3))
+        err = steps(v.double()) * 2.0 ** -24 * want.abs() + 1e-36
+        tiny = torch.finfo(DTYPES[out]).smallest_normal * torch.finfo(DTYPES[out]).eps
+        bound = err + half_step(DTYPES[out]) * (want.abs() + err) * (out != "fp32" or act != "none") + tiny
+        off = (y[0].double() - want).abs() > bound
+        assert not off.any(), (act, v[off][:4], y[0][off][:4], want[off][:4])
