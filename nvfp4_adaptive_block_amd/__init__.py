@@ -524,6 +524,16 @@ def _match(t, name: str, device, shape=None, dtype=None) -> int:
     return t.data_ptr()
 
 
+def _status_pointer(status, device):
+    """Address of the status word, if there is one: a tensor without elements has
+    none, and would be taken for no status."""
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise ValueError("status must hold a value")
+    return _match(status, "status", device, None, torch.int32)
+
+
 # The current stream's handle without a Stream object (2 us less a call) where
 # this torch has the function.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -628,7 +638,7 @@ def _linear(x, w, offs, bias, act, residual, out_dtype, out, x_gran, w_gran, wor
     else:
         _call(dev, lib.fos_linear_grouped, ctypes.byref(xo), ctypes.byref(wo),
               _match(offs, "offs", dev, (G,), torch.int32), G, M, N, K, epi, yp, out_code, work, room,
-              None if status is None else _match(status, "status", dev, None, torch.int32))
+              _status_pointer(status, dev))
     return y
 
 
@@ -733,7 +743,7 @@ def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0
           _match(loss, "loss", dev, (1,), torch.float32), _match(counts, "counts", dev, (E,), torch.int32),
           _match(offs, "offs", dev, (E,), torch.int32), _match(slope, "slope", dev, (E,), torch.float32),
           _match(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
-          None if status is None else _match(status, "status", dev, None, torch.int32))
+          _status_pointer(status, dev))
     return loss, counts, offs, slope
 
 

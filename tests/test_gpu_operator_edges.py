@@ -212,3 +212,13 @@ def test_activations_of_exact_values(M, N, K, out):
         bound = err + half_step(DTYPES[out]) * (want.abs() + err) * (out != "fp32" or act != "none") + tiny
         off = (y[0].double() - want).abs() > bound
         assert not off.any(), (act, v[off][:4], y[0][off][:4], want[off][:4])
+
+
+def test_an_empty_status_is_refused():
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    x = torch.ones(3, 32, dtype=torch.bfloat16, device="cuda")
+    w = make_w(8, 32, 1, "tensor", 1)[0]
+    with pytest.raises(ValueError, match="status"):
+        fos.fos_linear_grouped(x, w, torch.tensor([9], dtype=torch.int32, device="cuda"), status=none)
+    with pytest.raises(ValueError, match="status"):
+        fos.fos_balance_loss(x, torch.full((3, 1), 99, device="cuda"), status=none)

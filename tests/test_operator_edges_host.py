@@ -1,6 +1,7 @@
 """Arguments of the operators around the quantizer at the edges of what they
 take, on the host: every check runs before a device is touched."""
 import pytest
+import torch
 
 import nvfp4_adaptive_block_amd as fos
 from test_operators_host import C, INVALID, O, P, SHAPE, linear, operand
@@ -35,3 +36,13 @@ def test_operands_without_rows_need_no_row_scales(kw):
                                 dict(w=operand(0, 0, 0, 4, 2), N=0, y=0, G=2, offs=P(O))])
 def test_scales_that_there_are_are_needed(kw):
     assert linear(**kw) == INVALID
+
+
+def test_a_status_without_elements_is_refused():
+    host = torch.device("cpu")  # the checks are the same for any device
+    word = torch.zeros(1, dtype=torch.int32)
+    assert fos._status_pointer(None, host) is None
+    assert fos._status_pointer(word, host) == word.data_ptr()
+    for bad in (torch.zeros(0, dtype=torch.int32), torch.zeros(3, 0, dtype=torch.int32), word[:0]):
+        with pytest.raises(ValueError, match="must hold a value"):
+            fos._status_pointer(bad, host)
