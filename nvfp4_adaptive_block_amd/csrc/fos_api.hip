@@ -693,7 +693,6 @@ int run_linear(const fos_operand* x, const fos_operand* w, const int32_t* offs, 
     return fail(FOS_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld needed", (long long)(work ? work_bytes : 0), (long long)need);
   if (need > 0 && !aligned(work, 16)) return fail(FOS_ERR_ALIGN, "workspace not 16-byte aligned");
   if ((rc = check_device())) return rc;
-  if (M * N == 0) return FOS_OK;
   fos::LinearArgs a;
   memset(&a, 0, sizeof a);
   a.x = x->data;

@@ -222,3 +222,18 @@ def test_an_empty_status_is_refused():
         fos.fos_linear_grouped(x, w, torch.tensor([9], dtype=torch.int32, device="cuda"), status=none)
     with pytest.raises(ValueError, match="status"):
         fos.fos_balance_loss(x, torch.full((3, 1), 99, device="cuda"), status=none)
+
+
+@pytest.mark.parametrize("M,N", [(0, 16), (5, 0), (0, 0)])
+def test_offsets_are_reported_where_there_is_nothing_to_write(M, N):
+    G, K = 70, 32
+    x = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
+    w = (torch.zeros(G, N, K // 2, dtype=torch.uint8, device="cuda"),
+         torch.zeros(G, N, K // 16, dtype=torch.uint8, device="cuda"), torch.ones(1, device="cuda"))
+    for offs, bad in (([0] * G, False), ([0] * (G - 1) + [M], False), ([0] * 66 + [M + 1] + [M] * 3, True),
+                      ([-1] + [M] * (G - 1), True)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        assert fos.fos_linear_grouped(x, w, o, status=status).shape == (M, N)
+        assert int(status.item()) == (fos.STATUS_BAD_OFFS if bad else 0), offs
+        fos.fos_linear_grouped(x, w, o)
