@@ -504,6 +504,9 @@ def fos_quantize_grouped_fused_noalloc(x: torch.Tensor, offs: torch.Tensor, *, c
 # argument handling takes the host: these bindings pass plain integers to
 # ctypes, compare each tensor's properties once and switch devices only where
 # the current one is another.
+#
+# Like the quantizer's, their outputs are outside autograd's graph, whatever the
+# inputs require; only fos_balance_loss's loss is in it.
 
 
 def _mismatch(t, name, device, shape, dtype):
@@ -717,7 +720,18 @@ def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0
     [T, k] (int32 or int64, -1 for a dropped assignment). Returns (loss
     float32[1], counts int32[E], offs int32[E], slope float32[E]): the
     assignments per expert, the end offsets of groups padded to multiples of
-    ``align`` (what the grouped calls take), and what the backward call needs."""
+    ``align`` (what the grouped calls take), and what the backward call needs.
+
+    Where gradients are recorded and the logits require one, the loss (unless it
+    is a buffer that the caller passes) is differentiable with respect to them,
+    once, by fos_balance_loss_backward; the other outputs are constants."""
+    run = _balance_loss
+    if logits.requires_grad and loss is None and torch.is_grad_enabled():
+        run = _BalanceLoss.apply
+    return run(logits, idx, coef, mask, align, loss, counts, offs, slope, workspace, status)
+
+
+def _balance_loss(logits, idx, coef, mask, align, loss, counts, offs, slope, workspace, status):
     _need(logits, "logits")
     _need(idx, "idx")
     if logits.dim() != 2 or idx.dim() != 2 or idx.shape[0] != logits.shape[0]:
@@ -745,6 +759,25 @@ def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0
           _match(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
           _status_pointer(status, dev))
     return loss, counts, offs, slope
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, idx, coef, mask, align, loss, counts, offs, slope, workspace, status):
+        # a slope of the caller's may be written again before the backward pass
+        outs = _balance_loss(logits, idx, coef, mask, align, loss, counts, offs, None, workspace, status)
+        ctx.save_for_backward(logits, outs[3], mask)
+        if slope is not None:
+            _match(slope, "slope", logits.device, outs[3].shape, torch.float32)
+            outs = (*outs[:3], slope.copy_(outs[3]))
+        ctx.mark_non_differentiable(*outs[1:])
+        return outs
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss, *_):
+        logits, slope, mask = ctx.saved_tensors
+        return fos_balance_loss_backward(dloss.contiguous(), logits, slope, mask=mask), *(None,) * 10
 
 
 def fos_balance_workspace(T: int, E: int) -> int:

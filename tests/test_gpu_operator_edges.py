@@ -237,3 +237,80 @@ def test_offsets_are_reported_where_there_is_nothing_to_write(M, N):
         assert fos.fos_linear_grouped(x, w, o, status=status).shape == (M, N)
         assert int(status.item()) == (fos.STATUS_BAD_OFFS if bad else 0), offs
         fos.fos_linear_grouped(x, w, o)
+
+
+# ---------------------------------------------------------------- balance
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T", [0, 40, 3000])
+def test_balance_loss_is_in_the_graph_of_its_logits(dt, masked, T):
+    E = 33
+    x = torch.randn(T, 16, generator=gen(1)).cuda()
+    w = torch.randn(E, 16, generator=gen(2)).cuda().requires_grad_()
+    mask = cuda(torch.rand(T, generator=gen(3)) < 0.7) if masked else None
+    logits = (x @ w.t()).to(DTYPES[dt])
+    idx = logits.detach().float().topk(2, 1).indices
+    loss, counts, offs, slope = fos.fos_balance_loss(logits, idx, coef=0.5, mask=mask)
+    assert loss.requires_grad and not (counts.requires_grad or offs.requires_grad or slope.requires_grad)
+    with torch.no_grad():
+        plain = fos.fos_balance_loss(logits, idx, coef=0.5, mask=mask)
+    assert not plain[0].requires_grad
+    for a, b in zip((loss, counts, offs, slope), plain):
+        assert torch.equal(a.detach(), b)
+    # beside another loss of the same logits, its gradient is the explicit call's
+    other = (logits.float() ** 2).sum()
+    (other + 0.75 * loss.sum()).backward()
+    d = fos.fos_balance_loss_backward(torch.full((1,), 0.75, device="cuda"), logits.detach(), slope, mask=mask)
+    both = logits.detach().requires_grad_()
+    (both.float() ** 2).sum().backward()
+    want = ((both.grad + d).float().t() @ x) if T else torch.zeros_like(w)
+    assert (w.grad - want).abs().max() <= 4 * half_step(DTYPES[dt]) * (want.abs().max() + 1)
+    leaf = logits.detach().requires_grad_()
+    got, = torch.autograd.grad(fos.fos_balance_loss(leaf, idx, coef=0.5, mask=mask)[0], leaf,
+                               torch.full((1,), 0.75, device="cuda"))
+    assert got.dtype == leaf.dtype and torch.equal(got, d)
+
+
+def test_balance_loss_keeps_its_slope_for_the_backward_pass():
+    """The caller's buffers are written again before the first call's backward pass;
+    a loss that is such a buffer is outside the graph."""
+    logits = torch.randn(2, 50, 20, generator=gen(4)).cuda()
+    idx = logits.topk(3, 2).indices
+    slope, counts = torch.empty(20, device="cuda"), torch.empty(20, dtype=torch.int32, device="cuda")
+    leaves, losses = [logits[i].clone().requires_grad_() for i in range(2)], []
+    for leaf, i in zip(leaves, idx):
+        out = fos.fos_balance_loss(leaf, i, slope=slope, counts=counts)
+        assert out[3] is slope or out[3].data_ptr() == slope.data_ptr()
+        losses.append(out[0])
+    for leaf, loss, i in zip(leaves, losses, idx):
+        loss.backward()
+        s = fos.fos_balance_loss(leaf.detach(), i)[3]
+        one = torch.ones(1, device="cuda")
+        assert torch.equal(leaf.grad, fos.fos_balance_loss_backward(one, leaf.detach(), s))
+    assert torch.equal(slope, s)
+    buffer = torch.empty(1, device="cuda")
+    assert fos.fos_balance_loss(leaves[0], idx[0], loss=buffer)[0] is buffer and not buffer.requires_grad
+
+
+def test_balance_loss_and_its_gradient_in_a_graph():
+    T, E = 3000, 64
+    leaf = torch.randn(T, E, generator=gen(5)).cuda().requires_grad_()
+    idx = leaf.detach().topk(2, 1).indices
+    one = torch.ones(1, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss = fos.fos_balance_loss(leaf, idx)[0]
+        grad, = torch.autograd.grad(loss, leaf, one)
+    for k in range(4):
+        with torch.no_grad():
+            leaf.mul_(0.75)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        plain = leaf.detach()
+        want = fos.fos_balance_loss(plain, idx)
+        assert torch.equal(loss.detach(), want[0]), k
+        assert torch.equal(grad, fos.fos_balance_loss_backward(one, plain, want[3])), k
