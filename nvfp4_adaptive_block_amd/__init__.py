@@ -528,10 +528,8 @@ def _match(t, name: str, device, shape=None, dtype=None) -> int:
 
 
 def _status_pointer(status, device):
-    """Address of the status word, if there is one: a tensor without elements has
-    none, and would be taken for no status."""
-    if status is None:
-        return None
+    """Address of the status word. A tensor without elements has none, and would be
+    taken for no status."""
     if status.numel() < 1:
         raise ValueError("status must hold a value")
     return _match(status, "status", device, None, torch.int32)
@@ -641,7 +639,7 @@ def _linear(x, w, offs, bias, act, residual, out_dtype, out, x_gran, w_gran, wor
     else:
         _call(dev, lib.fos_linear_grouped, ctypes.byref(xo), ctypes.byref(wo),
               _match(offs, "offs", dev, (G,), torch.int32), G, M, N, K, epi, yp, out_code, work, room,
-              _status_pointer(status, dev))
+              None if status is None else _status_pointer(status, dev))
     return y
 
 
@@ -725,13 +723,8 @@ def fos_balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, coef: float = 0
     Where gradients are recorded and the logits require one, the loss (unless it
     is a buffer that the caller passes) is differentiable with respect to them,
     once, by fos_balance_loss_backward; the other outputs are constants."""
-    run = _balance_loss
     if logits.requires_grad and loss is None and torch.is_grad_enabled():
-        run = _BalanceLoss.apply
-    return run(logits, idx, coef, mask, align, loss, counts, offs, slope, workspace, status)
-
-
-def _balance_loss(logits, idx, coef, mask, align, loss, counts, offs, slope, workspace, status):
+        return _BalanceLoss.apply(logits, idx, coef, mask, align, counts, offs, slope, workspace, status)
     _need(logits, "logits")
     _need(idx, "idx")
     if logits.dim() != 2 or idx.dim() != 2 or idx.shape[0] != logits.shape[0]:
@@ -757,15 +750,16 @@ def _balance_loss(logits, idx, coef, mask, align, loss, counts, offs, slope, wor
           _match(loss, "loss", dev, (1,), torch.float32), _match(counts, "counts", dev, (E,), torch.int32),
           _match(offs, "offs", dev, (E,), torch.int32), _match(slope, "slope", dev, (E,), torch.float32),
           _match(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
-          _status_pointer(status, dev))
+          None if status is None else _status_pointer(status, dev))
     return loss, counts, offs, slope
 
 
 class _BalanceLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, idx, coef, mask, align, loss, counts, offs, slope, workspace, status):
+    def forward(ctx, logits, idx, coef, mask, align, counts, offs, slope, workspace, status):
         # a slope of the caller's may be written again before the backward pass
-        outs = _balance_loss(logits, idx, coef, mask, align, loss, counts, offs, None, workspace, status)
+        outs = fos_balance_loss(logits, idx, coef=coef, mask=mask, align=align, counts=counts, offs=offs,
+                                workspace=workspace, status=status)
         ctx.save_for_backward(logits, outs[3], mask)
         if slope is not None:
             _match(slope, "slope", logits.device, outs[3].shape, torch.float32)
@@ -777,7 +771,7 @@ class _BalanceLoss(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dloss, *_):
         logits, slope, mask = ctx.saved_tensors
-        return fos_balance_loss_backward(dloss.contiguous(), logits, slope, mask=mask), *(None,) * 10
+        return fos_balance_loss_backward(dloss.contiguous(), logits, slope, mask=mask), *(None,) * 9
 
 
 def fos_balance_workspace(T: int, E: int) -> int:
