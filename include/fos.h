@@ -449,7 +449,8 @@ int fos_linear_grouped(const fos_operand* x, const fos_operand* w, const int32_t
 
 /* Root-mean-square norm of a residual sum, with an 8-bit output: per row
  *   h = x + residual (x without one), v = weight h / sqrt(mean(h^2) + eps),
- *   s = max|v| / 448 (1 if every v is 0; at least 2^-126), q = E4M3(v / s).
+ *   s = max|v| / 448 (1 if every v is 0; at least 2^-126), q = E4M3(v / s),
+ * the quotient rounded to binary32 before.
  * The norm takes h before its rounding. K is any positive number.
  *   residual: nullable [M, K] of x's type.   weight: [K] of weight_dtype.
  *   q: uint8 [M, K];  scale: float [M]: an FOS_E4M3 operand, FOS_PER_ROW.
@@ -475,7 +476,8 @@ int fos_rmsnorm_quantize(const void* x, int dtype, int64_t M, int64_t K, const v
  *   offs:   nullable int32[E]: the running sum of c_e rounded up to multiples
  *           of `align` (>= 1), cumulative end offsets of padded groups.
  *   work:   fos_balance_workspace() bytes, 8-byte aligned, as for fos_linear.
- * A row of logits that are all -infinity has p = 0. */
+ * A row of logits that are all -infinity has p = 0. Column sums are binary64,
+ * but for up to 256 rows at a time. */
 int fos_balance_loss(const void* logits, int dtype, int64_t T, int E, const void* idx, int idx_bytes, int k,
                      const uint8_t* mask, float coef, int align, float* loss, int32_t* counts, int32_t* offs,
                      float* slope, void* work, int64_t work_bytes, int32_t* d_status, void* stream);

@@ -135,7 +135,7 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t t, const Co
 
 // v becomes its softmax; slots that are not the lane's own and rows that are
 // not live become 0. exp is the base-2 instruction: relative error about
-// |v - max| half steps. A NaN goes through exp into the sum and the whole row.
+// 1.5 |v - max| half steps. A NaN goes through exp into the sum and the whole row.
 template <int P, bool FULL>
 __device__ __forceinline__ void softmax(const Columns<P, FULL>& c, bool live, float (*v)[4]) {
   const float low = -__builtin_huge_valf();
@@ -472,7 +472,7 @@ hipError_t by_type(int dt, const BalanceArgs& a, bool backward, hipStream_t s) {
 
 // Up to 256 rows one workgroup does it all (128 x 64: 7 us, 10 with a second
 // launch; 512 x 256: 19 and 13); then 64 rows each, up to two workgroups per CU.
-// 65536 x 256 bf16, top 8: the forward pass reads 36 MB in 13 us and joins in 10
+// 65536 x 256 bf16, top 8: the forward pass reads 36 MB in 13 us and joins in 9
 // (latency), the backward pass moves 67 MB in 13 us, 5.2 TB/s, the rate of a copy.
 int balance_blocks(int64_t T, int) {
   const int64_t b = T <= 256 ? 1 : (T + 63) / 64;
