@@ -20,7 +20,7 @@
 // four sums are four neighbouring columns of one row of y.
 //
 // What bounds it: few rows, the weights' way from memory (64 experts of 2048 x
-// 7168 at decode: 297 MB in 74 us, 4.0 TB/s where a copy reaches 5.0); many
+// 7168 at decode: 297 MB in 73 us, 4.1 TB/s where a copy reaches 5.0); many
 // rows, the matrix units at the clock that the power limit leaves (8192 x 4096 x
 // 14336: 1.2 to 1.3 PFLOP/s; a loop of matrix instructions alone reaches 1.88,
 // the library's 16-bit product 1.45 to 1.53 without the decode).
@@ -267,7 +267,7 @@ __device__ __forceinline__ float gelu_tanh(float v) {
 }
 
 // One branch for all values, whose chains of instructions then run side by side
-// (8192 x 4096 x 4096 bf16 with gelu: 262 us; a branch per value took 9 more).
+// (8192 x 4096 x 4096 bf16 with gelu: a branch per value took 3 % longer).
 template <int R>
 __device__ __forceinline__ void activate(int act, f32x4 (&v)[R]) {
   auto each = [&](auto f) {
@@ -581,8 +581,8 @@ __device__ __forceinline__ uint32_t row_scales(u32x2 s, int from) {
 // are loaded four lanes to a row and turned through the wave's own LDS: a load
 // costs a cycle for every row that four consecutive lanes touch (16 x 4096 x
 // 14336: 21 us with a row per lane, 14 so). The waves' sums are joined through
-// LDS in wave order. 1 x 4096 x 14336 bf16: 10.5 us, 3.1 TB/s; 64 x 14336 x 4096:
-// 22 us.
+// LDS in wave order. 1 x 4096 x 14336 bf16: 10.2 us, 3.2 TB/s; 64 x 14336 x 4096:
+// 21 us.
 template <int XT, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 4 : 2) void k_linear_stream(LinearArgs a, int n_tiles) {
   constexpr bool BF16 = XT == kBF16, SX = XT == kXE4M3 || XT == kXNVFP4;
@@ -1078,7 +1078,7 @@ void k_linear_tile(LinearArgs a, uint32_t m_tiles, uint32_t n_tiles, int splits)
   // is R steps of four rows, as many as the registers hold (four for the third
   // workgroup of a CU); what it takes from memory is loaded one batch ahead, and
   // its rows go through each stage of the epilogue together. (1003 x 5003 x 2064
-  // with silu and a binary32 residual: 44 us, 55 with each row's stages apart.)
+  // with silu and a binary32 residual: 43 us, 55 with each row's stages apart.)
   constexpr int R = BM == 64 && XT == kFP16 ? 4 : 8;
   const Quad q(a, n0 + 4 * col);
   ColumnTail columns;
