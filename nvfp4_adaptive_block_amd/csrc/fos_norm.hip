@@ -85,7 +85,7 @@ struct Divider {
 #pragma unroll
       for (int j = 0; j < N; j++) {
         const float t0 = v[j] * inv;
-        t[j] = __builtin_fmaf(__builtin_fmaf(-t0, s, v[j]), inv, t0);
+        t[j] = __builtin_fmaf(-__builtin_fmaf(t0, s, -v[j]), inv, t0);  // (-0 stays -0)
       }
     }
 #pragma unroll

@@ -45,6 +45,17 @@ def test_norm_codes_at_the_middle_of_two(form):
         assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8)), seed
 
 
+@pytest.mark.parametrize("K", [40, 999, 40000])
+def test_norm_keeps_the_sign_of_zeros(K):
+    x = torch.randn(4, K, generator=gen(K))
+    x[:, ::3], x[:, 1::3] = -0.0, 0.0
+    x[1, 2::3] = -1e-30  # quotients that round to zero
+    x[1, 2] = 1.0
+    q, s, _ = fos.fos_rmsnorm_quantize(cuda(x), torch.ones(K, device="cuda"))
+    q = q.cpu().view(torch.uint8)
+    assert (q[:, ::3] == 0x80).all() and (q[:, 1::3] == 0).all() and (q[1, 5::3] == 0x80).all()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("K", [40, 999, 40000])
 def test_norm_rows_whose_rms_is_near_the_ends_of_binary32(dt, K):
