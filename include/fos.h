@@ -111,6 +111,7 @@ extern "C" {
 #define FOS_STATUS_BAD_OFFS 2        /* group offsets not monotone, not multiples of 16, or past M_alloc */
 #define FOS_STATUS_BARRIER_TIMEOUT 4 /* fused calls: the grid barrier did not complete in time (fos_set_barrier_poll_limit) */
 #define FOS_STATUS_BAD_INDEX 8       /* an expert index that is neither -1 nor below the number of experts */
+#define FOS_STATUS_BAD_CACHE 16      /* a length or a page number of a key/value cache out of its range */
 
 /* Bytes of the device workspace the fused calls (fos_quantize_fused,
  * fos_quantize_grouped_fused, fos_qdq_fused) need; the most groups the fused
@@ -488,6 +489,100 @@ int64_t fos_balance_workspace(int64_t T, int E);
  * forward call (counts are piecewise constant and have no gradient). */
 int fos_balance_loss_backward(const float* dloss, const void* logits, int dtype, int64_t T, int E,
                               const uint8_t* mask, const float* slope, void* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Key/value cache in NVFP4, for inference: new tokens' rows are quantized into
+ * pages, attention reads the codes, and a cache that has grown too long gives up
+ * the rows that got the least attention. Added within ABI version 6, as the
+ * operators above; the same holds for their float results (the append's codes
+ * are bitwise defined, as the quantizer's are).
+ *
+ * One side (keys or values) is a pool of pages of P rows for each of H heads; row
+ * (page, head, slot) has D values: codes uint8 [pages, H, P, D/2], block scales
+ * E4M3 [pages, H, P, D/16], S_dec float [pages, H, P], as fos_quantize writes rows
+ * with a scale each. table [B, W] holds each sequence's pages in order, lens [B]
+ * its tokens, the new ones of the call included; token i is in slot i % P of page
+ * table[b, i / P]. What lies behind a sequence's last token is never used, whatever
+ * it holds. A sequence may share pages with another where no call writes them.
+ * The tokens of a call are packed rows [T, heads, D], sequence b's are rows
+ * [offs[b-1], offs[b]) (offs[-1] = 0) and the last ones of its cache.
+ *   D is 32, 64, 96, 128, 192 or 256; P a multiple of 16; W P at most 2^30;
+ *   codes and sdec are 16-byte aligned, scales 4-byte.
+ * Found on the device, and reported in the nullable d_status: offsets that
+ * decrease or leave [0, T] (FOS_STATUS_BAD_OFFS; the rows' results are then
+ * unspecified); a length outside [0, W P], taken as the nearest that is inside, or,
+ * for the append, one below the number of new rows, and a page number that is not in [0,
+ * pages), whose keys are as if they were not there (FOS_STATUS_BAD_CACHE; reading
+ * calls report the lengths only). No access leaves the tensors. */
+typedef struct fos_kv_rows {
+    uint8_t* codes;
+    uint8_t* scales;
+    float* sdec;
+} fos_kv_rows;
+
+typedef struct fos_kv_cache {
+    fos_kv_rows k, v;
+    const int32_t* table; /* [B, W] */
+    const int32_t* lens;  /* [B] */
+    int64_t pages;        /* at least 1 */
+    int32_t B, W, H, P, D;
+} fos_kv_cache;
+
+/* Quantizes the rows k, v [T, H, D] of new tokens (bf16, fp16 or fp32; strides in
+ * elements from one token to the next, so that k and v may be parts of wider rows;
+ * 16-byte aligned rows) into the cache: row by row what fos_amax (FOS_AMAX_ROW) and
+ * fos_quantize (FOS_PER_ROW) give, bit for bit, but for S_dec of a row of zeros, which is 0.
+ * cfg is 1x16; its scale_gran is ignored. Rows at or past offs[B-1] are not
+ * read. Pages that are written must be one sequence's alone.
+ *   k_out, v_out: nullable [T, H, D] of the same type, contiguous: the values that
+ *                 the cache now holds for these rows, as fos_qdq gives them (rows
+ *                 past the last sequence: zero); may be k and v themselves. */
+int fos_kv_append(const void* k, const void* v, int dtype, int64_t T, int64_t k_stride, int64_t v_stride,
+                  const int32_t* offs, const fos_kv_cache* cache, const fos_config* cfg, void* k_out, void* v_out,
+                  int32_t* d_status, void* stream);
+
+/* Attention of the new tokens' queries over the cache (the new tokens' keys are in
+ * it: append first). q is [T, Hq, D], bf16 or fp16, Hq = G H query heads, G of them
+ * on each of the cache's; q_stride as above. For query i of sequence b's n new ones
+ *   s_j = scale q . k_j,  j < lens[b] - n + i + 1 if causal, else j < lens[b],
+ *   out = sum_j softmax_j(s) v_j in q's type,  lse = log sum_j exp(s_j).
+ * A query that sees no key, or whose every score is -infinity, and rows at or past
+ * offs[B-1], have out = 0 and lse = -infinity.
+ *   max_len: what the caller knows lens to be at most (0: W P). It shapes the
+ *            launch; results are right for longer ones too.
+ *   lse:     nullable float [T, Hq].
+ *   work:    fos_kv_attention_workspace() bytes, 16-byte aligned, as for fos_linear. */
+int fos_kv_attention(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride, const int32_t* offs,
+                     const fos_kv_cache* cache, float scale, int causal, int64_t max_len, void* out, float* lse,
+                     void* work, int64_t work_bytes, int32_t* d_status, void* stream);
+
+/* The bytes of work that fos_kv_attention needs; -1 for sizes that it refuses. */
+int64_t fos_kv_attention_workspace(int64_t T, int Hq, int64_t B, int64_t W, int H, int P, int D, int64_t max_len);
+
+/* Attention weights summed per key: acc[b, h, j] += sum of exp(s_j - lse) over the
+ * new tokens that see key j and the query heads of h, with lse of fos_kv_attention
+ * (of the same q, or of the part of its rows that is given here, the last ones of
+ * each sequence). acc: float [B, H, W P]; places at or past lens[b] are left as they
+ * are. A row whose lse is -infinity adds nothing. cache->v is not used. */
+int fos_kv_weights(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride, const int32_t* offs,
+                   const fos_kv_cache* cache, float scale, int causal, int64_t max_len, const float* lse, float* acc,
+                   int32_t* d_status, void* stream);
+
+/* Cuts sequences of n = lens[b] > budget tokens to budget tokens, each head on its
+ * own: the first `sinks` rows stay, the last `recent` rows stay, and of the rows
+ * between them the budget - sinks - recent with the largest acc (the lower index
+ * among equals; NaN is the lowest). Kept rows at or past budget - recent move, in
+ * order, to the places below it that are given up, in order; the last `recent` rows
+ * move to [budget - recent, budget) in theirs. acc [B, H, W P] moves along, and acc of
+ * [budget, n) becomes 0. Shorter sequences are left as they are. The order of the
+ * rows before the last ones is not the tokens' any more, which attention does not see.
+ *   new_lens: int32 [B], min(n, budget); not cache->lens itself.
+ *   work:     fos_kv_evict_workspace() bytes, 16-byte aligned.
+ * The pages of a sequence that is cut must be its own. One that has a page number
+ * out of range is left as it is (FOS_STATUS_BAD_CACHE, new_lens = n). */
+int fos_kv_evict(const fos_kv_cache* cache, float* acc, int budget, int sinks, int recent, int32_t* new_lens,
+                 void* work, int64_t work_bytes, int32_t* d_status, void* stream);
+int64_t fos_kv_evict_workspace(int64_t B, int H, int budget, int recent);
 
 #ifdef __cplusplus
 }

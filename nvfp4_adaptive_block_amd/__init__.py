@@ -34,6 +34,7 @@ STATUS_TILE_NONUNIFORM = 1
 STATUS_BAD_OFFS = 2
 STATUS_BARRIER_TIMEOUT = 4
 STATUS_BAD_INDEX = 8
+STATUS_BAD_CACHE = 16
 FUSED_WORKSPACE_BYTES = 16384  # FOS_FUSED_WORKSPACE_BYTES
 FUSED_MAX_GROUPS = 256  # FOS_FUSED_MAX_GROUPS
 
@@ -63,6 +64,16 @@ class _Operand(ctypes.Structure):
 class _Epilogue(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32),
                 ("activation", ctypes.c_int32)]
+
+
+class _KvRows(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("sdec", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", _KvRows), ("v", _KvRows), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("B", ctypes.c_int32), ("W", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("P", ctypes.c_int32), ("D", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -96,6 +107,12 @@ _SIGS = {
     "fos_balance_workspace": (_I64, [_I64, _I]),
     "fos_balance_loss": (_I, [_P, _I, _I64, _I, _P, _I, _I, _P, _F, _I, _P, _P, _P, _P, _P, _I64, _P, _P]),
     "fos_balance_loss_backward": (_I, [_P, _P, _I, _I64, _I, _P, _P, _P, _P]),
+    "fos_kv_append": (_I, [_P, _P, _I, _I64, _I64, _I64, _P, _P, ctypes.POINTER(_Config), _P, _P, _P, _P]),
+    "fos_kv_attention": (_I, [_P, _I, _I64, _I, _I64, _P, _P, _F, _I, _I64, _P, _P, _P, _I64, _P, _P]),
+    "fos_kv_attention_workspace": (_I64, [_I64, _I, _I64, _I64, _I, _I, _I, _I64]),
+    "fos_kv_weights": (_I, [_P, _I, _I64, _I, _I64, _P, _P, _F, _I, _I64, _P, _P, _P, _P]),
+    "fos_kv_evict": (_I, [_P, _P, _I, _I, _I, _P, _P, _I64, _P, _P]),
+    "fos_kv_evict_workspace": (_I64, [_I64, _I, _I, _I]),
 }
 EXPORTS = tuple(_SIGS)
 
@@ -799,3 +816,184 @@ def fos_balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, slope: 
           logits.data_ptr(), code, T, E, _mask_pointer(mask, T, dev),
           _match(slope, "slope", dev, (E,), torch.float32), _match(d, "out", dev, (T, E), logits.dtype))
     return d
+
+
+# ------------------------------------------------------------- key/value cache
+#
+# One side of the cache is (codes uint8[pages, H, P, D/2], scales uint8[pages, H, P,
+# D/16], sdec float32[pages, H, P]): pages of P rows for each of H heads, a row as
+# fos_quantize writes it with scale_gran="row". table int32[B, W] holds the pages of
+# each sequence in order, lens int32[B] its tokens, those of the call included, and
+# offs int32[B] the end row of each sequence's tokens among the packed ones.
+
+
+def _kv_rows(rows, name, device, shape):
+    codes, scales, sdec = rows
+    if shape is None:
+        if codes.dim() != 4:
+            raise ValueError(f"{name}'s codes must have shape ['pages', 'H', 'P', 'D / 2'], got {list(codes.shape)}")
+        shape = codes.shape
+    pages, H, P, half = shape
+    return _KvRows(_match(codes, f"{name}'s codes", device, shape, torch.uint8),
+                   _match(scales, f"{name}'s scales", device, (pages, H, P, half // 8), torch.uint8),
+                   _match(sdec, f"{name}'s sdec", device, (pages, H, P), torch.float32))
+
+
+def _kv_cache(k, v, table, lens):
+    """(_KvCache, device, B, W, H, P, D); v may be None."""
+    codes = k[0]
+    dev = codes.device
+    if not codes.is_cuda:
+        raise ValueError("the cache must be on a device")
+    kr = _kv_rows(k, "k_cache", dev, None)
+    pages, H, P, half = codes.shape
+    vr = kr if v is None else _kv_rows(v, "v_cache", dev, codes.shape)
+    if table.dim() != 2:
+        raise ValueError(f"table must have shape ['B', 'W'], got {list(table.shape)}")
+    B, W = table.shape
+    return (_KvCache(kr, vr, _match(table, "table", dev, None, torch.int32), _match(lens, "lens", dev, (B,), torch.int32),
+                     pages, B, W, H, P, 2 * half), dev, B, W, H, P, 2 * half)
+
+
+def _kv_tokens(x, name, device, heads, D):
+    """Address and token stride of [T, heads, D] rows, whose tokens may lie apart."""
+    if x.dim() != 3 or x.shape[2] != D or (heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{name} must have shape ['T', {heads or 'heads'}, {D}], got {list(x.shape)}")
+    stride = x.stride()
+    if x.device != device or (x.numel() and (stride[2] != 1 or (x.shape[1] > 1 and stride[1] != D))):
+        if x.device != device:
+            raise ValueError(f"{name} is on {x.device}, expected {device}")
+        raise ValueError(f"{name}'s tokens must be contiguous, got strides {list(stride)}")
+    return x.data_ptr(), stride[0] if x.shape[0] > 1 else x.shape[1] * D
+
+
+def fos_kv_cache(pages: int, heads: int, page: int, dim: int, device="cuda"):
+    """An empty side of a cache, (codes, scales, sdec), for `pages` pages of
+    `page` rows of `dim` values for each of `heads` heads."""
+    return (torch.zeros(pages, heads, page, dim // 2, dtype=torch.uint8, device=device),
+            torch.zeros(pages, heads, page, dim // 16, dtype=torch.uint8, device=device),
+            torch.zeros(pages, heads, page, dtype=torch.float32, device=device))
+
+
+def fos_kv_append(k: torch.Tensor, v: torch.Tensor, offs: torch.Tensor, k_cache, v_cache, table: torch.Tensor,
+                  lens: torch.Tensor, *, values: bool = False, k_out=None, v_out=None, status=None, **knobs):
+    """Quantize the rows k and v [T, H, D] of new tokens into the pages of their
+    sequences: rows [offs[b-1], offs[b]) are the last of sequence b's lens[b]
+    tokens. Tokens may lie apart (parts of a wider row). Returns (k_out, v_out),
+    what the cache then holds for these rows in k's dtype, with values=True or
+    where the outputs are passed, else None. ``knobs`` as for fos_quantize
+    (1x16 blocks, a float32 scale per row)."""
+    cache, dev, B, _, H, _, D = _kv_cache(k_cache, v_cache, table, lens)
+    kp, k_stride = _kv_tokens(k, "k", dev, H, D)
+    vp, v_stride = _kv_tokens(v, "v", dev, H, D)
+    shape, dtype = k.shape, k.dtype
+    code = _float_type(k, "k")
+    if v.shape != shape or v.dtype != dtype:
+        raise ValueError(f"v must be {dtype} {list(shape)} as k is, got {v.dtype} {list(v.shape)}")
+    if values:
+        k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
+    cfg = config(scale_gran="row", **knobs)
+    _call(dev, load_library().fos_kv_append, kp, vp, code, shape[0], k_stride, v_stride,
+          _match(offs, "offs", dev, (B,), torch.int32), ctypes.byref(cache), ctypes.byref(cfg),
+          None if k_out is None else _match(k_out, "k_out", dev, shape, dtype),
+          None if v_out is None else _match(v_out, "v_out", dev, shape, dtype),
+          None if status is None else _status_pointer(status, dev))
+    return k_out, v_out
+
+
+def _kv_queries(q, cache, dev, H, D):
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q must be bf16 or fp16, got {q.dtype}")
+    return _kv_tokens(q, "q", dev, None, D)
+
+
+def fos_kv_attention(q: torch.Tensor, offs: torch.Tensor, k_cache, v_cache, table: torch.Tensor, lens: torch.Tensor, *,
+                     scale: float | None = None, causal: bool = True, max_len: int = 0, out=None, lse=None,
+                     workspace=None, status=None):
+    """Attention of the queries q [T, Hq, D] (bf16 or fp16; Hq a multiple of the
+    cache's heads; tokens may lie apart) of the sequences' last tokens over the
+    cache, in which these tokens' keys already are. Returns (out [T, Hq, D], lse
+    float32[T, Hq]). scale defaults to D ** -0.5; causal lets a token see what
+    stands before it and itself; max_len (what the caller knows lens to be at
+    most; default: what the table holds) shapes the launch. Queries that see no
+    key, and rows past offs[-1], have out 0 and lse -inf."""
+    cache, dev, B, W, H, P, D = _kv_cache(k_cache, v_cache, table, lens)
+    qp, stride = _kv_queries(q, cache, dev, H, D)
+    shape, dtype = q.shape, q.dtype
+    T, Hq, _ = shape
+    lib = load_library()
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    if lse is None:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = lib.fos_kv_attention_workspace(T, Hq, B, W, H, P, D, max_len)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    work, room = (None, 0) if workspace is None else (_match(workspace, "workspace", dev),
+                                                      workspace.numel() * workspace.element_size())
+    _call(dev, lib.fos_kv_attention, qp, DTYPES[dtype], T, Hq, stride, _match(offs, "offs", dev, (B,), torch.int32),
+          ctypes.byref(cache), D ** -0.5 if scale is None else scale, causal, max_len,
+          _match(out, "out", dev, shape, dtype), _match(lse, "lse", dev, (T, Hq), torch.float32), work, room,
+          None if status is None else _status_pointer(status, dev))
+    return out, lse
+
+
+def fos_kv_attention_workspace(T: int, Hq: int, B: int, W: int, H: int, P: int, D: int, max_len: int = 0) -> int:
+    """Bytes of workspace of fos_kv_attention for T tokens of Hq query heads on a
+    cache of H heads, with a table [B, W] of pages of P rows of D values."""
+    need = load_library().fos_kv_attention_workspace(T, Hq, B, W, H, P, D, max_len)
+    if need < 0:
+        raise ValueError(f"unsupported sizes T={T} Hq={Hq} B={B} W={W} H={H} P={P} D={D}")
+    return need
+
+
+def fos_kv_weights(q: torch.Tensor, offs: torch.Tensor, k_cache, table: torch.Tensor, lens: torch.Tensor,
+                   lse: torch.Tensor, acc: torch.Tensor, *, scale: float | None = None, causal: bool = True,
+                   max_len: int = 0, status=None) -> torch.Tensor:
+    """Add to acc float32[B, H, W * P], per cached key, the attention weights that
+    the queries q give it, summed over the new tokens and the query heads of each
+    of the cache's; lse [T, Hq] of fos_kv_attention. q, offs and lse may be those
+    of each sequence's last tokens only. Returns acc; places at or past lens[b] are
+    left as they are."""
+    cache, dev, B, W, H, P, D = _kv_cache(k_cache, None, table, lens)
+    qp, stride = _kv_queries(q, cache, dev, H, D)
+    T, Hq, _ = q.shape
+    _call(dev, load_library().fos_kv_weights, qp, DTYPES[q.dtype], T, Hq, stride,
+          _match(offs, "offs", dev, (B,), torch.int32), ctypes.byref(cache), D ** -0.5 if scale is None else scale,
+          causal, max_len, _match(lse, "lse", dev, (T, Hq), torch.float32),
+          _match(acc, "acc", dev, (B, H, W * P), torch.float32),
+          None if status is None else _status_pointer(status, dev))
+    return acc
+
+
+def fos_kv_evict(acc: torch.Tensor, k_cache, v_cache, table: torch.Tensor, lens: torch.Tensor, budget: int, *,
+                 sinks: int = 0, recent: int = 0, new_lens=None, workspace=None, status=None) -> torch.Tensor:
+    """Cut sequences of more than `budget` tokens to that many, each head on its own:
+    the first `sinks` rows, the last `recent` rows and, of those between, the ones
+    with the largest acc float32[B, H, W * P] stay. Kept rows, and their acc, move
+    into the places that others gave up; the last rows end at the new length in
+    their order. Returns new_lens int32[B], min(lens, budget); lens itself is left."""
+    cache, dev, B, W, H, P, D = _kv_cache(k_cache, v_cache, table, lens)
+    lib = load_library()
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    if workspace is None:
+        need = lib.fos_kv_evict_workspace(B, H, budget, recent)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    work, room = (None, 0) if workspace is None else (_match(workspace, "workspace", dev),
+                                                      workspace.numel() * workspace.element_size())
+    _call(dev, lib.fos_kv_evict, ctypes.byref(cache), _match(acc, "acc", dev, (B, H, W * P), torch.float32), budget,
+          sinks, recent, _match(new_lens, "new_lens", dev, (B,), torch.int32), work, room,
+          None if status is None else _status_pointer(status, dev))
+    return new_lens
+
+
+def fos_kv_evict_workspace(B: int, H: int, budget: int, recent: int = 0) -> int:
+    """Bytes of workspace of fos_kv_evict."""
+    need = load_library().fos_kv_evict_workspace(B, H, budget, recent)
+    if need < 0:
+        raise ValueError(f"unsupported sizes B={B} H={H} budget={budget} recent={recent}")
+    return need

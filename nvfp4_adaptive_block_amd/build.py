@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfos.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("fos_api.hip", "fos_kernels.hip", "fos_linear.hip", "fos_norm.hip",
-                                            "fos_route.hip")]
+                                            "fos_route.hip", "fos_kv.hip", "fos_kv_attention.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

@@ -849,3 +849,217 @@ int fos_balance_loss_backward(const float* dloss, const void* logits, int dtype,
 }
 
 }  // extern "C"
+
+// ------------------------------------------------- key/value cache
+
+namespace {
+
+// Rows of one call, so that launches and 32-bit row numbers hold them, and the
+// places of a sequence.
+constexpr int64_t kMaxKvRows = int64_t(1) << 27, kMaxKvPlaces = int64_t(1) << 30;
+
+int check_kv_sizes(int64_t B, int64_t W, int H, int P, int D) {
+  if (B < 1 || W < 1 || H < 1 || P < 1) return fail(FOS_ERR_INVALID_ARG, "B, W, H and P must be positive");
+  if (D != 32 && D != 64 && D != 96 && D != 128 && D != 192 && D != 256)
+    return fail(FOS_ERR_SHAPE, "D must be 32, 64, 96, 128, 192 or 256, got %d", D);
+  if (P % 16) return fail(FOS_ERR_SHAPE, "P=%d is not a multiple of 16", P);
+  if (W > kMaxKvPlaces / P) return fail(FOS_ERR_SHAPE, "W*P exceeds 2^30 (W=%lld P=%d)", (long long)W, P);
+  if (B > (1 << 20) || H > (1 << 20) || B * H > (1 << 22))
+    return fail(FOS_ERR_SHAPE, "B, H at most 2^20 and B*H 2^22, got B=%lld H=%d", (long long)B, H);
+  return FOS_OK;
+}
+
+int check_kv_rows(const char* what, const fos_kv_rows& r) {
+  if (!r.codes || !r.scales || !r.sdec) return fail(FOS_ERR_INVALID_ARG, "cache: %s has a NULL pointer", what);
+  if (!aligned(r.codes, 16) || !aligned(r.sdec, 16) || !aligned(r.scales, 4))
+    return fail(FOS_ERR_ALIGN, "cache: %s's codes and sdec must be 16-byte aligned, its scales 4-byte", what);
+  return FOS_OK;
+}
+
+int check_kv_cache(const fos_kv_cache* c, bool values, fos::KvCache& to) {
+  int rc;
+  if (!c) return fail(FOS_ERR_INVALID_ARG, "cache is NULL");
+  if ((rc = check_kv_sizes(c->B, c->W, c->H, c->P, c->D))) return rc;
+  if (c->pages < 1) return fail(FOS_ERR_INVALID_ARG, "pages must be positive, got %lld", (long long)c->pages);
+  if (c->pages > kMaxElems / c->D / c->P / c->H) return fail(FOS_ERR_SHAPE, "the cache exceeds 2^40 values a side");
+  if ((rc = check_kv_rows("k", c->k)) || (values && (rc = check_kv_rows("v", c->v)))) return rc;
+  if (!c->table || !c->lens) return fail(FOS_ERR_INVALID_ARG, "cache: table and lens must be non-NULL");
+  if (!aligned(c->table, 4) || !aligned(c->lens, 4)) return fail(FOS_ERR_ALIGN, "cache: table/lens misaligned");
+  to.k = fos::KvRows{c->k.codes, c->k.scales, c->k.sdec};
+  to.v = fos::KvRows{c->v.codes, c->v.scales, c->v.sdec};
+  to.table = c->table;
+  to.lens = c->lens;
+  to.pages = c->pages;
+  to.B = c->B;
+  to.W = c->W;
+  to.H = c->H;
+  to.P = c->P;
+  to.D = c->D;
+  to.by_page = fos::fast_div((uint32_t)c->P);
+  return FOS_OK;
+}
+
+// Packed rows: T tokens of `heads` heads.
+int check_kv_tokens(const char* what, int64_t T, int64_t heads, int64_t D, int64_t stride, int bytes) {
+  if (T < 0) return fail(FOS_ERR_INVALID_ARG, "negative size T=%lld", (long long)T);
+  if (T > kMaxKvRows / heads) return fail(FOS_ERR_SHAPE, "%s: T times the heads exceeds 2^27", what);
+  if (T > 1 && (stride < heads * D || stride > kMaxElems / T))
+    return fail(FOS_ERR_SHAPE, "%s: a stride of %lld between tokens of %lld values", what, (long long)stride, (long long)(heads * D));
+  if (T > 1 && stride % (16 / bytes)) return fail(FOS_ERR_ALIGN, "%s: a stride of %lld leaves rows off the 16-byte grid", what, (long long)stride);
+  return FOS_OK;
+}
+
+int check_kv_queries(int dtype, int64_t T, int Hq, int64_t stride, int64_t B, int H, int D) {
+  int rc;
+  if (dtype != FOS_BF16 && dtype != FOS_FP16) return fail(FOS_ERR_DTYPE, "q must be bf16 or fp16, got dtype %d", dtype);
+  if (Hq < 1 || Hq % H) return fail(FOS_ERR_SHAPE, "%d query heads on %d heads of the cache", Hq, H);
+  if ((rc = check_kv_tokens("q", T, Hq, D, stride, 2))) return rc;
+  // tiles of 16 rows, as many again as there are sequences, for each head of the cache
+  if ((T * (Hq / H) / 16 + B + 1) * H >= (int64_t(1) << 24)) return fail(FOS_ERR_SHAPE, "too many rows for one launch");
+  return FOS_OK;
+}
+
+int kv_attend_args(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride, const int32_t* offs,
+                   const fos_kv_cache* cache, bool values, float scale, int causal, int64_t max_len, int32_t* d_status,
+                   fos::KvAttendArgs& a) {
+  int rc;
+  memset(&a, 0, sizeof a);
+  if ((rc = check_kv_cache(cache, values, a.c))) return rc;
+  if ((rc = check_kv_queries(dtype, T, Hq, q_stride, cache->B, cache->H, cache->D))) return rc;
+  if (!(scale >= -3e38f && scale <= 3e38f)) return fail(FOS_ERR_INVALID_ARG, "scale must be finite");
+  if (max_len < 0) return fail(FOS_ERR_INVALID_ARG, "max_len must not be negative");
+  if (T > 0 && !q) return fail(FOS_ERR_INVALID_ARG, "q is NULL");
+  if (!offs) return fail(FOS_ERR_INVALID_ARG, "offs is NULL");
+  if (!aligned(q, 16)) return fail(FOS_ERR_ALIGN, "q not 16-byte aligned");
+  if (!aligned(offs, 4) || !aligned(d_status, 4)) return fail(FOS_ERR_ALIGN, "offs/status misaligned");
+  const int64_t places = (int64_t)cache->W * cache->P;
+  a.q = q;
+  a.stride = q_stride;
+  a.offs = offs;
+  a.T = (int)T;
+  a.G = Hq / cache->H;
+  a.by_group = fos::fast_div((uint32_t)a.G);
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.causal = causal != 0;
+  a.max_len = max_len == 0 || max_len > places ? places : max_len;
+  a.splits = fos::kv_splits(T, cache->B, cache->H, a.G, cache->D, a.max_len);
+  a.status = d_status;
+  return FOS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fos_kv_append(const void* k, const void* v, int dtype, int64_t T, int64_t k_stride, int64_t v_stride,
+                  const int32_t* offs, const fos_kv_cache* cache, const fos_config* cfg, void* k_out, void* v_out,
+                  int32_t* d_status, void* stream) {
+  int rc;
+  fos::KvAppendArgs a;
+  memset(&a, 0, sizeof a);
+  if ((rc = check_dtype(dtype)) || (rc = check_cfg(cfg))) return rc;
+  if (cfg->block != FOS_BLOCK_1X16) return fail(FOS_ERR_CONFIG, "the cache holds 1x16 blocks");
+  if ((rc = check_kv_cache(cache, true, a.c))) return rc;
+  const int bytes = dtype == FOS_FP32 ? 4 : 2;
+  if ((rc = check_kv_tokens("k", T, cache->H, cache->D, k_stride, bytes))) return rc;
+  if ((rc = check_kv_tokens("v", T, cache->H, cache->D, v_stride, bytes))) return rc;
+  if (T > 0 && (!k || !v)) return fail(FOS_ERR_INVALID_ARG, "k and v must be non-NULL");
+  if (!offs) return fail(FOS_ERR_INVALID_ARG, "offs is NULL");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(FOS_ERR_ALIGN, "a tensor is not 16-byte aligned");
+  if (!aligned(offs, 4) || !aligned(d_status, 4)) return fail(FOS_ERR_ALIGN, "offs/status misaligned");
+  if ((rc = check_device())) return rc;
+  if (T == 0) return FOS_OK;
+  a.x[0] = k;
+  a.x[1] = v;
+  a.stride[0] = k_stride;
+  a.stride[1] = v_stride;
+  a.y[0] = k_out;
+  a.y[1] = v_out;
+  a.offs = offs;
+  a.T = (int)T;
+  a.by_head = fos::fast_div((uint32_t)cache->H);
+  a.recipe = cfg->recipe;
+  mode_of(cfg, a.metric, a.prec, a.order);
+  a.six_b = six_b(cfg);
+  a.status = d_status;
+  return launch_status(fos::launch_kv_append(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fos_kv_attention_workspace(int64_t T, int Hq, int64_t B, int64_t W, int H, int P, int D, int64_t max_len) {
+  if (check_kv_sizes(B, W, H, P, D) || max_len < 0) return -1;
+  if (check_kv_queries(FOS_BF16, T, Hq, (int64_t)Hq * D, B, H, D)) return -1;
+  const int64_t places = W * P;
+  const int splits = fos::kv_splits(T, (int)B, H, Hq / H, D, max_len == 0 || max_len > places ? places : max_len);
+  return fos::kv_attend_workspace(T, H, Hq / H, D, splits);
+}
+
+int fos_kv_attention(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride, const int32_t* offs,
+                     const fos_kv_cache* cache, float scale, int causal, int64_t max_len, void* out, float* lse,
+                     void* work, int64_t work_bytes, int32_t* d_status, void* stream) {
+  int rc;
+  fos::KvAttendArgs a;
+  if ((rc = kv_attend_args(q, dtype, T, Hq, q_stride, offs, cache, true, scale, causal, max_len, d_status, a))) return rc;
+  if (T > 0 && !out) return fail(FOS_ERR_INVALID_ARG, "out is NULL");
+  if (!aligned(out, 16)) return fail(FOS_ERR_ALIGN, "out not 16-byte aligned");
+  if (!aligned(lse, 4)) return fail(FOS_ERR_ALIGN, "lse misaligned");
+  const int64_t need = fos::kv_attend_workspace(T, cache->H, a.G, cache->D, a.splits);
+  if (need > 0 && (!work || work_bytes < need))
+    return fail(FOS_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld needed", (long long)(work ? work_bytes : 0), (long long)need);
+  if (need > 0 && !aligned(work, 16)) return fail(FOS_ERR_ALIGN, "workspace not 16-byte aligned");
+  if ((rc = check_device())) return rc;
+  if (T == 0) return FOS_OK;
+  a.out = out;
+  a.lse = lse;
+  a.work = work;
+  return launch_status(fos::launch_kv_attention(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+int fos_kv_weights(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride, const int32_t* offs,
+                   const fos_kv_cache* cache, float scale, int causal, int64_t max_len, const float* lse, float* acc,
+                   int32_t* d_status, void* stream) {
+  int rc;
+  fos::KvAttendArgs a;
+  if ((rc = kv_attend_args(q, dtype, T, Hq, q_stride, offs, cache, false, scale, causal, max_len, d_status, a))) return rc;
+  if ((T > 0 && !lse) || !acc) return fail(FOS_ERR_INVALID_ARG, "lse and acc must be non-NULL");
+  if (!aligned(lse, 4) || !aligned(acc, 4)) return fail(FOS_ERR_ALIGN, "lse/acc misaligned");
+  if ((rc = check_device())) return rc;
+  if (T == 0) return FOS_OK;
+  a.lse = const_cast<float*>(lse);
+  a.acc = acc;
+  return launch_status(fos::launch_kv_weights(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fos_kv_evict_workspace(int64_t B, int H, int budget, int recent) {
+  if (check_kv_sizes(B, 1, H, 16, 32)) return -1;
+  if (budget < 0 || recent < 0 || recent > budget || budget > kMaxKvPlaces) return -1;
+  return B * H * (int64_t)(budget - recent) * 8;
+}
+
+int fos_kv_evict(const fos_kv_cache* cache, float* acc, int budget, int sinks, int recent, int32_t* new_lens,
+                 void* work, int64_t work_bytes, int32_t* d_status, void* stream) {
+  int rc;
+  fos::KvEvictArgs a;
+  memset(&a, 0, sizeof a);
+  if ((rc = check_kv_cache(cache, true, a.c))) return rc;
+  if (budget < 0 || sinks < 0 || recent < 0 || budget > kMaxKvPlaces || (int64_t)sinks + recent > budget)
+    return fail(FOS_ERR_INVALID_ARG, "budget=%d must hold sinks=%d and recent=%d, none negative", budget, sinks, recent);
+  if (!acc || !new_lens) return fail(FOS_ERR_INVALID_ARG, "acc and new_lens must be non-NULL");
+  if (new_lens == cache->lens) return fail(FOS_ERR_INVALID_ARG, "new_lens must not be lens");
+  if (!aligned(acc, 4) || !aligned(new_lens, 4) || !aligned(d_status, 4)) return fail(FOS_ERR_ALIGN, "acc/new_lens/status misaligned");
+  const int64_t need = fos_kv_evict_workspace(cache->B, cache->H, budget, recent);
+  if (need > 0 && (!work || work_bytes < need))
+    return fail(FOS_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld needed", (long long)(work ? work_bytes : 0), (long long)need);
+  if (need > 0 && !aligned(work, 16)) return fail(FOS_ERR_ALIGN, "workspace not 16-byte aligned");
+  if ((rc = check_device())) return rc;
+  a.acc = acc;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.new_lens = new_lens;
+  a.moves = static_cast<int2*>(work);
+  a.status = d_status;
+  return launch_status(fos::launch_kv_evict(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,487 @@
+// fos_kv.hip: the NVFP4 key/value cache's writers: the append, which quantizes the
+// rows of new tokens into the sequences' pages, and the eviction, which keeps the
+// rows of the largest accumulated attention weight and closes the gaps.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fos_device.h"
+#include "fos_ops.h"
+#include "fos_rows.h"
+
+namespace fos {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------- append
+//
+// One lane has one block of 16 values, and the D/16 blocks of a row are
+// neighbouring lanes (2, 4, 8 or 16 of them, some idle where D/16 is no power of
+// two), so the row's amax crosses lanes by shifts and everything else stays in the
+// lane. Per row S_enc = 6B/amax and S_dec = 1/S_enc; per block both candidates are
+// encoded, decoded and compared as fos_quantize does, with the candidate's
+// multiplier by a division of its own: a table of all scales, which the quantizer
+// keeps per tensor, would be rebuilt for every row.
+
+template <int DT>
+__device__ __forceinline__ void load_block(const void* p, int64_t i, float* x) {
+  if constexpr (DT == kFP32) {
+    const u32x4* s = reinterpret_cast<const u32x4*>((const float*)p + i);
+    u32x4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = s[j];
+#pragma unroll
+    for (int j = 0; j < 16; j++) x[j] = __uint_as_float(v[j / 4][j % 4]);
+  } else {
+    const u32x4* s = reinterpret_cast<const u32x4*>((const uint16_t*)p + i);
+    const u32x4 v[2] = {s[0], s[1]};
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const uint32_t w = v[j / 4][j % 4];
+      x[2 * j] = DT == kBF16 ? bf16_lo(w) : f16_lo(w);
+      x[2 * j + 1] = DT == kBF16 ? bf16_hi(w) : f16_hi(w);
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_block(void* p, int64_t i, const float* y) {
+  if constexpr (DT == kFP32) {
+    u32x4* s = reinterpret_cast<u32x4*>((float*)p + i);
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      s[j] = u32x4{__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]), __float_as_uint(y[4 * j + 2]),
+                   __float_as_uint(y[4 * j + 3])};
+  } else {
+    u32x4* s = reinterpret_cast<u32x4*>((uint16_t*)p + i);
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      u32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        v[k] = DT == kBF16 ? pack_bf16(y[8 * j + 2 * k], y[8 * j + 2 * k + 1])
+                           : pack_f16(y[8 * j + 2 * k], y[8 * j + 2 * k + 1]);
+      s[j] = v;
+    }
+  }
+}
+
+// max |x| without the NaN elements, by the magnitudes' bits.
+__device__ __forceinline__ float amax16(const float* x) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const uint32_t m = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+    a = max(a, m <= 0x7F800000u ? m : 0u);
+  }
+  return __uint_as_float(a);
+}
+
+struct Encoded {
+  uint32_t c0, c1, scale;
+  float D;  // RN(scale S_dec)
+};
+
+// q: the block's amax over the candidate's top value.
+__device__ __forceinline__ Encoded encode(const float* x, float q, float S_enc, float S_dec) {
+  Encoded o;
+  o.scale = e4m3_code(q * S_enc);
+  const float sigma = e4m3_value(o.scale);
+  const float E = sigma == 0.0f ? 0.0f : __builtin_fminf(S_enc / sigma, kFltMax);
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) v[i] = x[i] != x[i] ? 6.0f : x[i] * E;
+  o.c0 = e2m1_pack8(v);
+  o.c1 = e2m1_pack8(v + 8);
+  o.D = sigma * S_dec;
+  return o;
+}
+
+__device__ __forceinline__ void decode(const Encoded& o, float* y) {
+  e2m1_unpack8(o.c0, y);
+  e2m1_unpack8(o.c1, y + 8);
+#pragma unroll
+  for (int i = 0; i < 16; i++) y[i] = y[i] * o.D;
+}
+
+template <int METRIC, int PREC, int ORDER>
+__device__ __forceinline__ float error16(const float* x, const float* y) {
+  float u[16];
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    float e0, e1;
+    if constexpr (PREC == kErrFP16) {
+      sub_f16x2(x[i], x[i + 1], y[i], y[i + 1], e0, e1);
+    } else {
+      e0 = x[i] - y[i];
+      e1 = x[i + 1] - y[i + 1];
+    }
+    u[i] = METRIC == kMAE ? __builtin_fabsf(e0) : e0 * e0;
+    u[i + 1] = METRIC == kMAE ? __builtin_fabsf(e1) : e1 * e1;
+  }
+  return ORDER == kOrderSeq ? seq16(u) : tree16(u);
+}
+
+// The better of the two candidates, and its values; a tie keeps map-to-6, and so
+// does a block with a NaN, whose errors compare false.
+template <int RECIPE, int METRIC, int PREC, int ORDER>
+__device__ __forceinline__ Encoded quantize16(const float* x, float S_enc, float S_dec, float* y) {
+  const float a = amax16(x);
+  const Encoded k6 = encode(x, div6(a), S_enc, S_dec);
+  decode(k6, y);
+  if constexpr (RECIPE == kNVFP4) return k6;
+  const Encoded k4 = encode(x, a * 0.25f, S_enc, S_dec);
+  float y4[16];
+  decode(k4, y4);
+  const bool four = error16<METRIC, PREC, ORDER>(x, y4) < error16<METRIC, PREC, ORDER>(x, y);
+#pragma unroll
+  for (int i = 0; i < 16; i++) y[i] = four ? y4[i] : y[i];
+  return four ? k4 : k6;
+}
+
+template <int DT, int RECIPE, int METRIC, int PREC, int ORDER>
+__global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, side = blockIdx.y;
+  const int blocks = a.c.D / 16;
+  const int sh = blocks <= 2 ? 1 : blocks <= 4 ? 2 : blocks <= 8 ? 3 : 4;  // log2 of the lanes per row
+  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * (64 >> sh);
+  const int64_t rows = (int64_t)a.T * a.c.H;
+  if (a.status && blockIdx.x == 0 && side == 0) {
+    for (int g = threadIdx.x; g < a.c.B; g += 256) {
+      const int e = a.offs[g], p = g ? a.offs[g - 1] : 0;
+      if (e < p || e > a.T) atomicOr(a.status, kStatusBadOffs);
+    }
+  }
+  if (first >= rows) return;
+  // the sequence of the wave's first token: the first whose end lies behind it
+  const int t0 = a.by_head.div((int)first);
+  int b = a.c.B;
+  for (int base = 0; base < a.c.B; base += 64) {
+    const int e = base + lane < a.c.B ? a.offs[base + lane] : INT32_MAX;
+    const unsigned long long hit = __ballot(e > t0);
+    if (hit) {
+      b = base + __ffsll(hit) - 1;
+      break;
+    }
+  }
+  const int64_t r = first + (lane >> sh);
+  const int j = lane & ((1 << sh) - 1);
+  const bool have = r < rows && j < blocks;
+  const int t = a.by_head.div((int)(r < rows ? r : rows - 1)), h = (int)(r < rows ? r : rows - 1) - t * a.c.H;
+  while (b < a.c.B && a.offs[b] <= t) b++;
+  const bool tail = b >= a.c.B;
+
+  float x[16], y[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) x[i] = 0.0f;
+  if (have && !tail) load_block<DT>(a.x[side], t * a.stride[side] + (int64_t)h * a.c.D + 16 * j, x);
+  float A = amax16(x);
+  for (int d = 1; d < 1 << sh; d <<= 1) A = __builtin_fmaxf(A, __shfl_xor(A, d, 64));
+  const float S_enc = global_encode_scale(A, a.six_b);
+  // a row of zeros has no size of its own: S_dec 0 keeps it from setting one
+  const float S_dec = A == 0.0f ? 0.0f : 1.0f / S_enc;
+  const Encoded o = quantize16<RECIPE, METRIC, PREC, ORDER>(x, S_enc, S_dec, y);
+  if (have && a.y[side]) {
+    if (tail) {
+#pragma unroll
+      for (int i = 0; i < 16; i++) y[i] = 0.0f;
+    }
+    store_block<DT>(a.y[side], r * a.c.D + 16 * j, y);
+  }
+  if (!have || tail) return;
+  int start = b ? a.offs[b - 1] : 0, end = a.offs[b];
+  if (start < 0) start = 0;
+  if (end > a.T) end = a.T;
+  const int len = a.c.lens[b];
+  const int64_t pos = (int64_t)len - (end - start) + (t - start);
+  const bool inside = pos >= 0 && pos < (int64_t)a.c.W * a.c.P;
+  int64_t page = -1;
+  int slot = 0;
+  if (inside) {
+    const int w = a.c.by_page.div((int)pos);
+    slot = (int)pos - w * a.c.P;
+    page = a.c.table[(int64_t)b * a.c.W + w];
+  }
+  if (page < 0 || page >= a.c.pages) {
+    if (a.status && j == 0) atomicOr(a.status, kStatusBadCache);
+    return;
+  }
+  const KvRows& to = side ? a.c.v : a.c.k;
+  const int64_t row = (page * a.c.H + h) * a.c.P + slot;
+  *reinterpret_cast<u32x2*>(to.codes + row * (a.c.D / 2) + 8 * j) = u32x2{o.c0, o.c1};
+  to.scales[row * blocks + j] = (uint8_t)o.scale;
+  if (j == 0) to.sdec[row] = S_dec;
+}
+
+template <int DT, int RECIPE, int METRIC, int PREC>
+void append(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
+  if (a.order == kOrderSeq)
+    k_kv_append<DT, RECIPE, METRIC, PREC, kOrderSeq><<<grid, 256, 0, s>>>(a);
+  else
+    k_kv_append<DT, RECIPE, METRIC, PREC, kOrderTree><<<grid, 256, 0, s>>>(a);
+}
+
+template <int DT>
+void append(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
+  if (a.recipe == kNVFP4) return append<DT, kNVFP4, kMSE, kErrExact>(a, grid, s);
+  if (a.metric == kMAE)
+    return a.prec == kErrFP16 ? append<DT, k4over6, kMAE, kErrFP16>(a, grid, s)
+                              : append<DT, k4over6, kMAE, kErrExact>(a, grid, s);
+  return a.prec == kErrFP16 ? append<DT, k4over6, kMSE, kErrFP16>(a, grid, s)
+                            : append<DT, k4over6, kMSE, kErrExact>(a, grid, s);
+}
+
+// ---------------------------------------------------------------- evict
+//
+// One workgroup has one head of one sequence. The weights' order is that of their
+// bits (made monotonic), so the smallest kept weight is found digit by digit from
+// the top, 11, 11 and 10 bits at a time, by histograms in LDS. Kept rows behind the
+// place where the middle of the shorter cache ends take the places before it that
+// are given up, in order; neither side of such a move is the other side of another,
+// so they run in any order. The last rows then move down together, a chunk at a
+// time, each read before it is written.
+
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+
+// Weights in order as unsigned numbers: NaN lowest, zeros alike.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);
+  return v != v ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
+}
+
+// Row of the cache at a position of sequence b.
+struct Rows {
+  const int32_t* table;
+  int64_t H;
+  int h, P;
+  FastDiv by_page;
+  __device__ __forceinline__ int64_t at(int pos) const {
+    const int w = by_page.div(pos);
+    return ((int64_t)table[w] * H + h) * P + (pos - w * P);
+  }
+};
+
+// A row's bytes: codes of both sides in pieces of 16 (the last 2 NC pieces of a
+// team's items), scales in pieces of 2, S_dec. Items of one row, in this order:
+// 2 NC code pieces, 2 NC scale pieces of 2 bytes, 2 S_dec.
+struct Piece {
+  u32x4 v;
+};
+__device__ __forceinline__ Piece read_piece(const KvCache& c, int NC, int64_t row, int i) {
+  Piece p;
+  if (i < 2 * NC) {
+    const KvRows& s = i < NC ? c.k : c.v;
+    p.v = *reinterpret_cast<const u32x4*>(s.codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC));
+  } else if (i < 4 * NC) {
+    i -= 2 * NC;
+    const KvRows& s = i < NC ? c.k : c.v;
+    p.v.x = *reinterpret_cast<const uint16_t*>(s.scales + row * (2 * NC) + 2 * (i < NC ? i : i - NC));
+  } else {
+    p.v.x = __float_as_uint(i == 4 * NC ? c.k.sdec[row] : c.v.sdec[row]);
+  }
+  return p;
+}
+__device__ __forceinline__ void write_piece(const KvCache& c, int NC, int64_t row, int i, const Piece& p) {
+  if (i < 2 * NC) {
+    const KvRows& s = i < NC ? c.k : c.v;
+    *reinterpret_cast<u32x4*>(s.codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC)) = p.v;
+  } else if (i < 4 * NC) {
+    i -= 2 * NC;
+    const KvRows& s = i < NC ? c.k : c.v;
+    *reinterpret_cast<uint16_t*>(s.scales + row * (2 * NC) + 2 * (i < NC ? i : i - NC)) = (uint16_t)p.v.x;
+  } else {
+    (i == 4 * NC ? c.k.sdec : c.v.sdec)[row] = __uint_as_float(p.v.x);
+  }
+}
+
+// The digit at `shift` of the wanted weight: counts are from the largest down.
+// Leaves how many of the digit's own are wanted in `want`, and how many there are.
+struct Digit {
+  uint32_t digit;
+  int want, of;
+};
+template <int BINS>
+__device__ Digit find_digit(const int* hist, int* share, int want) {
+  // thread t has the bins BINS - 1 - 2t and the one below
+  const int t = threadIdx.x, lane = t & 63;
+  int c0 = 0, c1 = 0;
+  if (2 * t < BINS) {
+    c0 = hist[BINS - 1 - 2 * t];
+    c1 = hist[BINS - 2 - 2 * t];
+  }
+  const int sum = wave_scan(c0 + c1);
+  if (lane == 63) share[t >> 6] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < (t >> 6); w++) before += share[w];
+  const int above = before + sum - c0 - c1;  // weights in the bins above this thread's
+  int* out = share + kWaves;
+  if (2 * t < BINS && above < want && above + c0 + c1 >= want) {
+    const bool first = above + c0 >= want;
+    out[0] = BINS - 1 - 2 * t - (first ? 0 : 1);
+    out[1] = want - above - (first ? 0 : c0);
+    out[2] = first ? c0 : c1;
+  }
+  __syncthreads();
+  return Digit{(uint32_t)out[0], out[1], out[2]};
+}
+
+__global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
+  __shared__ int hist[2048];
+  __shared__ int share[2 * kWaves + 4];
+  __shared__ int bad;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int b = blockIdx.x / a.c.H, h = blockIdx.x - b * a.c.H;
+  const int cap = a.c.W * a.c.P;
+  int n = a.c.lens[b];
+  const bool range = n < 0 || n > cap;
+  n = n < 0 ? 0 : n > cap ? cap : n;
+  const int32_t* table = a.c.table + (int64_t)b * a.c.W;
+  if (t == 0) bad = 0;
+  __syncthreads();
+  if (n > a.budget) {
+    for (int w = t; w < a.c.by_page.div(n - 1) + 1; w += kThreads)
+      if (table[w] < 0 || table[w] >= a.c.pages) bad = 1;
+  }
+  __syncthreads();
+  const bool stays = n <= a.budget || bad;
+  if (t == 0 && h == 0) {
+    a.new_lens[b] = stays ? n : a.budget;
+    if (a.status && (range || bad)) atomicOr(a.status, kStatusBadCache);
+  }
+  if (stays) return;
+
+  const int keep = a.budget - a.recent, lo = a.sinks, hi = n - a.recent;  // the middle: [lo, hi)
+  float* acc = a.acc + ((int64_t)b * a.c.H + h) * cap;
+  int2* moves = a.moves + ((int64_t)b * a.c.H + h) * keep;
+  const Rows rows{table, a.c.H, h, a.c.P, a.c.by_page};
+  int holes = 0;
+  if (keep > lo) {
+    // the smallest kept weight, and how many of its equals are kept
+    uint32_t found = 0, mask = 0;
+    Digit d{0, keep - lo, 0};
+#pragma unroll 1
+    for (int pass = 0; pass < 3; pass++) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t low = pass == 2 ? 1023u : 2047u;
+      hist[t] = 0;
+      hist[t + 1024] = 0;
+      __syncthreads();
+      for (int i = lo + t; i < hi; i += kThreads) {
+        const uint32_t o = order_of(acc[i]);
+        if ((o & mask) == found) atomicAdd(&hist[(o >> shift) & low], 1);
+      }
+      __syncthreads();
+      d = find_digit<2048>(hist, share, d.want);
+      found |= d.digit << shift;
+      mask |= low << shift;
+    }
+    // each wave has a stretch of the middle, in order
+    const int each = ((hi - lo + kWaves * 64 - 1) / (kWaves * 64)) * 64;
+    const int from = lo + wave * each, to = min(hi, from + each);
+    // equals of the smallest kept weight before this wave's (all of them are kept in most cases)
+    int equals = 0;
+    if (d.want < d.of) {
+      int c = 0;
+      for (int i = from; i < to; i += 64)
+        c += __popcll(__ballot(i + lane < to && order_of(acc[i + lane]) == found));
+      __syncthreads();
+      if (lane == 0) share[wave] = c;
+      __syncthreads();
+      for (int w = 0; w < wave; w++) equals += share[w];
+    }
+    const unsigned long long before = (1ull << lane) - 1;
+    int n_free = 0, n_moved = 0;
+#pragma unroll 1
+    for (int emit = 0; emit < 2; emit++) {
+      int eq = equals, f = 0, m = 0;
+      if (emit) {
+        __syncthreads();
+        if (lane == 0) {
+          share[wave] = n_free;
+          share[kWaves + wave] = n_moved;
+        }
+        __syncthreads();
+        for (int w = 0; w < wave; w++) {
+          f += share[w];
+          m += share[kWaves + w];
+        }
+        for (int w = 0; w < kWaves; w++) holes += share[w];
+      }
+      for (int i = from; i < to; i += 64) {
+        const int p = i + lane;
+        const uint32_t o = p < to ? order_of(acc[p]) : 0;
+        const unsigned long long same = __ballot(p < to && o == found);
+        const bool kept = p < to && (o > found || (o == found && eq + __popcll(same & before) < d.want));
+        eq += __popcll(same);
+        const unsigned long long is_free = __ballot(p < to && p < keep && !kept);
+        const unsigned long long is_moved = __ballot(kept && p >= keep);
+        if (emit) {
+          if ((is_free >> lane) & 1) moves[f + __popcll(is_free & before)].y = p;
+          if ((is_moved >> lane) & 1) moves[m + __popcll(is_moved & before)].x = p;
+        }
+        f += __popcll(is_free);
+        m += __popcll(is_moved);
+      }
+      n_free = f;
+      n_moved = m;
+    }
+    __syncthreads();
+  }
+  // teams of 16 lanes carry a row each
+  const int NC = a.c.D / 32, items = 4 * NC + 2, team = t >> 4, l16 = t & 15;
+  for (int i = team; i < holes; i += kThreads / 16) {
+    const int2 mv = moves[i];
+    const int64_t from = rows.at(mv.x), to = rows.at(mv.y);
+    for (int k = l16; k < items; k += 16) write_piece(a.c, NC, to, k, read_piece(a.c, NC, from, k));
+    if (l16 == 0) acc[mv.y] = acc[mv.x];
+  }
+  __syncthreads();
+  // the last rows: `gap` down. A chunk's rows are all read before any is written, and what
+  // a chunk writes lies below what later ones read.
+  const int gap = n - a.budget;
+  for (int i0 = 0; i0 < a.recent; i0 += kThreads / 16) {
+    const int i = keep + i0 + team;
+    Piece p[(4 * 8 + 2 + 15) / 16];
+    float w = 0.0f;
+    const bool have = i0 + team < a.recent;
+    if (have) {
+      const int64_t from = rows.at(i + gap);
+#pragma unroll
+      for (int k = 0; k < 3; k++)
+        if (l16 + 16 * k < items) p[k] = read_piece(a.c, NC, from, l16 + 16 * k);
+      if (l16 == 0) w = acc[i + gap];
+    }
+    __syncthreads();
+    if (have) {
+      const int64_t to = rows.at(i);
+#pragma unroll
+      for (int k = 0; k < 3; k++)
+        if (l16 + 16 * k < items) write_piece(a.c, NC, to, l16 + 16 * k, p[k]);
+      if (l16 == 0) acc[i] = w;
+    }
+  }
+  __syncthreads();
+  for (int i = a.budget + t; i < n; i += kThreads) acc[i] = 0.0f;
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(int dt, const KvAppendArgs& a, hipStream_t s) {
+  const int blocks = a.c.D / 16;
+  const int sh = blocks <= 2 ? 1 : blocks <= 4 ? 2 : blocks <= 8 ? 3 : 4;
+  const int64_t rows = (int64_t)a.T * a.c.H, per = 4 * (64 >> sh);
+  const dim3 grid((unsigned)((rows + per - 1) / per), 2);
+  if (dt == kBF16) append<kBF16>(a, grid, s);
+  else if (dt == kFP16) append<kFP16>(a, grid, s);
+  else append<kFP32>(a, grid, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t s) {
+  k_kv_evict<<<dim3((unsigned)(a.c.B * a.c.H)), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace fos

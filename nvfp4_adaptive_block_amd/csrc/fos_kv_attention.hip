@@ -1,0 +1,670 @@
+// fos_kv_attention.hip: attention over an NVFP4 key/value cache, and the sums of
+// its weights per cached key.
+//
+//   z_rj = scale log2(e) q_r . k_j,  o_r = sum_j 2^(z_rj - m) v_j / sum_j 2^(z_rj - m)
+//
+// A cached value is c b S with an E2M1 code c, an E4M3 block scale b and the row's
+// float32 S_dec. c b has at most 6 significant bits and lies in [2^-10, 2688], so it
+// is exact in fp16, which is what the matrix instructions take on both sides:
+//  - q in fp16 as it is; in bf16 times a power of two that brings the row's largest
+//    value to [2^14, 2^15). The 8 bits of a bf16 value are exact there down to
+//    2^-32 of the row's largest, and what is smaller is off by 2^-40 of it.
+//  - S_dec of a key multiplies the sum, in binary32.
+//  - S_dec of a value row multiplies the softmax's weight: p_rj = 2^(z_rj - m) S_j is
+//    rounded to fp16 (at most 2^-11 of its size, an eighth of what bf16 would round), and m
+//    runs along with the largest z_rj + log2 S_j, so the products that matter lie
+//    between 1/2 and 2^7 whatever the rows' sizes are. m only has to be near that maximum:
+//    log2 S is taken from the exponent bits, and m follows when it is left behind by
+//    more than kLag.
+// Sums, m and the softmax's denominator are binary32.
+//
+// Scores are computed as K Q^T: the matrix instruction leaves a query per lane and
+// four neighbouring keys in a lane's registers, which is what the second product
+// takes as its right operand (V^T P^T) if the order of the keys along the
+// contraction is the same on both sides; no lane exchanges a weight with another.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fos_device.h"
+#include "fos_ops.h"
+#include "fos_rows.h"
+
+namespace fos {
+namespace {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLowest = -kFltMax;  // m before any key
+constexpr float kLag = 6.0f;
+constexpr float kLeast = -90.0f;     // log2 S of rows without a size: 2^96 a key sums up to 2^127
+constexpr float kLn2 = 0.69314718055994531f;
+
+union Frag {
+  uint32_t u[4];
+  h8 h;
+};
+
+__device__ __forceinline__ uint32_t bits(h2 v) { return __builtin_bit_cast(uint32_t, v); }
+
+__device__ __forceinline__ f32x4 mfma16(const Frag& a, const Frag& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a.h, b.h, c, 0, 0, 0);
+}
+
+// Over the four lanes that have the same column (lane % 16).
+__device__ __forceinline__ float col_max(float v) {
+  auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float col_sum(float v) {
+  auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// Exponent of S (its floor's log2) for the running maximum; kLeast for 0.
+__device__ __forceinline__ float log2_of(float S) {
+  return __builtin_fmaxf((float)(__float_as_uint(S) >> 23) - 127.0f, kLeast);
+}
+
+// Eight codes of a dword times a block scale.
+__device__ __forceinline__ void decode8(uint32_t codes, h2 s, uint32_t* out) {
+  out[0] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 0) * s);
+  out[1] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 1) * s);
+  out[2] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 2) * s);
+  out[3] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3) * s);
+}
+
+// A quarter of a row of D = 32 NC values: 8 NC neighbouring values, NC dwords of
+// codes, and the scales of the blocks that they lie in.
+template <int NC> struct Quarter {
+  static constexpr int kScales = NC == 1 ? 1 : NC == 3 ? 2 : NC / 2;
+  uint32_t codes[NC];
+  uint32_t scales;  // kScales bytes
+
+  // the first block of quarter g
+  static __device__ __forceinline__ int block(int g) { return (g * NC) >> 1; }
+
+  __device__ __forceinline__ void load_scales(const uint8_t* row, int g) {
+    const uint8_t* p = row + block(g);
+    scales = 0;
+    if constexpr (NC == 4) {
+      scales = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (NC == 8) {
+      scales = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kScales; i++) scales |= (uint32_t)p[i] << (8 * i);
+    }
+  }
+  __device__ __forceinline__ void load_codes(const uint8_t* p) {
+    if constexpr (NC % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < NC; i += 4) {
+        const u32x4 v = reinterpret_cast<const u32x4*>(p)[i / 4];
+        codes[i] = v.x, codes[i + 1] = v.y, codes[i + 2] = v.z, codes[i + 3] = v.w;
+      }
+    } else if constexpr (NC % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < NC; i += 2) {
+        const u32x2 v = reinterpret_cast<const u32x2*>(p)[i / 2];
+        codes[i] = v.x, codes[i + 1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; i++) codes[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ void store_codes(uint8_t* p) const {
+    if constexpr (NC % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < NC; i += 4)
+        reinterpret_cast<u32x4*>(p)[i / 4] = u32x4{codes[i], codes[i + 1], codes[i + 2], codes[i + 3]};
+    } else if constexpr (NC % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < NC; i += 2) reinterpret_cast<u32x2*>(p)[i / 2] = u32x2{codes[i], codes[i + 1]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; i++) reinterpret_cast<uint32_t*>(p)[i] = codes[i];
+    }
+  }
+  // fp16 values; f[c] holds values 8c .. 8c + 7 of the quarter g
+  __device__ __forceinline__ void decode(int g, Frag* f) const {
+    h2 s[(kScales + 1) / 2 * 2];
+#pragma unroll
+    for (int i = 0; i < kScales; i += 2) {
+      const h2 p = i < 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales, 1.0f, false)
+                         : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales, 1.0f, true);
+      s[i] = __builtin_shufflevector(p, p, 0, 0);
+      s[i + 1] = __builtin_shufflevector(p, p, 1, 1);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      h2 m = s[0];
+      if constexpr (NC % 2 == 0) {
+        m = s[c / 2];
+      } else if constexpr (NC == 3) {
+        // an odd quarter starts in the middle of a block
+        const int at = ((g * NC + c) >> 1) - block(g);
+        m = at ? s[1] : s[0];
+      }
+      decode8(codes[c], m, f[c].u);
+    }
+  }
+};
+
+// The pages of one sequence and head.
+struct Pages {
+  const int32_t* table;
+  int64_t pages;
+  int H, h, P;
+  FastDiv by_page;
+  // First row of the 16 from `pos` on (a multiple of 16, so they are in one page).
+  // Where there is no such key (pos at or past len, or a page that is not one of the
+  // cache's) there = false and the row is the cache's first. Wave-uniform, and without
+  // a branch, at which the compiler would wait for all loads.
+  __device__ __forceinline__ int64_t row(int pos, int len, bool& there) const {
+    typedef __attribute__((address_space(4))) const int32_t* Const;
+    const bool inside = pos < len;
+    const int w = inside ? by_page.div(pos) : 0;
+    const int64_t page = ((Const)(const void*)table)[w];
+    there = inside && page >= 0 && page < pages;
+    return there ? (page * H + h) * P + (pos - w * P) : 0;
+  }
+};
+
+// What a wave loads of 32 keys, ahead of their use.
+template <int NC> struct Step {
+  Quarter<NC> k[2], v[2];
+  f32x4 ks[2], vs[2];
+  bool there[2];  // wave-uniform: a half's keys, but for those past the end
+
+  // Codes and the value rows' scales come with four lanes to a row, so that the
+  // wave's 64 pieces are neighbours in memory; the keys' scales and S_dec as the
+  // matrix instruction wants them.
+  template <bool VALUES>
+  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, int first, int len) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      const int64_t row = pg.row(first + 16 * u, len, there[u]);
+      k[u].load_codes(c.k.codes + row * (16 * NC) + lane * (4 * NC));
+      k[u].load_scales(c.k.scales + row * (2 * NC) + (lane & 15) * (2 * NC), g);
+      ks[u] = *reinterpret_cast<const f32x4*>(c.k.sdec + row + 4 * g);
+      if constexpr (VALUES) {
+        v[u].load_codes(c.v.codes + row * (16 * NC) + lane * (4 * NC));
+        v[u].load_scales(c.v.scales + row * (2 * NC) + (lane >> 2) * (2 * NC), lane & 3);
+        vs[u] = *reinterpret_cast<const f32x4*>(c.v.sdec + row + 4 * g);
+      }
+    }
+  }
+};
+
+// 16 x 4 pieces of a wave's LDS, a row's four pieces turned by its quad, so that the
+// lanes that an access serves together reach different banks.
+__device__ __forceinline__ int piece(int key, int part) { return key * 4 + (part ^ ((4 - (key >> 2)) & 3)); }
+
+template <int NC>
+__device__ __forceinline__ void turn_keys(uint8_t* lds, const Step<NC>& st, Frag (*f)[NC]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  wave_lds_order();
+#pragma unroll
+  for (int u = 0; u < 2; u++) st.k[u].store_codes(lds + u * 256 * NC + 4 * NC * piece(lane >> 2, lane & 3));
+  wave_lds_order();
+#pragma unroll
+  for (int u = 0; u < 2; u++) {
+    Quarter<NC> t;
+    t.load_codes(lds + u * 256 * NC + 4 * NC * piece(lane & 15, g));
+    t.scales = st.k[u].scales;
+    t.decode(g, f[u]);
+  }
+}
+
+// One row of q as fragments of quarter g; returns what undoes its power of two.
+template <int DT, int NC>
+__device__ __forceinline__ float load_q(const void* q, int64_t at, bool have, int g, Frag* f) {
+  const u32x4* p = reinterpret_cast<const u32x4*>((const uint16_t*)q + at + g * 8 * NC);
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    u32x4 v = {0, 0, 0, 0};
+    if (have) v = p[c];
+    f[c].u[0] = v.x, f[c].u[1] = v.y, f[c].u[2] = v.z, f[c].u[3] = v.w;
+  }
+  if constexpr (DT == kFP16) return 1.0f;
+  uint32_t top = 0;  // of the finite values' bits
+#pragma unroll
+  for (int c = 0; c < NC; c++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t lo = f[c].u[i] & 0x7FFFu, hi = (f[c].u[i] >> 16) & 0x7FFFu;
+      top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
+  const int e = (int)(__float_as_uint(col_max(__uint_as_float(top << 16))) >> 23);  // biased exponent of the largest
+  int up = 141 - e;  // it becomes 2^14
+  up = up > 126 ? 126 : up;
+  const float by = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+  for (int c = 0; c < NC; c++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) f[c].u[i] = pack_f16(bf16_lo(f[c].u[i]) * by, bf16_hi(f[c].u[i]) * by);
+  return __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+// Rows of a tile: r counts the sequence's new tokens and, within one, the query
+// heads of the cache's head.
+struct Row {
+  int64_t token;  // of the packed tensor
+  int head;       // of all query heads
+  int place;      // among the sequence's new tokens
+  bool have;
+};
+__device__ __forceinline__ Row row_of(const KvAttendArgs& a, const GroupTile& gt, int h, int r) {
+  Row o;
+  o.place = a.by_group.div(r);
+  o.head = h * a.G + (r - o.place * a.G);
+  o.have = o.place < gt.end - gt.start;
+  o.token = (int64_t)gt.start + (o.have ? o.place : 0);
+  return o;
+}
+
+__device__ __forceinline__ int length_of(const KvCache& c, int b) {
+  const int n = c.lens[b], cap = c.W * c.P;
+  return n < 0 ? 0 : n > cap ? cap : n;
+}
+
+// Reported by the first workgroup of a launch.
+__device__ __forceinline__ void check_cache(const KvAttendArgs& a) {
+  if (!a.status || blockIdx.x != 0 || blockIdx.y != 0) return;
+  for (int b = threadIdx.x; b < a.c.B; b += blockDim.x) {
+    const int e = a.offs[b], p = b ? a.offs[b - 1] : 0, n = a.c.lens[b];
+    if (e < p || e > a.T) atomicOr(a.status, kStatusBadOffs);
+    if (n < 0 || (int64_t)n > (int64_t)a.c.W * a.c.P) atomicOr(a.status, kStatusBadCache);
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+//
+// A workgroup has 16 rows and a part of their keys; its four waves take the part's
+// steps of 32 keys in turn, each on its own, and join in LDS at the end. Keys come
+// from memory once, a step ahead, to registers; codes of keys turn through the
+// wave's own LDS from the loads' order to the matrix instruction's, value rows are
+// decoded into it and read back transposed.
+
+template <int NC> struct StreamLds {
+  static constexpr int kRow = 64 * NC + 32;           // a value row in fp16, and a step of the banks
+  static constexpr int kKeys = 512 * NC;              // codes of 32 keys
+  static constexpr int kWave = kKeys + 32 * kRow;
+  static constexpr int kJoinRow = 32 * NC + 4;        // floats
+  static constexpr int kJoin = 4 * 16 * kJoinRow * 4 + 4 * 16 * 8;
+  static constexpr int kAll = 4 * kWave > kJoin ? 4 * kWave : kJoin;
+};
+
+template <int DT>
+__device__ __forceinline__ void store_out(void* out, int64_t i, const float* v) {  // 8 values
+  u32x4 w;
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    w[k] = DT == kBF16 ? pack_bf16(v[2 * k], v[2 * k + 1]) : pack_f16(v[2 * k], v[2 * k + 1]);
+  *reinterpret_cast<u32x4*>((uint16_t*)out + i) = w;
+}
+
+template <int DT, int NC>
+__global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs a) {
+  typedef StreamLds<NC> L;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[L::kAll];
+  constexpr int D = 32 * NC, DT16 = 2 * NC;  // tiles of 16 values
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
+  check_cache(a);
+  const int h = blockIdx.x % a.c.H, tile = blockIdx.x / a.c.H, part = blockIdx.y;
+  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 16, tile, a.G);
+  if (gt.g < 0) return;
+  const int n = gt.end - gt.start;
+  const int len = gt.g < a.c.B ? length_of(a.c, gt.g) : 0;
+  const Row row = row_of(a, gt, h, gt.tile * 16 + col);
+  // keys that this lane's row sees, and what all and any rows of the tile see
+  int limit = len, least = len, most = len;
+  if (a.causal) {
+    const int last = a.by_group.div(gt.tile * 16 + 15);
+    limit = max(0, min(len, len - n + row.place + 1));
+    least = max(0, min(len, len - n + a.by_group.div(gt.tile * 16) + 1));
+    most = max(0, min(len, len - n + last + 1));
+  }
+  if (!row.have) limit = 0;
+  const int steps = (most + 31) / 32;
+  const int each = max(4, (steps + a.splits - 1) / a.splits);
+  const int from = part * each, to = min(steps, from + each);
+
+  Frag q[NC];
+  const float undo = load_q<DT, NC>(a.q, row.token * a.stride + (int64_t)row.head * D, row.have, g, q);
+  const float qf = a.scale_log2 * undo;
+  f32x4 o[DT16];
+#pragma unroll
+  for (int t = 0; t < DT16; t++) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = kLowest, l = 0.0f;
+  uint8_t* keys = lds + wave * L::kWave;
+  uint8_t* vals = keys + L::kKeys;
+  const Pages pg{a.c.table + (int64_t)(gt.g < a.c.B ? gt.g : 0) * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
+
+  Step<NC> next;
+  int s = from + __builtin_amdgcn_readfirstlane(wave);
+  next.template load<true>(a.c, pg, 32 * s, len);
+  while (s < to) {
+    Step<NC> st = next;
+    const int first = 32 * s;
+    s += 4;
+    next.template load<true>(a.c, pg, 32 * s, len);  // past the last step: the cache's first rows, unused
+
+    Frag kf[2][NC];
+    turn_keys<NC>(keys, st, kf);
+    f32x4 sc[2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      sc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < NC; c++) sc[u] = mfma16(kf[u][c], q[c], sc[u]);
+    }
+    // value rows to fp16, zero where there is no key: a stale scale may be a NaN
+    const bool missing = first + 32 > len || !st.there[0] || !st.there[1];
+    if (missing) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+        if (!st.there[u] || first + 16 * u + (lane >> 2) >= len) st.v[u].scales = 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      Frag vf[NC];
+      st.v[u].decode(lane & 3, vf);
+#pragma unroll
+      for (int c = 0; c < NC; c++)
+        *reinterpret_cast<u32x4*>(vals + (16 * u + (lane >> 2)) * L::kRow + (lane & 3) * 16 * NC + 16 * c) =
+            u32x4{vf[c].u[0], vf[c].u[1], vf[c].u[2], vf[c].u[3]};
+    }
+    // scores to weights
+    float z[8], top = kLowest;
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) z[4 * u + i] = sc[u][i] * (st.ks[u][i] * qf);
+    const bool partly = first + 32 > least || missing;
+    if (partly) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (!st.there[u] || first + 16 * u + 4 * g + i >= limit) z[4 * u + i] = -__builtin_huge_valf();
+    }
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, z[4 * u + i] + log2_of(st.vs[u][i]));
+    top = col_max(top);
+    if (__any(top > m + kLag)) {
+      const float now = __builtin_fmaxf(m, top);
+      const float f = __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < DT16; t++) o[t] *= f;
+    }
+    Frag p;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const float e = __builtin_amdgcn_exp2f(z[i] - m);
+      l += e;
+      w[i] = e * st.vs[i / 4][i % 4];
+    }
+    if (partly) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) w[i] = z[i] == -__builtin_huge_valf() ? 0.0f : w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) p.u[i] = pack_f16(w[2 * i], w[2 * i + 1]);
+    wave_lds_order();
+#pragma unroll
+    for (int t = 0; t < DT16; t++) {
+      Frag v;
+      const uint8_t* at = vals + (4 * g + (col >> 2)) * L::kRow + 32 * t + (col & 3) * 8;
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4*)(at + 16 * u * L::kRow));
+        const u32x2 y = __builtin_bit_cast(u32x2, x);
+        v.u[2 * u] = y.x;
+        v.u[2 * u + 1] = y.y;
+      }
+      o[t] = mfma16(v, p, o[t]);
+    }
+  }
+
+  // join the waves
+  l = col_sum(l);
+  __syncthreads();
+  float* join = reinterpret_cast<float*>(lds);
+  float2* ml = reinterpret_cast<float2*>(lds + 4 * 16 * L::kJoinRow * 4);
+  if (g == 0) ml[wave * 16 + col] = float2{m, l};
+#pragma unroll
+  for (int t = 0; t < DT16; t++)
+    *reinterpret_cast<f32x4*>(join + (wave * 16 + col) * L::kJoinRow + 16 * t + 4 * g) = o[t];
+  __syncthreads();
+  const int r = threadIdx.x >> 4, piece0 = threadIdx.x & 15;
+  const Row to_row = row_of(a, gt, h, gt.tile * 16 + r);
+  if (!to_row.have) return;
+  float M = kLowest, sum = 0.0f, f[4];
+#pragma unroll
+  for (int w = 0; w < 4; w++) M = __builtin_fmaxf(M, ml[w * 16 + r].x);
+#pragma unroll
+  for (int w = 0; w < 4; w++) {
+    f[w] = __builtin_amdgcn_exp2f(ml[w * 16 + r].x - M);
+    sum += f[w] * ml[w * 16 + r].y;
+  }
+  const int64_t at = to_row.token * ((int64_t)a.c.H * a.G) + to_row.head;
+  const bool whole = a.splits == 1;
+  const float by = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+  for (int d = piece0 * 8; d < D; d += 128) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; w++) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(join + (w * 16 + r) * L::kJoinRow + d);
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] += f[w] * p[i / 4][i % 4];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] *= by;
+    if (whole) {
+      store_out<DT>(a.out, at * D + d, v);
+    } else {
+      float* po = (float*)a.work + (at * a.splits + part) * D + d;
+      *reinterpret_cast<f32x4*>(po) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(po + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  if (piece0 == 0) {
+    if (whole) {
+      if (a.lse) a.lse[at] = sum == 0.0f ? -__builtin_huge_valf() : (M + __log2f(sum)) * kLn2;
+    } else {
+      float2* pm = reinterpret_cast<float2*>((float*)a.work + (int64_t)a.T * a.c.H * a.G * a.splits * D);
+      pm[at * a.splits + part] = float2{M, sum};
+    }
+  }
+}
+
+// Joins the parts of a row: a wave per row, the parts' m and sums in its lanes.
+template <int DT, int NC>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttendArgs a) {
+  constexpr int D = 32 * NC;
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = (int64_t)a.T * a.c.H * a.G, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= rows) return;
+  const float* po = (const float*)a.work + at * a.splits * D;
+  const float2* pm = reinterpret_cast<const float2*>((const float*)a.work + rows * a.splits * D) + at * a.splits;
+  float2 ml = {kLowest, 0.0f};
+  if (lane < a.splits) ml = pm[lane];
+  float M = ml.x;
+  for (int d = 1; d < 64; d <<= 1) M = __builtin_fmaxf(M, __shfl_xor(M, d, 64));
+  const float f = __builtin_amdgcn_exp2f(ml.x - M);
+  float sum = f * ml.y;
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+  // parts without a key are nothing
+  unsigned long long live = __ballot(!(ml.y == 0.0f));
+  constexpr int kEach = (D + 63) / 64;
+  float v[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; i++) v[i] = 0.0f;
+  while (live) {
+    const int s = __ffsll(live) - 1;
+    live &= live - 1;
+    const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+#pragma unroll
+    for (int i = 0; i < kEach; i++)
+      if (lane + 64 * i < D) v[i] += w * po[(int64_t)s * D + lane + 64 * i];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; i++)
+    if (lane + 64 * i < D) {
+      const uint32_t two = DT == kBF16 ? pack_bf16(v[i] * by, 0.0f) : pack_f16(v[i] * by, 0.0f);
+      ((uint16_t*)a.out)[at * D + lane + 64 * i] = (uint16_t)two;
+    }
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -__builtin_huge_valf() : (M + __log2f(sum)) * kLn2;
+}
+
+// ---------------------------------------------------------------- weights
+//
+// A wave has 32 keys, decoded once to registers, and passes over all rows of the
+// sequence's new tokens in tiles of 16; each lane sums its keys' weights over the
+// tiles, and the sixteen columns join at the end. A key belongs to one wave, so the
+// sums are added to what is there without atomics, in an order that is always the
+// same.
+
+template <int DT, int NC>
+__global__ __launch_bounds__(256) void k_kv_weights(KvAttendArgs a) {
+  constexpr int D = 32 * NC;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * 512 * NC];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
+  check_cache(a);
+  const int h = blockIdx.x % a.c.H, b = blockIdx.x / a.c.H;
+  GroupTile gt;
+  gt.g = b;
+  gt.start = b ? a.offs[b - 1] : 0;
+  gt.end = a.offs[b];
+  gt.start = gt.start < 0 ? 0 : gt.start > a.T ? a.T : gt.start;
+  gt.end = gt.end < gt.start ? gt.start : gt.end > a.T ? a.T : gt.end;
+  gt.tile = 0;
+  const int n = gt.end - gt.start, len = length_of(a.c, b);
+  if (n == 0) return;
+  const Pages pg{a.c.table + (int64_t)b * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
+  float* acc = a.acc + ((int64_t)b * a.c.H + h) * ((int64_t)a.c.W * a.c.P);
+  for (int64_t base = (int64_t)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(wave); 32 * base < len;
+       base += (int64_t)gridDim.y * 4) {
+    const int first = 32 * (int)base;
+    Step<NC> st;
+    st.template load<false>(a.c, pg, first, len);
+    Frag kf[2][NC];
+    turn_keys<NC>(lds + wave * 512 * NC, st, kf);
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) sum[i] = 0.0f;
+    // under a causal mask the first token that sees the first key is first - (len - n)
+    int r0 = a.causal ? max(0, first - (len - n)) * a.G & ~15 : 0;
+    for (; r0 < n * a.G; r0 += 16) {
+      const Row row = row_of(a, gt, h, r0 + col);
+      Frag q[NC];
+      const float undo = load_q<DT, NC>(a.q, row.token * a.stride + (int64_t)row.head * D, row.have, g, q);
+      const float qf = a.scale_log2 * undo;
+      const float lse = row.have ? a.lse[row.token * ((int64_t)a.c.H * a.G) + row.head] : 0.0f;
+      int limit = a.causal ? min(len, len - n + row.place + 1) : len;
+      if (!row.have || lse == -__builtin_huge_valf()) limit = 0;  // such a row has no weights
+      const float ref = lse * 1.44269504088896341f;
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < NC; c++) sc = mfma16(kf[u][c], q[c], sc);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const float e = __builtin_amdgcn_exp2f(sc[i] * (st.ks[u][i] * qf) - ref);
+          sum[4 * u + i] += first + 16 * u + 4 * g + i < limit ? e : 0.0f;
+        }
+      }
+    }
+    // over the sixteen columns
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) sum[i] += __shfl_xor(sum[i], d, 64);
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+      if (st.there[u] && col < 4) {
+        const int j = first + 16 * u + 4 * g + col;
+        const float w = col == 0 ? sum[4 * u] : col == 1 ? sum[4 * u + 1] : col == 2 ? sum[4 * u + 2] : sum[4 * u + 3];
+        if (j < len) acc[j] += w;
+      }
+  }
+}
+
+template <int DT, int NC>
+hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.T * a.G;
+  const int64_t tiles = rows / 16 + a.c.B + 1;  // no fewer than the sequences' tiles and the tail's
+  k_kv_stream<DT, NC><<<dim3((unsigned)(tiles * a.c.H), (unsigned)a.splits), 256, 0, s>>>(a);
+  if (a.splits > 1) k_kv_join<DT, NC><<<dim3((unsigned)((rows * a.c.H + 3) / 4)), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int DT, int NC>
+hipError_t weights(const KvAttendArgs& a, hipStream_t s) {
+  const int64_t heads = (int64_t)a.c.B * a.c.H;
+  int64_t chunks = (a.max_len + 127) / 128;
+  chunks = chunks < 1 ? 1 : chunks > 65535 ? 65535 : chunks;
+  k_kv_weights<DT, NC><<<dim3((unsigned)heads, (unsigned)chunks), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run(bool attention, const KvAttendArgs& a, hipStream_t s) {
+  switch (a.c.D / 32) {
+    case 1: return attention ? attend<DT, 1>(a, s) : weights<DT, 1>(a, s);
+    case 2: return attention ? attend<DT, 2>(a, s) : weights<DT, 2>(a, s);
+    case 3: return attention ? attend<DT, 3>(a, s) : weights<DT, 3>(a, s);
+    case 4: return attention ? attend<DT, 4>(a, s) : weights<DT, 4>(a, s);
+    case 6: return attention ? attend<DT, 6>(a, s) : weights<DT, 6>(a, s);
+    case 8: return attention ? attend<DT, 8>(a, s) : weights<DT, 8>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+int kv_splits(int64_t T, int B, int H, int G, int D, int64_t max_len) {
+  (void)D;
+  const int64_t per = (T * G / B + 15) / 16, tiles = (per < 1 ? 1 : per) * B * H;
+  const int64_t most = (max_len + 255) / 256;  // eight steps: two a wave
+  int64_t s = 1024 / tiles;
+  if (s > most) s = most;
+  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+int64_t kv_attend_workspace(int64_t T, int H, int G, int D, int splits) {
+  return splits > 1 ? T * H * G * splits * (D + 2) * 4 : 0;
+}
+
+hipError_t launch_kv_attention(int dt, const KvAttendArgs& a, hipStream_t s) {
+  return dt == kBF16 ? run<kBF16>(true, a, s) : run<kFP16>(true, a, s);
+}
+
+hipError_t launch_kv_weights(int dt, const KvAttendArgs& a, hipStream_t s) {
+  return dt == kBF16 ? run<kBF16>(false, a, s) : run<kFP16>(false, a, s);
+}
+
+}  // namespace fos

@@ -30,6 +30,7 @@
 #include "fos_device.h"
 #include "fos_ops.h"
 #include "fos_plan.h"
+#include "fos_rows.h"
 
 namespace fos {
 namespace {
@@ -157,69 +158,6 @@ __device__ __forceinline__ f32x4 mfma(const Frag& w, const Frag& x, f32x4 c) {
 }
 
 // ---------------------------------------------------------------- groups
-
-// What a workgroup works on: rows [m0, end) of x with weight g; g < 0: no
-// such tile; g == G: the tail past the last group, which is written as zero.
-struct RowTile {
-  int64_t m0, end;
-  int g;
-};
-
-// Inclusive sum over the wave's lanes in lane order, by shifts within rows of
-// 16 lanes and two broadcasts of a row's last lane.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_add(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_scan(int v) {
-  v = dpp_add<0x111, 0xF>(v);  // row_shr:1
-  v = dpp_add<0x112, 0xF>(v);
-  v = dpp_add<0x114, 0xF>(v);
-  v = dpp_add<0x118, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15, into rows 1 and 3
-  return dpp_add<0x143, 0xC>(v);  // row_bcast:31, into rows 2 and 3
-}
-
-// Tile `t` of the rows cut into groups and each group into tiles of `rows`
-// rows, in group order, the tail last. The wave holds 64 groups' offsets at a
-// time, one per lane, and finds the tile by a running sum of the groups' tile
-// counts. Offsets are clamped to [previous, M], so a bad one sends no access out
-// of bounds. M is at most 2^30, so row and tile counts fit an int.
-__device__ RowTile find_tile(const int32_t* offs, int G, int M, int rows, int t) {
-  const int lane = threadIdx.x & 63;
-  int prev = 0, tiles = 0;  // of the groups before this batch
-  for (int base = 0; base <= G; base += 64) {
-    const int g = base + lane;
-    const bool have = g <= G;
-    int end = g < G ? offs[g] : M;
-    int start = g == 0 ? 0 : g <= G ? offs[g - 1] : M;
-    if (__ballot(have && (start < prev || end < start || end > M))) {
-      // offsets that break the contract: running maximum of the clamped ends
-      end = end > M ? M : end < prev ? prev : end;
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(end, d, 64);
-        if (lane >= d && o > end) end = o;
-      }
-      start = __shfl_up(end, 1, 64);
-      if (lane == 0) start = prev;
-    }
-    const int n = have ? (int)((uint32_t)(end - start + rows - 1) / (uint32_t)rows) : 0;
-    const int sum = wave_scan(n);
-    const unsigned long long hit = __ballot(tiles + sum > t);
-    if (hit) {
-      const int l = __ffsll(hit) - 1;
-      const int first = tiles + __builtin_amdgcn_readlane(sum - n, l);
-      RowTile r;
-      r.m0 = (int64_t)__builtin_amdgcn_readlane(start, l) + (int64_t)(t - first) * rows;
-      r.end = __builtin_amdgcn_readlane(end, l);
-      r.g = base + l;
-      return r;
-    }
-    tiles += __builtin_amdgcn_readlane(sum, 63);
-    prev = __builtin_amdgcn_readlane(end, 63);
-  }
-  return RowTile{0, 0, -1};
-}
 
 // The first wave of a launch reports offsets that break the contract.
 __device__ void check_offs(const LinearArgs& a) {
@@ -461,16 +399,6 @@ __device__ __forceinline__ GlobalBytes scalar(const uint8_t* p) {
   GlobalBytes g = (GlobalBytes)p;
   asm volatile("" : "+s"(g));
   return g;
-}
-
-// Between LDS accesses of one wave that different lanes make to the same place.
-// The hardware runs a wave's LDS operations in order; the compiler, which sees
-// one lane at a time, moves no memory access past this, and it is no instruction.
-// (A pair of wavefront fences in place of the asm made the forms of 16-bit
-// activations spill: 64 x 14336 x 4096 bf16 60 us, 21 with this.)
-__device__ __forceinline__ void wave_lds_order() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // Where the LDS tiles keep a row's 16-byte chunks. LDS serves a 16-byte read of

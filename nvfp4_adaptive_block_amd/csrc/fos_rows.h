@@ -1,0 +1,98 @@
+// fos_rows.h: rows that come in groups by cumulative end offsets, and the order of
+// a wave's own LDS accesses. Shared by the products (fos_linear.hip) and the
+// key/value cache (fos_kv.hip, fos_kv_attention.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fos {
+
+// Between LDS accesses of one wave that different lanes make to the same place.
+// The hardware runs a wave's LDS operations in order; the compiler, which sees
+// one lane at a time, moves no memory access past this, and it is no instruction.
+// (A pair of wavefront fences in place of the asm made the forms of 16-bit
+// activations spill: 64 x 14336 x 4096 bf16 60 us, 21 with this.)
+__device__ __forceinline__ void wave_lds_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A tile of a group's rows: the rows [start, end) that the group has, and the
+// tile's number among the group's. g < 0: no such tile; g == G: the tail past the
+// last group.
+struct GroupTile {
+  int start, end, g, tile;
+};
+
+// What a workgroup works on: rows [m0, end) of x with weight g; g < 0: no
+// such tile; g == G: the tail past the last group, which is written as zero.
+struct RowTile {
+  int64_t m0, end;
+  int g;
+};
+
+// Inclusive sum over the wave's lanes in lane order, by shifts within rows of
+// 16 lanes and two broadcasts of a row's last lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15, into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);  // row_bcast:31, into rows 2 and 3
+}
+
+// Tile `t` of the rows cut into groups and each group into tiles of `rows`
+// rows, in group order, the tail last. The wave holds 64 groups' offsets at a
+// time, one per lane, and finds the tile by a running sum of the groups' tile
+// counts. Offsets are clamped to [previous, M], so a bad one sends no access out
+// of bounds. Each row of a group stands for `per` rows of its tiles. M per is at
+// most 2^31 - 1 less a tile, so row and tile counts fit an int.
+__device__ __forceinline__ GroupTile find_group_tile(const int32_t* offs, int G, int M, int rows, int t, int per) {
+  const int lane = threadIdx.x & 63;
+  int prev = 0, tiles = 0;  // of the groups before this batch
+  for (int base = 0; base <= G; base += 64) {
+    const int g = base + lane;
+    const bool have = g <= G;
+    int end = g < G ? offs[g] : M;
+    int start = g == 0 ? 0 : g <= G ? offs[g - 1] : M;
+    if (__ballot(have && (start < prev || end < start || end > M))) {
+      // offsets that break the contract: running maximum of the clamped ends
+      end = end > M ? M : end < prev ? prev : end;
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(end, d, 64);
+        if (lane >= d && o > end) end = o;
+      }
+      start = __shfl_up(end, 1, 64);
+      if (lane == 0) start = prev;
+    }
+    const int n = have ? (int)((uint32_t)((end - start) * per + rows - 1) / (uint32_t)rows) : 0;
+    const int sum = wave_scan(n);
+    const unsigned long long hit = __ballot(tiles + sum > t);
+    if (hit) {
+      const int l = __ffsll(hit) - 1;
+      const int first = tiles + __builtin_amdgcn_readlane(sum - n, l);
+      GroupTile r;
+      r.start = __builtin_amdgcn_readlane(start, l);
+      r.end = __builtin_amdgcn_readlane(end, l);
+      r.g = base + l;
+      r.tile = t - first;
+      return r;
+    }
+    tiles += __builtin_amdgcn_readlane(sum, 63);
+    prev = __builtin_amdgcn_readlane(end, 63);
+  }
+  return GroupTile{0, 0, -1, 0};
+}
+
+__device__ inline RowTile find_tile(const int32_t* offs, int G, int M, int rows, int t) {
+  const GroupTile r = find_group_tile(offs, G, M, rows, t, 1);
+  return RowTile{(int64_t)r.start + (int64_t)r.tile * rows, r.end, r.g};
+}
+
+}  // namespace fos
