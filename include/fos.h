@@ -507,7 +507,7 @@ int fos_balance_loss_backward(const float* dloss, const void* logits, int dtype,
  * The tokens of a call are packed rows [T, heads, D], sequence b's are rows
  * [offs[b-1], offs[b]) (offs[-1] = 0) and the last ones of its cache.
  *   D is 32, 64, 96, 128, 192 or 256; P a multiple of 16; W P at most 2^30;
- *   codes and sdec are 16-byte aligned, scales 4-byte.
+ *   codes, scales and sdec are 16-byte aligned.
  * Found on the device, and reported in the nullable d_status: offsets that
  * decrease or leave [0, T] (FOS_STATUS_BAD_OFFS; the rows' results are then
  * unspecified); a length outside [0, W P], taken as the nearest that is inside, or,

@@ -871,8 +871,8 @@ int check_kv_sizes(int64_t B, int64_t W, int H, int P, int D) {
 
 int check_kv_rows(const char* what, const fos_kv_rows& r) {
   if (!r.codes || !r.scales || !r.sdec) return fail(FOS_ERR_INVALID_ARG, "cache: %s has a NULL pointer", what);
-  if (!aligned(r.codes, 16) || !aligned(r.sdec, 16) || !aligned(r.scales, 4))
-    return fail(FOS_ERR_ALIGN, "cache: %s's codes and sdec must be 16-byte aligned, its scales 4-byte", what);
+  if (!aligned(r.codes, 16) || !aligned(r.sdec, 16) || !aligned(r.scales, 16))
+    return fail(FOS_ERR_ALIGN, "cache: %s's codes, scales and sdec must be 16-byte aligned", what);
   return FOS_OK;
 }
 

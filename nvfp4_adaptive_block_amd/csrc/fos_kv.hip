@@ -243,6 +243,7 @@ void append(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
 // time, each read before it is written.
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kBatch = 8;  // loads of weights in flight
 
 // Weights in order as unsigned numbers: NaN lowest, zeros alike.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -262,38 +263,39 @@ struct Rows {
   }
 };
 
-// A row's bytes: codes of both sides in pieces of 16 (the last 2 NC pieces of a
-// team's items), scales in pieces of 2, S_dec. Items of one row, in this order:
-// 2 NC code pieces, 2 NC scale pieces of 2 bytes, 2 S_dec.
-struct Piece {
-  u32x4 v;
+// What a row is moved as: 2 NC pieces of 16 bytes of codes, the scales of either
+// side, either S_dec, and its weight; a lane has one of them at a time.
+template <int NC> struct Mover {
+  static constexpr int kItems = 2 * NC + 5;
+  struct __attribute__((packed, aligned(NC == 8 ? 16 : NC == 4 ? 8 : NC % 2 ? 2 : 4))) Scales {
+    uint16_t v[NC];
+  };
+  union Piece {
+    u32x4 codes;
+    Scales scales;
+    float f;
+  };
+  static __device__ __forceinline__ Piece read(const KvCache& c, const float* acc, int64_t row, int pos, int i) {
+    Piece p;
+    if (i < 2 * NC) {
+      p.codes = *reinterpret_cast<const u32x4*>((i < NC ? c.k : c.v).codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC));
+    } else if (i < 2 * NC + 2) {
+      p.scales = *reinterpret_cast<const Scales*>((i == 2 * NC ? c.k : c.v).scales + row * (2 * NC));
+    } else if (i < kItems) {
+      p.f = i == 2 * NC + 4 ? acc[pos] : (i == 2 * NC + 2 ? c.k : c.v).sdec[row];
+    }
+    return p;
+  }
+  static __device__ __forceinline__ void write(const KvCache& c, float* acc, int64_t row, int pos, int i, const Piece& p) {
+    if (i < 2 * NC) {
+      *reinterpret_cast<u32x4*>((i < NC ? c.k : c.v).codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC)) = p.codes;
+    } else if (i < 2 * NC + 2) {
+      *reinterpret_cast<Scales*>((i == 2 * NC ? c.k : c.v).scales + row * (2 * NC)) = p.scales;
+    } else if (i < kItems) {
+      (i == 2 * NC + 4 ? acc + pos : (i == 2 * NC + 2 ? c.k : c.v).sdec + row)[0] = p.f;
+    }
+  }
 };
-__device__ __forceinline__ Piece read_piece(const KvCache& c, int NC, int64_t row, int i) {
-  Piece p;
-  if (i < 2 * NC) {
-    const KvRows& s = i < NC ? c.k : c.v;
-    p.v = *reinterpret_cast<const u32x4*>(s.codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC));
-  } else if (i < 4 * NC) {
-    i -= 2 * NC;
-    const KvRows& s = i < NC ? c.k : c.v;
-    p.v.x = *reinterpret_cast<const uint16_t*>(s.scales + row * (2 * NC) + 2 * (i < NC ? i : i - NC));
-  } else {
-    p.v.x = __float_as_uint(i == 4 * NC ? c.k.sdec[row] : c.v.sdec[row]);
-  }
-  return p;
-}
-__device__ __forceinline__ void write_piece(const KvCache& c, int NC, int64_t row, int i, const Piece& p) {
-  if (i < 2 * NC) {
-    const KvRows& s = i < NC ? c.k : c.v;
-    *reinterpret_cast<u32x4*>(s.codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC)) = p.v;
-  } else if (i < 4 * NC) {
-    i -= 2 * NC;
-    const KvRows& s = i < NC ? c.k : c.v;
-    *reinterpret_cast<uint16_t*>(s.scales + row * (2 * NC) + 2 * (i < NC ? i : i - NC)) = (uint16_t)p.v.x;
-  } else {
-    (i == 4 * NC ? c.k.sdec : c.v.sdec)[row] = __uint_as_float(p.v.x);
-  }
-}
 
 // The digit at `shift` of the wanted weight: counts are from the largest down.
 // Leaves how many of the digit's own are wanted in `want`, and how many there are.
@@ -327,7 +329,9 @@ __device__ Digit find_digit(const int* hist, int* share, int want) {
   return Digit{(uint32_t)out[0], out[1], out[2]};
 }
 
+template <int NC>
 __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
+  typedef Mover<NC> M;
   __shared__ int hist[2048];
   __shared__ int share[2 * kWaves + 4];
   __shared__ int bad;
@@ -368,9 +372,15 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
       hist[t] = 0;
       hist[t + 1024] = 0;
       __syncthreads();
-      for (int i = lo + t; i < hi; i += kThreads) {
-        const uint32_t o = order_of(acc[i]);
-        if ((o & mask) == found) atomicAdd(&hist[(o >> shift) & low], 1);
+      for (int i = lo + t; i < hi; i += kBatch * kThreads) {
+        float v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; k++) v[k] = acc[min(i + k * kThreads, hi - 1)];
+#pragma unroll
+        for (int k = 0; k < kBatch; k++) {
+          const uint32_t o = order_of(v[k]);
+          if (i + k * kThreads < hi && (o & mask) == found) atomicAdd(&hist[(o >> shift) & low], 1);
+        }
       }
       __syncthreads();
       d = find_digit<2048>(hist, share, d.want);
@@ -409,57 +419,77 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
         }
         for (int w = 0; w < kWaves; w++) holes += share[w];
       }
-      for (int i = from; i < to; i += 64) {
-        const int p = i + lane;
-        const uint32_t o = p < to ? order_of(acc[p]) : 0;
-        const unsigned long long same = __ballot(p < to && o == found);
-        const bool kept = p < to && (o > found || (o == found && eq + __popcll(same & before) < d.want));
-        eq += __popcll(same);
-        const unsigned long long is_free = __ballot(p < to && p < keep && !kept);
-        const unsigned long long is_moved = __ballot(kept && p >= keep);
-        if (emit) {
-          if ((is_free >> lane) & 1) moves[f + __popcll(is_free & before)].y = p;
-          if ((is_moved >> lane) & 1) moves[m + __popcll(is_moved & before)].x = p;
+      for (int i = from; i < to; i += 64 * kBatch) {
+        float v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; k++) v[k] = acc[min(i + 64 * k + lane, hi - 1)];
+#pragma unroll
+        for (int k = 0; k < kBatch; k++) {
+          const int p = i + 64 * k + lane;
+          const uint32_t o = order_of(v[k]);
+          const unsigned long long same = __ballot(p < to && o == found);
+          const bool kept = p < to && (o > found || (o == found && eq + __popcll(same & before) < d.want));
+          eq += __popcll(same);
+          const unsigned long long is_free = __ballot(p < to && p < keep && !kept);
+          const unsigned long long is_moved = __ballot(kept && p >= keep);
+          if (emit) {
+            if ((is_free >> lane) & 1) moves[f + __popcll(is_free & before)].y = p;
+            if ((is_moved >> lane) & 1) moves[m + __popcll(is_moved & before)].x = p;
+          }
+          f += __popcll(is_free);
+          m += __popcll(is_moved);
         }
-        f += __popcll(is_free);
-        m += __popcll(is_moved);
       }
       n_free = f;
       n_moved = m;
     }
     __syncthreads();
   }
-  // teams of 16 lanes carry a row each
-  const int NC = a.c.D / 32, items = 4 * NC + 2, team = t >> 4, l16 = t & 15;
-  for (int i = team; i < holes; i += kThreads / 16) {
-    const int2 mv = moves[i];
-    const int64_t from = rows.at(mv.x), to = rows.at(mv.y);
-    for (int k = l16; k < items; k += 16) write_piece(a.c, NC, to, k, read_piece(a.c, NC, from, k));
-    if (l16 == 0) acc[mv.y] = acc[mv.x];
+  // teams of 16 lanes carry a row each, several at a time
+  constexpr int kTeams = kThreads / 16, kRounds = (M::kItems + 15) / 16, kRows = kRounds == 1 ? 8 : 4;
+  const int team = t >> 4, l16 = t & 15;
+  for (int i0 = team; i0 < holes; i0 += kRows * kTeams) {
+    int2 mv[kRows];
+    typename M::Piece p[kRows][kRounds];
+#pragma unroll
+    for (int r = 0; r < kRows; r++) mv[r] = moves[min(i0 + r * kTeams, holes - 1)];
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+      const int64_t from = rows.at(mv[r].x);
+#pragma unroll
+      for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, acc, from, mv[r].x, l16 + 16 * k);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+      const int64_t to = rows.at(mv[r].y);
+      if (i0 + r * kTeams < holes) {
+#pragma unroll
+        for (int k = 0; k < kRounds; k++) M::write(a.c, acc, to, mv[r].y, l16 + 16 * k, p[r][k]);
+      }
+    }
   }
   __syncthreads();
   // the last rows: `gap` down. A chunk's rows are all read before any is written, and what
   // a chunk writes lies below what later ones read.
   const int gap = n - a.budget;
-  for (int i0 = 0; i0 < a.recent; i0 += kThreads / 16) {
-    const int i = keep + i0 + team;
-    Piece p[(4 * 8 + 2 + 15) / 16];
-    float w = 0.0f;
-    const bool have = i0 + team < a.recent;
-    if (have) {
-      const int64_t from = rows.at(i + gap);
+  for (int i0 = 0; i0 < a.recent; i0 += kRows * kTeams) {
+    typename M::Piece p[kRows][kRounds];
 #pragma unroll
-      for (int k = 0; k < 3; k++)
-        if (l16 + 16 * k < items) p[k] = read_piece(a.c, NC, from, l16 + 16 * k);
-      if (l16 == 0) w = acc[i + gap];
+    for (int r = 0; r < kRows; r++) {
+      const int pos = keep + min(i0 + r * kTeams + team, a.recent - 1) + gap;
+      const int64_t from = rows.at(pos);
+#pragma unroll
+      for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, acc, from, pos, l16 + 16 * k);
     }
     __syncthreads();
-    if (have) {
-      const int64_t to = rows.at(i);
 #pragma unroll
-      for (int k = 0; k < 3; k++)
-        if (l16 + 16 * k < items) write_piece(a.c, NC, to, l16 + 16 * k, p[k]);
-      if (l16 == 0) acc[i] = w;
+    for (int r = 0; r < kRows; r++) {
+      const int i = i0 + r * kTeams + team;
+      const int64_t to = rows.at(keep + min(i, a.recent - 1));
+      if (i < a.recent) {
+#pragma unroll
+        for (int k = 0; k < kRounds; k++) M::write(a.c, acc, to, keep + i, l16 + 16 * k, p[r][k]);
+      }
     }
   }
   __syncthreads();
@@ -480,7 +510,15 @@ hipError_t launch_kv_append(int dt, const KvAppendArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t s) {
-  k_kv_evict<<<dim3((unsigned)(a.c.B * a.c.H)), kThreads, 0, s>>>(a);
+  const unsigned grid = (unsigned)(a.c.B * a.c.H);
+  switch (a.c.D / 32) {
+    case 1: k_kv_evict<1><<<grid, kThreads, 0, s>>>(a); break;
+    case 2: k_kv_evict<2><<<grid, kThreads, 0, s>>>(a); break;
+    case 3: k_kv_evict<3><<<grid, kThreads, 0, s>>>(a); break;
+    case 4: k_kv_evict<4><<<grid, kThreads, 0, s>>>(a); break;
+    case 6: k_kv_evict<6><<<grid, kThreads, 0, s>>>(a); break;
+    case 8: k_kv_evict<8><<<grid, kThreads, 0, s>>>(a); break;
+  }
   return hipGetLastError();
 }
 

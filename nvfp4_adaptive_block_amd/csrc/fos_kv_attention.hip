@@ -37,6 +37,7 @@ typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -44,6 +45,7 @@ constexpr float kLowest = -kFltMax;  // m before any key
 constexpr float kLag = 6.0f;
 constexpr float kLeast = -90.0f;     // log2 S of rows without a size: 2^96 a key sums up to 2^127
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kMaxParts = 256;
 
 union Frag {
   uint32_t u[4];
@@ -228,31 +230,41 @@ __device__ __forceinline__ void turn_keys(uint8_t* lds, const Step<NC>& st, Frag
   }
 }
 
-// One row of q as fragments of quarter g; returns what undoes its power of two.
-template <int DT, int NC>
-__device__ __forceinline__ float load_q(const void* q, int64_t at, bool have, int g, Frag* f) {
-  const u32x4* p = reinterpret_cast<const u32x4*>((const uint16_t*)q + at + g * 8 * NC);
+// max over the lanes that share a row of q: the four of a column, or its two halves.
+template <bool QUARTERS>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (QUARTERS) return col_max(v);
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+// One row of q as N fragments of eight values, `step` values apart from `at` on;
+// returns what undoes its power of two.
+template <int DT, int N, bool QUARTERS>
+__device__ __forceinline__ float load_q(const void* q, int64_t at, int step, bool have, Frag* f) {
+  const uint16_t* p = (const uint16_t*)q + at;
 #pragma unroll
-  for (int c = 0; c < NC; c++) {
+  for (int c = 0; c < N; c++) {
     u32x4 v = {0, 0, 0, 0};
-    if (have) v = p[c];
+    if (have) v = *reinterpret_cast<const u32x4*>(p + c * step);
     f[c].u[0] = v.x, f[c].u[1] = v.y, f[c].u[2] = v.z, f[c].u[3] = v.w;
   }
   if constexpr (DT == kFP16) return 1.0f;
   uint32_t top = 0;  // of the finite values' bits
 #pragma unroll
-  for (int c = 0; c < NC; c++)
+  for (int c = 0; c < N; c++)
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const uint32_t lo = f[c].u[i] & 0x7FFFu, hi = (f[c].u[i] >> 16) & 0x7FFFu;
       top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
     }
-  const int e = (int)(__float_as_uint(col_max(__uint_as_float(top << 16))) >> 23);  // biased exponent of the largest
+  // biased exponent of the largest
+  const int e = (int)(__float_as_uint(row_max<QUARTERS>(__uint_as_float(top << 16))) >> 23);
   int up = 141 - e;  // it becomes 2^14
   up = up > 126 ? 126 : up;
   const float by = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
-  for (int c = 0; c < NC; c++)
+  for (int c = 0; c < N; c++)
 #pragma unroll
     for (int i = 0; i < 4; i++) f[c].u[i] = pack_f16(bf16_lo(f[c].u[i]) * by, bf16_hi(f[c].u[i]) * by);
   return __uint_as_float((uint32_t)(127 - up) << 23);
@@ -343,7 +355,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
   const int from = part * each, to = min(steps, from + each);
 
   Frag q[NC];
-  const float undo = load_q<DT, NC>(a.q, row.token * a.stride + (int64_t)row.head * D, row.have, g, q);
+  const float undo = load_q<DT, NC, true>(a.q, row.token * a.stride + (int64_t)row.head * D + g * 8 * NC, 8, row.have, q);
   const float qf = a.scale_log2 * undo;
   f32x4 o[DT16];
 #pragma unroll
@@ -499,40 +511,306 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
   }
 }
 
-// Joins the parts of a row: a wave per row, the parts' m and sums in its lanes.
+// ---------------------------------------------------------------- many rows
+//
+// A workgroup has 128 rows, 32 of them to a wave, and walks over their keys 64 at a
+// time. A wave decodes 16 of the 64 keys' rows to fp16 into LDS, one step ahead of
+// their use and with the codes of the step after that on their way, and all four
+// waves read them: keys as rows, values transposed.
+
+typedef __attribute__((address_space(3))) s4* LdsS4;
+
+template <int NC> struct TileLds {
+  static constexpr int kKeys = 64;
+  // rows in bytes: sixteen neighbouring rows' pieces of 16 bytes in different banks;
+  // four neighbouring rows' pieces of 64 bytes
+  static constexpr int kK = 64 * NC + 16, kV = 64 * NC % 128 ? 64 * NC : 64 * NC + 64;
+  static constexpr int kSide = kKeys * (kK + kV);
+  static constexpr int kOut = 32 * (64 * NC + 16);  // a wave's rows of the result
+};
+
+template <int NC> struct TileStep {
+  Quarter<NC> k, v;
+  float sdec;
+  bool there;  // wave-uniform
+  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, int first, int wave, int len) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = pg.row(first + 16 * wave, len, there);
+    k.load_codes(c.k.codes + row * (16 * NC) + lane * (4 * NC));
+    k.load_scales(c.k.scales + row * (2 * NC) + (lane >> 2) * (2 * NC), lane & 3);
+    v.load_codes(c.v.codes + row * (16 * NC) + lane * (4 * NC));
+    v.load_scales(c.v.scales + row * (2 * NC) + (lane >> 2) * (2 * NC), lane & 3);
+    sdec = ((lane & 16) ? c.v.sdec : c.k.sdec)[row + (lane & 15)];
+  }
+};
+
 template <int DT, int NC>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttendArgs a) {
+__global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a) {
+  typedef TileLds<NC> L;
   constexpr int D = 32 * NC;
-  const int lane = threadIdx.x & 63;
-  const int64_t rows = (int64_t)a.T * a.c.H * a.G, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * L::kSide > 4 * L::kOut ? 2 * L::kSide : 4 * L::kOut];
+  __shared__ __attribute__((aligned(16))) float sizes[2][3][L::kKeys];  // S_dec of keys and of values, its log2
+  __shared__ int gone[2][4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  check_cache(a);
+  // the last tiles of a sequence see the most keys: they start first
+  const int tiles = gridDim.x / a.c.H;
+  const int h = blockIdx.x % a.c.H, tile = tiles - 1 - blockIdx.x / a.c.H, part = blockIdx.y;
+  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 128, tile, a.G);
+  if (gt.g < 0) return;
+  const int n = gt.end - gt.start;
+  const int len = gt.g < a.c.B ? length_of(a.c, gt.g) : 0;
+  const int r0 = gt.tile * 128 + wave * 32;
+  const Row row = row_of(a, gt, h, r0 + col);
+  int limit = len, least = len, most = len, all = len;
+  if (a.causal) {
+    limit = max(0, min(len, len - n + row.place + 1));
+    least = max(0, min(len, len - n + a.by_group.div(r0) + 1));
+    most = max(0, min(len, len - n + a.by_group.div(r0 + 31) + 1));
+    all = max(0, min(len, len - n + a.by_group.div(gt.tile * 128 + 127) + 1));
+  }
+  if (!row.have) limit = 0;
+  const int steps = (all + L::kKeys - 1) / L::kKeys;
+  const int each = max(4, (steps + a.splits - 1) / a.splits);
+  const int from = part * each, to = min(steps, from + each);
+
+  Frag q[2 * NC];
+  const float undo =
+      load_q<DT, 2 * NC, false>(a.q, row.token * a.stride + (int64_t)row.head * D + 8 * half, 16, row.have, q);
+  const float qf = a.scale_log2 * undo;
+  f32x16 o[NC];
+#pragma unroll
+  for (int t = 0; t < NC; t++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) o[t][i] = 0.0f;
+  float m = kLowest, l = 0.0f;
+  const Pages pg{a.c.table + (int64_t)(gt.g < a.c.B ? gt.g : 0) * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
+
+  TileStep<NC> st;
+  // a step's rows, decoded, to its side of the LDS
+  auto put = [&](int step) {
+    const int side = step & 1, key = 16 * wave + (lane >> 2), first = step * L::kKeys;
+    const bool none = !st.there || first + key >= len;
+    if (none) st.k.scales = st.v.scales = 0;  // a stale scale may be a NaN
+    Frag f[NC];
+    uint8_t* kp = lds + side * L::kSide + key * L::kK + (lane & 3) * 16 * NC;
+    st.k.decode(lane & 3, f);
+#pragma unroll
+    for (int c = 0; c < NC; c++) *reinterpret_cast<u32x4*>(kp + 16 * c) = u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
+    uint8_t* vp = lds + side * L::kSide + L::kKeys * L::kK + key * L::kV + (lane & 3) * 16 * NC;
+    st.v.decode(lane & 3, f);
+#pragma unroll
+    for (int c = 0; c < NC; c++) *reinterpret_cast<u32x4*>(vp + 16 * c) = u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
+    if (lane < 32) {
+      const int j = 16 * wave + (lane & 15);
+      const float S = !st.there || first + j >= len ? 0.0f : st.sdec;
+      sizes[side][lane >> 4][j] = S;
+      if (lane >= 16) sizes[side][2][j] = log2_of(S);
+      if (lane == 0) gone[side][wave] = !st.there;
+    }
+  };
+
+  if (from < to) {
+    st.load(a.c, pg, from * L::kKeys, wave, len);
+    put(from);
+    st.load(a.c, pg, (from + 1) * L::kKeys, wave, len);
+  }
+  __syncthreads();
+  for (int s = from; s < to; s++) {
+    const int side = s & 1, first = s * L::kKeys;
+    if (s + 1 < to) {
+      put(s + 1);
+      st.load(a.c, pg, (s + 2) * L::kKeys, wave, len);  // past the last step: the cache's first rows, unused
+    }
+    if (first < most) {
+      const uint8_t* kp = lds + side * L::kSide + col * L::kK + 16 * half;
+      f32x16 x[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; kb++) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) x[kb][i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2 * NC; c++) {
+          Frag f;
+          const u32x4 t = *reinterpret_cast<const u32x4*>(kp + 32 * kb * L::kK + 32 * c);
+          f.u[0] = t.x, f.u[1] = t.y, f.u[2] = t.z, f.u[3] = t.w;
+          x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.h, q[c].h, x[kb], 0, 0, 0);
+        }
+      }
+      // a lane's sixteen keys of 32: 8a + 4 half + 0..3
+      const bool partly =
+          first + L::kKeys > least || gone[side][0] || gone[side][1] || gone[side][2] || gone[side][3];
+      float top = kLowest;
+#pragma unroll
+      for (int kb = 0; kb < 2; kb++)
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          const int j = 32 * kb + 8 * b + 4 * half;
+          const f32x4 ks = *reinterpret_cast<const f32x4*>(&sizes[side][0][j]);
+          const f32x4 lv = *reinterpret_cast<const f32x4*>(&sizes[side][2][j]);
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            float z = x[kb][4 * b + i] * (ks[i] * qf);
+            if (partly && (first + j + i >= limit || gone[side][j >> 4])) z = -__builtin_huge_valf();
+            x[kb][4 * b + i] = z;
+            top = __builtin_fmaxf(top, z + lv[i]);
+          }
+        }
+      top = row_max<false>(top);
+      if (__any(top > m + kLag)) {
+        const float now = __builtin_fmaxf(m, top);
+        const float f = __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < NC; t++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) o[t][i] *= f;
+      }
+      Frag p[2][2];
+#pragma unroll
+      for (int kb = 0; kb < 2; kb++)
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          const f32x4 vs = *reinterpret_cast<const f32x4*>(&sizes[side][1][32 * kb + 8 * b + 4 * half]);
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const float e = __builtin_amdgcn_exp2f(x[kb][4 * b + i] - m);
+            l += e;
+            w[i] = e * vs[i];
+            if (partly && x[kb][4 * b + i] == -__builtin_huge_valf()) w[i] = 0.0f;
+          }
+          p[kb][b >> 1].u[2 * (b & 1)] = pack_f16(w[0], w[1]);
+          p[kb][b >> 1].u[2 * (b & 1) + 1] = pack_f16(w[2], w[3]);
+        }
+      // lanes of sixteen: which half of the keys' fours, which half of 32 values
+      const int i16 = lane & 15;
+      const uint8_t* vp = lds + side * L::kSide + L::kKeys * L::kK + (4 * half + (i16 >> 2)) * L::kV +
+                          ((lane >> 4) & 1) * 32 + (i16 & 3) * 8;
+#pragma unroll
+      for (int kb = 0; kb < 2; kb++)
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+          for (int t = 0; t < NC; t++) {
+            Frag f;
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+              const u32x2 y = __builtin_bit_cast(
+                  u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)(vp + (32 * kb + 16 * c + 8 * u) * L::kV + 64 * t)));
+              f.u[2 * u] = y.x;
+              f.u[2 * u + 1] = y.y;
+            }
+            o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.h, p[kb][c].h, o[t], 0, 0, 0);
+          }
+    }
+    __syncthreads();
+  }
+
+  const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+  l = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+  const int64_t at = row.token * ((int64_t)a.c.H * a.G) + row.head;
+  if (a.splits > 1) {
+    if (!row.have) return;
+    float* po = (float*)a.work + (at * a.splits + part) * D + 4 * half;
+#pragma unroll
+    for (int t = 0; t < NC; t++)
+#pragma unroll
+      for (int b = 0; b < 4; b++)
+        *reinterpret_cast<f32x4*>(po + 32 * t + 8 * b) = f32x4{o[t][4 * b], o[t][4 * b + 1], o[t][4 * b + 2], o[t][4 * b + 3]};
+    if (half == 0) {
+      float2* pm = reinterpret_cast<float2*>((float*)a.work + (int64_t)a.T * a.c.H * a.G * a.splits * D);
+      pm[at * a.splits + part] = float2{m, l};
+    }
+    return;
+  }
+  // the result's rows turn through the wave's own LDS to whole pieces of 16 bytes
+  const float by = l == 0.0f ? 0.0f : 1.0f / l;
+  constexpr int kRow = 64 * NC + 16;
+  uint8_t* mine = lds + wave * L::kOut;
+#pragma unroll
+  for (int t = 0; t < NC; t++)
+#pragma unroll
+    for (int b = 0; b < 4; b++) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[i] = o[t][4 * b + i] * by;
+      const u32x2 w = DT == kBF16 ? u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}
+                                  : u32x2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
+      *reinterpret_cast<u32x2*>(mine + col * kRow + 64 * t + 16 * b + 8 * half) = w;
+    }
+  wave_lds_order();
+#pragma unroll
+  for (int i = 0; i < 2 * NC; i++) {
+    const int e = i * 64 + lane, r = e / (4 * NC), piece16 = e % (4 * NC);
+    const Row to_row = row_of(a, gt, h, r0 + r);
+    if (to_row.have)
+      *reinterpret_cast<u32x4*>((uint16_t*)a.out + (to_row.token * ((int64_t)a.c.H * a.G) + to_row.head) * D + 8 * piece16) =
+          *reinterpret_cast<const u32x4*>(mine + r * kRow + 16 * piece16);
+  }
+  if (half == 0 && row.have && a.lse) a.lse[at] = l == 0.0f ? -__builtin_huge_valf() : (m + __log2f(l)) * kLn2;
+}
+
+// Joins the parts of a row. A wave has a row where there are few parts, else a
+// workgroup of four waves, each with every fourth part.
+template <int DT, int NC, int WAVES>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttendArgs a) {
+  constexpr int D = 32 * NC, kEach = (D + 63) / 64, kParts = WAVES == 1 ? 64 : kMaxParts;
+  __shared__ float share[4 * kParts];
+  __shared__ float sums[4][kEach * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t rows = (int64_t)a.T * a.c.H * a.G;
+  const int64_t at = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
   if (at >= rows) return;
   const float* po = (const float*)a.work + at * a.splits * D;
   const float2* pm = reinterpret_cast<const float2*>((const float*)a.work + rows * a.splits * D) + at * a.splits;
-  float2 ml = {kLowest, 0.0f};
-  if (lane < a.splits) ml = pm[lane];
-  float M = ml.x;
+  float2 ml[kParts / 64];
+  float M = kLowest;
+#pragma unroll
+  for (int i = 0; i < kParts / 64; i++) {
+    ml[i] = float2{kLowest, 0.0f};
+    if (lane + 64 * i < a.splits) ml[i] = pm[lane + 64 * i];
+    M = __builtin_fmaxf(M, ml[i].x);
+  }
   for (int d = 1; d < 64; d <<= 1) M = __builtin_fmaxf(M, __shfl_xor(M, d, 64));
-  const float f = __builtin_amdgcn_exp2f(ml.x - M);
-  float sum = f * ml.y;
+  float sum = 0.0f;
+  float* f = share + wave * kParts;
+#pragma unroll
+  for (int i = 0; i < kParts / 64; i++) {
+    const float e = __builtin_amdgcn_exp2f(ml[i].x - M);
+    f[lane + 64 * i] = e;
+    sum += e * ml[i].y;
+  }
+  wave_lds_order();
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
   const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-  // parts without a key are nothing
-  unsigned long long live = __ballot(!(ml.y == 0.0f));
-  constexpr int kEach = (D + 63) / 64;
   float v[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; i++) v[i] = 0.0f;
-  while (live) {
-    const int s = __ffsll(live) - 1;
-    live &= live - 1;
-    const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+  // a part without a key holds zeros
+#pragma unroll 4
+  for (int s = WAVES == 1 ? 0 : wave; s < a.splits; s += WAVES) {
 #pragma unroll
     for (int i = 0; i < kEach; i++)
-      if (lane + 64 * i < D) v[i] += w * po[(int64_t)s * D + lane + 64 * i];
+      if (D % 64 == 0 || lane + 64 * i < D) v[i] += f[s] * po[(int64_t)s * D + lane + 64 * i];
+  }
+  if constexpr (WAVES > 1) {
+#pragma unroll
+    for (int i = 0; i < kEach; i++) sums[wave][lane + 64 * i] = v[i];
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+      v[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; w++) v[i] += sums[w][lane + 64 * i];
+    }
   }
 #pragma unroll
   for (int i = 0; i < kEach; i++)
-    if (lane + 64 * i < D) {
+    if (D % 64 == 0 || lane + 64 * i < D) {
       const uint32_t two = DT == kBF16 ? pack_bf16(v[i] * by, 0.0f) : pack_f16(v[i] * by, 0.0f);
       ((uint16_t*)a.out)[at * D + lane + 64 * i] = (uint16_t)two;
     }
@@ -580,7 +858,7 @@ __global__ __launch_bounds__(256) void k_kv_weights(KvAttendArgs a) {
     for (; r0 < n * a.G; r0 += 16) {
       const Row row = row_of(a, gt, h, r0 + col);
       Frag q[NC];
-      const float undo = load_q<DT, NC>(a.q, row.token * a.stride + (int64_t)row.head * D, row.have, g, q);
+      const float undo = load_q<DT, NC, true>(a.q, row.token * a.stride + (int64_t)row.head * D + g * 8 * NC, 8, row.have, q);
       const float qf = a.scale_log2 * undo;
       const float lse = row.have ? a.lse[row.token * ((int64_t)a.c.H * a.G) + row.head] : 0.0f;
       int limit = a.causal ? min(len, len - n + row.place + 1) : len;
@@ -613,12 +891,23 @@ __global__ __launch_bounds__(256) void k_kv_weights(KvAttendArgs a) {
   }
 }
 
+// Whether sequences have rows enough, on the whole, for the tile kernel.
+bool kv_tiled(int64_t T, int B, int G) { return T * G > (int64_t)32 * B; }
+
 template <int DT, int NC>
 hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.T * a.G;
-  const int64_t tiles = rows / 16 + a.c.B + 1;  // no fewer than the sequences' tiles and the tail's
-  k_kv_stream<DT, NC><<<dim3((unsigned)(tiles * a.c.H), (unsigned)a.splits), 256, 0, s>>>(a);
-  if (a.splits > 1) k_kv_join<DT, NC><<<dim3((unsigned)((rows * a.c.H + 3) / 4)), 256, 0, s>>>(a);
+  const int per = kv_tiled(a.T, a.c.B, a.G) ? 128 : 16;
+  const int64_t tiles = rows / per + a.c.B + 1;  // no fewer than the sequences' tiles and the tail's
+  const dim3 grid((unsigned)(tiles * a.c.H), (unsigned)a.splits);
+  if (per == 128)
+    k_kv_tile<DT, NC><<<grid, 256, 0, s>>>(a);
+  else
+    k_kv_stream<DT, NC><<<grid, 256, 0, s>>>(a);
+  if (a.splits > 8)
+    k_kv_join<DT, NC, 4><<<dim3((unsigned)(rows * a.c.H)), 256, 0, s>>>(a);
+  else if (a.splits > 1)
+    k_kv_join<DT, NC, 1><<<dim3((unsigned)((rows * a.c.H + 3) / 4)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -648,11 +937,13 @@ hipError_t run(bool attention, const KvAttendArgs& a, hipStream_t s) {
 
 int kv_splits(int64_t T, int B, int H, int G, int D, int64_t max_len) {
   (void)D;
-  const int64_t per = (T * G / B + 15) / 16, tiles = (per < 1 ? 1 : per) * B * H;
-  const int64_t most = (max_len + 255) / 256;  // eight steps: two a wave
-  int64_t s = 1024 / tiles;
+  const bool tiled = kv_tiled(T, B, G);
+  const int64_t rows = tiled ? 128 : 16, step = tiled ? 64 : 32;
+  const int64_t per = (T * G / B + rows - 1) / rows, tiles = (per < 1 ? 1 : per) * B * H;
+  const int64_t most = (max_len + 8 * step - 1) / (8 * step);  // eight steps
+  int64_t s = (tiled ? 512 : 1024) / tiles;
   if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  return (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
 }
 
 int64_t kv_attend_workspace(int64_t T, int H, int G, int D, int splits) {
