@@ -1033,7 +1033,7 @@ int fos_kv_weights(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride
 int64_t fos_kv_evict_workspace(int64_t B, int H, int budget, int recent) {
   if (check_kv_sizes(B, 1, H, 16, 32)) return -1;
   if (budget < 0 || recent < 0 || recent > budget || budget > kMaxKvPlaces) return -1;
-  return B * H * (int64_t)(budget - recent) * 8;
+  return B * H * (int64_t)(budget - recent) * 8 + B * H * 4;
 }
 
 int fos_kv_evict(const fos_kv_cache* cache, float* acc, int budget, int sinks, int recent, int32_t* new_lens,
@@ -1048,9 +1048,9 @@ int fos_kv_evict(const fos_kv_cache* cache, float* acc, int budget, int sinks, i
   if (new_lens == cache->lens) return fail(FOS_ERR_INVALID_ARG, "new_lens must not be lens");
   if (!aligned(acc, 4) || !aligned(new_lens, 4) || !aligned(d_status, 4)) return fail(FOS_ERR_ALIGN, "acc/new_lens/status misaligned");
   const int64_t need = fos_kv_evict_workspace(cache->B, cache->H, budget, recent);
-  if (need > 0 && (!work || work_bytes < need))
+  if (!work || work_bytes < need)
     return fail(FOS_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld needed", (long long)(work ? work_bytes : 0), (long long)need);
-  if (need > 0 && !aligned(work, 16)) return fail(FOS_ERR_ALIGN, "workspace not 16-byte aligned");
+  if (!aligned(work, 16)) return fail(FOS_ERR_ALIGN, "workspace not 16-byte aligned");
   if ((rc = check_device())) return rc;
   a.acc = acc;
   a.budget = budget;
@@ -1058,6 +1058,7 @@ int fos_kv_evict(const fos_kv_cache* cache, float* acc, int budget, int sinks, i
   a.recent = recent;
   a.new_lens = new_lens;
   a.moves = static_cast<int2*>(work);
+  a.counts = reinterpret_cast<int*>(a.moves + (int64_t)cache->B * cache->H * (budget - recent));
   a.status = d_status;
   return launch_status(fos::launch_kv_evict(a, static_cast<hipStream_t>(stream)));
 }

@@ -13,6 +13,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __amdgpu_buffer_rsrc_t Rsrc;
 
 // ---------------------------------------------------------------- append
 //
@@ -243,7 +244,6 @@ void append(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
 // time, each read before it is written.
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBatch = 8;  // loads of weights in flight
 
 // Weights in order as unsigned numbers: NaN lowest, zeros alike.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -329,171 +329,292 @@ __device__ Digit find_digit(const int* hist, int* share, int want) {
   return Digit{(uint32_t)out[0], out[1], out[2]};
 }
 
+// One head of one sequence, and what there is to do.
+struct Cut {
+  int b, h, n;
+  bool whole;  // stays as it is
+  float* acc;
+  int2* moves;
+  Rows rows;
+};
+// n is cut to the table; a sequence with a page that is none stays. Uniform over the
+// workgroup; `bad` is a word of its LDS.
+__device__ Cut find_cut(const KvEvictArgs& a, int bh, int* bad) {
+  Cut c;
+  c.b = bh / a.c.H;
+  c.h = bh - c.b * a.c.H;
+  const int cap = a.c.W * a.c.P, len = a.c.lens[c.b];
+  c.n = len < 0 ? 0 : len > cap ? cap : len;
+  const int32_t* table = a.c.table + (int64_t)c.b * a.c.W;
+  c.acc = a.acc + (int64_t)bh * cap;
+  c.moves = a.moves + (int64_t)bh * (a.budget - a.recent);
+  c.rows = Rows{table, a.c.H, c.h, a.c.P, a.c.by_page};
+  if (threadIdx.x == 0) *bad = 0;
+  __syncthreads();
+  if (c.n > a.budget) {
+    for (int w = threadIdx.x; w <= a.c.by_page.div(c.n - 1); w += blockDim.x)
+      if (table[w] < 0 || table[w] >= a.c.pages) *bad = 1;
+  }
+  __syncthreads();
+  c.whole = c.n <= a.budget || *bad;
+  if (threadIdx.x == 0 && c.h == 0) {
+    a.new_lens[c.b] = c.whole ? c.n : a.budget;
+    if (a.status && (len != c.n || *bad)) atomicOr(a.status, kStatusBadCache);
+  }
+  return c;
+}
+
+// The moves of the middle, in order; returns their number. A lane holds BATCH weights at a
+// time.
+template <int BATCH>
+__device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* share) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int keep = a.budget - a.recent, lo = a.sinks, hi = cut.n - a.recent;  // the middle: [lo, hi)
+  if (keep <= lo) return 0;
+  const float* acc = cut.acc;
+  // each wave has a stretch of the middle, in order, BATCH x 64 weights at a time; a
+  // stretch of one batch is read once and stays in registers
+  const int each = ((hi - lo + kWaves * 64 - 1) / (kWaves * 64)) * 64;
+  const int from = min(hi, lo + wave * each), to = min(hi, from + each);
+  const bool held = each <= 64 * BATCH;
+  uint32_t o[BATCH];
+  auto read = [&](int i) {
+    const Rsrc r = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(acc + i), (short)0, 4 * min(to - i, 64 * BATCH), 0x00020000);
+    uint32_t v[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; k++) v[k] = __builtin_amdgcn_raw_buffer_load_b32(r, 4 * (64 * k + lane), 0, 0);
+#pragma unroll
+    for (int k = 0; k < BATCH; k++) o[k] = order_of(__uint_as_float(v[k]));
+  };
+  if (held && from < to) read(from);
+  // f(the first of 64 places, this lane's weight's order, whether it has one) along the wave's stretch
+  auto stretch = [&](auto f) {
+    for (int i = from; i < to; i += 64 * BATCH) {
+      if (!held) read(i);
+#pragma unroll
+      for (int k = 0; k < BATCH; k++) {
+        if (i + 64 * k >= to) break;
+        f(i + 64 * k, o[k], i + 64 * k + lane < to);
+      }
+    }
+  };
+  // the smallest kept weight, and how many of its equals are kept
+  uint32_t found = 0, mask = 0;
+  Digit d{0, keep - lo, 0};
+#pragma unroll 1
+  for (int pass = 0; pass < 3; pass++) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t low = pass == 2 ? 1023u : 2047u;
+    hist[t] = 0;
+    hist[t + 1024] = 0;
+    __syncthreads();
+    stretch([&](int, uint32_t w, bool have) {
+      if (have && (w & mask) == found) atomicAdd(&hist[(w >> shift) & low], 1);
+    });
+    __syncthreads();
+    d = find_digit<2048>(hist, share, d.want);
+    found |= d.digit << shift;
+    mask |= low << shift;
+  }
+  // equals of the smallest kept weight before this wave's, where only some are kept
+  const bool some = d.want < d.of;
+  int equals = 0;
+  if (some) {
+    int c = 0;
+    stretch([&](int, uint32_t w, bool have) { c += __popcll(__ballot(have && w == found)); });
+    if (lane == 0) share[wave] = c;
+    __syncthreads();
+    for (int w = 0; w < wave; w++) equals += share[w];
+    __syncthreads();
+  }
+  // the places below `keep` that are given up, and the kept ones from there on: counted, then written
+  auto below = [](unsigned long long m) {
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+  };
+  int n_free = 0, n_moved = 0, eq = equals;
+  int2* out = nullptr;
+  auto visit = [&](int i, uint32_t w, bool have) {
+    bool kept = have && w >= found;
+    if (some) {
+      const unsigned long long same = __ballot(have && w == found);
+      if (w == found && eq + below(same) >= d.want) kept = false;
+      eq += __popcll(same);
+    }
+    if (i < keep) {
+      const bool is = have && !kept && i + lane < keep;
+      const unsigned long long m = __ballot(is);
+      if (out && is) out[n_free + below(m)].y = i + lane;
+      n_free += __popcll(m);
+    }
+    if (i + 64 > keep) {
+      const bool is = kept && i + lane >= keep;
+      const unsigned long long m = __ballot(is);
+      if (out && is) out[n_moved + below(m)].x = i + lane;
+      n_moved += __popcll(m);
+    }
+  };
+  stretch(visit);
+  if (lane == 0) {
+    share[wave] = n_free;
+    share[kWaves + wave] = n_moved;
+  }
+  __syncthreads();
+  int holes = 0;
+  n_free = n_moved = 0;
+  eq = equals;
+  for (int w = 0; w < kWaves; w++) {
+    if (w < wave) {
+      n_free += share[w];
+      n_moved += share[kWaves + w];
+    }
+    holes += share[w];
+  }
+  out = cut.moves;
+  stretch(visit);
+  return holes;
+}
+
+// Rows are moved by teams of 16 lanes, several at a time.
 template <int NC>
-__global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
+struct Teams {
   typedef Mover<NC> M;
+  static constexpr int kRounds = (M::kItems + 15) / 16, kRows = kRounds == 1 ? 8 : 4;
+  typedef typename M::Piece Held[kRows][kRounds];
+
+  // Moves first, first + step, ... below `holes`.
+  static __device__ __forceinline__ void move(const KvEvictArgs& a, const Cut& cut, int holes, int first, int step) {
+    const int l16 = threadIdx.x & 15;
+    for (int i0 = first; i0 < holes; i0 += kRows * step) {
+      int2 mv[kRows];
+      Held p;
+#pragma unroll
+      for (int r = 0; r < kRows; r++)
+        if (i0 + r * step < holes) mv[r] = cut.moves[i0 + r * step];
+#pragma unroll
+      for (int r = 0; r < kRows; r++)
+        if (i0 + r * step < holes) {
+          const int64_t from = cut.rows.at(mv[r].x);
+#pragma unroll
+          for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, cut.acc, from, mv[r].x, l16 + 16 * k);
+        }
+#pragma unroll
+      for (int r = 0; r < kRows; r++)
+        if (i0 + r * step < holes) {
+          const int64_t to = cut.rows.at(mv[r].y);
+#pragma unroll
+          for (int k = 0; k < kRounds; k++) M::write(a.c, cut.acc, to, mv[r].y, l16 + 16 * k, p[r][k]);
+        }
+    }
+  }
+
+  // The last rows, `gap` down, by one workgroup of THREADS or by `parts` of them. A chunk's rows
+  // are all read before any is written, and what a chunk writes lies below what later ones read;
+  // where the rows' places and those they come from have none in common, chunks are
+  // independent and each part has its own, else the first part has all. The weights behind
+  // the cut are cleared, those of a chunk's rows by the part that has it.
+  template <int THREADS>
+  static __device__ __forceinline__ void shift(const KvEvictArgs& a, const Cut& cut, int part, int parts) {
+    constexpr int kTeams = THREADS / 16;
+    const int team = threadIdx.x >> 4, l16 = threadIdx.x & 15, keep = a.budget - a.recent, gap = cut.n - a.budget;
+    const bool apart = gap >= a.recent;
+    if (!apart) {
+      if (part > 0) return;
+      parts = 1;
+    }
+    for (int i = a.budget + part * THREADS + threadIdx.x; i < cut.n - a.recent; i += parts * THREADS) cut.acc[i] = 0.0f;
+    for (int i0 = part * kRows * kTeams; i0 < a.recent; i0 += parts * kRows * kTeams) {
+      Held p;
+#pragma unroll
+      for (int r = 0; r < kRows; r++) {
+        const int i = i0 + r * kTeams + team;
+        if (i < a.recent) {
+          const int64_t from = cut.rows.at(keep + i + gap);
+#pragma unroll
+          for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, cut.acc, from, keep + i + gap, l16 + 16 * k);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRows; r++) {
+        const int i = i0 + r * kTeams + team;
+        if (i < a.recent) {
+          const int64_t to = cut.rows.at(keep + i);
+#pragma unroll
+          for (int k = 0; k < kRounds; k++) M::write(a.c, cut.acc, to, keep + i, l16 + 16 * k, p[r][k]);
+          if (apart && l16 == 0) cut.acc[keep + i + gap] = 0.0f;
+        }
+      }
+    }
+    if (apart) return;
+    __syncthreads();
+    for (int i = max(a.budget, cut.n - a.recent) + threadIdx.x; i < cut.n; i += THREADS) cut.acc[i] = 0.0f;
+  }
+};
+
+// All of it in one launch, or (ALL = false) the search for the moves alone, whose number
+// goes to counts (-1 for a sequence that stays as it is).
+template <int NC, bool ALL>
+__global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
   __shared__ int hist[2048];
   __shared__ int share[2 * kWaves + 4];
   __shared__ int bad;
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int b = blockIdx.x / a.c.H, h = blockIdx.x - b * a.c.H;
-  const int cap = a.c.W * a.c.P;
-  int n = a.c.lens[b];
-  const bool range = n < 0 || n > cap;
-  n = n < 0 ? 0 : n > cap ? cap : n;
-  const int32_t* table = a.c.table + (int64_t)b * a.c.W;
-  if (t == 0) bad = 0;
-  __syncthreads();
-  if (n > a.budget) {
-    for (int w = t; w < a.c.by_page.div(n - 1) + 1; w += kThreads)
-      if (table[w] < 0 || table[w] >= a.c.pages) bad = 1;
+  const Cut cut = find_cut(a, blockIdx.x, &bad);
+  if (cut.whole) {
+    if (!ALL && threadIdx.x == 0) a.counts[blockIdx.x] = -1;
+    return;
   }
-  __syncthreads();
-  const bool stays = n <= a.budget || bad;
-  if (t == 0 && h == 0) {
-    a.new_lens[b] = stays ? n : a.budget;
-    if (a.status && (range || bad)) atomicOr(a.status, kStatusBadCache);
+  // (32 in both: 128 heads of 1088 tokens 36 us instead of 17, for the code's size and spills;
+  // 8 in both: 32 heads of 32768 tokens 40 us instead of 29)
+  const int holes = find_moves<ALL ? 8 : 32>(a, cut, hist, share);
+  if constexpr (ALL) {
+    __syncthreads();
+    Teams<NC>::move(a, cut, holes, threadIdx.x >> 4, kThreads / 16);
+    __syncthreads();
+    Teams<NC>::template shift<kThreads>(a, cut, 0, 1);
+  } else if (threadIdx.x == 0) {
+    a.counts[blockIdx.x] = holes;
   }
-  if (stays) return;
+}
 
-  const int keep = a.budget - a.recent, lo = a.sinks, hi = n - a.recent;  // the middle: [lo, hi)
-  float* acc = a.acc + ((int64_t)b * a.c.H + h) * cap;
-  int2* moves = a.moves + ((int64_t)b * a.c.H + h) * keep;
-  const Rows rows{table, a.c.H, h, a.c.P, a.c.by_page};
-  int holes = 0;
-  if (keep > lo) {
-    // the smallest kept weight, and how many of its equals are kept
-    uint32_t found = 0, mask = 0;
-    Digit d{0, keep - lo, 0};
-#pragma unroll 1
-    for (int pass = 0; pass < 3; pass++) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t low = pass == 2 ? 1023u : 2047u;
-      hist[t] = 0;
-      hist[t + 1024] = 0;
-      __syncthreads();
-      for (int i = lo + t; i < hi; i += kBatch * kThreads) {
-        float v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; k++) v[k] = acc[min(i + k * kThreads, hi - 1)];
-#pragma unroll
-        for (int k = 0; k < kBatch; k++) {
-          const uint32_t o = order_of(v[k]);
-          if (i + k * kThreads < hi && (o & mask) == found) atomicAdd(&hist[(o >> shift) & low], 1);
-        }
-      }
-      __syncthreads();
-      d = find_digit<2048>(hist, share, d.want);
-      found |= d.digit << shift;
-      mask |= low << shift;
-    }
-    // each wave has a stretch of the middle, in order
-    const int each = ((hi - lo + kWaves * 64 - 1) / (kWaves * 64)) * 64;
-    const int from = lo + wave * each, to = min(hi, from + each);
-    // equals of the smallest kept weight before this wave's (all of them are kept in most cases)
-    int equals = 0;
-    if (d.want < d.of) {
-      int c = 0;
-      for (int i = from; i < to; i += 64)
-        c += __popcll(__ballot(i + lane < to && order_of(acc[i + lane]) == found));
-      __syncthreads();
-      if (lane == 0) share[wave] = c;
-      __syncthreads();
-      for (int w = 0; w < wave; w++) equals += share[w];
-    }
-    const unsigned long long before = (1ull << lane) - 1;
-    int n_free = 0, n_moved = 0;
-#pragma unroll 1
-    for (int emit = 0; emit < 2; emit++) {
-      int eq = equals, f = 0, m = 0;
-      if (emit) {
-        __syncthreads();
-        if (lane == 0) {
-          share[wave] = n_free;
-          share[kWaves + wave] = n_moved;
-        }
-        __syncthreads();
-        for (int w = 0; w < wave; w++) {
-          f += share[w];
-          m += share[kWaves + w];
-        }
-        for (int w = 0; w < kWaves; w++) holes += share[w];
-      }
-      for (int i = from; i < to; i += 64 * kBatch) {
-        float v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; k++) v[k] = acc[min(i + 64 * k + lane, hi - 1)];
-#pragma unroll
-        for (int k = 0; k < kBatch; k++) {
-          const int p = i + 64 * k + lane;
-          const uint32_t o = order_of(v[k]);
-          const unsigned long long same = __ballot(p < to && o == found);
-          const bool kept = p < to && (o > found || (o == found && eq + __popcll(same & before) < d.want));
-          eq += __popcll(same);
-          const unsigned long long is_free = __ballot(p < to && p < keep && !kept);
-          const unsigned long long is_moved = __ballot(kept && p >= keep);
-          if (emit) {
-            if ((is_free >> lane) & 1) moves[f + __popcll(is_free & before)].y = p;
-            if ((is_moved >> lane) & 1) moves[m + __popcll(is_moved & before)].x = p;
-          }
-          f += __popcll(is_free);
-          m += __popcll(is_moved);
-        }
-      }
-      n_free = f;
-      n_moved = m;
-    }
-    __syncthreads();
+// The second and third launch: what the first has found.
+__device__ __forceinline__ Cut found_cut(const KvEvictArgs& a, int bh) {
+  Cut c;
+  c.b = bh / a.c.H;
+  c.h = bh - c.b * a.c.H;
+  c.whole = false;
+  const int cap = a.c.W * a.c.P, len = a.c.lens[c.b];
+  c.n = len > cap ? cap : len;
+  c.acc = a.acc + (int64_t)bh * cap;
+  c.moves = a.moves + (int64_t)bh * (a.budget - a.recent);
+  c.rows = Rows{a.c.table + (int64_t)c.b * a.c.W, a.c.H, c.h, a.c.P, a.c.by_page};
+  return c;
+}
+
+template <int NC>
+__global__ __launch_bounds__(256) void k_kv_move(KvEvictArgs a) {
+  const int holes = a.counts[blockIdx.x];
+  if ((int)blockIdx.y * 16 >= holes) return;
+  Teams<NC>::move(a, found_cut(a, blockIdx.x), holes, blockIdx.y * 16 + (threadIdx.x >> 4), gridDim.y * 16);
+}
+
+template <int NC>
+__global__ __launch_bounds__(256) void k_kv_shift(KvEvictArgs a) {
+  if (a.counts[blockIdx.x] < 0) return;
+  Teams<NC>::template shift<256>(a, found_cut(a, blockIdx.x), blockIdx.y, gridDim.y);
+}
+
+template <int NC>
+void evict(const KvEvictArgs& a, hipStream_t s) {
+  const unsigned heads = (unsigned)(a.c.B * a.c.H);
+  const int keep = a.budget - a.recent;
+  if (heads >= 128 || keep <= 512) {
+    k_kv_evict<NC, true><<<heads, kThreads, 0, s>>>(a);
+    return;
   }
-  // teams of 16 lanes carry a row each, several at a time
-  constexpr int kTeams = kThreads / 16, kRounds = (M::kItems + 15) / 16, kRows = kRounds == 1 ? 8 : 4;
-  const int team = t >> 4, l16 = t & 15;
-  for (int i0 = team; i0 < holes; i0 += kRows * kTeams) {
-    int2 mv[kRows];
-    typename M::Piece p[kRows][kRounds];
-#pragma unroll
-    for (int r = 0; r < kRows; r++) mv[r] = moves[min(i0 + r * kTeams, holes - 1)];
-#pragma unroll
-    for (int r = 0; r < kRows; r++) {
-      const int64_t from = rows.at(mv[r].x);
-#pragma unroll
-      for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, acc, from, mv[r].x, l16 + 16 * k);
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; r++) {
-      const int64_t to = rows.at(mv[r].y);
-      if (i0 + r * kTeams < holes) {
-#pragma unroll
-        for (int k = 0; k < kRounds; k++) M::write(a.c, acc, to, mv[r].y, l16 + 16 * k, p[r][k]);
-      }
-    }
-  }
-  __syncthreads();
-  // the last rows: `gap` down. A chunk's rows are all read before any is written, and what
-  // a chunk writes lies below what later ones read.
-  const int gap = n - a.budget;
-  for (int i0 = 0; i0 < a.recent; i0 += kRows * kTeams) {
-    typename M::Piece p[kRows][kRounds];
-#pragma unroll
-    for (int r = 0; r < kRows; r++) {
-      const int pos = keep + min(i0 + r * kTeams + team, a.recent - 1) + gap;
-      const int64_t from = rows.at(pos);
-#pragma unroll
-      for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, acc, from, pos, l16 + 16 * k);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kRows; r++) {
-      const int i = i0 + r * kTeams + team;
-      const int64_t to = rows.at(keep + min(i, a.recent - 1));
-      if (i < a.recent) {
-#pragma unroll
-        for (int k = 0; k < kRounds; k++) M::write(a.c, acc, to, keep + i, l16 + 16 * k, p[r][k]);
-      }
-    }
-  }
-  __syncthreads();
-  for (int i = a.budget + t; i < n; i += kThreads) acc[i] = 0.0f;
+  const int each = 16 * Teams<NC>::kRows;
+  k_kv_evict<NC, false><<<heads, kThreads, 0, s>>>(a);
+  k_kv_move<NC><<<dim3(heads, (unsigned)min((keep + each - 1) / each, 64)), 256, 0, s>>>(a);
+  k_kv_shift<NC><<<dim3(heads, 4), 256, 0, s>>>(a);
 }
 
 }  // namespace
@@ -510,14 +631,13 @@ hipError_t launch_kv_append(int dt, const KvAppendArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.c.B * a.c.H);
   switch (a.c.D / 32) {
-    case 1: k_kv_evict<1><<<grid, kThreads, 0, s>>>(a); break;
-    case 2: k_kv_evict<2><<<grid, kThreads, 0, s>>>(a); break;
-    case 3: k_kv_evict<3><<<grid, kThreads, 0, s>>>(a); break;
-    case 4: k_kv_evict<4><<<grid, kThreads, 0, s>>>(a); break;
-    case 6: k_kv_evict<6><<<grid, kThreads, 0, s>>>(a); break;
-    case 8: k_kv_evict<8><<<grid, kThreads, 0, s>>>(a); break;
+    case 1: evict<1>(a, s); break;
+    case 2: evict<2>(a, s); break;
+    case 3: evict<3>(a, s); break;
+    case 4: evict<4>(a, s); break;
+    case 6: evict<6>(a, s); break;
+    case 8: evict<8>(a, s); break;
   }
   return hipGetLastError();
 }

@@ -819,75 +819,158 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttendArgs a) {
 
 // ---------------------------------------------------------------- weights
 //
-// A wave has 32 keys, decoded once to registers, and passes over all rows of the
-// sequence's new tokens in tiles of 16; each lane sums its keys' weights over the
-// tiles, and the sixteen columns join at the end. A key belongs to one wave, so the
-// sums are added to what is there without atomics, in an order that is always the
-// same.
+// A workgroup stages 128 rows of q in LDS, in fp16, and passes over its keys, 32 to a
+// wave at a time, decoded to registers. Here the keys are the columns of the matrix
+// instruction's result, so that a lane has one key and sums its weights over the rows
+// in its own registers. A key belongs to one wave, so the sums are added to what is there
+// without atomics, in an order that is always the same.
+
+// Half a row: 16 NC neighbouring values, in NC blocks.
+template <int NC> struct Half {
+  struct __attribute__((packed, aligned(NC == 8 ? 8 : NC == 4 ? 4 : NC % 2 ? 1 : 2))) Scales {
+    uint8_t v[NC];
+  };
+  Scales scales;
+  __device__ __forceinline__ void decode(const Quarter<NC>* codes, Frag* f) const {
+    uint32_t w[(NC + 3) / 4] = {};
+#pragma unroll
+    for (int i = 0; i < NC; i++) w[i / 4] |= (uint32_t)scales.v[i] << (8 * (i % 4));
+#pragma unroll
+    for (int i = 0; i < NC; i += 2) {
+      const h2 p = i & 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w[i / 4], 1.0f, true)
+                         : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w[i / 4], 1.0f, false);
+      const h2 lo = __builtin_shufflevector(p, p, 0, 0), hi = __builtin_shufflevector(p, p, 1, 1);
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        if (2 * i + j < 2 * NC) {
+          const int c = 2 * i + j;  // fragments 2i, 2i + 1 are block i, the next two block i + 1
+          decode8(codes[c / NC].codes[c % NC], j < 2 ? lo : hi, f[c].u);
+        }
+    }
+  }
+};
+
+template <int NC> struct KeyStep {
+  Quarter<NC> k[2];  // codes alone, as loaded: four lanes to a row
+  Half<NC> half;     // scales, and S_dec, of the lane's own key
+  float sdec;
+  bool there[2];     // wave-uniform
+  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, int first, int len) {
+    const int lane = threadIdx.x & 63;
+    int64_t row[2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      row[u] = pg.row(first + 16 * u, len, there[u]);
+      k[u].load_codes(c.k.codes + row[u] * (16 * NC) + lane * (4 * NC));
+    }
+    const int64_t mine = ((lane & 16) ? row[1] : row[0]) + (lane & 15);
+    half.scales = *reinterpret_cast<const typename Half<NC>::Scales*>(c.k.scales + mine * (2 * NC) + (lane >> 5) * NC);
+    sdec = c.k.sdec[mine];
+  }
+};
 
 template <int DT, int NC>
-__global__ __launch_bounds__(256) void k_kv_weights(KvAttendArgs a) {
-  constexpr int D = 32 * NC;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * 512 * NC];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
+__global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArgs a) {
+  constexpr int D = 32 * NC, kRows = 128, kRow = 64 * NC + 16;
+  __shared__ __attribute__((aligned(16))) uint8_t qs[kRows * kRow];
+  __shared__ __attribute__((aligned(16))) uint8_t turn[4 * 512 * NC];
+  __shared__ __attribute__((aligned(16))) float factor[kRows], ref[kRows];
+  __shared__ __attribute__((aligned(16))) int limits[kRows];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, col = lane & 31;
   check_cache(a);
   const int h = blockIdx.x % a.c.H, b = blockIdx.x / a.c.H;
   GroupTile gt;
   gt.g = b;
+  gt.tile = 0;
   gt.start = b ? a.offs[b - 1] : 0;
   gt.end = a.offs[b];
   gt.start = gt.start < 0 ? 0 : gt.start > a.T ? a.T : gt.start;
   gt.end = gt.end < gt.start ? gt.start : gt.end > a.T ? a.T : gt.end;
-  gt.tile = 0;
-  const int n = gt.end - gt.start, len = length_of(a.c, b);
-  if (n == 0) return;
+  const int n = gt.end - gt.start, len = length_of(a.c, b), rows = n * a.G;
   const Pages pg{a.c.table + (int64_t)b * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
   float* acc = a.acc + ((int64_t)b * a.c.H + h) * ((int64_t)a.c.W * a.c.P);
-  for (int64_t base = (int64_t)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(wave); 32 * base < len;
-       base += (int64_t)gridDim.y * 4) {
-    const int first = 32 * (int)base;
-    Step<NC> st;
-    st.template load<false>(a.c, pg, first, len);
-    Frag kf[2][NC];
-    turn_keys<NC>(lds + wave * 512 * NC, st, kf);
-    float sum[8];
+  uint8_t* mine = turn + wave * 512 * NC;
+  if ((int64_t)blockIdx.y * 128 >= len) return;
+  for (int g0 = 0; g0 < rows; g0 += kRows) {
+    // keys that any of these rows sees
+    const int most = a.causal ? min(len, len - n + a.by_group.div(min(g0 + kRows, rows) - 1) + 1) : len;
+    if ((int64_t)blockIdx.y * 128 >= most) continue;
+    KeyStep<NC> next;
+    const int stride = (int)gridDim.y * 128;
+    int first = (int)(blockIdx.y * 4 + wave) * 32;
+    next.load(a.c, pg, first, len);
+    __syncthreads();
+    {
+      const Row row = row_of(a, gt, h, g0 + 32 * wave + col);
+      Frag q[2 * NC];
+      const float undo = load_q<DT, 2 * NC, false>(
+          a.q, row.token * a.stride + (int64_t)row.head * D + half * 16 * NC, 8, row.have, q);
+      uint8_t* to = qs + (32 * wave + col) * kRow + half * 32 * NC;
 #pragma unroll
-    for (int i = 0; i < 8; i++) sum[i] = 0.0f;
-    // under a causal mask the first token that sees the first key is first - (len - n)
-    int r0 = a.causal ? max(0, first - (len - n)) * a.G & ~15 : 0;
-    for (; r0 < n * a.G; r0 += 16) {
-      const Row row = row_of(a, gt, h, r0 + col);
-      Frag q[NC];
-      const float undo = load_q<DT, NC, true>(a.q, row.token * a.stride + (int64_t)row.head * D + g * 8 * NC, 8, row.have, q);
-      const float qf = a.scale_log2 * undo;
-      const float lse = row.have ? a.lse[row.token * ((int64_t)a.c.H * a.G) + row.head] : 0.0f;
-      int limit = a.causal ? min(len, len - n + row.place + 1) : len;
-      if (!row.have || lse == -__builtin_huge_valf()) limit = 0;  // such a row has no weights
-      const float ref = lse * 1.44269504088896341f;
-#pragma unroll
-      for (int u = 0; u < 2; u++) {
-        f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < NC; c++) sc = mfma16(kf[u][c], q[c], sc);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const float e = __builtin_amdgcn_exp2f(sc[i] * (st.ks[u][i] * qf) - ref);
-          sum[4 * u + i] += first + 16 * u + 4 * g + i < limit ? e : 0.0f;
-        }
+      for (int c = 0; c < 2 * NC; c++)
+        *reinterpret_cast<u32x4*>(to + 16 * c) = u32x4{q[c].u[0], q[c].u[1], q[c].u[2], q[c].u[3]};
+      if (half == 0) {
+        float lse = row.have ? a.lse[row.token * ((int64_t)a.c.H * a.G) + row.head] : 0.0f;
+        // a row that sees nothing has no weights: 2^-infinity
+        if (!row.have || lse == -__builtin_huge_valf()) lse = __builtin_huge_valf();
+        factor[32 * wave + col] = a.scale_log2 * undo;
+        ref[32 * wave + col] = lse * 1.44269504088896341f;
+        limits[32 * wave + col] = a.causal ? min(len, len - n + row.place + 1) : len;
       }
     }
-    // over the sixteen columns
+    __syncthreads();
+    for (; first < most; first += stride) {
+      const KeyStep<NC> st = next;
+      next.load(a.c, pg, first <= INT32_MAX - stride ? first + stride : INT32_MAX - 63, len);
+      Frag kf[2 * NC];
+      wave_lds_order();
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+      for (int u = 0; u < 2; u++) st.k[u].store_codes(mine + u * 256 * NC + 4 * NC * piece(lane >> 2, lane & 3));
+      wave_lds_order();
+      Quarter<NC> codes[2];
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) sum[i] += __shfl_xor(sum[i], d, 64);
+      for (int i = 0; i < 2; i++)
+        codes[i].load_codes(mine + (col >> 4) * 256 * NC + 4 * NC * piece(col & 15, 2 * half + i));
+      st.half.decode(codes, kf);
+      float sum = 0.0f;
+#pragma unroll 1
+      for (int rt = 0; rt < kRows && g0 + rt < rows; rt += 32) {
+        f32x16 x;
 #pragma unroll
-    for (int u = 0; u < 2; u++)
-      if (st.there[u] && col < 4) {
-        const int j = first + 16 * u + 4 * g + col;
-        const float w = col == 0 ? sum[4 * u] : col == 1 ? sum[4 * u + 1] : col == 2 ? sum[4 * u + 2] : sum[4 * u + 3];
-        if (j < len) acc[j] += w;
+        for (int i = 0; i < 16; i++) x[i] = 0.0f;
+        const uint8_t* qp = qs + (rt + col) * kRow + half * 32 * NC;
+#pragma unroll
+        for (int c = 0; c < 2 * NC; c++) {
+          Frag f;
+          const u32x4 t = *reinterpret_cast<const u32x4*>(qp + 16 * c);
+          f.u[0] = t.x, f.u[1] = t.y, f.u[2] = t.z, f.u[3] = t.w;
+          x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.h, kf[c].h, x, 0, 0, 0);
+        }
+        const bool partly = a.causal && first + 32 > len - n + a.by_group.div(g0 + rt) + 1;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          if (g0 + rt + 8 * i >= rows) break;
+          const int r = rt + 8 * i + 4 * half;
+          const f32x4 f = *reinterpret_cast<const f32x4*>(factor + r), z = *reinterpret_cast<const f32x4*>(ref + r);
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) e[j] = __builtin_amdgcn_exp2f(x[4 * i + j] * (st.sdec * f[j]) - z[j]);
+          if (partly) {
+            const int4 lim = *reinterpret_cast<const int4*>(limits + r);
+            const int l4[4] = {lim.x, lim.y, lim.z, lim.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              if (first + col >= l4[j]) e[j] = 0.0f;
+          }
+          sum += (e[0] + e[1]) + (e[2] + e[3]);
+        }
       }
+      const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+      sum = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+      const bool there = (lane & 16) ? st.there[1] : st.there[0];
+      if (half == 0 && there && first + col < len) acc[first + col] += sum;
+    }
   }
 }
 
@@ -913,9 +996,10 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
 
 template <int DT, int NC>
 hipError_t weights(const KvAttendArgs& a, hipStream_t s) {
-  const int64_t heads = (int64_t)a.c.B * a.c.H;
-  int64_t chunks = (a.max_len + 127) / 128;
-  chunks = chunks < 1 ? 1 : chunks > 65535 ? 65535 : chunks;
+  const int64_t heads = (int64_t)a.c.B * a.c.H, most = (a.max_len + 127) / 128;
+  int64_t chunks = 1024 / heads;
+  chunks = chunks > most ? most : chunks;
+  chunks = chunks < 1 ? 1 : chunks;
   k_kv_weights<DT, NC><<<dim3((unsigned)heads, (unsigned)chunks), 256, 0, s>>>(a);
   return hipGetLastError();
 }

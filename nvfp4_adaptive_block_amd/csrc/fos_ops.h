@@ -163,6 +163,7 @@ struct KvEvictArgs {
   int budget, sinks, recent;
   int32_t* new_lens;     // [B]
   int2* moves;           // [B, H, budget - recent] (from, to)
+  int* counts;           // [B, H]
   int32_t* status;       // nullable
 };
 hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t s);

@@ -137,7 +137,6 @@ def test_calls_without_tokens_need_no_rows():
     assert append(T=0, k=None, v=None) in (0, DEVICE)
     assert attention(T=0, q=None, out=None, lse=None) in (0, DEVICE)
     assert weights(T=0, q=None, lse=None) in (0, DEVICE)
-    assert evict(budget=8, sinks=0, recent=8, work=None) in (0, DEVICE)
 
 
 def test_workspaces():
@@ -149,8 +148,8 @@ def test_workspaces():
         fos.fos_kv_attention_workspace(1, 4, 1, 4, 2, 64, 128, -1)
     with pytest.raises(ValueError):
         fos.fos_kv_evict_workspace(1, 2, 10, 11)
-    assert fos.fos_kv_evict_workspace(2, 3, 100, 40) == 2 * 3 * 60 * 8
-    assert fos.fos_kv_evict_workspace(2, 3, 40, 40) == 0
+    assert fos.fos_kv_evict_workspace(2, 3, 100, 40) == 2 * 3 * 60 * 8 + 2 * 3 * 4
+    assert fos.fos_kv_evict_workspace(2, 3, 40, 40) == 2 * 3 * 4
     # more keys, no smaller a workspace; none where there are rows enough
     sizes = [fos.fos_kv_attention_workspace(1, 8, 1, w, 2, 64, 128) for w in (1, 8, 64, 1024)]
     assert sizes == sorted(sizes) and sizes[-1] > 0
