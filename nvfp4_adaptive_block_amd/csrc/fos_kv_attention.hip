@@ -411,7 +411,10 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
       for (int u = 0; u < 2; u++)
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          if (!st.there[u] || first + 16 * u + 4 * g + i >= limit) z[4 * u + i] = -__builtin_huge_valf();
+          if (!st.there[u] || first + 16 * u + 4 * g + i >= limit) {
+            z[4 * u + i] = -__builtin_huge_valf();
+            st.vs[u][i] = 0.0f;  // which may be a stale NaN
+          }
     }
 #pragma unroll
     for (int u = 0; u < 2; u++)
@@ -433,10 +436,6 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
       const float e = __builtin_amdgcn_exp2f(z[i] - m);
       l += e;
       w[i] = e * st.vs[i / 4][i % 4];
-    }
-    if (partly) {
-#pragma unroll
-      for (int i = 0; i < 8; i++) w[i] = z[i] == -__builtin_huge_valf() ? 0.0f : w[i];
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) p.u[i] = pack_f16(w[2 * i], w[2 * i + 1]);
@@ -549,7 +548,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
   typedef TileLds<NC> L;
   constexpr int D = 32 * NC;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * L::kSide > 4 * L::kOut ? 2 * L::kSide : 4 * L::kOut];
-  __shared__ __attribute__((aligned(16))) float sizes[2][3][L::kKeys];  // S_dec of keys and of values, its log2
+  __shared__ __attribute__((aligned(16))) float sizes[2][3][L::kKeys];  // S_dec of keys times the scale, of values, its log2
   __shared__ int gone[2][4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
@@ -578,7 +577,6 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
   Frag q[2 * NC];
   const float undo =
       load_q<DT, 2 * NC, false>(a.q, row.token * a.stride + (int64_t)row.head * D + 8 * half, 16, row.have, q);
-  const float qf = a.scale_log2 * undo;
   f32x16 o[NC];
 #pragma unroll
   for (int t = 0; t < NC; t++)
@@ -605,7 +603,8 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
     if (lane < 32) {
       const int j = 16 * wave + (lane & 15);
       const float S = !st.there || first + j >= len ? 0.0f : st.sdec;
-      sizes[side][lane >> 4][j] = S;
+      // the scale with the keys', so that what is left for a query is its power of two
+      sizes[side][lane >> 4][j] = lane < 16 ? S * a.scale_log2 : S;
       if (lane >= 16) sizes[side][2][j] = log2_of(S);
       if (lane == 0) gone[side][wave] = !st.there;
     }
@@ -638,24 +637,34 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
           x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.h, q[c].h, x[kb], 0, 0, 0);
         }
       }
-      // a lane's sixteen keys of 32: 8a + 4 half + 0..3
-      const bool partly =
-          first + L::kKeys > least || gone[side][0] || gone[side][1] || gone[side][2] || gone[side][3];
+      // a lane's sixteen keys of 32: 8b + 4 half + 0..3
+#pragma unroll
+      for (int kb = 0; kb < 2; kb++)
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          const f32x4 ks = *reinterpret_cast<const f32x4*>(&sizes[side][0][32 * kb + 8 * b + 4 * half]);
+#pragma unroll
+          for (int i = 0; i < 4; i++) x[kb][4 * b + i] *= ks[i];
+        }
+      if (first + L::kKeys > least || gone[side][0] + gone[side][1] + gone[side][2] + gone[side][3]) {
+#pragma unroll
+        for (int kb = 0; kb < 2; kb++)
+#pragma unroll
+          for (int b = 0; b < 4; b++) {
+            const int j = 32 * kb + 8 * b + 4 * half;
+            const int past = gone[side][j >> 4] ? 0 : limit - first - j;  // keys from here on are not seen
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[kb][4 * b + i] = i < past ? x[kb][4 * b + i] : -__builtin_huge_valf();
+          }
+      }
       float top = kLowest;
 #pragma unroll
       for (int kb = 0; kb < 2; kb++)
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-          const int j = 32 * kb + 8 * b + 4 * half;
-          const f32x4 ks = *reinterpret_cast<const f32x4*>(&sizes[side][0][j]);
-          const f32x4 lv = *reinterpret_cast<const f32x4*>(&sizes[side][2][j]);
+          const f32x4 lv = *reinterpret_cast<const f32x4*>(&sizes[side][2][32 * kb + 8 * b + 4 * half]);
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            float z = x[kb][4 * b + i] * (ks[i] * qf);
-            if (partly && (first + j + i >= limit || gone[side][j >> 4])) z = -__builtin_huge_valf();
-            x[kb][4 * b + i] = z;
-            top = __builtin_fmaxf(top, z + lv[i]);
-          }
+          for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, __builtin_fmaf(x[kb][4 * b + i], undo, lv[i]));
         }
       top = row_max<false>(top);
       if (__any(top > m + kLag)) {
@@ -677,10 +686,9 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
           float w[4];
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const float e = __builtin_amdgcn_exp2f(x[kb][4 * b + i] - m);
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[kb][4 * b + i], undo, -m));
             l += e;
             w[i] = e * vs[i];
-            if (partly && x[kb][4 * b + i] == -__builtin_huge_valf()) w[i] = 0.0f;
           }
           p[kb][b >> 1].u[2 * (b & 1)] = pack_f16(w[0], w[1]);
           p[kb][b >> 1].u[2 * (b & 1) + 1] = pack_f16(w[2], w[3]);
@@ -955,7 +963,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArg
           const f32x4 f = *reinterpret_cast<const f32x4*>(factor + r), z = *reinterpret_cast<const f32x4*>(ref + r);
           float e[4];
 #pragma unroll
-          for (int j = 0; j < 4; j++) e[j] = __builtin_amdgcn_exp2f(x[4 * i + j] * (st.sdec * f[j]) - z[j]);
+          for (int j = 0; j < 4; j++) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[4 * i + j] * st.sdec, f[j], -z[j]));
           if (partly) {
             const int4 lim = *reinterpret_cast<const int4*>(limits + r);
             const int l4[4] = {lim.x, lim.y, lim.z, lim.w};
@@ -997,7 +1005,7 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
 template <int DT, int NC>
 hipError_t weights(const KvAttendArgs& a, hipStream_t s) {
   const int64_t heads = (int64_t)a.c.B * a.c.H, most = (a.max_len + 127) / 128;
-  int64_t chunks = 1024 / heads;
+  int64_t chunks = 512 / heads;
   chunks = chunks > most ? most : chunks;
   chunks = chunks < 1 ? 1 : chunks;
   k_kv_weights<DT, NC><<<dim3((unsigned)heads, (unsigned)chunks), 256, 0, s>>>(a);
