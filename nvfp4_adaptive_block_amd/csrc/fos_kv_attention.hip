@@ -169,18 +169,21 @@ struct Pages {
   int64_t pages;
   int H, h, P;
   FastDiv by_page;
-  // First row of the 16 from `pos` on (a multiple of 16, so they are in one page).
-  // Where there is no such key (pos at or past len, or a page that is not one of the
-  // cache's) there = false and the row is the cache's first. Wave-uniform, and without
-  // a branch, at which the compiler would wait for all loads.
-  __device__ __forceinline__ int64_t row(int pos, int len, bool& there) const {
+  // The page of the 16 rows from `pos` on (a multiple of 16, so they are in one); -1 at
+  // or past len. Wave-uniform, as are the next two.
+  __device__ __forceinline__ int page(int pos, int len) const {
     typedef __attribute__((address_space(4))) const int32_t* Const;
-    const bool inside = pos < len;
-    const int w = inside ? by_page.div(pos) : 0;
-    const int64_t page = ((Const)(const void*)table)[w];
-    there = inside && page >= 0 && page < pages;
-    return there ? (page * H + h) * P + (pos - w * P) : 0;
+    const int at = ((Const)(const void*)table)[pos < len ? by_page.div(pos) : 0];
+    return pos < len ? at : -1;
   }
+  // The first of these rows. Where there is no such key (no page, or one that is not the
+  // cache's) there = false and the row is the cache's first: without a branch, at which
+  // the compiler would wait for all loads.
+  __device__ __forceinline__ int64_t row(int page, int pos, bool& there) const {
+    there = page >= 0 && page < pages;
+    return there ? ((int64_t)page * H + h) * P + (pos - by_page.div(pos) * P) : 0;
+  }
+  __device__ __forceinline__ int64_t row_at(int pos, int len, bool& there) const { return row(page(pos, len), pos, there); }
 };
 
 // What a wave loads of 32 keys, ahead of their use.
@@ -197,7 +200,7 @@ template <int NC> struct Step {
     const int lane = threadIdx.x & 63, g = lane >> 4;
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      const int64_t row = pg.row(first + 16 * u, len, there[u]);
+      const int64_t row = pg.row_at(first + 16 * u, len, there[u]);
       k[u].load_codes(c.k.codes + row * (16 * NC) + lane * (4 * NC));
       k[u].load_scales(c.k.scales + row * (2 * NC) + (lane & 15) * (2 * NC), g);
       ks[u] = *reinterpret_cast<const f32x4*>(c.k.sdec + row + 4 * g);
@@ -513,28 +516,36 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
 // ---------------------------------------------------------------- many rows
 //
 // A workgroup has 128 rows, 32 of them to a wave, and walks over their keys 64 at a
-// time. A wave decodes 16 of the 64 keys' rows to fp16 into LDS, one step ahead of
-// their use and with the codes of the step after that on their way, and all four
-// waves read them: keys as rows, values transposed.
+// time. A wave decodes 16 of the 64 keys' rows to fp16 into LDS, one step ahead of their
+// use and with the codes of the step after that on their way, and all four waves read
+// them: keys as rows, values transposed.
 
 typedef __attribute__((address_space(3))) s4* LdsS4;
 
 template <int NC> struct TileLds {
   static constexpr int kKeys = 64;
-  // rows in bytes: sixteen neighbouring rows' pieces of 16 bytes in different banks;
-  // four neighbouring rows' pieces of 64 bytes
-  static constexpr int kK = 64 * NC + 16, kV = 64 * NC % 128 ? 64 * NC : 64 * NC + 64;
+  // A key's row, in bytes: sixteen neighbouring rows' pieces of 16 bytes are in different
+  // banks. A value's: where it is a multiple of the banks' 256 bytes, its pieces of 16 are
+  // turned by 5 (row % 4), so that both four rows' pieces of 64 bytes (the transposed
+  // reads) and sixteen lanes' pieces of 16 (the writes) are.
+  static constexpr bool kTurned = NC % 4 == 0;
+  static constexpr int kK = 64 * NC + 16, kV = kTurned || 64 * NC % 128 ? 64 * NC : 64 * NC + 64;
   static constexpr int kSide = kKeys * (kK + kV);
   static constexpr int kOut = 32 * (64 * NC + 16);  // a wave's rows of the result
+  static constexpr int kAll = 2 * kSide > 4 * kOut ? 2 * kSide : 4 * kOut;
+  static __device__ __forceinline__ int value(int row, int piece16) {
+    return row * kV + 16 * (kTurned ? piece16 ^ (5 * (row & 3)) : piece16);
+  }
 };
 
+// Sixteen rows of either side, by one wave.
 template <int NC> struct TileStep {
   Quarter<NC> k, v;
-  float sdec;
+  float sdec;  // lanes 0-15 (of each half): of the keys, 16-31: of the values
   bool there;  // wave-uniform
-  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, int first, int wave, int len) {
+  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, int page, int first) {
     const int lane = threadIdx.x & 63;
-    const int64_t row = pg.row(first + 16 * wave, len, there);
+    const int64_t row = pg.row(page, first, there);
     k.load_codes(c.k.codes + row * (16 * NC) + lane * (4 * NC));
     k.load_scales(c.k.scales + row * (2 * NC) + (lane >> 2) * (2 * NC), lane & 3);
     v.load_codes(c.v.codes + row * (16 * NC) + lane * (4 * NC));
@@ -543,13 +554,24 @@ template <int NC> struct TileStep {
   }
 };
 
+// The order that the scheduler is asked for: `n` times a matrix instruction, `valu` others
+// and `reads` of LDS.
+#define FOS_INTERLEAVE(n, valu, reads)                      \
+  _Pragma("unroll") for (int i_ = 0; i_ < (n); i_++) {      \
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      \
+    __builtin_amdgcn_sched_group_barrier(0x002, valu, 0);   \
+    __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);  \
+  }
+
 template <int DT, int NC>
-__global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a) {
+__global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a) {
   typedef TileLds<NC> L;
   constexpr int D = 32 * NC;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * L::kSide > 4 * L::kOut ? 2 * L::kSide : 4 * L::kOut];
-  __shared__ __attribute__((aligned(16))) float sizes[2][3][L::kKeys];  // S_dec of keys times the scale, of values, its log2
-  __shared__ int gone[2][4];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[L::kAll];
+  // Per step: S_dec of keys times the scale, of values, its log2, each of 64 keys; which
+  // sixteens are not there; and places that the other lanes write to.
+  constexpr int kValues = L::kKeys, kLog2 = 2 * L::kKeys, kGone = 3 * L::kKeys, kNowhere = 3 * L::kKeys + 4;
+  __shared__ __attribute__((aligned(16))) float sizes[2][3 * L::kKeys + 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
   check_cache(a);
@@ -562,6 +584,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
   const int len = gt.g < a.c.B ? length_of(a.c, gt.g) : 0;
   const int r0 = gt.tile * 128 + wave * 32;
   const Row row = row_of(a, gt, h, r0 + col);
+  // keys that this lane's row sees; that all and any rows of the wave, and any of the workgroup, see
   int limit = len, least = len, most = len, all = len;
   if (a.causal) {
     limit = max(0, min(len, len - n + row.place + 1));
@@ -586,73 +609,94 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
   const Pages pg{a.c.table + (int64_t)(gt.g < a.c.B ? gt.g : 0) * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
 
   TileStep<NC> st;
-  // a step's rows, decoded, to its side of the LDS
+  int page = 0;  // of this wave's rows of the step that is loaded next
+  const int my_key = 16 * wave + (lane >> 2), my_size = 16 * wave + (lane & 15);
+  const int to_size = lane < 16 ? my_size : lane < 32 ? kValues + my_size : kNowhere;
+  const int to_log2 = lane >= 16 && lane < 32 ? kLog2 + my_size : kNowhere + 1;
+  const int to_gone = lane == 0 ? kGone + wave : kNowhere + 2;
+  // the keys' scale goes with their S_dec, so that what is left for a query is its power of two
+  const float size_by = lane < 16 ? a.scale_log2 : 1.0f;
+  // This wave's rows of a step, decoded, to the step's side of the LDS, without a branch, so that
+  // it can run beside matrix instructions. Zeros where there is no key: a stale scale may be a NaN.
   auto put = [&](int step) {
-    const int side = step & 1, key = 16 * wave + (lane >> 2), first = step * L::kKeys;
-    const bool none = !st.there || first + key >= len;
-    if (none) st.k.scales = st.v.scales = 0;  // a stale scale may be a NaN
+    const int side = step & 1, first = step * L::kKeys;
+    if (!st.there || first + my_key >= len) st.k.scales = st.v.scales = 0;
     Frag f[NC];
-    uint8_t* kp = lds + side * L::kSide + key * L::kK + (lane & 3) * 16 * NC;
+    uint8_t* base = lds + side * L::kSide;
     st.k.decode(lane & 3, f);
 #pragma unroll
-    for (int c = 0; c < NC; c++) *reinterpret_cast<u32x4*>(kp + 16 * c) = u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
-    uint8_t* vp = lds + side * L::kSide + L::kKeys * L::kK + key * L::kV + (lane & 3) * 16 * NC;
+    for (int c = 0; c < NC; c++)
+      *reinterpret_cast<u32x4*>(base + my_key * L::kK + 16 * ((lane & 3) * NC + c)) =
+          u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
     st.v.decode(lane & 3, f);
 #pragma unroll
-    for (int c = 0; c < NC; c++) *reinterpret_cast<u32x4*>(vp + 16 * c) = u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
-    if (lane < 32) {
-      const int j = 16 * wave + (lane & 15);
-      const float S = !st.there || first + j >= len ? 0.0f : st.sdec;
-      // the scale with the keys', so that what is left for a query is its power of two
-      sizes[side][lane >> 4][j] = lane < 16 ? S * a.scale_log2 : S;
-      if (lane >= 16) sizes[side][2][j] = log2_of(S);
-      if (lane == 0) gone[side][wave] = !st.there;
-    }
+    for (int c = 0; c < NC; c++)
+      *reinterpret_cast<u32x4*>(base + L::kKeys * L::kK + L::value(my_key, (lane & 3) * NC + c)) =
+          u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
+    const float S = !st.there || first + my_size >= len ? 0.0f : st.sdec;
+    sizes[side][to_size] = S * size_by;
+    sizes[side][to_log2] = log2_of(S);
+    sizes[side][to_gone] = st.there ? 0.0f : 1.0f;
+  };
+  auto load = [&](int step) {  // past the last step: the cache's first rows, which put() makes zeros
+    const int first = step * L::kKeys + 16 * wave;
+    st.load(a.c, pg, page, first);
+    page = pg.page(first + L::kKeys, len);
   };
 
   if (from < to) {
-    st.load(a.c, pg, from * L::kKeys, wave, len);
+    page = pg.page(from * L::kKeys + 16 * wave, len);
+    load(from);
     put(from);
-    st.load(a.c, pg, (from + 1) * L::kKeys, wave, len);
+    load(from + 1);
   }
   __syncthreads();
   for (int s = from; s < to; s++) {
     const int side = s & 1, first = s * L::kKeys;
-    if (s + 1 < to) {
-      put(s + 1);
-      st.load(a.c, pg, (s + 2) * L::kKeys, wave, len);  // past the last step: the cache's first rows, unused
-    }
+    const float* size = sizes[side];
     if (first < most) {
       const uint8_t* kp = lds + side * L::kSide + col * L::kK + 16 * half;
       f32x16 x[2];
+      Frag kf[2][2 * NC];
+      const f32x4 absent = *reinterpret_cast<const f32x4*>(size + kGone);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int kb = 0; kb < 2; kb++)
+#pragma unroll
+        for (int c = 0; c < 2 * NC; c++) {
+          const u32x4 t = *reinterpret_cast<const u32x4*>(kp + 32 * kb * L::kK + 32 * c);
+          kf[kb][c].u[0] = t.x, kf[kb][c].u[1] = t.y, kf[kb][c].u[2] = t.z, kf[kb][c].u[3] = t.w;
+        }
 #pragma unroll
       for (int kb = 0; kb < 2; kb++) {
 #pragma unroll
         for (int i = 0; i < 16; i++) x[kb][i] = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 2 * NC; c++) {
-          Frag f;
-          const u32x4 t = *reinterpret_cast<const u32x4*>(kp + 32 * kb * L::kK + 32 * c);
-          f.u[0] = t.x, f.u[1] = t.y, f.u[2] = t.z, f.u[3] = t.w;
-          x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.h, q[c].h, x[kb], 0, 0, 0);
-        }
+        for (int c = 0; c < 2 * NC; c++)
+          x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[kb][c].h, q[c].h, x[kb], 0, 0, 0);
       }
+      put(s + 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+      FOS_INTERLEAVE(4 * NC - 4, 5, 1)
+      FOS_INTERLEAVE(4, 5, 0)
+      __builtin_amdgcn_sched_barrier(0);
+      load(s + 2);
       // a lane's sixteen keys of 32: 8b + 4 half + 0..3
 #pragma unroll
       for (int kb = 0; kb < 2; kb++)
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-          const f32x4 ks = *reinterpret_cast<const f32x4*>(&sizes[side][0][32 * kb + 8 * b + 4 * half]);
+          const f32x4 ks = *reinterpret_cast<const f32x4*>(size + 32 * kb + 8 * b + 4 * half);
 #pragma unroll
           for (int i = 0; i < 4; i++) x[kb][4 * b + i] *= ks[i];
         }
-      if (first + L::kKeys > least || gone[side][0] + gone[side][1] + gone[side][2] + gone[side][3]) {
+      if (first + L::kKeys > least || __builtin_amdgcn_readfirstlane(__float_as_int(absent[0] + absent[1] + absent[2] + absent[3]))) {
 #pragma unroll
         for (int kb = 0; kb < 2; kb++)
 #pragma unroll
           for (int b = 0; b < 4; b++) {
-            const int j = 32 * kb + 8 * b + 4 * half;
-            const int past = gone[side][j >> 4] ? 0 : limit - first - j;  // keys from here on are not seen
+            const int j = 32 * kb + 8 * b;
+            const int past = absent[j >> 4] != 0.0f ? 0 : limit - first - j - 4 * half;  // keys from here on are not seen
 #pragma unroll
             for (int i = 0; i < 4; i++) x[kb][4 * b + i] = i < past ? x[kb][4 * b + i] : -__builtin_huge_valf();
           }
@@ -662,7 +706,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
       for (int kb = 0; kb < 2; kb++)
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-          const f32x4 lv = *reinterpret_cast<const f32x4*>(&sizes[side][2][32 * kb + 8 * b + 4 * half]);
+          const f32x4 lv = *reinterpret_cast<const f32x4*>(size + kLog2 + 32 * kb + 8 * b + 4 * half);
 #pragma unroll
           for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, __builtin_fmaf(x[kb][4 * b + i], undo, lv[i]));
         }
@@ -677,12 +721,25 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
 #pragma unroll
           for (int i = 0; i < 16; i++) o[t][i] *= f;
       }
-      Frag p[2][2];
+      // a sixteen of lanes reads four keys' rows, 16 values of each: which four, which half of 32 values
+      const int i16 = lane & 15;
+      const uint8_t* vp = lds + side * L::kSide + L::kKeys * L::kK + 8 * (i16 & 1);
+      Frag vf[4][NC], p[4];
+      auto read_values = [&](int c) {
 #pragma unroll
-      for (int kb = 0; kb < 2; kb++)
+        for (int t = 0; t < NC; t++)
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            const int key = 16 * c + 8 * u + 4 * half + (i16 >> 2), at = 4 * t + 2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1);
+            const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)(vp + L::value(key, at))));
+            vf[c][t].u[2 * u] = y.x;
+            vf[c][t].u[2 * u + 1] = y.y;
+          }
+      };
+      auto weigh = [&](int kb) {
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-          const f32x4 vs = *reinterpret_cast<const f32x4*>(&sizes[side][1][32 * kb + 8 * b + 4 * half]);
+          const f32x4 vs = *reinterpret_cast<const f32x4*>(size + kValues + 32 * kb + 8 * b + 4 * half);
           float w[4];
 #pragma unroll
           for (int i = 0; i < 4; i++) {
@@ -690,29 +747,34 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
             l += e;
             w[i] = e * vs[i];
           }
-          p[kb][b >> 1].u[2 * (b & 1)] = pack_f16(w[0], w[1]);
-          p[kb][b >> 1].u[2 * (b & 1) + 1] = pack_f16(w[2], w[3]);
-        }
-      // lanes of sixteen: which half of the keys' fours, which half of 32 values
-      const int i16 = lane & 15;
-      const uint8_t* vp = lds + side * L::kSide + L::kKeys * L::kK + (4 * half + (i16 >> 2)) * L::kV +
-                          ((lane >> 4) & 1) * 32 + (i16 & 3) * 8;
 #pragma unroll
-      for (int kb = 0; kb < 2; kb++)
-#pragma unroll
-        for (int c = 0; c < 2; c++)
-#pragma unroll
-          for (int t = 0; t < NC; t++) {
-            Frag f;
-#pragma unroll
-            for (int u = 0; u < 2; u++) {
-              const u32x2 y = __builtin_bit_cast(
-                  u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)(vp + (32 * kb + 16 * c + 8 * u) * L::kV + 64 * t)));
-              f.u[2 * u] = y.x;
-              f.u[2 * u + 1] = y.y;
-            }
-            o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.h, p[kb][c].h, o[t], 0, 0, 0);
+          for (int i = 0; i < 2; i++) {
+            const f32x2 two = {w[2 * i], w[2 * i + 1]};
+            p[2 * kb + (b >> 1)].u[2 * (b & 1) + i] = bits(__builtin_convertvector(two, h2));
           }
+        }
+      };
+      auto add = [&](int c) {
+#pragma unroll
+        for (int t = 0; t < NC; t++) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[c][t].h, p[c].h, o[t], 0, 0, 0);
+      };
+      read_values(0);
+      __builtin_amdgcn_sched_barrier(0);
+      weigh(0);
+      read_values(1);
+      __builtin_amdgcn_sched_barrier(0);
+      add(0);
+      add(1);
+      weigh(1);
+      read_values(2);
+      FOS_INTERLEAVE(2 * NC, 72 / (2 * NC), 2)
+      __builtin_amdgcn_sched_barrier(0);
+      read_values(3);
+      add(2);
+      add(3);
+    } else {
+      put(s + 1);
+      load(s + 2);
     }
     __syncthreads();
   }
@@ -737,7 +799,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
   // the result's rows turn through the wave's own LDS to whole pieces of 16 bytes
   const float by = l == 0.0f ? 0.0f : 1.0f / l;
   constexpr int kRow = 64 * NC + 16;
-  uint8_t* mine = lds + wave * L::kOut;
+  uint8_t* turned = lds + wave * L::kOut;
 #pragma unroll
   for (int t = 0; t < NC; t++)
 #pragma unroll
@@ -747,7 +809,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
       for (int i = 0; i < 4; i++) v[i] = o[t][4 * b + i] * by;
       const u32x2 w = DT == kBF16 ? u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}
                                   : u32x2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
-      *reinterpret_cast<u32x2*>(mine + col * kRow + 64 * t + 16 * b + 8 * half) = w;
+      *reinterpret_cast<u32x2*>(turned + col * kRow + 64 * t + 16 * b + 8 * half) = w;
     }
   wave_lds_order();
 #pragma unroll
@@ -756,7 +818,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 2 : 1) void k_kv_tile(KvAttendArgs a
     const Row to_row = row_of(a, gt, h, r0 + r);
     if (to_row.have)
       *reinterpret_cast<u32x4*>((uint16_t*)a.out + (to_row.token * ((int64_t)a.c.H * a.G) + to_row.head) * D + 8 * piece16) =
-          *reinterpret_cast<const u32x4*>(mine + r * kRow + 16 * piece16);
+          *reinterpret_cast<const u32x4*>(turned + r * kRow + 16 * piece16);
   }
   if (half == 0 && row.have && a.lse) a.lse[at] = l == 0.0f ? -__builtin_huge_valf() : (m + __log2f(l)) * kLn2;
 }
@@ -868,7 +930,7 @@ template <int NC> struct KeyStep {
     int64_t row[2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      row[u] = pg.row(first + 16 * u, len, there[u]);
+      row[u] = pg.row_at(first + 16 * u, len, there[u]);
       k[u].load_codes(c.k.codes + row[u] * (16 * NC) + lane * (4 * NC));
     }
     const int64_t mine = ((lane & 16) ? row[1] : row[0]) + (lane & 15);
