@@ -38,6 +38,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) s4* LdsS4;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -186,52 +187,33 @@ struct Pages {
   __device__ __forceinline__ int64_t row_at(int pos, int len, bool& there) const { return row(page(pos, len), pos, there); }
 };
 
-// What a wave loads of 32 keys, ahead of their use.
+// What a wave loads of 32 keys, ahead of their use. Codes and the value rows' scales come
+// with four lanes to a row, so that the wave's 64 pieces are neighbours in memory, the
+// keys' scales as the matrix instruction wants them, and S_dec one to a lane: of the keys
+// to the lower half, of the values to the upper.
 template <int NC> struct Step {
   Quarter<NC> k[2], v[2];
-  f32x4 ks[2], vs[2];
+  float sdec;
   bool there[2];  // wave-uniform: a half's keys, but for those past the end
 
-  // Codes and the value rows' scales come with four lanes to a row, so that the
-  // wave's 64 pieces are neighbours in memory; the keys' scales and S_dec as the
-  // matrix instruction wants them.
-  template <bool VALUES>
-  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, int first, int len) {
+  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, const int (&page)[2], int first) {
     const int lane = threadIdx.x & 63, g = lane >> 4;
+    int64_t row[2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      const int64_t row = pg.row_at(first + 16 * u, len, there[u]);
-      k[u].load_codes(c.k.codes + row * (16 * NC) + lane * (4 * NC));
-      k[u].load_scales(c.k.scales + row * (2 * NC) + (lane & 15) * (2 * NC), g);
-      ks[u] = *reinterpret_cast<const f32x4*>(c.k.sdec + row + 4 * g);
-      if constexpr (VALUES) {
-        v[u].load_codes(c.v.codes + row * (16 * NC) + lane * (4 * NC));
-        v[u].load_scales(c.v.scales + row * (2 * NC) + (lane >> 2) * (2 * NC), lane & 3);
-        vs[u] = *reinterpret_cast<const f32x4*>(c.v.sdec + row + 4 * g);
-      }
+      row[u] = pg.row(page[u], first + 16 * u, there[u]);
+      k[u].load_codes(c.k.codes + row[u] * (16 * NC) + lane * (4 * NC));
+      k[u].load_scales(c.k.scales + row[u] * (2 * NC) + (lane & 15) * (2 * NC), g);
+      v[u].load_codes(c.v.codes + row[u] * (16 * NC) + lane * (4 * NC));
+      v[u].load_scales(c.v.scales + row[u] * (2 * NC) + (lane >> 2) * (2 * NC), lane & 3);
     }
+    sdec = ((lane & 32) ? c.v.sdec : c.k.sdec)[((lane & 16) ? row[1] : row[0]) + (lane & 15)];
   }
 };
 
 // 16 x 4 pieces of a wave's LDS, a row's four pieces turned by its quad, so that the
 // lanes that an access serves together reach different banks.
 __device__ __forceinline__ int piece(int key, int part) { return key * 4 + (part ^ ((4 - (key >> 2)) & 3)); }
-
-template <int NC>
-__device__ __forceinline__ void turn_keys(uint8_t* lds, const Step<NC>& st, Frag (*f)[NC]) {
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  wave_lds_order();
-#pragma unroll
-  for (int u = 0; u < 2; u++) st.k[u].store_codes(lds + u * 256 * NC + 4 * NC * piece(lane >> 2, lane & 3));
-  wave_lds_order();
-#pragma unroll
-  for (int u = 0; u < 2; u++) {
-    Quarter<NC> t;
-    t.load_codes(lds + u * 256 * NC + 4 * NC * piece(lane & 15, g));
-    t.scales = st.k[u].scales;
-    t.decode(g, f[u]);
-  }
-}
 
 // max over the lanes that share a row of q: the four of a column, or its two halves.
 template <bool QUARTERS>
@@ -314,9 +296,17 @@ __device__ __forceinline__ void check_cache(const KvAttendArgs& a) {
 // decoded into it and read back transposed.
 
 template <int NC> struct StreamLds {
-  static constexpr int kRow = 64 * NC + 32;           // a value row in fp16, and a step of the banks
+  // A value row in fp16. Where it is a multiple of the banks' 256 bytes its pieces of 16
+  // are turned by its number, so that the lanes that an access serves together reach
+  // different banks; else it is a step of the banks apart from the next.
+  static constexpr bool kTurned = NC % 4 == 0;
+  static constexpr int kRow = kTurned ? 64 * NC : 64 * NC + 32;
+  static __device__ __forceinline__ int value(int row, int piece16) {
+    return row * kRow + 16 * (kTurned ? piece16 ^ (5 * (row & 3)) ^ ((row >> 1) & 2) : piece16);
+  }
   static constexpr int kKeys = 512 * NC;              // codes of 32 keys
-  static constexpr int kWave = kKeys + 32 * kRow;
+  static constexpr int kSizes = kKeys + 32 * kRow;    // S_dec of 32 keys and of their values
+  static constexpr int kWave = kSizes + 256;
   static constexpr int kJoinRow = 32 * NC + 4;        // floats
   static constexpr int kJoin = 4 * 16 * kJoinRow * 4 + 4 * 16 * 8;
   static constexpr int kAll = 4 * kWave > kJoin ? 4 * kWave : kJoin;
@@ -366,63 +356,84 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
   float m = kLowest, l = 0.0f;
   uint8_t* keys = lds + wave * L::kWave;
   uint8_t* vals = keys + L::kKeys;
+  float* sizes = reinterpret_cast<float*>(keys + L::kSizes);
   const Pages pg{a.c.table + (int64_t)(gt.g < a.c.B ? gt.g : 0) * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
 
+  // pages a step ahead of the loads, loads a step ahead of their use; past the last step
+  // the cache's first rows, unused
   Step<NC> next;
+  int page[2];
   int s = from + __builtin_amdgcn_readfirstlane(wave);
-  next.template load<true>(a.c, pg, 32 * s, len);
+  auto find = [&](int first) {
+#pragma unroll
+    for (int u = 0; u < 2; u++) page[u] = pg.page(first + 16 * u, len);
+  };
+  find(32 * s);
+  if (s < to) {
+    next.load(a.c, pg, page, 32 * s);
+    find(32 * (s + 4));
+  }
   while (s < to) {
-    Step<NC> st = next;
+    const Step<NC> st = next;
     const int first = 32 * s;
     s += 4;
-    next.template load<true>(a.c, pg, 32 * s, len);  // past the last step: the cache's first rows, unused
+    next.load(a.c, pg, page, 32 * s);
+    find(32 * (s + 4));
 
-    Frag kf[2][NC];
-    turn_keys<NC>(keys, st, kf);
+    const bool missing = first + 32 > len || !st.there[0] || !st.there[1];
+    wave_lds_order();
+#pragma unroll
+    for (int u = 0; u < 2; u++) st.k[u].store_codes(keys + u * 256 * NC + 4 * NC * piece(lane >> 2, lane & 3));
+    sizes[lane] = st.sdec;
+    wave_lds_order();
     f32x4 sc[2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
+      Quarter<NC> t;
+      t.load_codes(keys + u * 256 * NC + 4 * NC * piece(col, g));
+      t.scales = st.k[u].scales;
+      Frag kf[NC];
+      t.decode(g, kf);
       sc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < NC; c++) sc[u] = mfma16(kf[u][c], q[c], sc[u]);
+      for (int c = 0; c < NC; c++) sc[u] = mfma16(kf[c], q[c], sc[u]);
     }
     // value rows to fp16, zero where there is no key: a stale scale may be a NaN
-    const bool missing = first + 32 > len || !st.there[0] || !st.there[1];
-    if (missing) {
-#pragma unroll
-      for (int u = 0; u < 2; u++)
-        if (!st.there[u] || first + 16 * u + (lane >> 2) >= len) st.v[u].scales = 0;
-    }
 #pragma unroll
     for (int u = 0; u < 2; u++) {
+      Quarter<NC> t = st.v[u];
+      if (missing && (!st.there[u] || first + 16 * u + (lane >> 2) >= len)) t.scales = 0;
       Frag vf[NC];
-      st.v[u].decode(lane & 3, vf);
+      t.decode(lane & 3, vf);
 #pragma unroll
       for (int c = 0; c < NC; c++)
-        *reinterpret_cast<u32x4*>(vals + (16 * u + (lane >> 2)) * L::kRow + (lane & 3) * 16 * NC + 16 * c) =
+        *reinterpret_cast<u32x4*>(vals + L::value(16 * u + (lane >> 2), (lane & 3) * NC + c)) =
             u32x4{vf[c].u[0], vf[c].u[1], vf[c].u[2], vf[c].u[3]};
     }
     // scores to weights
     float z[8], top = kLowest;
+    f32x4 vs[2];
 #pragma unroll
-    for (int u = 0; u < 2; u++)
+    for (int u = 0; u < 2; u++) {
+      const f32x4 ks = *reinterpret_cast<const f32x4*>(sizes + 16 * u + 4 * g);
+      vs[u] = *reinterpret_cast<const f32x4*>(sizes + 32 + 16 * u + 4 * g);
 #pragma unroll
-      for (int i = 0; i < 4; i++) z[4 * u + i] = sc[u][i] * (st.ks[u][i] * qf);
-    const bool partly = first + 32 > least || missing;
-    if (partly) {
+      for (int i = 0; i < 4; i++) z[4 * u + i] = sc[u][i] * (ks[i] * qf);
+    }
+    if (first + 32 > least || missing) {
 #pragma unroll
       for (int u = 0; u < 2; u++)
 #pragma unroll
         for (int i = 0; i < 4; i++)
           if (!st.there[u] || first + 16 * u + 4 * g + i >= limit) {
             z[4 * u + i] = -__builtin_huge_valf();
-            st.vs[u][i] = 0.0f;  // which may be a stale NaN
+            vs[u][i] = 0.0f;  // which may be a stale NaN
           }
     }
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, z[4 * u + i] + log2_of(st.vs[u][i]));
+      for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, z[4 * u + i] + log2_of(vs[u][i]));
     top = col_max(top);
     if (__any(top > m + kLag)) {
       const float now = __builtin_fmaxf(m, top);
@@ -438,20 +449,21 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
     for (int i = 0; i < 8; i++) {
       const float e = __builtin_amdgcn_exp2f(z[i] - m);
       l += e;
-      w[i] = e * st.vs[i / 4][i % 4];
+      w[i] = e * vs[i / 4][i % 4];
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) p.u[i] = pack_f16(w[2 * i], w[2 * i + 1]);
+    for (int i = 0; i < 4; i++) {
+      const f32x2 two = {w[2 * i], w[2 * i + 1]};
+      p.u[i] = bits(__builtin_convertvector(two, h2));
+    }
     wave_lds_order();
 #pragma unroll
     for (int t = 0; t < DT16; t++) {
       Frag v;
-      const uint8_t* at = vals + (4 * g + (col >> 2)) * L::kRow + 32 * t + (col & 3) * 8;
 #pragma unroll
       for (int u = 0; u < 2; u++) {
-        const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s4*)(at + 16 * u * L::kRow));
-        const u32x2 y = __builtin_bit_cast(u32x2, x);
+        const uint8_t* at = vals + L::value(16 * u + 4 * g + (col >> 2), 2 * t + ((col >> 1) & 1)) + 8 * (col & 1);
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)at));
         v.u[2 * u] = y.x;
         v.u[2 * u + 1] = y.y;
       }
@@ -519,8 +531,6 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
 // time. A wave decodes 16 of the 64 keys' rows to fp16 into LDS, one step ahead of their
 // use and with the codes of the step after that on their way, and all four waves read
 // them: keys as rows, values transposed.
-
-typedef __attribute__((address_space(3))) s4* LdsS4;
 
 template <int NC> struct TileLds {
   static constexpr int kKeys = 64;
