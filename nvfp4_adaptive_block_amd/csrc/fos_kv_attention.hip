@@ -272,8 +272,9 @@ __device__ __forceinline__ Row row_of(const KvAttendArgs& a, const GroupTile& gt
   return o;
 }
 
-__device__ __forceinline__ int length_of(const KvCache& c, int b) {
-  const int n = c.lens[b], cap = c.W * c.P;
+// A length, cut to what the table holds.
+__device__ __forceinline__ int length_of(const KvCache& c, int n) {
+  const int cap = c.W * c.P;
   return n < 0 ? 0 : n > cap ? cap : n;
 }
 
@@ -285,6 +286,17 @@ __device__ __forceinline__ void check_cache(const KvAttendArgs& a) {
     if (e < p || e > a.T) atomicOr(a.status, kStatusBadOffs);
     if (n < 0 || (int64_t)n > (int64_t)a.c.W * a.c.P) atomicOr(a.status, kStatusBadCache);
   }
+}
+
+// A workgroup's work, from its number: heads of the cache run fastest, so that eight of
+// them are on an XCD each, then the parts of the keys, so that a tile that there is not
+// leaves no XCD without work.
+struct Place {
+  int h, part, tile;
+};
+__device__ __forceinline__ Place place_of(const KvAttendArgs& a) {
+  const uint32_t r = blockIdx.x / (uint32_t)a.c.H;
+  return Place{(int)(blockIdx.x - r * a.c.H), (int)(r % (uint32_t)a.splits), (int)(r / (uint32_t)a.splits)};
 }
 
 // ---------------------------------------------------------------- few rows
@@ -328,11 +340,12 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
   constexpr int D = 32 * NC, DT16 = 2 * NC;  // tiles of 16 values
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
   check_cache(a);
-  const int h = blockIdx.x % a.c.H, tile = blockIdx.x / a.c.H, part = blockIdx.y;
-  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 16, tile, a.G);
+  const Place at_ = place_of(a);
+  const int h = at_.h, tile = at_.tile, part = at_.part;
+  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 16, tile, a.G, a.c.lens);
   if (gt.g < 0) return;
   const int n = gt.end - gt.start;
-  const int len = gt.g < a.c.B ? length_of(a.c, gt.g) : 0;
+  const int len = length_of(a.c, gt.value);  // of the tail 0
   const Row row = row_of(a, gt, h, gt.tile * 16 + col);
   // keys that this lane's row sees, and what all and any rows of the tile see
   int limit = len, least = len, most = len;
@@ -586,12 +599,12 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   const int half = lane >> 5, col = lane & 31;
   check_cache(a);
   // the last tiles of a sequence see the most keys: they start first
-  const int tiles = gridDim.x / a.c.H;
-  const int h = blockIdx.x % a.c.H, tile = tiles - 1 - blockIdx.x / a.c.H, part = blockIdx.y;
-  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 128, tile, a.G);
+  const Place at_ = place_of(a);
+  const int h = at_.h, tile = (int)gridDim.x / (a.c.H * a.splits) - 1 - at_.tile, part = at_.part;
+  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 128, tile, a.G, a.c.lens);
   if (gt.g < 0) return;
   const int n = gt.end - gt.start;
-  const int len = gt.g < a.c.B ? length_of(a.c, gt.g) : 0;
+  const int len = length_of(a.c, gt.value);  // of the tail 0
   const int r0 = gt.tile * 128 + wave * 32;
   const Row row = row_of(a, gt, h, r0 + col);
   // keys that this lane's row sees; that all and any rows of the wave, and any of the workgroup, see
@@ -834,12 +847,12 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
 }
 
 // Joins the parts of a row. A wave has a row where there are few parts, else a
-// workgroup of four waves, each with every fourth part.
+// workgroup of sixteen waves, each with every sixteenth part.
 template <int DT, int NC, int WAVES>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttendArgs a) {
+__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_kv_join(KvAttendArgs a) {
   constexpr int D = 32 * NC, kEach = (D + 63) / 64, kParts = WAVES == 1 ? 64 : kMaxParts;
-  __shared__ float share[4 * kParts];
-  __shared__ float sums[4][kEach * 64];
+  __shared__ float share[WAVES == 1 ? 4 * kParts : kParts];
+  __shared__ float sums[WAVES][kEach * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t rows = (int64_t)a.T * a.c.H * a.G;
   const int64_t at = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
@@ -856,21 +869,24 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttendArgs a) {
   }
   for (int d = 1; d < 64; d <<= 1) M = __builtin_fmaxf(M, __shfl_xor(M, d, 64));
   float sum = 0.0f;
-  float* f = share + wave * kParts;
+  float* f = WAVES == 1 ? share + wave * kParts : share;
 #pragma unroll
   for (int i = 0; i < kParts / 64; i++) {
     const float e = __builtin_amdgcn_exp2f(ml[i].x - M);
-    f[lane + 64 * i] = e;
+    if (WAVES == 1 || wave == 0) f[lane + 64 * i] = e;
     sum += e * ml[i].y;
   }
-  wave_lds_order();
+  if constexpr (WAVES > 1)
+    __syncthreads();
+  else
+    wave_lds_order();
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
   const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
   float v[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; i++) v[i] = 0.0f;
   // a part without a key holds zeros
-#pragma unroll 4
+#pragma unroll 8
   for (int s = WAVES == 1 ? 0 : wave; s < a.splits; s += WAVES) {
 #pragma unroll
     for (int i = 0; i < kEach; i++)
@@ -885,7 +901,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttendArgs a) {
     for (int i = 0; i < kEach; i++) {
       v[i] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; w++) v[i] += sums[w][lane + 64 * i];
+      for (int w = 0; w < WAVES; w++) v[i] += sums[w][lane + 64 * i];
     }
   }
 #pragma unroll
@@ -967,7 +983,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArg
   gt.end = a.offs[b];
   gt.start = gt.start < 0 ? 0 : gt.start > a.T ? a.T : gt.start;
   gt.end = gt.end < gt.start ? gt.start : gt.end > a.T ? a.T : gt.end;
-  const int n = gt.end - gt.start, len = length_of(a.c, b), rows = n * a.G;
+  const int n = gt.end - gt.start, len = length_of(a.c, a.c.lens[b]), rows = n * a.G;
   const Pages pg{a.c.table + (int64_t)b * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
   float* acc = a.acc + ((int64_t)b * a.c.H + h) * ((int64_t)a.c.W * a.c.P);
   uint8_t* mine = turn + wave * 512 * NC;
@@ -1062,13 +1078,13 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.T * a.G;
   const int per = kv_tiled(a.T, a.c.B, a.G) ? 128 : 16;
   const int64_t tiles = rows / per + a.c.B + 1;  // no fewer than the sequences' tiles and the tail's
-  const dim3 grid((unsigned)(tiles * a.c.H), (unsigned)a.splits);
+  const dim3 grid((unsigned)(tiles * a.c.H * a.splits));
   if (per == 128)
     k_kv_tile<DT, NC><<<grid, 256, 0, s>>>(a);
   else
     k_kv_stream<DT, NC><<<grid, 256, 0, s>>>(a);
   if (a.splits > 8)
-    k_kv_join<DT, NC, 4><<<dim3((unsigned)(rows * a.c.H)), 256, 0, s>>>(a);
+    k_kv_join<DT, NC, 16><<<dim3((unsigned)(rows * a.c.H)), 1024, 0, s>>>(a);
   else if (a.splits > 1)
     k_kv_join<DT, NC, 1><<<dim3((unsigned)((rows * a.c.H + 3) / 4)), 256, 0, s>>>(a);
   return hipGetLastError();
@@ -1099,13 +1115,18 @@ hipError_t run(bool attention, const KvAttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int kv_splits(int64_t T, int B, int H, int G, int D, int64_t max_len) {
-  (void)D;
+// Few rows: where the tiles alone fill the chip's 256 CUs, workgroups enough to even out
+// lengths (64 sequences of 2500 to 8192 tokens on 8 heads: 1024 workgroups 103 us, 2304 96);
+// else about as many as run at once (131072 keys for one token on 4 heads: 512 to 2304 25 to
+// 27 us, 384 30; 17 sequences of up to 2999 tokens, 12 heads of 64: 512 22.8, 1024 19.4, 1536
+// 21.2). A part has four steps at least, one to a wave (1001 keys: 8.2 us; of two 9.4, of
+// eight 9.7).
+int kv_splits(int64_t T, int B, int H, int G, int64_t max_len) {
   const bool tiled = kv_tiled(T, B, G);
-  const int64_t rows = tiled ? 128 : 16, step = tiled ? 64 : 32;
+  const int64_t rows = tiled ? 128 : 16, least = tiled ? 512 : 128;
   const int64_t per = (T * G / B + rows - 1) / rows, tiles = (per < 1 ? 1 : per) * B * H;
-  const int64_t most = (max_len + 8 * step - 1) / (8 * step);  // eight steps
-  int64_t s = (tiled ? 512 : 1024) / tiles;
+  const int64_t most = (max_len + least - 1) / least;
+  int64_t s = (tiled ? 512 : tiles >= 256 ? 2304 : 1024) / tiles;
   if (s > most) s = most;
   return (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
 }

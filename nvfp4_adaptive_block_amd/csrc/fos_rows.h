@@ -23,6 +23,7 @@ __device__ __forceinline__ void wave_lds_order() {
 // last group.
 struct GroupTile {
   int start, end, g, tile;
+  int value;  // the group's, where find_group_tile is given one per group
 };
 
 // What a workgroup works on: rows [m0, end) of x with weight g; g < 0: no
@@ -53,13 +54,15 @@ __device__ __forceinline__ int wave_scan(int v) {
 // counts. Offsets are clamped to [previous, M], so a bad one sends no access out
 // of bounds. Each row of a group stands for `per` rows of its tiles. M per is at
 // most 2^31 - 1 less a tile, so row and tile counts fit an int.
-__device__ __forceinline__ GroupTile find_group_tile(const int32_t* offs, int G, int M, int rows, int t, int per) {
+__device__ __forceinline__ GroupTile find_group_tile(const int32_t* offs, int G, int M, int rows, int t, int per,
+                                                     const int32_t* values = nullptr) {
   const int lane = threadIdx.x & 63;
   int prev = 0, tiles = 0;  // of the groups before this batch
   for (int base = 0; base <= G; base += 64) {
     const int g = base + lane;
     const bool have = g <= G;
     int end = g < G ? offs[g] : M;
+    const int value = values && g < G ? values[g] : 0;
     int start = g == 0 ? 0 : g <= G ? offs[g - 1] : M;
     if (__ballot(have && (start < prev || end < start || end > M))) {
       // offsets that break the contract: running maximum of the clamped ends
@@ -82,12 +85,13 @@ __device__ __forceinline__ GroupTile find_group_tile(const int32_t* offs, int G,
       r.end = __builtin_amdgcn_readlane(end, l);
       r.g = base + l;
       r.tile = t - first;
+      r.value = __builtin_amdgcn_readlane(value, l);
       return r;
     }
     tiles += __builtin_amdgcn_readlane(sum, 63);
     prev = __builtin_amdgcn_readlane(end, 63);
   }
-  return GroupTile{0, 0, -1, 0};
+  return GroupTile{0, 0, -1, 0, 0};
 }
 
 __device__ inline RowTile find_tile(const int32_t* offs, int G, int M, int rows, int t) {
