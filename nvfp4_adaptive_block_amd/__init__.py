@@ -10,7 +10,9 @@ a gfx950, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Sequence
 
 import torch
@@ -64,16 +66,6 @@ class _Operand(ctypes.Structure):
 class _Epilogue(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32),
                 ("activation", ctypes.c_int32)]
-
-
-class _KvRows(ctypes.Structure):
-    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("sdec", ctypes.c_void_p)]
-
-
-class _KvCache(ctypes.Structure):
-    _fields_ = [("k", _KvRows), ("v", _KvRows), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
-                ("pages", ctypes.c_int64), ("B", ctypes.c_int32), ("W", ctypes.c_int32), ("H", ctypes.c_int32),
-                ("P", ctypes.c_int32), ("D", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -827,44 +819,90 @@ def fos_balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, slope: 
 # offs int32[B] the end row of each sequence's tokens among the packed ones.
 
 
-def _kv_rows(rows, name, device, shape):
-    codes, scales, sdec = rows
-    if shape is None:
-        if codes.dim() != 4:
-            raise ValueError(f"{name}'s codes must have shape ['pages', 'H', 'P', 'D / 2'], got {list(codes.shape)}")
-        shape = codes.shape
-    pages, H, P, half = shape
-    return _KvRows(_match(codes, f"{name}'s codes", device, shape, torch.uint8),
-                   _match(scales, f"{name}'s scales", device, (pages, H, P, half // 8), torch.uint8),
-                   _match(sdec, f"{name}'s sdec", device, (pages, H, P), torch.float32))
+# A fos_kv_cache, packed: a ctypes structure of the same fields takes three times as long
+# to fill. An instance of bytes is passed as its address.
+_KV_CACHE = struct.Struct("8Pq5i4x")
+
+
+def _kv_device(index):
+    return torch.device("cuda", index) if index >= 0 else torch.device("cpu")
+
+
+def _kv_at(t, name, index, shape, dtype) -> int:
+    """Address of a contiguous tensor on device `index`, checked."""
+    if t.get_device() != index or t.dtype is not dtype or not t.is_contiguous() or t.shape != shape:
+        _mismatch(t, name, _kv_device(index), shape, dtype)
+    return t.data_ptr()
 
 
 def _kv_cache(k, v, table, lens):
-    """(_KvCache, device, B, W, H, P, D); v may be None."""
-    codes = k[0]
-    dev = codes.device
-    if not codes.is_cuda:
+    """(packed fos_kv_cache, device index, B, W, H, P, D); v may be None."""
+    codes, scales, sdec = k
+    index = codes.get_device()
+    if index < 0:
         raise ValueError("the cache must be on a device")
-    kr = _kv_rows(k, "k_cache", dev, None)
-    pages, H, P, half = codes.shape
-    vr = kr if v is None else _kv_rows(v, "v_cache", dev, codes.shape)
+    shape = codes.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_cache's codes must have shape ['pages', 'H', 'P', 'D / 2'], got {list(shape)}")
+    pages, H, P, half = shape
+    of_scales, of_sdec = (pages, H, P, half // 8), (pages, H, P)
+    at = [_kv_at(codes, "k_cache's codes", index, shape, torch.uint8),
+          _kv_at(scales, "k_cache's scales", index, of_scales, torch.uint8),
+          _kv_at(sdec, "k_cache's sdec", index, of_sdec, torch.float32)]
+    if v is None:
+        at += at
+    else:
+        codes, scales, sdec = v
+        at += (_kv_at(codes, "v_cache's codes", index, shape, torch.uint8),
+               _kv_at(scales, "v_cache's scales", index, of_scales, torch.uint8),
+               _kv_at(sdec, "v_cache's sdec", index, of_sdec, torch.float32))
     if table.dim() != 2:
         raise ValueError(f"table must have shape ['B', 'W'], got {list(table.shape)}")
     B, W = table.shape
-    return (_KvCache(kr, vr, _match(table, "table", dev, None, torch.int32), _match(lens, "lens", dev, (B,), torch.int32),
-                     pages, B, W, H, P, 2 * half), dev, B, W, H, P, 2 * half)
+    return (_KV_CACHE.pack(*at, _kv_at(table, "table", index, (B, W), torch.int32),
+                           _kv_at(lens, "lens", index, (B,), torch.int32), pages, B, W, H, P, 2 * half),
+            index, B, W, H, P, 2 * half)
 
 
-def _kv_tokens(x, name, device, heads, D):
+def _kv_tokens(x, name, index, heads, D):
     """Address and token stride of [T, heads, D] rows, whose tokens may lie apart."""
-    if x.dim() != 3 or x.shape[2] != D or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{name} must have shape ['T', {heads or 'heads'}, {D}], got {list(x.shape)}")
-    stride = x.stride()
-    if x.device != device or (x.numel() and (stride[2] != 1 or (x.shape[1] > 1 and stride[1] != D))):
-        if x.device != device:
-            raise ValueError(f"{name} is on {x.device}, expected {device}")
-        raise ValueError(f"{name}'s tokens must be contiguous, got strides {list(stride)}")
-    return x.data_ptr(), stride[0] if x.shape[0] > 1 else x.shape[1] * D
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must have shape ['T', {heads or 'heads'}, {D}], got {list(shape)}")
+    if x.get_device() != index:
+        raise ValueError(f"{name} is on {x.device}, expected cuda:{index}")
+    T, n, _ = shape
+    apart, between, inner = x.stride()
+    if T * n and (inner != 1 or (n > 1 and between != D)):
+        raise ValueError(f"{name}'s tokens must be contiguous, got strides {[apart, between, inner]}")
+    return x.data_ptr(), apart if T > 1 else n * D
+
+
+def _kv_call(index, fn, *args):
+    """fn(*args, current stream of the device) with the device current; raises on an error code."""
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        _check(rc)
+
+
+def _kv_room(workspace, need, index):
+    """(address, bytes, tensor) of a workspace: the caller's, or a new one."""
+    if workspace is None:
+        if need <= 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=_kv_device(index))
+        return workspace.data_ptr(), need, workspace
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        _mismatch(workspace, "workspace", _kv_device(index), None, None)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _kv_status(status, index):
+    return None if status is None else _status_pointer(status, _kv_device(index))
 
 
 def fos_kv_cache(pages: int, heads: int, page: int, dim: int, device="cuda"):
@@ -875,6 +913,11 @@ def fos_kv_cache(pages: int, heads: int, page: int, dim: int, device="cuda"):
             torch.zeros(pages, heads, page, dtype=torch.float32, device=device))
 
 
+@functools.lru_cache(maxsize=None)
+def _kv_config(**knobs):
+    return ctypes.byref(config(scale_gran="row", **knobs))
+
+
 def fos_kv_append(k: torch.Tensor, v: torch.Tensor, offs: torch.Tensor, k_cache, v_cache, table: torch.Tensor,
                   lens: torch.Tensor, *, values: bool = False, k_out=None, v_out=None, status=None, **knobs):
     """Quantize the rows k and v [T, H, D] of new tokens into the pages of their
@@ -883,29 +926,32 @@ def fos_kv_append(k: torch.Tensor, v: torch.Tensor, offs: torch.Tensor, k_cache,
     what the cache then holds for these rows in k's dtype, with values=True or
     where the outputs are passed, else None. ``knobs`` as for fos_quantize
     (1x16 blocks, a float32 scale per row)."""
-    cache, dev, B, _, H, _, D = _kv_cache(k_cache, v_cache, table, lens)
-    kp, k_stride = _kv_tokens(k, "k", dev, H, D)
-    vp, v_stride = _kv_tokens(v, "v", dev, H, D)
+    cache, index, B, _, H, _, D = _kv_cache(k_cache, v_cache, table, lens)
+    kp, k_stride = _kv_tokens(k, "k", index, H, D)
+    vp, v_stride = _kv_tokens(v, "v", index, H, D)
     shape, dtype = k.shape, k.dtype
     code = _float_type(k, "k")
-    if v.shape != shape or v.dtype != dtype:
+    if v.shape != shape or v.dtype is not dtype:
         raise ValueError(f"v must be {dtype} {list(shape)} as k is, got {v.dtype} {list(v.shape)}")
     if values:
-        k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
-    cfg = config(scale_gran="row", **knobs)
-    _call(dev, load_library().fos_kv_append, kp, vp, code, shape[0], k_stride, v_stride,
-          _match(offs, "offs", dev, (B,), torch.int32), ctypes.byref(cache), ctypes.byref(cfg),
-          None if k_out is None else _match(k_out, "k_out", dev, shape, dtype),
-          None if v_out is None else _match(v_out, "v_out", dev, shape, dtype),
-          None if status is None else _status_pointer(status, dev))
+        k_out = torch.empty(shape, dtype=dtype, device=k.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=k.device) if v_out is None else v_out
+    _kv_call(index, load_library().fos_kv_append, kp, vp, code, shape[0], k_stride, v_stride,
+             _kv_at(offs, "offs", index, (B,), torch.int32), cache, _kv_config(**knobs),
+             None if k_out is None else _kv_at(k_out, "k_out", index, shape, dtype),
+             None if v_out is None else _kv_at(v_out, "v_out", index, shape, dtype), _kv_status(status, index))
     return k_out, v_out
 
 
-def _kv_queries(q, cache, dev, H, D):
-    if q.dtype not in (torch.bfloat16, torch.float16):
+def _kv_queries(q, index, D):
+    if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise ValueError(f"q must be bf16 or fp16, got {q.dtype}")
-    return _kv_tokens(q, "q", dev, None, D)
+    return _kv_tokens(q, "q", index, None, D)
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv_attention_room(*sizes) -> int:
+    return load_library().fos_kv_attention_workspace(*sizes)
 
 
 def fos_kv_attention(q: torch.Tensor, offs: torch.Tensor, k_cache, v_cache, table: torch.Tensor, lens: torch.Tensor, *,
@@ -918,25 +964,25 @@ def fos_kv_attention(q: torch.Tensor, offs: torch.Tensor, k_cache, v_cache, tabl
     stands before it and itself; max_len (what the caller knows lens to be at
     most; default: what the table holds) shapes the launch. Queries that see no
     key, and rows past offs[-1], have out 0 and lse -inf."""
-    cache, dev, B, W, H, P, D = _kv_cache(k_cache, v_cache, table, lens)
-    qp, stride = _kv_queries(q, cache, dev, H, D)
+    cache, index, B, W, H, P, D = _kv_cache(k_cache, v_cache, table, lens)
+    qp, stride = _kv_queries(q, index, D)
     shape, dtype = q.shape, q.dtype
     T, Hq, _ = shape
-    lib = load_library()
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        to_out = out.data_ptr()
+    else:
+        to_out = _kv_at(out, "out", index, shape, dtype)
     if lse is None:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=dev)
-    if workspace is None:
-        need = lib.fos_kv_attention_workspace(T, Hq, B, W, H, P, D, max_len)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    work, room = (None, 0) if workspace is None else (_match(workspace, "workspace", dev),
-                                                      workspace.numel() * workspace.element_size())
-    _call(dev, lib.fos_kv_attention, qp, DTYPES[dtype], T, Hq, stride, _match(offs, "offs", dev, (B,), torch.int32),
-          ctypes.byref(cache), D ** -0.5 if scale is None else scale, causal, max_len,
-          _match(out, "out", dev, shape, dtype), _match(lse, "lse", dev, (T, Hq), torch.float32), work, room,
-          None if status is None else _status_pointer(status, dev))
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        to_lse = lse.data_ptr()
+    else:
+        to_lse = _kv_at(lse, "lse", index, (T, Hq), torch.float32)
+    need = 0 if workspace is not None else _kv_attention_room(T, Hq, B, W, H, P, D, max_len)
+    work, room, workspace = _kv_room(workspace, need, index)
+    _kv_call(index, load_library().fos_kv_attention, qp, DTYPES[dtype], T, Hq, stride,
+             _kv_at(offs, "offs", index, (B,), torch.int32), cache, D ** -0.5 if scale is None else scale, causal,
+             max_len, to_out, to_lse, work, room, _kv_status(status, index))
     return out, lse
 
 
@@ -957,14 +1003,13 @@ def fos_kv_weights(q: torch.Tensor, offs: torch.Tensor, k_cache, table: torch.Te
     of the cache's; lse [T, Hq] of fos_kv_attention. q, offs and lse may be those
     of each sequence's last tokens only. Returns acc; places at or past lens[b] are
     left as they are."""
-    cache, dev, B, W, H, P, D = _kv_cache(k_cache, None, table, lens)
-    qp, stride = _kv_queries(q, cache, dev, H, D)
+    cache, index, B, W, H, P, D = _kv_cache(k_cache, None, table, lens)
+    qp, stride = _kv_queries(q, index, D)
     T, Hq, _ = q.shape
-    _call(dev, load_library().fos_kv_weights, qp, DTYPES[q.dtype], T, Hq, stride,
-          _match(offs, "offs", dev, (B,), torch.int32), ctypes.byref(cache), D ** -0.5 if scale is None else scale,
-          causal, max_len, _match(lse, "lse", dev, (T, Hq), torch.float32),
-          _match(acc, "acc", dev, (B, H, W * P), torch.float32),
-          None if status is None else _status_pointer(status, dev))
+    _kv_call(index, load_library().fos_kv_weights, qp, DTYPES[q.dtype], T, Hq, stride,
+             _kv_at(offs, "offs", index, (B,), torch.int32), cache, D ** -0.5 if scale is None else scale, causal, max_len,
+             _kv_at(lse, "lse", index, (T, Hq), torch.float32), _kv_at(acc, "acc", index, (B, H, W * P), torch.float32),
+             _kv_status(status, index))
     return acc
 
 
@@ -975,19 +1020,17 @@ def fos_kv_evict(acc: torch.Tensor, k_cache, v_cache, table: torch.Tensor, lens:
     with the largest acc float32[B, H, W * P] stay. Kept rows, and their acc, move
     into the places that others gave up; the last rows end at the new length in
     their order. Returns new_lens int32[B], min(lens, budget); lens itself is left."""
-    cache, dev, B, W, H, P, D = _kv_cache(k_cache, v_cache, table, lens)
+    cache, index, B, W, H, P, _ = _kv_cache(k_cache, v_cache, table, lens)
     lib = load_library()
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    if workspace is None:
-        need = lib.fos_kv_evict_workspace(B, H, budget, recent)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    work, room = (None, 0) if workspace is None else (_match(workspace, "workspace", dev),
-                                                      workspace.numel() * workspace.element_size())
-    _call(dev, lib.fos_kv_evict, ctypes.byref(cache), _match(acc, "acc", dev, (B, H, W * P), torch.float32), budget,
-          sinks, recent, _match(new_lens, "new_lens", dev, (B,), torch.int32), work, room,
-          None if status is None else _status_pointer(status, dev))
+        new_lens = torch.empty_like(lens)
+        to_lens = new_lens.data_ptr()
+    else:
+        to_lens = _kv_at(new_lens, "new_lens", index, (B,), torch.int32)
+    need = 0 if workspace is not None else lib.fos_kv_evict_workspace(B, H, budget, recent)
+    work, room, workspace = _kv_room(workspace, need, index)
+    _kv_call(index, lib.fos_kv_evict, cache, _kv_at(acc, "acc", index, (B, H, W * P), torch.float32), budget, sinks,
+             recent, to_lens, work, room, _kv_status(status, index))
     return new_lens
 
 

@@ -11,12 +11,27 @@ INVALID, DTYPE, SHAPE, ALIGN, CONFIG, DEVICE = 1, 2, 3, 4, 5, 6
 Q, K, S, D_, T_, L, O, Y, A, W_ = (0x10000 * i for i in range(1, 11))
 
 
+class Rows(ctypes.Structure):  # fos_kv_rows
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("sdec", ctypes.c_void_p)]
+
+
+class Cache(ctypes.Structure):  # fos_kv_cache
+    _fields_ = [("k", Rows), ("v", Rows), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), *((name, ctypes.c_int32) for name in "BWHPD")]
+
+
 def rows(codes=K, scales=S, sdec=D_):
-    return fos._KvRows(codes, scales, sdec)
+    return Rows(codes, scales, sdec)
 
 
 def cache(k=None, v=None, table=T_, lens=L, pages=9, B=2, W=4, H=3, P=64, D=128):
-    return fos._KvCache(k or rows(), v or rows(), table, lens, pages, B, W, H, P, D)
+    return Cache(k or rows(), v or rows(), table, lens, pages, B, W, H, P, D)
+
+
+def test_the_packed_cache_is_the_structure():
+    c = cache(v=rows(K + 16, S + 32, D_ + 48))
+    packed = fos._KV_CACHE.pack(K, S, D_, K + 16, S + 32, D_ + 48, T_, L, 9, 2, 4, 3, 64, 128)
+    assert packed == bytes(c) and len(packed) == ctypes.sizeof(Cache)
 
 
 def checked(rc):
@@ -80,7 +95,7 @@ def test_cache_refusals(call, want, kw):
 def test_values_are_needed_where_they_are_read(call):
     assert call(cache(v=rows(codes=0))) == INVALID
     assert call(cache(v=rows(sdec=D_ + 8))) == ALIGN
-    assert weights(cache(v=fos._KvRows(0, 0, 0))) in (0, DEVICE)
+    assert weights(cache(v=Rows(0, 0, 0))) in (0, DEVICE)
 
 
 @pytest.mark.parametrize("want,kw", [
@@ -156,26 +171,32 @@ def test_workspaces():
     assert fos.fos_kv_attention_workspace(8192, 32, 1, 128, 8, 64, 128) == 0
 
 
-def host_cache(pages=3, H=2, P=16, D=64):
-    return fos.fos_kv_cache(pages, H, P, D, device="cpu")
-
-
 def test_python_checks():
-    k, v = host_cache(), host_cache()
+    """On host tensors, whose device index is -1; a cache on the host is refused."""
+    k, v = (fos.fos_kv_cache(3, 2, 16, 64, device="cpu") for _ in range(2))
     table, lens = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
-    with pytest.raises(ValueError, match="on a device"):
-        fos.fos_kv_attention(torch.zeros(2, 4, 64, dtype=torch.bfloat16), lens, k, v, table, lens)
-    host = torch.device("cpu")
-    assert fos._kv_rows(k, "k_cache", host, None).codes == k[0].data_ptr()
-    with pytest.raises(ValueError, match="scales"):
-        fos._kv_rows((k[0], k[1][..., :2], k[2]), "k_cache", host, None)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    for call in (lambda: fos.fos_kv_attention(q, lens, k, v, table, lens),
+                 lambda: fos.fos_kv_append(q, q, lens, k, v, table, lens),
+                 lambda: fos.fos_kv_weights(q, lens, k, table, lens, lens, lens),
+                 lambda: fos.fos_kv_evict(lens, k, v, table, lens, 4)):
+        with pytest.raises(ValueError, match="on a device"):
+            call()
+    assert fos._kv_at(k[0], "codes", -1, (3, 2, 16, 32), torch.uint8) == k[0].data_ptr()
+    for bad in ((3, 2, 16, 31), torch.uint8), ((3, 2, 16, 32), torch.int8):
+        with pytest.raises(ValueError):
+            fos._kv_at(k[0], "codes", -1, *bad)
     with pytest.raises(ValueError):
-        fos._kv_rows((k[0], k[1], k[2].double()), "k_cache", host, None)
-    with pytest.raises(ValueError, match="codes"):
-        fos._kv_rows((k[0][0], k[1], k[2]), "k_cache", host, None)
+        fos._kv_at(k[0], "codes", 0, (3, 2, 16, 32), torch.uint8)
+    with pytest.raises(ValueError):
+        fos._kv_at(k[0].transpose(1, 2), "codes", -1, (3, 16, 2, 32), torch.uint8)
+    with pytest.raises(ValueError, match="bf16 or fp16"):
+        fos._kv_queries(q.float(), -1, 64)
     wide = torch.zeros(5, 6, 64)
-    assert fos._kv_tokens(wide[:, 2:4], "k", host, 2, 64)[1] == 6 * 64
-    assert fos._kv_tokens(wide[:1, 2:4], "k", host, 2, 64)[1] == 2 * 64
+    assert fos._kv_tokens(wide[:, 2:4], "k", -1, 2, 64)[1] == 6 * 64
+    assert fos._kv_tokens(wide[:1, 2:4], "k", -1, 2, 64)[1] == 2 * 64
     for bad in (wide[:, ::2], wide[..., :32], wide[:, :2].transpose(0, 2), wide[:, 0]):
         with pytest.raises(ValueError):
-            fos._kv_tokens(bad, "k", host, bad.shape[1], 64)
+            fos._kv_tokens(bad, "k", -1, bad.shape[1], 64)
+    with pytest.raises(ValueError):
+        fos._kv_tokens(wide, "k", 0, 6, 64)
