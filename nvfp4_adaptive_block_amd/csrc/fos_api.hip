@@ -942,7 +942,8 @@ int kv_attend_args(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.causal = causal != 0;
   a.max_len = max_len == 0 || max_len > places ? places : max_len;
-  a.splits = fos::kv_splits(T, cache->B, cache->H, a.G, a.max_len);
+  a.splits = fos::kv_splits(T, cache->B, cache->H, a.G, cache->D, a.max_len);
+  a.wide = fos::kv_wide(T, cache->B, cache->H, a.G, cache->D, a.max_len);
   a.status = d_status;
   return FOS_OK;
 }
@@ -990,7 +991,7 @@ int64_t fos_kv_attention_workspace(int64_t T, int Hq, int64_t B, int64_t W, int 
   if (check_kv_sizes(B, W, H, P, D) || max_len < 0) return -1;
   if (check_kv_queries(FOS_BF16, T, Hq, (int64_t)Hq * D, B, H, D)) return -1;
   const int64_t places = W * P;
-  const int splits = fos::kv_splits(T, (int)B, H, Hq / H, max_len == 0 || max_len > places ? places : max_len);
+  const int splits = fos::kv_splits(T, (int)B, H, Hq / H, D, max_len == 0 || max_len > places ? places : max_len);
   return fos::kv_attend_workspace(T, H, Hq / H, D, splits);
 }
 

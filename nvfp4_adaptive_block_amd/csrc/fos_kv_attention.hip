@@ -301,13 +301,13 @@ __device__ __forceinline__ Place place_of(const KvAttendArgs& a) {
 
 // ---------------------------------------------------------------- few rows
 //
-// A workgroup has 16 rows and a part of their keys; its four waves take the part's
-// steps of 32 keys in turn, each on its own, and join in LDS at the end. Keys come
+// A workgroup has 16 rows and a part of their keys; its four (or eight) waves take the
+// part's steps of 32 keys in turn, each on its own, and join in LDS at the end. Keys come
 // from memory once, a step ahead, to registers; codes of keys turn through the
 // wave's own LDS from the loads' order to the matrix instruction's, value rows are
 // decoded into it and read back transposed.
 
-template <int NC> struct StreamLds {
+template <int NC, int WAVES> struct StreamLds {
   // A value row in fp16. Where it is a multiple of the banks' 256 bytes its pieces of 16
   // are turned by its number, so that the lanes that an access serves together reach
   // different banks; else it is a step of the banks apart from the next.
@@ -320,8 +320,8 @@ template <int NC> struct StreamLds {
   static constexpr int kSizes = kKeys + 32 * kRow;    // S_dec of 32 keys and of their values
   static constexpr int kWave = kSizes + 256;
   static constexpr int kJoinRow = 32 * NC + 4;        // floats
-  static constexpr int kJoin = 4 * 16 * kJoinRow * 4 + 4 * 16 * 8;
-  static constexpr int kAll = 4 * kWave > kJoin ? 4 * kWave : kJoin;
+  static constexpr int kJoin = WAVES * 16 * kJoinRow * 4 + WAVES * 16 * 8;
+  static constexpr int kAll = WAVES * kWave > kJoin ? WAVES * kWave : kJoin;
 };
 
 template <int DT>
@@ -333,9 +333,9 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, const float* v) 
   *reinterpret_cast<u32x4*>((uint16_t*)out + i) = w;
 }
 
-template <int DT, int NC>
-__global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs a) {
-  typedef StreamLds<NC> L;
+template <int DT, int NC, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs a) {
+  typedef StreamLds<NC, WAVES> L;
   __shared__ __attribute__((aligned(16))) uint8_t lds[L::kAll];
   constexpr int D = 32 * NC, DT16 = 2 * NC;  // tiles of 16 values
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
   }
   if (!row.have) limit = 0;
   const int steps = (most + 31) / 32;
-  const int each = max(4, (steps + a.splits - 1) / a.splits);
+  const int each = max(WAVES, (steps + a.splits - 1) / a.splits);
   const int from = part * each, to = min(steps, from + each);
 
   Frag q[NC];
@@ -384,14 +384,14 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
   find(32 * s);
   if (s < to) {
     next.load(a.c, pg, page, 32 * s);
-    find(32 * (s + 4));
+    find(32 * (s + WAVES));
   }
   while (s < to) {
     const Step<NC> st = next;
     const int first = 32 * s;
-    s += 4;
+    s += WAVES;
     next.load(a.c, pg, page, 32 * s);
-    find(32 * (s + 4));
+    find(32 * (s + WAVES));
 
     const bool missing = first + 32 > len || !st.there[0] || !st.there[1];
     wave_lds_order();
@@ -488,32 +488,33 @@ __global__ __launch_bounds__(256, NC <= 4 ? 3 : 2) void k_kv_stream(KvAttendArgs
   l = col_sum(l);
   __syncthreads();
   float* join = reinterpret_cast<float*>(lds);
-  float2* ml = reinterpret_cast<float2*>(lds + 4 * 16 * L::kJoinRow * 4);
+  float2* ml = reinterpret_cast<float2*>(lds + WAVES * 16 * L::kJoinRow * 4);
   if (g == 0) ml[wave * 16 + col] = float2{m, l};
 #pragma unroll
   for (int t = 0; t < DT16; t++)
     *reinterpret_cast<f32x4*>(join + (wave * 16 + col) * L::kJoinRow + 16 * t + 4 * g) = o[t];
   __syncthreads();
-  const int r = threadIdx.x >> 4, piece0 = threadIdx.x & 15;
+  constexpr int kEach = 4 * WAVES;  // threads to a row
+  const int r = threadIdx.x / kEach, piece0 = threadIdx.x % kEach;
   const Row to_row = row_of(a, gt, h, gt.tile * 16 + r);
   if (!to_row.have) return;
-  float M = kLowest, sum = 0.0f, f[4];
+  float M = kLowest, sum = 0.0f, f[WAVES];
 #pragma unroll
-  for (int w = 0; w < 4; w++) M = __builtin_fmaxf(M, ml[w * 16 + r].x);
+  for (int w = 0; w < WAVES; w++) M = __builtin_fmaxf(M, ml[w * 16 + r].x);
 #pragma unroll
-  for (int w = 0; w < 4; w++) {
+  for (int w = 0; w < WAVES; w++) {
     f[w] = __builtin_amdgcn_exp2f(ml[w * 16 + r].x - M);
     sum += f[w] * ml[w * 16 + r].y;
   }
   const int64_t at = to_row.token * ((int64_t)a.c.H * a.G) + to_row.head;
   const bool whole = a.splits == 1;
   const float by = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-  for (int d = piece0 * 8; d < D; d += 128) {
+  for (int d = piece0 * 8; d < D; d += 8 * kEach) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; w++) {
+    for (int w = 0; w < WAVES; w++) {
       const f32x4* p = reinterpret_cast<const f32x4*>(join + (w * 16 + r) * L::kJoinRow + d);
 #pragma unroll
       for (int i = 0; i < 8; i++) v[i] += f[w] * p[i / 4][i % 4];
@@ -1081,8 +1082,10 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(tiles * a.c.H * a.splits));
   if (per == 128)
     k_kv_tile<DT, NC><<<grid, 256, 0, s>>>(a);
+  else if (a.wide)
+    k_kv_stream<DT, NC, NC == 8 ? 4 : 8><<<grid, NC == 8 ? 256 : 512, 0, s>>>(a);
   else
-    k_kv_stream<DT, NC><<<grid, 256, 0, s>>>(a);
+    k_kv_stream<DT, NC, 4><<<grid, 256, 0, s>>>(a);
   if (a.splits > 8)
     k_kv_join<DT, NC, 16><<<dim3((unsigned)(rows * a.c.H)), 1024, 0, s>>>(a);
   else if (a.splits > 1)
@@ -1115,13 +1118,21 @@ hipError_t run(bool attention, const KvAttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// A short cache of few sequences is left whole, by eight waves to a workgroup (LDS holds as
+// many for D up to 192): one launch instead of two and no workspace (1001 keys, one token, 8
+// heads of 128: TIMES).
+bool kv_wide(int64_t T, int B, int H, int G, int D, int64_t max_len) {
+  return !kv_tiled(T, B, G) && D <= 192 && max_len <= 1024 && (T * G / B + 15) / 16 * B * H < 128;
+}
+
 // Few rows: where the tiles alone fill the chip's 256 CUs, workgroups enough to even out
 // lengths (64 sequences of 2500 to 8192 tokens on 8 heads: 1024 workgroups 103 us, 2304 96);
 // else about as many as run at once (131072 keys for one token on 4 heads: 512 to 2304 25 to
 // 27 us, 384 30; 17 sequences of up to 2999 tokens, 12 heads of 64: 512 22.8, 1024 19.4, 1536
 // 21.2). A part has four steps at least, one to a wave (1001 keys: 8.2 us; of two 9.4, of
 // eight 9.7).
-int kv_splits(int64_t T, int B, int H, int G, int64_t max_len) {
+int kv_splits(int64_t T, int B, int H, int G, int D, int64_t max_len) {
+  if (kv_wide(T, B, H, G, D, max_len)) return 1;
   const bool tiled = kv_tiled(T, B, G);
   const int64_t rows = tiled ? 128 : 16, least = tiled ? 512 : 128;
   const int64_t per = (T * G / B + rows - 1) / rows, tiles = (per < 1 ? 1 : per) * B * H;

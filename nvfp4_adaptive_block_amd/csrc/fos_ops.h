@@ -147,12 +147,15 @@ struct KvAttendArgs {
   float* lse;            // [T, H G]; nullable for attention, an input for weights
   float* acc;            // weights: [B, H, W P]
   int splits;            // parts of the keys per tile of rows
+  bool wide;
   int64_t max_len;
   void* work;
   int32_t* status;       // nullable
 };
 // Parts that the keys are cut into, from sizes that the host knows.
-int kv_splits(int64_t T, int B, int H, int G, int64_t max_len);
+int kv_splits(int64_t T, int B, int H, int G, int D, int64_t max_len);
+// Whether the few-rows kernel has eight waves to a workgroup.
+bool kv_wide(int64_t T, int B, int H, int G, int D, int64_t max_len);
 int64_t kv_attend_workspace(int64_t T, int H, int G, int D, int splits);
 hipError_t launch_kv_attention(int dt, const KvAttendArgs& a, hipStream_t s);
 hipError_t launch_kv_weights(int dt, const KvAttendArgs& a, hipStream_t s);
