@@ -223,16 +223,15 @@ __device__ __forceinline__ float row_max(float v) {
   return __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
-// One row of q as N fragments of eight values, `step` values apart from `at` on;
-// returns what undoes its power of two.
+// One row of q as N fragments of eight values, `step` values apart from `at` on, or zeros
+// (at is a row of q in any case); returns what undoes its power of two.
 template <int DT, int N, bool QUARTERS>
 __device__ __forceinline__ float load_q(const void* q, int64_t at, int step, bool have, Frag* f) {
   const uint16_t* p = (const uint16_t*)q + at;
 #pragma unroll
   for (int c = 0; c < N; c++) {
-    u32x4 v = {0, 0, 0, 0};
-    if (have) v = *reinterpret_cast<const u32x4*>(p + c * step);
-    f[c].u[0] = v.x, f[c].u[1] = v.y, f[c].u[2] = v.z, f[c].u[3] = v.w;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(p + c * step);
+    f[c].u[0] = have ? v.x : 0, f[c].u[1] = have ? v.y : 0, f[c].u[2] = have ? v.z : 0, f[c].u[3] = have ? v.w : 0;
   }
   if constexpr (DT == kFP16) return 1.0f;
   uint32_t top = 0;  // of the finite values' bits
@@ -301,8 +300,8 @@ __device__ __forceinline__ Place place_of(const KvAttendArgs& a) {
 
 // ---------------------------------------------------------------- few rows
 //
-// A workgroup has 16 rows and a part of their keys; its four (or eight) waves take the
-// part's steps of 32 keys in turn, each on its own, and join in LDS at the end. Keys come
+// A workgroup has 16 rows and a part of their keys; its four waves (twelve for a short
+// cache that is left whole) take the part's steps of 32 keys in turn, each on its own, and join in LDS at the end. Keys come
 // from memory once, a step ahead, to registers; codes of keys turn through the
 // wave's own LDS from the loads' order to the matrix instruction's, value rows are
 // decoded into it and read back transposed.
@@ -916,8 +915,8 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_kv_join(KvAtt
 
 // ---------------------------------------------------------------- weights
 //
-// A workgroup stages 128 rows of q in LDS, in fp16, and passes over its keys, 32 to a
-// wave at a time, decoded to registers. Here the keys are the columns of the matrix
+// A workgroup stages 256 rows of q (or 32, where sequences have no more) in LDS, in fp16,
+// and passes over its keys, 32 to a wave at a time, decoded to registers. Here the keys are the columns of the matrix
 // instruction's result, so that a lane has one key and sums its weights over the rows
 // in its own registers. A key belongs to one wave, so the sums are added to what is there
 // without atomics, in an order that is always the same.
@@ -952,12 +951,12 @@ template <int NC> struct KeyStep {
   Half<NC> half;     // scales, and S_dec, of the lane's own key
   float sdec;
   bool there[2];     // wave-uniform
-  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, int first, int len) {
+  __device__ __forceinline__ void load(const KvCache& c, const Pages& pg, const int (&page)[2], int first) {
     const int lane = threadIdx.x & 63;
     int64_t row[2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      row[u] = pg.row_at(first + 16 * u, len, there[u]);
+      row[u] = pg.row(page[u], first + 16 * u, there[u]);
       k[u].load_codes(c.k.codes + row[u] * (16 * NC) + lane * (4 * NC));
     }
     const int64_t mine = ((lane & 16) ? row[1] : row[0]) + (lane & 15);
@@ -966,9 +965,9 @@ template <int NC> struct KeyStep {
   }
 };
 
-template <int DT, int NC>
-__global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArgs a) {
-  constexpr int D = 32 * NC, kRows = 128, kRow = 64 * NC + 16;
+template <int DT, int NC, int kRows>
+__global__ __launch_bounds__(256, kRows == 32 && NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArgs a) {
+  constexpr int D = 32 * NC, kRow = 64 * NC + 16;
   __shared__ __attribute__((aligned(16))) uint8_t qs[kRows * kRow];
   __shared__ __attribute__((aligned(16))) uint8_t turn[4 * 512 * NC];
   __shared__ __attribute__((aligned(16))) float factor[kRows], ref[kRows];
@@ -990,20 +989,31 @@ __global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArg
   uint8_t* mine = turn + wave * 512 * NC;
   if ((int64_t)blockIdx.y * 128 >= len) return;
   for (int g0 = 0; g0 < rows; g0 += kRows) {
-    // keys that any of these rows sees
+    // keys that all of these rows see, and that any does
+    const int least = a.causal ? min(len, len - n + a.by_group.div(g0) + 1) : len;
     const int most = a.causal ? min(len, len - n + a.by_group.div(min(g0 + kRows, rows) - 1) + 1) : len;
     if ((int64_t)blockIdx.y * 128 >= most) continue;
+    // pages a step ahead of the loads, loads a step ahead of their use
     KeyStep<NC> next;
     const int stride = (int)gridDim.y * 128;
-    int first = (int)(blockIdx.y * 4 + wave) * 32;
-    next.load(a.c, pg, first, len);
+    int first = (int)(blockIdx.y * 4 + wave) * 32, page[2];
+    auto after = [&](int pos) { return pos <= INT32_MAX - stride - 63 ? pos + stride : INT32_MAX - 63; };
+    auto find = [&](int pos) {
+#pragma unroll
+      for (int u = 0; u < 2; u++) page[u] = pg.page(pos + 16 * u, len);
+    };
+    find(first);
+    next.load(a.c, pg, page, first);
+    find(after(first));
     __syncthreads();
-    {
-      const Row row = row_of(a, gt, h, g0 + 32 * wave + col);
+#pragma unroll
+    for (int r0 = 32 * wave; r0 < kRows; r0 += 128) {
+      if (g0 + r0 >= rows) break;
+      const Row row = row_of(a, gt, h, g0 + r0 + col);
       Frag q[2 * NC];
       const float undo = load_q<DT, 2 * NC, false>(
           a.q, row.token * a.stride + (int64_t)row.head * D + half * 16 * NC, 8, row.have, q);
-      uint8_t* to = qs + (32 * wave + col) * kRow + half * 32 * NC;
+      uint8_t* to = qs + (r0 + col) * kRow + half * 32 * NC;
 #pragma unroll
       for (int c = 0; c < 2 * NC; c++)
         *reinterpret_cast<u32x4*>(to + 16 * c) = u32x4{q[c].u[0], q[c].u[1], q[c].u[2], q[c].u[3]};
@@ -1011,15 +1021,16 @@ __global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArg
         float lse = row.have ? a.lse[row.token * ((int64_t)a.c.H * a.G) + row.head] : 0.0f;
         // a row that sees nothing has no weights: 2^-infinity
         if (!row.have || lse == -__builtin_huge_valf()) lse = __builtin_huge_valf();
-        factor[32 * wave + col] = a.scale_log2 * undo;
-        ref[32 * wave + col] = lse * 1.44269504088896341f;
-        limits[32 * wave + col] = a.causal ? min(len, len - n + row.place + 1) : len;
+        factor[r0 + col] = a.scale_log2 * undo;
+        ref[r0 + col] = lse * 1.44269504088896341f;
+        limits[r0 + col] = a.causal ? min(len, len - n + row.place + 1) : len;
       }
     }
     __syncthreads();
     for (; first < most; first += stride) {
       const KeyStep<NC> st = next;
-      next.load(a.c, pg, first <= INT32_MAX - stride ? first + stride : INT32_MAX - 63, len);
+      next.load(a.c, pg, page, after(first));
+      find(after(after(first)));
       Frag kf[2 * NC];
       wave_lds_order();
 #pragma unroll
@@ -1031,8 +1042,7 @@ __global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArg
         codes[i].load_codes(mine + (col >> 4) * 256 * NC + 4 * NC * piece(col & 15, 2 * half + i));
       st.half.decode(codes, kf);
       float sum = 0.0f;
-#pragma unroll 1
-      for (int rt = 0; rt < kRows && g0 + rt < rows; rt += 32) {
+      auto product = [&](int rt) {
         f32x16 x;
 #pragma unroll
         for (int i = 0; i < 16; i++) x[i] = 0.0f;
@@ -1044,23 +1054,46 @@ __global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArg
           f.u[0] = t.x, f.u[1] = t.y, f.u[2] = t.z, f.u[3] = t.w;
           x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.h, kf[c].h, x, 0, 0, 0);
         }
-        const bool partly = a.causal && first + 32 > len - n + a.by_group.div(g0 + rt) + 1;
+        return x;
+      };
+      // the weights of rows r .. r + 3, of which a lane has its key's
+      auto weigh = [&](const f32x16& x, int i, int r, bool partly) {
+        const f32x4 f = *reinterpret_cast<const f32x4*>(factor + r), z = *reinterpret_cast<const f32x4*>(ref + r);
+        float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          if (g0 + rt + 8 * i >= rows) break;
-          const int r = rt + 8 * i + 4 * half;
-          const f32x4 f = *reinterpret_cast<const f32x4*>(factor + r), z = *reinterpret_cast<const f32x4*>(ref + r);
-          float e[4];
+        for (int j = 0; j < 4; j++) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[4 * i + j] * st.sdec, f[j], -z[j]));
+        if (partly) {
+          const int4 lim = *reinterpret_cast<const int4*>(limits + r);
+          const int l4[4] = {lim.x, lim.y, lim.z, lim.w};
 #pragma unroll
-          for (int j = 0; j < 4; j++) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[4 * i + j] * st.sdec, f[j], -z[j]));
-          if (partly) {
-            const int4 lim = *reinterpret_cast<const int4*>(limits + r);
-            const int l4[4] = {lim.x, lim.y, lim.z, lim.w};
+          for (int j = 0; j < 4; j++) e[j] = first + col < l4[j] ? e[j] : 0.0f;
+        }
+        sum += (e[0] + e[1]) + (e[2] + e[3]);
+      };
+      if (kRows > 32 && first + 32 <= least) {
+        // rows that all see all keys: the next tile's matrix instructions beside this one's exponentials
+        f32x16 x = product(0);
+#pragma unroll 1
+        for (int rt = 0; rt < kRows && g0 + rt < rows; rt += 32) {
+          __builtin_amdgcn_sched_barrier(0);
+          const f32x16 next = product(rt + 32 < kRows ? rt + 32 : rt);
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-              if (first + col >= l4[j]) e[j] = 0.0f;
+          for (int i = 0; i < 4; i++) weigh(x, i, rt + 8 * i + 4 * half, false);
+          __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+          FOS_INTERLEAVE(2 * NC, 64 / (2 * NC), 2)
+          __builtin_amdgcn_sched_barrier(0);
+          x = next;
+        }
+      } else {
+#pragma unroll 1
+        for (int rt = 0; rt < kRows && g0 + rt < rows; rt += 32) {
+          const f32x16 x = product(rt);
+          const bool partly = a.causal && first + 32 > len - n + a.by_group.div(g0 + rt) + 1;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            if (g0 + rt + 8 * i >= rows) break;
+            weigh(x, i, rt + 8 * i + 4 * half, partly);
           }
-          sum += (e[0] + e[1]) + (e[2] + e[3]);
         }
       }
       const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
@@ -1074,6 +1107,10 @@ __global__ __launch_bounds__(256, NC <= 4 ? 4 : 2) void k_kv_weights(KvAttendArg
 // Whether sequences have rows enough, on the whole, for the tile kernel.
 bool kv_tiled(int64_t T, int B, int G) { return T * G > (int64_t)32 * B; }
 
+// Waves that one workgroup's LDS holds, of a whole cache (kv_wide).
+template <int NC>
+constexpr int kWideWaves = NC <= 4 ? 12 : NC == 6 ? 8 : 4;
+
 template <int DT, int NC>
 hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.T * a.G;
@@ -1083,7 +1120,7 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
   if (per == 128)
     k_kv_tile<DT, NC><<<grid, 256, 0, s>>>(a);
   else if (a.wide)
-    k_kv_stream<DT, NC, NC == 8 ? 4 : 8><<<grid, NC == 8 ? 256 : 512, 0, s>>>(a);
+    k_kv_stream<DT, NC, kWideWaves<NC>><<<grid, 64 * kWideWaves<NC>, 0, s>>>(a);
   else
     k_kv_stream<DT, NC, 4><<<grid, 256, 0, s>>>(a);
   if (a.splits > 8)
@@ -1095,11 +1132,16 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
 
 template <int DT, int NC>
 hipError_t weights(const KvAttendArgs& a, hipStream_t s) {
+  const bool few = (int64_t)a.T * a.G <= (int64_t)32 * a.c.B;
   const int64_t heads = (int64_t)a.c.B * a.c.H, most = (a.max_len + 127) / 128;
-  int64_t chunks = 512 / heads;
+  int64_t chunks = (few ? 1280 : 512) / heads;
   chunks = chunks > most ? most : chunks;
   chunks = chunks < 1 ? 1 : chunks;
-  k_kv_weights<DT, NC><<<dim3((unsigned)heads, (unsigned)chunks), 256, 0, s>>>(a);
+  const dim3 grid((unsigned)heads, (unsigned)chunks);
+  if (few)
+    k_kv_weights<DT, NC, 32><<<grid, 256, 0, s>>>(a);
+  else
+    k_kv_weights<DT, NC, 256><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -1118,8 +1160,8 @@ hipError_t run(bool attention, const KvAttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// A short cache of few sequences is left whole, by eight waves to a workgroup (LDS holds as
-// many for D up to 192): one launch instead of two and no workspace (1001 keys, one token, 8
+// A short cache of few sequences is left whole, by twelve waves to a workgroup (eight for
+// D 192, which LDS holds): one launch instead of two and no workspace (1001 keys, one token, 8
 // heads of 128: TIMES).
 bool kv_wide(int64_t T, int B, int H, int G, int D, int64_t max_len) {
   return !kv_tiled(T, B, G) && D <= 192 && max_len <= 1024 && (T * G / B + 15) / 16 * B * H < 128;

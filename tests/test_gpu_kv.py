@@ -361,9 +361,9 @@ def check_weights(cache, q, new, causal=True, scale=None, **kw):
     assert_guard(raw)
     want, bound = ref.weights(cache, q, new, lse.cpu(), causal, scale)
     want = want + start.double().cpu()
-    # rows come 128 at a time: each such part is added to what is there in binary32, which
-    # rounds a total of at most the result by half a step, 2^-24 of it at most
-    parts = torch.tensor([max(1, -(-n * q.shape[1] // cache.H // 128)) for n in new], dtype=torch.float64)
+    # rows come 32 or 256 at a time: each such part is added to what is there in binary32,
+    # which rounds a total of at most the result by half a step, 2^-24 of it at most
+    parts = torch.tensor([max(1, -(-n * q.shape[1] // cache.H // 32)) for n in new], dtype=torch.float64)
     assert_within(acc, want, bound + ref.E24 * parts[:, None, None] * want.abs(), "acc")
     for b, n in enumerate(cache.lens):
         assert same(acc[b, :, n:], start[b, :, n:])
