@@ -68,15 +68,29 @@ __device__ __forceinline__ void store_block(void* p, int64_t i, const float* y) 
   }
 }
 
-// max |x| without the NaN elements, by the magnitudes' bits.
+// max |x| without the NaN elements: by the magnitudes' bits where there may be some.
+template <bool NANS>
 __device__ __forceinline__ float amax16(const float* x) {
-  uint32_t a = 0;
+  if constexpr (NANS) {
+    uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
-    const uint32_t m = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-    a = max(a, m <= 0x7F800000u ? m : 0u);
+    for (int i = 0; i < 16; i++) {
+      const uint32_t m = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      a = max(a, m <= 0x7F800000u ? m : 0u);
+    }
+    return __uint_as_float(a);
+  } else {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i++) a = __builtin_fmaxf(a, __builtin_fabsf(x[i]));
+    return a;
   }
-  return __uint_as_float(a);
+}
+__device__ __forceinline__ bool any_nan16(const float* x) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < 16; i++) m = __builtin_elementwise_maximum(m, x[i]);
+  return m != m;
 }
 
 struct Encoded {
@@ -85,6 +99,7 @@ struct Encoded {
 };
 
 // q: the block's amax over the candidate's top value.
+template <bool NANS>
 __device__ __forceinline__ Encoded encode(const float* x, float q, float S_enc, float S_dec) {
   Encoded o;
   o.scale = e4m3_code(q * S_enc);
@@ -92,7 +107,7 @@ __device__ __forceinline__ Encoded encode(const float* x, float q, float S_enc, 
   const float E = sigma == 0.0f ? 0.0f : __builtin_fminf(S_enc / sigma, kFltMax);
   float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; i++) v[i] = x[i] != x[i] ? 6.0f : x[i] * E;
+  for (int i = 0; i < 16; i++) v[i] = NANS && x[i] != x[i] ? 6.0f : x[i] * E;
   o.c0 = e2m1_pack8(v);
   o.c1 = e2m1_pack8(v + 8);
   o.D = sigma * S_dec;
@@ -124,21 +139,18 @@ __device__ __forceinline__ float error16(const float* x, const float* y) {
   return ORDER == kOrderSeq ? seq16(u) : tree16(u);
 }
 
-// The better of the two candidates, and its values; a tie keeps map-to-6, and so
-// does a block with a NaN, whose errors compare false.
-template <int RECIPE, int METRIC, int PREC, int ORDER>
-__device__ __forceinline__ Encoded quantize16(const float* x, float S_enc, float S_dec, float* y) {
-  const float a = amax16(x);
-  const Encoded k6 = encode(x, div6(a), S_enc, S_dec);
-  decode(k6, y);
+// The better of the two candidates for a block whose amax is a; a tie keeps map-to-6, and
+// so does a block with a NaN, whose errors compare false.
+template <int RECIPE, int METRIC, int PREC, int ORDER, bool NANS>
+__device__ __forceinline__ Encoded quantize16(const float* x, float a, float S_enc, float S_dec) {
+  const Encoded k6 = encode<NANS>(x, div6(a), S_enc, S_dec);
   if constexpr (RECIPE == kNVFP4) return k6;
-  const Encoded k4 = encode(x, a * 0.25f, S_enc, S_dec);
-  float y4[16];
-  decode(k4, y4);
-  const bool four = error16<METRIC, PREC, ORDER>(x, y4) < error16<METRIC, PREC, ORDER>(x, y);
-#pragma unroll
-  for (int i = 0; i < 16; i++) y[i] = four ? y4[i] : y[i];
-  return four ? k4 : k6;
+  const Encoded k4 = encode<NANS>(x, a * 0.25f, S_enc, S_dec);
+  float y[16];
+  decode(k6, y);
+  const float e6 = error16<METRIC, PREC, ORDER>(x, y);
+  decode(k4, y);
+  return error16<METRIC, PREC, ORDER>(x, y) < e6 ? k4 : k6;
 }
 
 template <int DT, int RECIPE, int METRIC, int PREC, int ORDER>
@@ -173,17 +185,22 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
   while (b < a.c.B && a.offs[b] <= t) b++;
   const bool tail = b >= a.c.B;
 
-  float x[16], y[16];
+  float x[16];
 #pragma unroll
   for (int i = 0; i < 16; i++) x[i] = 0.0f;
   if (have && !tail) load_block<DT>(a.x[side], t * a.stride[side] + (int64_t)h * a.c.D + 16 * j, x);
-  float A = amax16(x);
+  const bool nans = __any(any_nan16(x));
+  const float top = nans ? amax16<true>(x) : amax16<false>(x);
+  float A = top;
   for (int d = 1; d < 1 << sh; d <<= 1) A = __builtin_fmaxf(A, __shfl_xor(A, d, 64));
   const float S_enc = global_encode_scale(A, a.six_b);
   // a row of zeros has no size of its own: S_dec 0 keeps it from setting one
   const float S_dec = A == 0.0f ? 0.0f : 1.0f / S_enc;
-  const Encoded o = quantize16<RECIPE, METRIC, PREC, ORDER>(x, S_enc, S_dec, y);
+  const Encoded o = nans ? quantize16<RECIPE, METRIC, PREC, ORDER, true>(x, top, S_enc, S_dec)
+                         : quantize16<RECIPE, METRIC, PREC, ORDER, false>(x, top, S_enc, S_dec);
   if (have && a.y[side]) {
+    float y[16];
+    decode(o, y);
     if (tail) {
 #pragma unroll
       for (int i = 0; i < 16; i++) y[i] = 0.0f;
