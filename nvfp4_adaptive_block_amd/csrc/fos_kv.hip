@@ -52,8 +52,8 @@ __device__ __forceinline__ void store_block(void* p, int64_t i, const float* y) 
     u32x4* s = reinterpret_cast<u32x4*>((float*)p + i);
 #pragma unroll
     for (int j = 0; j < 4; j++)
-      s[j] = u32x4{__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]), __float_as_uint(y[4 * j + 2]),
-                   __float_as_uint(y[4 * j + 3])};
+      __builtin_nontemporal_store(u32x4{__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]),
+                                        __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3])}, s + j);
   } else {
     u32x4* s = reinterpret_cast<u32x4*>((uint16_t*)p + i);
 #pragma unroll
@@ -63,7 +63,7 @@ __device__ __forceinline__ void store_block(void* p, int64_t i, const float* y) 
       for (int k = 0; k < 4; k++)
         v[k] = DT == kBF16 ? pack_bf16(y[8 * j + 2 * k], y[8 * j + 2 * k + 1])
                            : pack_f16(y[8 * j + 2 * k], y[8 * j + 2 * k + 1]);
-      s[j] = v;
+      __builtin_nontemporal_store(v, s + j);
     }
   }
 }
