@@ -280,37 +280,58 @@ struct Rows {
   }
 };
 
-// What a row is moved as: 2 NC pieces of 16 bytes of codes, the scales of either
-// side, either S_dec, and its weight; a lane has one of them at a time.
+// What a row is moved as: 2 NC pieces of 16 bytes of codes; the scales of either side in
+// pieces of four bytes (two, where NC is odd), either S_dec and its weight, a lane each. A
+// lane has the same piece of every row that its team moves, so a row is two loads and two
+// stores.
 template <int NC> struct Mover {
-  static constexpr int kItems = 2 * NC + 5;
-  struct __attribute__((packed, aligned(NC == 8 ? 16 : NC == 4 ? 8 : NC % 2 ? 2 : 4))) Scales {
-    uint16_t v[NC];
-  };
+  static constexpr int kSmall = NC % 2 ? 2 : 4, kScales = 2 * NC / kSmall;  // bytes, pieces a side
+  static constexpr int kItems = 2 * NC + 2 * kScales + 3;
   union Piece {
     u32x4 codes;
-    Scales scales;
-    float f;
+    uint32_t small;
   };
-  static __device__ __forceinline__ Piece read(const KvCache& c, const float* acc, int64_t row, int pos, int i) {
-    Piece p;
+  uint8_t* base;   // of the first row's piece
+  int64_t step;    // from one row to the next
+  int item;
+
+  __device__ __forceinline__ Mover(const KvCache& c, float* acc, int i) {
+    item = i;
+    const KvRows& s = (i < 2 * NC ? i < NC : i < 2 * NC + 2 * kScales ? i < 2 * NC + kScales : i == kItems - 3) ? c.k : c.v;
     if (i < 2 * NC) {
-      p.codes = *reinterpret_cast<const u32x4*>((i < NC ? c.k : c.v).codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC));
-    } else if (i < 2 * NC + 2) {
-      p.scales = *reinterpret_cast<const Scales*>((i == 2 * NC ? c.k : c.v).scales + row * (2 * NC));
-    } else if (i < kItems) {
-      p.f = i == 2 * NC + 4 ? acc[pos] : (i == 2 * NC + 2 ? c.k : c.v).sdec[row];
+      base = s.codes + 16 * (i < NC ? i : i - NC);
+      step = 16 * NC;
+    } else if (i < 2 * NC + 2 * kScales) {
+      base = s.scales + kSmall * ((i - 2 * NC) % kScales);
+      step = 2 * NC;
+    } else {
+      base = i == kItems - 1 ? (uint8_t*)acc : (uint8_t*)s.sdec;
+      step = 4;
     }
+  }
+  // `pos`: the row's place, by which the weights go
+  __device__ __forceinline__ uint8_t* at(int64_t row, int pos) const {
+    return base + (item == kItems - 1 ? pos : row) * step;
+  }
+  __device__ __forceinline__ Piece read(int64_t row, int pos) const {
+    Piece p;
+    const uint8_t* q = at(row, pos);
+    if (item < 2 * NC)
+      p.codes = *reinterpret_cast<const u32x4*>(q);
+    else if (kSmall == 2 && item < 2 * NC + 2 * kScales)
+      p.small = *reinterpret_cast<const uint16_t*>(q);
+    else if (item < kItems)
+      p.small = *reinterpret_cast<const uint32_t*>(q);
     return p;
   }
-  static __device__ __forceinline__ void write(const KvCache& c, float* acc, int64_t row, int pos, int i, const Piece& p) {
-    if (i < 2 * NC) {
-      *reinterpret_cast<u32x4*>((i < NC ? c.k : c.v).codes + row * (16 * NC) + 16 * (i < NC ? i : i - NC)) = p.codes;
-    } else if (i < 2 * NC + 2) {
-      *reinterpret_cast<Scales*>((i == 2 * NC ? c.k : c.v).scales + row * (2 * NC)) = p.scales;
-    } else if (i < kItems) {
-      (i == 2 * NC + 4 ? acc + pos : (i == 2 * NC + 2 ? c.k : c.v).sdec + row)[0] = p.f;
-    }
+  __device__ __forceinline__ void write(int64_t row, int pos, const Piece& p) const {
+    uint8_t* q = at(row, pos);
+    if (item < 2 * NC)
+      *reinterpret_cast<u32x4*>(q) = p.codes;
+    else if (kSmall == 2 && item < 2 * NC + 2 * kScales)
+      *reinterpret_cast<uint16_t*>(q) = (uint16_t)p.small;
+    else if (item < kItems)
+      *reinterpret_cast<uint32_t*>(q) = p.small;
   }
 };
 
@@ -491,16 +512,17 @@ __device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* 
   return holes;
 }
 
-// Rows are moved by teams of 16 lanes, several at a time.
+// Rows are moved by teams of 16 lanes (32, where a row has more pieces), several at a time.
 template <int NC>
 struct Teams {
   typedef Mover<NC> M;
-  static constexpr int kRounds = (M::kItems + 15) / 16, kRows = kRounds == 1 ? 8 : 4;
-  typedef typename M::Piece Held[kRows][kRounds];
+  static constexpr int kLanes = M::kItems <= 16 ? 16 : 32, kRows = 8;
+  static_assert(M::kItems <= 32);
+  typedef typename M::Piece Held[kRows];
 
   // Moves first, first + step, ... below `holes`.
   static __device__ __forceinline__ void move(const KvEvictArgs& a, const Cut& cut, int holes, int first, int step) {
-    const int l16 = threadIdx.x & 15;
+    const M piece(a.c, cut.acc, threadIdx.x % kLanes);
     for (int i0 = first; i0 < holes; i0 += kRows * step) {
       int2 mv[kRows];
       Held p;
@@ -510,16 +532,12 @@ struct Teams {
 #pragma unroll
       for (int r = 0; r < kRows; r++)
         if (i0 + r * step < holes) {
-          const int64_t from = cut.rows.at(mv[r].x);
-#pragma unroll
-          for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, cut.acc, from, mv[r].x, l16 + 16 * k);
+          p[r] = piece.read(cut.rows.at(mv[r].x), mv[r].x);
         }
 #pragma unroll
       for (int r = 0; r < kRows; r++)
         if (i0 + r * step < holes) {
-          const int64_t to = cut.rows.at(mv[r].y);
-#pragma unroll
-          for (int k = 0; k < kRounds; k++) M::write(a.c, cut.acc, to, mv[r].y, l16 + 16 * k, p[r][k]);
+          piece.write(cut.rows.at(mv[r].y), mv[r].y, p[r]);
         }
     }
   }
@@ -531,8 +549,9 @@ struct Teams {
   // the cut are cleared, those of a chunk's rows by the part that has it.
   template <int THREADS>
   static __device__ __forceinline__ void shift(const KvEvictArgs& a, const Cut& cut, int part, int parts) {
-    constexpr int kTeams = THREADS / 16;
-    const int team = threadIdx.x >> 4, l16 = threadIdx.x & 15, keep = a.budget - a.recent, gap = cut.n - a.budget;
+    constexpr int kTeams = THREADS / kLanes;
+    const M piece(a.c, cut.acc, threadIdx.x % kLanes);
+    const int team = threadIdx.x / kLanes, keep = a.budget - a.recent, gap = cut.n - a.budget;
     const bool apart = gap >= a.recent;
     if (!apart) {
       if (part > 0) return;
@@ -545,9 +564,7 @@ struct Teams {
       for (int r = 0; r < kRows; r++) {
         const int i = i0 + r * kTeams + team;
         if (i < a.recent) {
-          const int64_t from = cut.rows.at(keep + i + gap);
-#pragma unroll
-          for (int k = 0; k < kRounds; k++) p[r][k] = M::read(a.c, cut.acc, from, keep + i + gap, l16 + 16 * k);
+          p[r] = piece.read(cut.rows.at(keep + i + gap), keep + i + gap);
         }
       }
       __syncthreads();
@@ -555,10 +572,8 @@ struct Teams {
       for (int r = 0; r < kRows; r++) {
         const int i = i0 + r * kTeams + team;
         if (i < a.recent) {
-          const int64_t to = cut.rows.at(keep + i);
-#pragma unroll
-          for (int k = 0; k < kRounds; k++) M::write(a.c, cut.acc, to, keep + i, l16 + 16 * k, p[r][k]);
-          if (apart && l16 == 0) cut.acc[keep + i + gap] = 0.0f;
+          piece.write(cut.rows.at(keep + i), keep + i, p[r]);
+          if (apart && threadIdx.x % kLanes == M::kItems - 1) cut.acc[keep + i + gap] = 0.0f;
         }
       }
     }
@@ -585,7 +600,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
   const int holes = find_moves<ALL ? 8 : 32>(a, cut, hist, share);
   if constexpr (ALL) {
     __syncthreads();
-    Teams<NC>::move(a, cut, holes, threadIdx.x >> 4, kThreads / 16);
+    Teams<NC>::move(a, cut, holes, threadIdx.x / Teams<NC>::kLanes, kThreads / Teams<NC>::kLanes);
     __syncthreads();
     Teams<NC>::template shift<kThreads>(a, cut, 0, 1);
   } else if (threadIdx.x == 0) {
@@ -610,8 +625,9 @@ __device__ __forceinline__ Cut found_cut(const KvEvictArgs& a, int bh) {
 template <int NC>
 __global__ __launch_bounds__(256) void k_kv_move(KvEvictArgs a) {
   const int holes = a.counts[blockIdx.x];
-  if ((int)blockIdx.y * 16 >= holes) return;
-  Teams<NC>::move(a, found_cut(a, blockIdx.x), holes, blockIdx.y * 16 + (threadIdx.x >> 4), gridDim.y * 16);
+  constexpr int kTeams = 256 / Teams<NC>::kLanes;
+  if ((int)blockIdx.y * kTeams >= holes) return;
+  Teams<NC>::move(a, found_cut(a, blockIdx.x), holes, blockIdx.y * kTeams + threadIdx.x / Teams<NC>::kLanes, gridDim.y * kTeams);
 }
 
 template <int NC>
@@ -628,7 +644,7 @@ void evict(const KvEvictArgs& a, hipStream_t s) {
     k_kv_evict<NC, true><<<heads, kThreads, 0, s>>>(a);
     return;
   }
-  const int each = 16 * Teams<NC>::kRows;
+  const int each = 256 / Teams<NC>::kLanes * Teams<NC>::kRows;
   k_kv_evict<NC, false><<<heads, kThreads, 0, s>>>(a);
   k_kv_move<NC><<<dim3(heads, (unsigned)min((keep + each - 1) / each, 64)), 256, 0, s>>>(a);
   k_kv_shift<NC><<<dim3(heads, 4), 256, 0, s>>>(a);
