@@ -11,7 +11,7 @@
 //    2^-32 of the row's largest, and what is smaller is off by 2^-40 of it.
 //  - S_dec of a key multiplies the sum, in binary32.
 //  - S_dec of a value row multiplies the softmax's weight: p_rj = 2^(z_rj - m) S_j is
-//    rounded to fp16 (at most 2^-11 of its size, an eighth of what bf16 would round), and m
+//    rounded to fp16 (at most 2^-11 of its size, an eighth of what bf16 rounds), and m
 //    runs along with the largest z_rj + log2 S_j, so the products that matter lie
 //    between 1/2 and 2^7 whatever the rows' sizes are. m only has to be near that maximum:
 //    log2 S is taken from the exponent bits, and m follows when it is left behind by
@@ -76,6 +76,21 @@ __device__ __forceinline__ float col_sum(float v) {
 // Exponent of S (its floor's log2) for the running maximum; kLeast for 0.
 __device__ __forceinline__ float log2_of(float S) {
   return __builtin_fmaxf((float)(__float_as_uint(S) >> 23) - 127.0f, kLeast);
+}
+
+// Two weights in fp16. For fp16 results what the rounding leaves out is kept too, and
+// multiplied in a second product: alone it would cost as much precision as the result's
+// own rounding (at most 2^-11 each; measured 2.1e-4 of a result's norm with it, 2.7e-4
+// to 3.3e-4 without). A bf16 result's rounding is eight times as large.
+template <int DT>
+__device__ __forceinline__ uint32_t round_pair(float a, float b, uint32_t& rest) {
+  const f32x2 two = {a, b};
+  const h2 near = __builtin_convertvector(two, h2);
+  if constexpr (DT == kFP16) {
+    const f32x2 left = {a - (float)near.x, b - (float)near.y};
+    rest = bits(__builtin_convertvector(left, h2));
+  }
+  return bits(near);
 }
 
 // Eight codes of a dword times a block scale.
@@ -455,7 +470,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 #pragma unroll
       for (int t = 0; t < DT16; t++) o[t] *= f;
     }
-    Frag p;
+    Frag p, rest;
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -464,10 +479,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
       w[i] = e * vs[i / 4][i % 4];
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const f32x2 two = {w[2 * i], w[2 * i + 1]};
-      p.u[i] = bits(__builtin_convertvector(two, h2));
-    }
+    for (int i = 0; i < 4; i++) p.u[i] = round_pair<DT>(w[2 * i], w[2 * i + 1], rest.u[i]);
     wave_lds_order();
 #pragma unroll
     for (int t = 0; t < DT16; t++) {
@@ -480,6 +492,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
         v.u[2 * u + 1] = y.y;
       }
       o[t] = mfma16(v, p, o[t]);
+      if constexpr (DT == kFP16) o[t] = mfma16(v, rest, o[t]);
     }
   }
 
@@ -747,7 +760,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
       // a sixteen of lanes reads four keys' rows, 16 values of each: which four, which half of 32 values
       const int i16 = lane & 15;
       const uint8_t* vp = lds + side * L::kSide + L::kKeys * L::kK + 8 * (i16 & 1);
-      Frag vf[4][NC], p[4];
+      Frag vf[4][NC], p[4], rest[4];
       auto read_values = [&](int c) {
 #pragma unroll
         for (int t = 0; t < NC; t++)
@@ -771,15 +784,17 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
             w[i] = e * vs[i];
           }
 #pragma unroll
-          for (int i = 0; i < 2; i++) {
-            const f32x2 two = {w[2 * i], w[2 * i + 1]};
-            p[2 * kb + (b >> 1)].u[2 * (b & 1) + i] = bits(__builtin_convertvector(two, h2));
-          }
+          for (int i = 0; i < 2; i++)
+            p[2 * kb + (b >> 1)].u[2 * (b & 1) + i] =
+                round_pair<DT>(w[2 * i], w[2 * i + 1], rest[2 * kb + (b >> 1)].u[2 * (b & 1) + i]);
         }
       };
       auto add = [&](int c) {
 #pragma unroll
-        for (int t = 0; t < NC; t++) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[c][t].h, p[c].h, o[t], 0, 0, 0);
+        for (int t = 0; t < NC; t++) {
+          o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[c][t].h, p[c].h, o[t], 0, 0, 0);
+          if constexpr (DT == kFP16) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[c][t].h, rest[c].h, o[t], 0, 0, 0);
+        }
       };
       read_values(0);
       __builtin_amdgcn_sched_barrier(0);
