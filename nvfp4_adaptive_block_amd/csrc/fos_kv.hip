@@ -636,11 +636,19 @@ __global__ __launch_bounds__(256) void k_kv_shift(KvEvictArgs a) {
   Teams<NC>::template shift<256>(a, found_cut(a, blockIdx.x), blockIdx.y, gridDim.y);
 }
 
+// Three launches where there may be many moves and one workgroup to a head leaves the chip
+// idle or reads its weights often (it holds 8192 of them, 32768 with the search alone).
+// One launch and three, heads of 128, us: 8 heads, 1024 kept of 2304 rows 19.5 and 22.7,
+// 1536 of 8192 31.1 and 28.5, 4096 of 8192 39.7 and 27.2; 128 heads, 2048 of 8192 44.7 and
+// 46.6, 2048 of 32768 102 and 88. Few moves of a long sequence would gain too (8 heads,
+// 1024 of 32768: 59 and 44), but the host knows the table's width, not the lengths, and
+// short sequences under a wide table would lose (640 rows: 13.1 and 21.8).
 template <int NC>
 void evict(const KvEvictArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)(a.c.B * a.c.H);
   const int keep = a.budget - a.recent;
-  if (heads >= 128 || keep <= 512) {
+  const int64_t cap = (int64_t)a.c.W * a.c.P;
+  if (min((int64_t)keep - a.sinks, cap - a.budget) <= 1024 || (heads >= 128 && cap <= 16384)) {
     k_kv_evict<NC, true><<<heads, kThreads, 0, s>>>(a);
     return;
   }
