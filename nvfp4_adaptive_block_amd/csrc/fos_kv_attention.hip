@@ -199,7 +199,6 @@ struct Pages {
     there = page >= 0 && page < pages;
     return there ? ((int64_t)page * H + h) * P + (pos - by_page.div(pos) * P) : 0;
   }
-  __device__ __forceinline__ int64_t row_at(int pos, int len, bool& there) const { return row(page(pos, len), pos, there); }
 };
 
 // What a wave loads of 32 keys, ahead of their use. Codes and the value rows' scales come
@@ -861,8 +860,9 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   if (half == 0 && row.have && a.lse) a.lse[at] = l == 0.0f ? -__builtin_huge_valf() : (m + __log2f(l)) * kLn2;
 }
 
-// Joins the parts of a row. A wave has a row where there are few parts, else a
-// workgroup of sixteen waves, each with every sixteenth part.
+// Joins the parts of a row. A wave has a row where there are at most 64 parts, else a
+// workgroup of sixteen waves, each with every sixteenth part. Bound by its launch and the
+// parts' bytes, which the caches hold.
 template <int DT, int NC, int WAVES>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_kv_join(KvAttendArgs a) {
   constexpr int D = 32 * NC, kEach = (D + 63) / 64, kParts = WAVES == 1 ? 64 : kMaxParts;
@@ -1119,8 +1119,21 @@ __global__ __launch_bounds__(256, kRows == 32 && NC <= 4 ? 4 : 2) void k_kv_weig
   }
 }
 
-// Whether sequences have rows enough, on the whole, for the tile kernel.
-bool kv_tiled(int64_t T, int B, int G) { return T * G > (int64_t)32 * B; }
+// Tiles of `rows` rows, of the mean sequence.
+int64_t kv_tiles(int64_t T, int B, int H, int G, int64_t rows) {
+  const int64_t per = (T * G / B + rows - 1) / rows;
+  return (per < 1 ? 1 : per) * B * H;
+}
+
+// The tile kernel from 49 rows to a sequence on, unless the other's smallest parts are so few
+// that the chip runs them at once. Few rows and tiles, us, heads of 128 unless said: 8 heads of
+// 8192 keys, 32 rows 17.1 and 18.1, 48 19.9 and 18.6, 96 24.5 and 21.1; 4 sequences of that 32
+// rows 26.4 and 35.8, 64 38.8 and 39.6, 96 54 and 42; 16 of 2048 keys, 32 rows 35.3 and 36.5, 64
+// 44 and 39.8; 8 heads of 64 with 2048 keys, 256 rows 13.8 and 14.5; 8 heads of 1024 keys, 256
+// rows 15.5 and 18.3.
+bool kv_tiled(int64_t T, int B, int H, int G, int64_t max_len) {
+  return T * G > (int64_t)48 * B && kv_tiles(T, B, H, G, 16) * ((max_len + 127) / 128) > 2048;
+}
 
 // Waves that one workgroup's LDS holds, of a whole cache (kv_wide).
 template <int NC>
@@ -1129,7 +1142,7 @@ constexpr int kWideWaves = NC <= 4 ? 12 : NC == 6 ? 8 : 4;
 template <int DT, int NC>
 hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.T * a.G;
-  const int per = kv_tiled(a.T, a.c.B, a.G) ? 128 : 16;
+  const int per = kv_tiled(a.T, a.c.B, a.c.H, a.G, a.max_len) ? 128 : 16;
   const int64_t tiles = rows / per + a.c.B + 1;  // no fewer than the sequences' tiles and the tail's
   const dim3 grid((unsigned)(tiles * a.c.H * a.splits));
   if (per == 128)
@@ -1138,7 +1151,9 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
     k_kv_stream<DT, NC, kWideWaves<NC>><<<grid, 64 * kWideWaves<NC>, 0, s>>>(a);
   else
     k_kv_stream<DT, NC, 4><<<grid, 256, 0, s>>>(a);
-  if (a.splits > 8)
+  // one wave to a row and sixteen, us of attention: 32 parts, 32 rows 8.9 and 9.6; 64 parts, 8 rows
+  // 10.8 and 10.0, 128 rows 12.3 and 13.2; 9 parts, 4096 rows 35.2 and 49.6
+  if (a.splits > 64 || (a.splits > 32 && rows * a.c.H < 64))
     k_kv_join<DT, NC, 16><<<dim3((unsigned)(rows * a.c.H)), 1024, 0, s>>>(a);
   else if (a.splits > 1)
     k_kv_join<DT, NC, 1><<<dim3((unsigned)((rows * a.c.H + 3) / 4)), 256, 0, s>>>(a);
@@ -1147,6 +1162,10 @@ hipError_t attend(const KvAttendArgs& a, hipStream_t s) {
 
 template <int DT, int NC>
 hipError_t weights(const KvAttendArgs& a, hipStream_t s) {
+  // 32 rows in LDS and four workgroups to a CU, or 256 and two, us: 8 heads of 8192 keys, 32 rows
+  // 5.8 and 6.3, 64 9.3 and 7.9; 16 sequences of 2048 keys, 32 rows 9.6 and 11.6, 128 28.6 and 21.4.
+  // Workgroups: as many as run at once (64 heads of 4096 keys, a token each: 256 workgroups 11.4 us,
+  // 512 to 1280 8.8, 2048 11.1; 8 heads of 32768 keys, 256 rows: 256 43, 512 33.5, 1024 40).
   const bool few = (int64_t)a.T * a.G <= (int64_t)32 * a.c.B;
   const int64_t heads = (int64_t)a.c.B * a.c.H, most = (a.max_len + 127) / 128;
   int64_t chunks = (few ? 1280 : 512) / heads;
@@ -1176,27 +1195,38 @@ hipError_t run(bool attention, const KvAttendArgs& a, hipStream_t s) {
 }  // namespace
 
 // A short cache of few sequences is left whole, by twelve waves to a workgroup (eight for
-// D 192, which LDS holds): one launch instead of two and no workspace (1001 keys, one token, 8
-// heads of 128: TIMES).
+// D 192: what LDS holds), with one launch and no workspace. One token on 8 heads of 128, 1000
+// keys: 11.7 us instead of 9.0 in parts, but the call 14.0 instead of 21.3; 16 such sequences
+// 13.6 instead of 16.2. (Eight waves: 12.4.)
 bool kv_wide(int64_t T, int B, int H, int G, int D, int64_t max_len) {
-  return !kv_tiled(T, B, G) && D <= 192 && max_len <= 1024 && (T * G / B + 15) / 16 * B * H < 128;
+  return !kv_tiled(T, B, H, G, max_len) && D <= 192 && max_len <= 1024 && kv_tiles(T, B, H, G, 16) < 128;
 }
 
-// Few rows: where the tiles alone fill the chip's 256 CUs, workgroups enough to even out
-// lengths (64 sequences of 2500 to 8192 tokens on 8 heads: 1024 workgroups 103 us, 2304 96);
-// else about as many as run at once (131072 keys for one token on 4 heads: 512 to 2304 25 to
-// 27 us, 384 30; 17 sequences of up to 2999 tokens, 12 heads of 64: 512 22.8, 1024 19.4, 1536
-// 21.2). A part has four steps at least, one to a wave (1001 keys: 8.2 us; of two 9.4, of
-// eight 9.7).
+// Parts of the keys. Few rows: where the tiles alone fill the chip's 256 CUs, workgroups enough
+// to even out lengths (64 sequences of 2500 to 8192 tokens on 8 heads: 1024 workgroups 103 us,
+// 2304 96); else about as many as run at once (131072 keys for one token on 4 heads: 512 to
+// 2304 25 to 27 us, 384 30; 17 sequences of up to 2999 tokens, 12 heads of 64: 512 22.8, 1024
+// 19.4, 1536 21.2). A part has four steps at least, one to a wave (1001 keys: 8.2 us; of two
+// 9.4, of eight 9.7).
+// Tiles: 512 workgroups, two to a CU, of eight steps or more, but no fewer than 256 where that
+// leaves four (8 heads of 8192 keys, 96 rows, parts of 512 keys 25.5 us, 256 21.1; 256 rows,
+// 512 workgroups of 256 keys 33.4, 256 of 512 29.5).
 int kv_splits(int64_t T, int B, int H, int G, int D, int64_t max_len) {
   if (kv_wide(T, B, H, G, D, max_len)) return 1;
-  const bool tiled = kv_tiled(T, B, G);
-  const int64_t rows = tiled ? 128 : 16, least = tiled ? 512 : 128;
-  const int64_t per = (T * G / B + rows - 1) / rows, tiles = (per < 1 ? 1 : per) * B * H;
-  const int64_t most = (max_len + least - 1) / least;
-  int64_t s = (tiled ? 512 : tiles >= 256 ? 2304 : 1024) / tiles;
-  if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
+  auto parts = [=](int64_t tiles, int64_t groups, int64_t least) {
+    const int64_t s = groups / tiles, most = (max_len + least - 1) / least;
+    return (int)(s > most ? most : s);
+  };
+  int s;
+  if (kv_tiled(T, B, H, G, max_len)) {
+    const int64_t tiles = kv_tiles(T, B, H, G, 128);
+    const int x = parts(tiles, 512, 512), y = parts(tiles, 256, 256);
+    s = x > y ? x : y;
+  } else {
+    const int64_t tiles = kv_tiles(T, B, H, G, 16);
+    s = parts(tiles, tiles >= 256 ? 2304 : 1024, 128);
+  }
+  return s < 1 ? 1 : s > kMaxParts ? kMaxParts : s;
 }
 
 int64_t kv_attend_workspace(int64_t T, int H, int G, int D, int splits) {

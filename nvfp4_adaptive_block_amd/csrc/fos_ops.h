@@ -154,7 +154,7 @@ struct KvAttendArgs {
 };
 // Parts that the keys are cut into, from sizes that the host knows.
 int kv_splits(int64_t T, int B, int H, int G, int D, int64_t max_len);
-// Whether the few-rows kernel has eight waves to a workgroup.
+// Whether a short cache is left whole, by more waves to a workgroup.
 bool kv_wide(int64_t T, int B, int H, int G, int D, int64_t max_len);
 int64_t kv_attend_workspace(int64_t T, int H, int G, int D, int splits);
 hipError_t launch_kv_attention(int dt, const KvAttendArgs& a, hipStream_t s);

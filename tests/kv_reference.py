@@ -106,6 +106,11 @@ def attention(cache, q, new, causal=True, scale=None):
             size = (w * vd[:, None]) @ vv.abs()
             # weights: the scores' errors, three steps of the exponential; the sums of L terms
             ew = torch.where(w > 0, err, torch.zeros_like(err)).amax(-1) + 3 * 2.0 ** -23
+            # m lies within 7 of max_j z_j + log2 max(S_j, 2^-90), so for a weight that counts |z_j - m|
+            # is at most the largest |log2 max(S_j, 2^-90)| and 7: it is rounded when it is taken
+            # (2^-24 of it), between parts (2^-24), and as log2 of the sum of L such (a step, 2^-23)
+            far = vd.clamp_min(2.0 ** -90).log2().abs().amax(-1) + 7 + math.log2(L)
+            ew = ew + 4 * E24 * math.log(2) * far[:, None]
             es = (4 * math.sqrt(L) + 16) * E24
             # weights times S_dec in fp16: half a step of fp16, 2^-11, or below fp16's normal range
             # 2^-25 of the unit 2^m. m is the running maximum of z_j + log2 max(S_j, 2^-90), so in the

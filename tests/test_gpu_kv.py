@@ -14,6 +14,7 @@ from synthdata import raw_bits
 
 pytestmark = pytest.mark.gpu
 DIMS = [32, 64, 96, 128, 192, 256]
+LONG = 10 ** 6  # an expected length at which 49 rows to a sequence go in tiles of 128
 
 
 def ends(new):
@@ -211,17 +212,29 @@ def test_attention_groups(G, P, dtype):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("D", DIMS)
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_attention_many_tokens(D, dtype, causal):
+@pytest.mark.parametrize("max_len", [0, LONG])
+def test_attention_many_tokens(D, dtype, causal, max_len):
     """Prompts, chunks behind a prefix, sequences without new tokens, a padded tail,
     and more new tokens than the cache has: their first see no key."""
     lens, new = [150, 300, 40, 0, 33], [150, 70, 0, 3, 47]
     cache = ref.Cache(lens, 2, D, 32, seed=D + 7)
-    check_attention(cache, ref.queries(sum(new) + 5, 4, D, dtype, D, 2.0), new, causal)
+    check_attention(cache, ref.queries(sum(new) + 5, 4, D, dtype, D, 2.0), new, causal, max_len=max_len)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attention_whole_tiles(D, dtype, causal):
+    """Heads enough for tiles whose keys are not in parts."""
+    cache = ref.Cache([150, 33, 5], 30, D, 16, seed=D)
+    new = [80, 30, 5]
+    assert fos.fos_kv_attention_workspace(118, 240, 3, cache.W, 30, 16, D) == 0
+    check_attention(cache, ref.queries(118, 240, D, dtype, D), new, causal)
 
 
 @pytest.mark.parametrize("H,G,n,L", [(1, 1, 1, 5000), (2, 4, 1, 3001), (1, 8, 5, 2500), (3, 2, 130, 1111), (1, 4, 600, 600),
                                      (8, 4, 33, 700), (1, 1, 257, 900)])
-@pytest.mark.parametrize("max_len", [0, 100, 10 ** 6])
+@pytest.mark.parametrize("max_len", [0, 100, LONG])
 def test_attention_splits(H, G, n, L, max_len):
     """Whatever the caller expects the length to be."""
     cache = ref.Cache([L, L // 3 + n], H, 128, 64, seed=L)
@@ -235,8 +248,8 @@ def test_attention_wide_table_of_a_short_cache():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("n", [1, 40])
-def test_attention_extreme_rows(n, dtype):
+@pytest.mark.parametrize("n,max_len", [(1, 0), (40, 0), (40, LONG)])
+def test_attention_extreme_rows(n, max_len, dtype):
     """Value rows of very different size, among them one that is huge where its weight
     is tiny and rows of zeros with the largest weight; queries of any size and scale."""
     cache = ref.Cache([200], 2, 128, 64, seed=8)
@@ -250,38 +263,39 @@ def test_attention_extreme_rows(n, dtype):
     q[:, 0] = (8 * kv[0, 150] / kv[0, 150].norm()).to(q.dtype)
     q[:, 1] *= 1e-3 if dtype == "fp16" else 1e-25
     q[:, 2] *= 30
-    check_attention(cache, q, [n])
-    check_attention(cache, q, [n], scale=-0.03)
-    check_attention(cache, q, [n], scale=0.0)
+    check_attention(cache, q, [n], max_len=max_len)
+    check_attention(cache, q, [n], scale=-0.03, max_len=max_len)
+    check_attention(cache, q, [n], scale=0.0, max_len=max_len)
     if dtype == "bf16":
         q[:, 3] *= 1e20
-        check_attention(cache, q, [n], scale=1e-21)
+        check_attention(cache, q, [n], scale=1e-21, max_len=max_len)
 
 
 @pytest.mark.parametrize("size_k,size_v", [(1e-20, 1e-25), (1e3, 1e8), (1e15, 1e25)])
 def test_attention_sizes_of_the_cache(size_k, size_v):
     cache = ref.Cache([100, 40], 2, 64, 16, seed=10, sizes=(size_k, size_v))
     check_attention(cache, ref.queries(7, 4, 64, "bf16", 11), [4, 3], scale=0.02 / size_k)
+    check_attention(cache, ref.queries(90, 4, 64, "bf16", 11), [60, 30], scale=0.02 / size_k, max_len=LONG)
 
 
-@pytest.mark.parametrize("n", [1, 50])
-def test_attention_not_a_number(n):
+@pytest.mark.parametrize("n,max_len", [(1, 0), (50, 0), (50, LONG)])
+def test_attention_not_a_number(n, max_len):
     """A query with a NaN or an infinity is NaN; others are as without it."""
     cache = ref.Cache([90], 2, 128, 16, seed=12)
     q = ref.queries(n, 4, 128, "bf16", 13)
-    out, lse, _ = attend(cache, q, [n])
+    out, lse, _ = attend(cache, q, [n], max_len=max_len)
     bad = q.clone()
     bad[0, 1, 77] = math.nan
     bad[n - 1, 2, 3] = math.inf
-    got, got_lse, _ = attend(cache, bad, [n])
+    got, got_lse, _ = attend(cache, bad, [n], max_len=max_len)
     hit = torch.zeros(n, 4, dtype=torch.bool)
     hit[0, 1] = hit[n - 1, 2] = True
     assert torch.isnan(got.cpu()[hit]).all() and torch.isnan(got_lse.cpu()[hit]).all()
     assert same(got[~hit.cuda()], out[~hit.cuda()]) and same(got_lse[~hit.cuda()], lse[~hit.cuda()])
 
 
-@pytest.mark.parametrize("n", [1, 3, 60])
-def test_attention_strides_and_repeats(n):
+@pytest.mark.parametrize("n,max_len", [(1, 0), (3, 0), (60, 0), (60, LONG)])
+def test_attention_strides_and_repeats(n, max_len):
     """Queries inside wider rows; the same bits again, on any workspace and another stream."""
     cache = ref.Cache([400, 77], 2, 128, 64, seed=14)
     T = 2 * n
@@ -289,58 +303,61 @@ def test_attention_strides_and_repeats(n):
     q = wide[:, 2:10]
     k, v, table, lens = cache.on_device()
     args = (ends([n, n]), k, v, table, lens)
-    out, lse = fos.fos_kv_attention(q, *args)
-    again, lse2 = fos.fos_kv_attention(q.contiguous(), *args)
+    out, lse = fos.fos_kv_attention(q, *args, max_len=max_len)
+    again, lse2 = fos.fos_kv_attention(q.contiguous(), *args, max_len=max_len)
     assert same(out, again) and same(lse, lse2)
-    need = fos.fos_kv_attention_workspace(T, 8, 2, cache.W, 2, 64, 128)
+    need = fos.fos_kv_attention_workspace(T, 8, 2, cache.W, 2, 64, 128, max_len)
     ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
-        third, _ = fos.fos_kv_attention(q, *args, workspace=ws)
+        third, _ = fos.fos_kv_attention(q, *args, workspace=ws, max_len=max_len)
     s.synchronize()
     assert same(out, third) and (ws[need:] == 255).all()
 
 
-def test_attention_bad_cache():
+@pytest.mark.parametrize("n,max_len", [(2, 0), (60, 0), (60, LONG)])
+def test_attention_bad_cache(n, max_len):
     """Pages that are none hold no keys; lengths past the table end with it."""
     cache = ref.Cache([64, 50], 2, 64, 16, seed=16)
-    q = ref.queries(4, 4, 64, "bf16", 17)
+    q = ref.queries(2 * n, 4, 64, "bf16", 17)
     keep = cache.table.clone()
     cache.table[0, 1] = cache.pages
     cache.table[0, 3] = -1
-    out, lse, _ = attend(cache, q, [2, 2], causal=False)
+    out, lse, _ = attend(cache, q, [n, n], causal=False, max_len=max_len)
     # the same with the two pages left out
     cache.table = keep.clone()
     cache.table[0, 1] = keep[0, 2]
     cache.lens[0] = 32
-    want, bound, want_lse, lb = ref.attention(cache, q, [2, 2], causal=False)
+    want, bound, want_lse, lb = ref.attention(cache, q, [n, n], causal=False)
     assert_within(out, want, bound, "out")
     assert_within(lse, want_lse, lb, "lse")
     # no page at all
     cache.table[0] = -1
     cache.lens[0] = 64
-    out, lse, _ = attend(cache, q, [2, 2])
-    assert (out[:2] == 0).all() and (lse[:2] == -math.inf).all()
+    out, lse, _ = attend(cache, q, [n, n], max_len=max_len)
+    assert (out[:n] == 0).all() and (lse[:n] == -math.inf).all()
     # lengths outside [0, W P]
     cache.table = keep
     cache.lens = [10 ** 6, -5]
-    out, lse, status = attend(cache, q, [2, 2])
+    out, lse, status = attend(cache, q, [n, n], max_len=max_len)
     assert status == fos.STATUS_BAD_CACHE
     cache.lens = [64, 0]
-    want, bound, want_lse, lb = ref.attention(cache, q, [2, 2])
+    want, bound, want_lse, lb = ref.attention(cache, q, [n, n])
     assert_within(out, want, bound, "out")
-    assert (lse[2:] == -math.inf).all()
+    assert (lse[n:] == -math.inf).all()
 
 
-def test_attention_bad_offsets():
+@pytest.mark.parametrize("n,max_len", [(4, 0), (100, 0), (100, LONG)])
+def test_attention_bad_offsets(n, max_len):
     cache = ref.Cache([64, 50], 2, 64, 16, seed=16)
     k, v, table, lens = cache.on_device()
-    q = ref.queries(4, 4, 64, "bf16", 17).cuda()
-    for offs in ([3, 2], [2, 9], [-1, 4]):
+    q = ref.queries(n, 4, 64, "bf16", 17).cuda()
+    for offs in ([n - 1, n - 2], [2, n + 5], [-1, n]):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         out, raw = guarded(q.shape, q.dtype)
-        fos.fos_kv_attention(q, torch.tensor(offs, dtype=torch.int32).cuda(), k, v, table, lens, out=out, status=status)
+        fos.fos_kv_attention(q, torch.tensor(offs, dtype=torch.int32).cuda(), k, v, table, lens, out=out, status=status,
+                             max_len=max_len)
         assert int(status.item()) == fos.STATUS_BAD_OFFS
         assert_guard(raw)
 
@@ -410,8 +427,8 @@ def test_weights_of_the_last_tokens():
 # ------------------------------------------------------------------- evict
 
 
-def check_evict(lens, H, D, P, budget, sinks, recent, seed=0, acc=None):
-    cache = ref.Cache(lens, H, D, P, seed)
+def check_evict(lens, H, D, P, budget, sinks, recent, seed=0, acc=None, W=None):
+    cache = ref.Cache(lens, H, D, P, seed, W=W)
     shape = (cache.B, H, cache.W * P)
     acc = torch.exp(2 * torch.randn(*shape, generator=gen(seed + 1))) if acc is None else acc(shape)
     kc, vc, table, lens_d = cache.on_device()
@@ -428,7 +445,7 @@ def check_evict(lens, H, D, P, budget, sinks, recent, seed=0, acc=None):
     came, want_acc = ref.evict(cache, acc, budget, sinks, recent)
     assert same(acc_d, want_acc)
     for side, got in zip(cache.sides, (kc, vc)):
-        want = [t.clone() for t in side]
+        got, want = [t.cpu() for t in got], [t.clone() for t in side]
         for (b, h), src in came.items():
             for i, j in enumerate(src):
                 to, of = int(cache.table[b, i // P]), int(cache.table[b, j // P])
@@ -455,6 +472,18 @@ def test_evict_shares(budget, sinks, recent):
 @pytest.mark.parametrize("n,budget,recent", [(3000, 500, 100), (2500, 2400, 1000), (1025, 1024, 128), (5000, 4000, 70)])
 def test_evict_long(n, budget, recent):
     check_evict([n], 2, 64, 64, budget, 4, recent, seed=n)
+
+
+@pytest.mark.parametrize("D", DIMS)
+def test_evict_many_moves(D):
+    """Enough of them for launches of their own; sequences of any length beside them."""
+    check_evict([2700, 1250, 1500, 40, 0, 1401], 2, D, 64, 1400, 4, 200, seed=D)
+
+
+@pytest.mark.parametrize("W", [41, 300])
+def test_evict_many_heads(W):
+    """128 of them, with many moves, under a table of their length and a wider one."""
+    check_evict([2600, 30], 64, 32, 64, 1200, 4, 40, seed=W, W=W)
 
 
 ODD = [math.nan, math.inf, -math.inf, 0.0, -0.0, 1.0, 1.0000001, -1.0, 1e-40, -1e-40, 3e38]
