@@ -262,10 +262,10 @@ void append(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 
-// Weights in order as unsigned numbers: NaN lowest, zeros alike.
+// Weights in order as unsigned numbers: NaN lowest, zeros alike; 0 is no weight.
 __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);
-  return v != v ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
+  return v != v ? 1u : (u >> 31) ? ~u : u | 0x80000000u;
 }
 
 // Row of the cache at a position of sequence b.
@@ -403,7 +403,10 @@ __device__ Cut find_cut(const KvEvictArgs& a, int bh, int* bad) {
 }
 
 // The moves of the middle, in order; returns their number. A lane holds BATCH weights at a
-// time.
+// time. One CU has all of a head's, and is bound by the instructions for each (32768 weights:
+// read 3 us, the three digits 4, 2 and 2, counted 2, written 3): lanes past the end hold the
+// lowest order, which is counted but never wanted, instead of being masked (54 to 52 us for
+// 32 heads of up to 32768 rows cut to 4096).
 template <int BATCH>
 __device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* share) {
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -422,17 +425,17 @@ __device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* 
 #pragma unroll
     for (int k = 0; k < BATCH; k++) v[k] = __builtin_amdgcn_raw_buffer_load_b32(r, 4 * (64 * k + lane), 0, 0);
 #pragma unroll
-    for (int k = 0; k < BATCH; k++) o[k] = order_of(__uint_as_float(v[k]));
+    for (int k = 0; k < BATCH; k++) o[k] = i + 64 * k + lane < to ? order_of(__uint_as_float(v[k])) : 0u;
   };
   if (held && from < to) read(from);
-  // f(the first of 64 places, this lane's weight's order, whether it has one) along the wave's stretch
+  // f(the first of 64 places, the order of this lane's weight) along the wave's stretch
   auto stretch = [&](auto f) {
     for (int i = from; i < to; i += 64 * BATCH) {
       if (!held) read(i);
 #pragma unroll
       for (int k = 0; k < BATCH; k++) {
         if (i + 64 * k >= to) break;
-        f(i + 64 * k, o[k], i + 64 * k + lane < to);
+        f(i + 64 * k, o[k]);
       }
     }
   };
@@ -446,8 +449,8 @@ __device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* 
     hist[t] = 0;
     hist[t + 1024] = 0;
     __syncthreads();
-    stretch([&](int, uint32_t w, bool have) {
-      if (have && (w & mask) == found) atomicAdd(&hist[(w >> shift) & low], 1);
+    stretch([&](int, uint32_t w) {
+      if ((w & mask) == found) atomicAdd(&hist[(w >> shift) & low], 1);
     });
     __syncthreads();
     d = find_digit<2048>(hist, share, d.want);
@@ -459,7 +462,7 @@ __device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* 
   int equals = 0;
   if (some) {
     int c = 0;
-    stretch([&](int, uint32_t w, bool have) { c += __popcll(__ballot(have && w == found)); });
+    stretch([&](int, uint32_t w) { c += __popcll(__ballot(w == found)); });
     if (lane == 0) share[wave] = c;
     __syncthreads();
     for (int w = 0; w < wave; w++) equals += share[w];
@@ -469,29 +472,26 @@ __device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* 
   auto below = [](unsigned long long m) {
     return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
   };
+  const int ends = min(keep, to);
   int n_free = 0, n_moved = 0, eq = equals;
-  int2* out = nullptr;
-  auto visit = [&](int i, uint32_t w, bool have) {
-    bool kept = have && w >= found;
+  // whether a place below `keep` is given up, and whether one behind is kept
+  auto look = [&](int i, uint32_t w, bool& is_free, bool& is_moved) {
+    bool kept = w >= found;
     if (some) {
-      const unsigned long long same = __ballot(have && w == found);
+      const unsigned long long same = __ballot(w == found);
       if (w == found && eq + below(same) >= d.want) kept = false;
       eq += __popcll(same);
     }
-    if (i < keep) {
-      const bool is = have && !kept && i + lane < keep;
-      const unsigned long long m = __ballot(is);
-      if (out && is) out[n_free + below(m)].y = i + lane;
-      n_free += __popcll(m);
-    }
-    if (i + 64 > keep) {
-      const bool is = kept && i + lane >= keep;
-      const unsigned long long m = __ballot(is);
-      if (out && is) out[n_moved + below(m)].x = i + lane;
-      n_moved += __popcll(m);
-    }
+    const bool in = i + lane < ends;
+    is_free = in && !kept;
+    is_moved = kept && !in;
   };
-  stretch(visit);
+  stretch([&](int i, uint32_t w) {
+    bool is_free, is_moved;
+    look(i, w, is_free, is_moved);
+    n_free += __popcll(__ballot(is_free));
+    n_moved += __popcll(__ballot(is_moved));
+  });
   if (lane == 0) {
     share[wave] = n_free;
     share[kWaves + wave] = n_moved;
@@ -507,8 +507,16 @@ __device__ int find_moves(const KvEvictArgs& a, const Cut& cut, int* hist, int* 
     }
     holes += share[w];
   }
-  out = cut.moves;
-  stretch(visit);
+  int2* out = cut.moves;
+  stretch([&](int i, uint32_t w) {
+    bool is_free, is_moved;
+    look(i, w, is_free, is_moved);
+    const unsigned long long f = __ballot(is_free), m = __ballot(is_moved);
+    if (is_free) out[n_free + below(f)].y = i + lane;
+    if (is_moved) out[n_moved + below(m)].x = i + lane;
+    n_free += __popcll(f);
+    n_moved += __popcll(m);
+  });
   return holes;
 }
 
