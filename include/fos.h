@@ -506,7 +506,8 @@ int fos_balance_loss_backward(const float* dloss, const void* logits, int dtype,
  * it holds. A sequence may share pages with another where no call writes them.
  * The tokens of a call are packed rows [T, heads, D], sequence b's are rows
  * [offs[b-1], offs[b]) (offs[-1] = 0) and the last ones of its cache.
- *   D is 32, 64, 96, 128, 192 or 256; P a multiple of 16; W P at most 2^30;
+ *   D is 32, 64, 96, 128, 192 or 256; P a multiple of 16; W P at most 2^30, B and H
+ *   2^20, B H below 2^22, T times the heads at most 2^27;
  *   codes, scales and sdec are 16-byte aligned.
  * Found on the device, and reported in the nullable d_status: offsets that
  * decrease or leave [0, T] (FOS_STATUS_BAD_OFFS; the rows' results are then
@@ -576,7 +577,7 @@ int fos_kv_weights(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride
  * move to [budget - recent, budget) in theirs. acc [B, H, W P] moves along, and acc of
  * [budget, n) becomes 0. Shorter sequences are left as they are. The order of the
  * rows before the last ones is not the tokens' any more, which attention does not see.
- *   new_lens: int32 [B], min(n, budget); not cache->lens itself.
+ *   new_lens: int32 [B], min(n, budget); apart from cache->lens.
  *   work:     fos_kv_evict_workspace() bytes, 16-byte aligned.
  * The pages of a sequence that is cut must be its own. One that has a page number
  * out of range is left as it is (FOS_STATUS_BAD_CACHE, new_lens = n). */

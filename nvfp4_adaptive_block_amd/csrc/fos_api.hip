@@ -864,8 +864,8 @@ int check_kv_sizes(int64_t B, int64_t W, int H, int P, int D) {
     return fail(FOS_ERR_SHAPE, "D must be 32, 64, 96, 128, 192 or 256, got %d", D);
   if (P % 16) return fail(FOS_ERR_SHAPE, "P=%d is not a multiple of 16", P);
   if (W > kMaxKvPlaces / P) return fail(FOS_ERR_SHAPE, "W*P exceeds 2^30 (W=%lld P=%d)", (long long)W, P);
-  if (B > (1 << 20) || H > (1 << 20) || B * H > (1 << 22))
-    return fail(FOS_ERR_SHAPE, "B, H at most 2^20 and B*H 2^22, got B=%lld H=%d", (long long)B, H);
+  if (B > (1 << 20) || H > (1 << 20) || B * H >= (1 << 22))  // the eviction has 1024 threads for each
+    return fail(FOS_ERR_SHAPE, "B, H at most 2^20 and B*H below 2^22, got B=%lld H=%d", (long long)B, H);
   return FOS_OK;
 }
 
@@ -1046,7 +1046,8 @@ int fos_kv_evict(const fos_kv_cache* cache, float* acc, int budget, int sinks, i
   if (budget < 0 || sinks < 0 || recent < 0 || budget > kMaxKvPlaces || (int64_t)sinks + recent > budget)
     return fail(FOS_ERR_INVALID_ARG, "budget=%d must hold sinks=%d and recent=%d, none negative", budget, sinks, recent);
   if (!acc || !new_lens) return fail(FOS_ERR_INVALID_ARG, "acc and new_lens must be non-NULL");
-  if (new_lens == cache->lens) return fail(FOS_ERR_INVALID_ARG, "new_lens must not be lens");
+  if (new_lens < cache->lens + cache->B && cache->lens < new_lens + cache->B)
+    return fail(FOS_ERR_INVALID_ARG, "new_lens must not overlap lens");
   if (!aligned(acc, 4) || !aligned(new_lens, 4) || !aligned(d_status, 4)) return fail(FOS_ERR_ALIGN, "acc/new_lens/status misaligned");
   const int64_t need = fos_kv_evict_workspace(cache->B, cache->H, budget, recent);
   if (!work || work_bytes < need)

@@ -315,10 +315,17 @@ __device__ __forceinline__ Place place_of(const KvAttendArgs& a) {
 // ---------------------------------------------------------------- few rows
 //
 // A workgroup has 16 rows and a part of their keys; its four waves (twelve for a short
-// cache that is left whole) take the part's steps of 32 keys in turn, each on its own, and join in LDS at the end. Keys come
-// from memory once, a step ahead, to registers; codes of keys turn through the
-// wave's own LDS from the loads' order to the matrix instruction's, value rows are
-// decoded into it and read back transposed.
+// cache that is left whole) take the part's steps of 32 keys in turn, each on its own, and
+// join in LDS at the end. Keys come from memory once, a step ahead, to registers; codes of
+// keys turn through the wave's own LDS from the loads' order to the matrix instruction's,
+// value rows are decoded into it and read back transposed.
+//
+// A key and its value of D are 9 D / 8 + 8 bytes, from 4 to 16 rows use them, so memory is the
+// bound where there is work enough: 64 sequences of 2500 to 8192 tokens, 8 heads of 128, 416 MB
+// in 91 us and a join of 5, 4.3 TB/s. One sequence of 131072 tokens on 4 heads, 80 MB, takes 23 us
+// (3.4 TB/s): each of 1024 workgroups has eight steps, and its start and end weigh. Two steps ahead
+// lost (17 x 12 heads of 64: 21.5 us for 19.4), and so did branches around the loads. Three waves
+// to a SIMD where registers allow it (D up to 128).
 
 template <int NC, int WAVES> struct StreamLds {
   // A value row in fp16. Where it is a multiple of the banks' 256 bytes its pieces of 16
@@ -556,6 +563,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 // time. A wave decodes 16 of the 64 keys' rows to fp16 into LDS, one step ahead of their
 // use and with the codes of the step after that on their way, and all four waves read
 // them: keys as rows, values transposed.
+//
+// 4 D operations for each row and key are the bound, but the vector units' part (decode, scale,
+// maximum, exponential, conversion) nearly fills the time beside them: 8192 new tokens, 32 query
+// heads of 128, 0.56 PFLOP in 695 us, 800 TFLOP/s; matrix units busy 30 % of the cycles, vector
+// units 50 to 57 %, LDS 45 %. Decode goes beside the first product and exponentials beside the
+// second, which the scheduler is told. Two workgroups to a CU for D 96 and 128 (three of 32 keys:
+// 730 us; bounded to three with spills: 947). Not kept: the next step's first product beside this
+// one's softmax (816 us), a wave's priority raised in its products (738 for 722 then), raw codes
+// two steps ahead. D 256 fills 256 registers and spills 47, one workgroup to a CU: 512 TFLOP/s.
 
 template <int NC> struct TileLds {
   static constexpr int kKeys = 64;
@@ -931,10 +947,16 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_kv_join(KvAtt
 // ---------------------------------------------------------------- weights
 //
 // A workgroup stages 256 rows of q (or 32, where sequences have no more) in LDS, in fp16,
-// and passes over its keys, 32 to a wave at a time, decoded to registers. Here the keys are the columns of the matrix
-// instruction's result, so that a lane has one key and sums its weights over the rows
-// in its own registers. A key belongs to one wave, so the sums are added to what is there
-// without atomics, in an order that is always the same.
+// and passes over its keys, 32 to a wave at a time, decoded to registers. Here the keys are
+// the columns of the matrix instruction's result, so that a lane has one key and sums its
+// weights over the rows in its own registers. A key belongs to one wave, so the sums are
+// added to what is there without atomics, in an order that is always the same.
+//
+// Keys alone are read, 9 D / 16 + 4 bytes each, and 4 bytes of sums read and written. 16 sequences
+// of up to 4096 tokens on 8 heads of 128, a token each, 28 MB: 12.4 us, the chain of a workgroup's
+// start and three or four steps. 64 new tokens of 32 query heads over 32768 keys, 17.4 GFLOP: 33 us,
+// bound by the exponentials of 256 rows for each key beside the products (128 rows staged: 44 us
+// for 40 then).
 
 // Half a row: 16 NC neighbouring values, in NC blocks.
 template <int NC> struct Half {

@@ -80,7 +80,7 @@ def test_what_is_right_passes_every_check(call):
     (INVALID, dict(B=0)), (INVALID, dict(W=0)), (INVALID, dict(H=0)), (INVALID, dict(P=0)), (INVALID, dict(P=-16)),
     (SHAPE, dict(P=24)), (SHAPE, dict(P=8)), (SHAPE, dict(D=0)), (SHAPE, dict(D=16)), (SHAPE, dict(D=80)),
     (SHAPE, dict(D=160)), (SHAPE, dict(D=512)), (SHAPE, dict(D=-64)), (SHAPE, dict(W=2 ** 30, P=16)),
-    (SHAPE, dict(B=2 ** 20 + 1)), (SHAPE, dict(B=2 ** 20, H=8)), (INVALID, dict(pages=0)), (INVALID, dict(pages=-1)),
+    (SHAPE, dict(B=2 ** 20 + 1)), (SHAPE, dict(B=2 ** 20, H=8)), (SHAPE, dict(B=2 ** 20, H=4)), (INVALID, dict(pages=0)), (INVALID, dict(pages=-1)),
     (SHAPE, dict(pages=2 ** 40)), (INVALID, dict(table=0)), (INVALID, dict(lens=0)), (ALIGN, dict(table=T_ + 2)),
     (ALIGN, dict(lens=L + 1)), (INVALID, dict(k=rows(codes=0))), (INVALID, dict(k=rows(scales=0))),
     (INVALID, dict(k=rows(sdec=0))), (ALIGN, dict(k=rows(codes=K + 8))), (ALIGN, dict(k=rows(scales=S + 2))),
@@ -140,7 +140,7 @@ def test_attention_refusals():
 @pytest.mark.parametrize("want,kw", [
     (INVALID, dict(budget=-1)), (INVALID, dict(sinks=-1)), (INVALID, dict(recent=-1)), (INVALID, dict(sinks=40, recent=25)),
     (INVALID, dict(recent=65, sinks=0)), (INVALID, dict(budget=2 ** 30 + 1)), (INVALID, dict(acc=None)), (INVALID, dict(new=None)),
-    (INVALID, dict(new=L)), (ALIGN, dict(acc=A + 2)), (ALIGN, dict(new=Y + 2)), (ALIGN, dict(st=A + 3)), (INVALID, dict(room=10)),
+    (INVALID, dict(new=L)), (INVALID, dict(new=L + 4)), (INVALID, dict(new=L - 4)), (ALIGN, dict(acc=A + 2)), (ALIGN, dict(new=Y + 2)), (ALIGN, dict(st=A + 3)), (INVALID, dict(room=10)),
     (INVALID, dict(work=None)), (ALIGN, dict(work=W_ + 8)),
 ])
 def test_evict_refusals(want, kw):
