@@ -619,3 +619,64 @@ def test_captured_decode_step():
             assert same(a, b), i
         shadow = [t.clone() for t in state]
     assert lens.tolist() == [102, 53]
+
+
+def test_cache_past_32_bits():
+    """Pages behind more than 2^32 bytes of codes: the same bits as in a small pool."""
+    H, P, D, pages = 16, 64, 128, 70000
+    cache = ref.Cache([300, 129], H, D, P, seed=21)
+    small = cache.on_device()
+    up = pages - cache.pages
+    far = []
+    for side in small[:2]:
+        big = (torch.empty(pages, H, P, D // 2, dtype=torch.uint8, device="cuda"),
+               torch.empty(pages, H, P, D // 16, dtype=torch.uint8, device="cuda"),
+               torch.empty(pages, H, P, device="cuda"))
+        for t, b in zip(side, big):
+            b[up:] = t
+        far.append(big)
+    assert far[0][0].numel() > 2 ** 32
+    pools = [(*small, 0), (*far, small[2] + up, small[3], up)]  # stale entries stay out of range
+    k = torch.randn(5, H, D, generator=gen(22)).bfloat16().cuda()
+    results = []
+    for kc, vc, table, lens, at in pools:
+        fos.fos_kv_append(k, -k, ends([3, 2]), kc, vc, table, lens)
+        got = []
+        for n, max_len in ((1, 0), (60, LONG)):
+            q = ref.queries(2 * n, 2 * H, D, "bf16", 23).cuda()
+            out, lse = fos.fos_kv_attention(q, ends([n, n]), kc, vc, table, lens, max_len=max_len)
+            acc = torch.zeros(2, H, cache.W * P, device="cuda")
+            got += [out, lse, fos.fos_kv_weights(q, ends([n, n]), kc, table, lens, lse, acc)]
+        got.append(fos.fos_kv_evict(acc, kc, vc, table, lens, 100, sinks=2, recent=30).clone())
+        got += [t[at:].clone() for side in (kc, vc) for t in side]
+        results.append(got)
+    for a, b in zip(*results):
+        assert same(a, b)
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_calls_on_two_streams(n):
+    """The same calls on two streams at once, each with workspaces of its own."""
+    cache = ref.Cache([700, 333], 2, 128, 64, seed=24)
+    kc, vc, table, lens = cache.on_device()
+    q = ref.queries(2 * n, 8, 128, "bf16", 25).cuda()
+    offs = ends([n, n])
+
+    def calls():
+        k, v = (tuple(t.clone() for t in side) for side in (kc, vc))
+        acc = torch.zeros(2, 2, cache.W * 64, device="cuda")
+        out, lse = fos.fos_kv_attention(q, offs, k, v, table, lens, max_len=LONG)
+        fos.fos_kv_weights(q, offs, k, table, lens, lse, acc)
+        cut = fos.fos_kv_evict(acc, k, v, table, lens, 300, sinks=4, recent=64)
+        return [out, lse, acc, cut, *fos.fos_kv_attention(q, offs, k, v, table, cut)]
+
+    want = calls()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(calls())
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(same(a, b) for a, b in zip(g, want))
