@@ -6,7 +6,7 @@
 // A cached value is c b S with an E2M1 code c, an E4M3 block scale b and the row's
 // float32 S_dec. c b has at most 6 significant bits and lies in [2^-10, 2688], so it
 // is exact in fp16, which is what the matrix instructions take on both sides:
-//  - q in fp16 as it is; in bf16 times a power of two that brings the row's largest
+//  - q in fp16 as it is; in bf16 times a power of two that brings the row's (or the tile's) largest
 //    value to [2^14, 2^15). The 8 bits of a bf16 value are exact there down to
 //    2^-32 of the row's largest, and what is smaller is off by 2^-40 of it.
 //  - S_dec of a key multiplies the sum, in binary32.
@@ -238,16 +238,20 @@ __device__ __forceinline__ float row_max(float v) {
 }
 
 // One row of q as N fragments of eight values, `step` values apart from `at` on, or zeros
-// (at is a row of q in any case); returns what undoes its power of two.
-template <int DT, int N, bool QUARTERS>
-__device__ __forceinline__ float load_q(const void* q, int64_t at, int step, bool have, Frag* f) {
+// (at is a row of q in any case).
+template <int N>
+__device__ __forceinline__ void read_q(const void* q, int64_t at, int step, bool have, Frag* f) {
   const uint16_t* p = (const uint16_t*)q + at;
 #pragma unroll
   for (int c = 0; c < N; c++) {
     const u32x4 v = *reinterpret_cast<const u32x4*>(p + c * step);
     f[c].u[0] = have ? v.x : 0, f[c].u[1] = have ? v.y : 0, f[c].u[2] = have ? v.z : 0, f[c].u[3] = have ? v.w : 0;
   }
-  if constexpr (DT == kFP16) return 1.0f;
+}
+
+// Biased exponent of a bf16 row's largest finite value.
+template <int N, bool QUARTERS>
+__device__ __forceinline__ int q_exponent(const Frag* f) {
   uint32_t top = 0;  // of the finite values' bits
 #pragma unroll
   for (int c = 0; c < N; c++)
@@ -256,9 +260,13 @@ __device__ __forceinline__ float load_q(const void* q, int64_t at, int step, boo
       const uint32_t lo = f[c].u[i] & 0x7FFFu, hi = (f[c].u[i] >> 16) & 0x7FFFu;
       top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
     }
-  // biased exponent of the largest
-  const int e = (int)(__float_as_uint(row_max<QUARTERS>(__uint_as_float(top << 16))) >> 23);
-  int up = 141 - e;  // it becomes 2^14
+  return (int)(__float_as_uint(row_max<QUARTERS>(__uint_as_float(top << 16))) >> 23);
+}
+
+// bf16 to fp16, times the power of two that brings exponent e to 2^14; returns what undoes it.
+template <int N>
+__device__ __forceinline__ float scale_q(Frag* f, int e) {
+  int up = 141 - e;
   up = up > 126 ? 126 : up;
   const float by = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
@@ -266,6 +274,13 @@ __device__ __forceinline__ float load_q(const void* q, int64_t at, int step, boo
 #pragma unroll
     for (int i = 0; i < 4; i++) f[c].u[i] = pack_f16(bf16_lo(f[c].u[i]) * by, bf16_hi(f[c].u[i]) * by);
   return __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+template <int DT, int N, bool QUARTERS>
+__device__ __forceinline__ float load_q(const void* q, int64_t at, int step, bool have, Frag* f) {
+  read_q<N>(q, at, step, have, f);
+  if constexpr (DT == kFP16) return 1.0f;
+  return scale_q<N>(f, q_exponent<N, QUARTERS>(f));
 }
 
 // Rows of a tile: r counts the sequence's new tokens and, within one, the query
@@ -566,12 +581,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 //
 // 4 D operations for each row and key are the bound, but the vector units' part (decode, scale,
 // maximum, exponential, conversion) nearly fills the time beside them: 8192 new tokens, 32 query
-// heads of 128, 0.56 PFLOP in 695 us, 800 TFLOP/s; matrix units busy 30 % of the cycles, vector
-// units 50 to 57 %, LDS 45 %. Decode goes beside the first product and exponentials beside the
+// heads of 128, 0.56 PFLOP in 679 us, 817 TFLOP/s; matrix units busy 30 % of the cycles, vector
+// units 50 to 57 %, LDS 45 % (a little before the last step). Decode goes beside the first product and exponentials beside the
 // second, which the scheduler is told. Two workgroups to a CU for D 96 and 128 (three of 32 keys:
 // 730 us; bounded to three with spills: 947). Not kept: the next step's first product beside this
 // one's softmax (816 us), a wave's priority raised in its products (738 for 722 then), raw codes
-// two steps ahead. D 256 fills 256 registers and spills 47, one workgroup to a CU: 512 TFLOP/s.
+// two steps ahead. D 256 fills 256 registers and spills 53, one workgroup to a CU: 506 TFLOP/s.
 
 template <int NC> struct TileLds {
   static constexpr int kKeys = 64;
@@ -623,6 +638,8 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   // sixteens are not there; and places that the other lanes write to.
   constexpr int kValues = L::kKeys, kLog2 = 2 * L::kKeys, kGone = 3 * L::kKeys, kNowhere = 3 * L::kKeys + 4;
   __shared__ __attribute__((aligned(16))) float sizes[2][3 * L::kKeys + 8];
+  __shared__ __attribute__((aligned(16))) float ones[L::kKeys];
+  __shared__ int ends[8];  // largest and least exponent of a wave's rows of q
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
   check_cache(a);
@@ -649,8 +666,28 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   const int from = part * each, to = min(steps, from + each);
 
   Frag q[2 * NC];
-  const float undo =
-      load_q<DT, 2 * NC, false>(a.q, row.token * a.stride + (int64_t)row.head * D + 8 * half, 16, row.have, q);
+  read_q<2 * NC>(a.q, row.token * a.stride + (int64_t)row.head * D + 8 * half, 16, row.have, q);
+  if (threadIdx.x < L::kKeys) ones[threadIdx.x] = 1.0f;
+  // bf16 rows of about one size have one power of two, which then goes with the keys' sizes: a
+  // multiplication less for each score (8192 new tokens, 32 heads of 128: 675 us for 708). The
+  // smallest row's values are then good to 2^-32 of its largest, and sizes grow no larger.
+  bool common = true;
+  float undo = 1.0f, undo_all = 1.0f;
+  if constexpr (DT == kBF16) {
+    int e = q_exponent<2 * NC, false>(q);
+    int hi = e, lo = e ? e : 255;
+    for (int d = 1; d < 32; d <<= 1) {
+      hi = max(hi, __shfl_xor(hi, d, 64));
+      lo = min(lo, __shfl_xor(lo, d, 64));
+    }
+    if (lane == 0) ends[wave] = hi, ends[4 + wave] = lo;
+    __syncthreads();
+    hi = max(max(ends[0], ends[1]), max(ends[2], ends[3]));
+    lo = min(min(ends[4], ends[5]), min(ends[6], ends[7]));
+    common = __builtin_amdgcn_readfirstlane(hi - lo <= 8 && hi <= 141 && hi >= 77);
+    undo = scale_q<2 * NC>(q, common ? hi : e);
+    if (common) undo_all = undo, undo = 1.0f;
+  }
   f32x16 o[NC];
 #pragma unroll
   for (int t = 0; t < NC; t++)
@@ -666,7 +703,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   const int to_log2 = lane >= 16 && lane < 32 ? kLog2 + my_size : kNowhere + 1;
   const int to_gone = lane == 0 ? kGone + wave : kNowhere + 2;
   // the keys' scale goes with their S_dec, so that what is left for a query is its power of two
-  const float size_by = lane < 16 ? a.scale_log2 : 1.0f;
+  const float size_by = lane < 16 ? a.scale_log2 : 1.0f, size_undo = lane < 16 ? undo_all : 1.0f;
   // This wave's rows of a step, decoded, to the step's side of the LDS, without a branch, so that
   // it can run beside matrix instructions. Zeros where there is no key: a stale scale may be a NaN.
   auto put = [&](int step) {
@@ -685,7 +722,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
       *reinterpret_cast<u32x4*>(base + L::kKeys * L::kK + L::value(my_key, (lane & 3) * NC + c)) =
           u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
     const float S = !st.there || first + my_size >= len ? 0.0f : st.sdec;
-    sizes[side][to_size] = S * size_by;
+    sizes[side][to_size] = S * size_by * size_undo;
     sizes[side][to_log2] = log2_of(S);
     sizes[side][to_gone] = st.there ? 0.0f : 1.0f;
   };
@@ -732,34 +769,33 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
       FOS_INTERLEAVE(4, 5, 0)
       __builtin_amdgcn_sched_barrier(0);
       load(s + 2);
-      // a lane's sixteen keys of 32: 8b + 4 half + 0..3
-#pragma unroll
-      for (int kb = 0; kb < 2; kb++)
-#pragma unroll
-        for (int b = 0; b < 4; b++) {
-          const f32x4 ks = *reinterpret_cast<const f32x4*>(size + 32 * kb + 8 * b + 4 * half);
-#pragma unroll
-          for (int i = 0; i < 4; i++) x[kb][4 * b + i] *= ks[i];
-        }
-      if (first + L::kKeys > least || __builtin_amdgcn_readfirstlane(__float_as_int(absent[0] + absent[1] + absent[2] + absent[3]))) {
+      // a lane's sixteen keys of 32: 8b + 4 half + 0..3. What they are multiplied by below: the
+      // keys' sizes, or where a key is not seen or rows differ much, ones, after the sizes here
+      const bool edge = first + L::kKeys > least || __builtin_amdgcn_readfirstlane(__float_as_int(absent[0] + absent[1] + absent[2] + absent[3]));
+      const float* by = size;
+      if (edge || !common) {
+        by = ones;
 #pragma unroll
         for (int kb = 0; kb < 2; kb++)
 #pragma unroll
           for (int b = 0; b < 4; b++) {
+            const f32x4 ks = *reinterpret_cast<const f32x4*>(size + 32 * kb + 8 * b + 4 * half);
             const int j = 32 * kb + 8 * b;
             const int past = absent[j >> 4] != 0.0f ? 0 : limit - first - j - 4 * half;  // keys from here on are not seen
 #pragma unroll
-            for (int i = 0; i < 4; i++) x[kb][4 * b + i] = i < past ? x[kb][4 * b + i] : -__builtin_huge_valf();
+            for (int i = 0; i < 4; i++)
+              x[kb][4 * b + i] = i < past ? x[kb][4 * b + i] * ks[i] * undo : -__builtin_huge_valf();
           }
       }
+      auto size_of = [&](int kb, int b) { return *reinterpret_cast<const f32x4*>(by + 32 * kb + 8 * b + 4 * half); };
       float top = kLowest;
 #pragma unroll
       for (int kb = 0; kb < 2; kb++)
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-          const f32x4 lv = *reinterpret_cast<const f32x4*>(size + kLog2 + 32 * kb + 8 * b + 4 * half);
+          const f32x4 lv = *reinterpret_cast<const f32x4*>(size + kLog2 + 32 * kb + 8 * b + 4 * half), ks = size_of(kb, b);
 #pragma unroll
-          for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, __builtin_fmaf(x[kb][4 * b + i], undo, lv[i]));
+          for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, __builtin_fmaf(x[kb][4 * b + i], ks[i], lv[i]));
         }
       top = row_max<false>(top);
       if (__any(top > m + kLag)) {
@@ -790,11 +826,11 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
       auto weigh = [&](int kb) {
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-          const f32x4 vs = *reinterpret_cast<const f32x4*>(size + kValues + 32 * kb + 8 * b + 4 * half);
+          const f32x4 vs = *reinterpret_cast<const f32x4*>(size + kValues + 32 * kb + 8 * b + 4 * half), ks = size_of(kb, b);
           float w[4];
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[kb][4 * b + i], undo, -m));
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[kb][4 * b + i], ks[i], -m));
             l += e;
             w[i] = e * vs[i];
           }

@@ -14,7 +14,8 @@ from synthdata import raw_bits
 
 pytestmark = pytest.mark.gpu
 DIMS = [32, 64, 96, 128, 192, 256]
-LONG = 10 ** 6  # an expected length at which 49 rows to a sequence go in tiles of 128
+LONG = 10 ** 6  # an expected length, past any table's: with a table of WIDE pages 49 rows to a
+WIDE = 2 ** 14  # sequence go in tiles of 128
 
 
 def ends(new):
@@ -35,8 +36,16 @@ def assert_guard(raw, pad=64):
     assert (edge == torch.tensor(77.0).to(raw.dtype).float().item()).all(), "wrote outside the output"
 
 
+def assert_tiles(cache, q):
+    """The rule by which the rows go in tiles of 128."""
+    rows = len(q) * q.shape[1] // cache.H // cache.B
+    assert rows > 48 and -(-rows // 16) * cache.B * cache.H * -(-cache.W * cache.P // 128) > 2048
+
+
 def attend(cache, q, new, **kw):
     """(out, lse, status) of the packed queries, into guarded outputs."""
+    if kw.get("max_len") == LONG and cache.W == WIDE:
+        assert_tiles(cache, q)
     k, v, table, lens = cache.on_device()
     out, raw = guarded(q.shape, q.dtype)
     lse, raw_l = guarded(q.shape[:2], torch.float32)
@@ -217,7 +226,7 @@ def test_attention_many_tokens(D, dtype, causal, max_len):
     """Prompts, chunks behind a prefix, sequences without new tokens, a padded tail,
     and more new tokens than the cache has: their first see no key."""
     lens, new = [150, 300, 40, 0, 33], [150, 70, 0, 3, 47]
-    cache = ref.Cache(lens, 2, D, 32, seed=D + 7)
+    cache = ref.Cache(lens, 2, D, 32, seed=D + 7, W=WIDE if max_len else None)
     check_attention(cache, ref.queries(sum(new) + 5, 4, D, dtype, D, 2.0), new, causal, max_len=max_len)
 
 
@@ -228,6 +237,7 @@ def test_attention_whole_tiles(D, dtype, causal):
     """Heads enough for tiles whose keys are not in parts."""
     cache = ref.Cache([150, 33, 5], 30, D, 16, seed=D)
     new = [80, 30, 5]
+    assert_tiles(cache, ref.queries(118, 240, 1, dtype, 0))
     assert fos.fos_kv_attention_workspace(118, 240, 3, cache.W, 30, 16, D) == 0
     check_attention(cache, ref.queries(118, 240, D, dtype, D), new, causal)
 
@@ -237,7 +247,7 @@ def test_attention_whole_tiles(D, dtype, causal):
 @pytest.mark.parametrize("max_len", [0, 100, LONG])
 def test_attention_splits(H, G, n, L, max_len):
     """Whatever the caller expects the length to be."""
-    cache = ref.Cache([L, L // 3 + n], H, 128, 64, seed=L)
+    cache = ref.Cache([L, L // 3 + n], H, 128, 64, seed=L, W=WIDE if max_len == LONG and n * G > 48 else None)
     check_attention(cache, ref.queries(2 * n, H * G, 128, "bf16", n), [n, n], max_len=max_len)
 
 
@@ -252,7 +262,7 @@ def test_attention_wide_table_of_a_short_cache():
 def test_attention_extreme_rows(n, max_len, dtype):
     """Value rows of very different size, among them one that is huge where its weight
     is tiny and rows of zeros with the largest weight; queries of any size and scale."""
-    cache = ref.Cache([200], 2, 128, 64, seed=8)
+    cache = ref.Cache([200], 2, 128, 64, seed=8, W=WIDE if max_len else None)
     sd = cache.sides[1][2]
     where = [(int(cache.table[0, p // 64]), p % 64) for p in (3, 77, 150)]
     for i, (page, slot) in enumerate(where):
@@ -271,17 +281,28 @@ def test_attention_extreme_rows(n, max_len, dtype):
         check_attention(cache, q, [n], scale=1e-21, max_len=max_len)
 
 
+@pytest.mark.parametrize("apart", [2.0 ** -7, 2.0 ** -12, 0.0])
+@pytest.mark.parametrize("size", [1e-18, 1.0, 1e6])
+def test_attention_tile_of_rows_of_two_sizes(size, apart):
+    """Rows near enough for one power of two and too far for it, and rows of zeros."""
+    cache = ref.Cache([200], 2, 64, 16, seed=26, W=WIDE)
+    q = ref.queries(70, 4, 64, "bf16", 27)
+    q[::3] *= apart
+    check_attention(cache, q * size, [70], scale=0.125 / size, max_len=LONG)
+
+
 @pytest.mark.parametrize("size_k,size_v", [(1e-20, 1e-25), (1e3, 1e8), (1e15, 1e25)])
 def test_attention_sizes_of_the_cache(size_k, size_v):
     cache = ref.Cache([100, 40], 2, 64, 16, seed=10, sizes=(size_k, size_v))
     check_attention(cache, ref.queries(7, 4, 64, "bf16", 11), [4, 3], scale=0.02 / size_k)
+    cache = ref.Cache([100, 40], 2, 64, 16, seed=10, sizes=(size_k, size_v), W=WIDE)
     check_attention(cache, ref.queries(90, 4, 64, "bf16", 11), [60, 30], scale=0.02 / size_k, max_len=LONG)
 
 
 @pytest.mark.parametrize("n,max_len", [(1, 0), (50, 0), (50, LONG)])
 def test_attention_not_a_number(n, max_len):
     """A query with a NaN or an infinity is NaN; others are as without it."""
-    cache = ref.Cache([90], 2, 128, 16, seed=12)
+    cache = ref.Cache([90], 2, 128, 16, seed=12, W=WIDE if max_len else None)
     q = ref.queries(n, 4, 128, "bf16", 13)
     out, lse, _ = attend(cache, q, [n], max_len=max_len)
     bad = q.clone()
@@ -297,7 +318,7 @@ def test_attention_not_a_number(n, max_len):
 @pytest.mark.parametrize("n,max_len", [(1, 0), (3, 0), (60, 0), (60, LONG)])
 def test_attention_strides_and_repeats(n, max_len):
     """Queries inside wider rows; the same bits again, on any workspace and another stream."""
-    cache = ref.Cache([400, 77], 2, 128, 64, seed=14)
+    cache = ref.Cache([400, 77], 2, 128, 64, seed=14, W=WIDE if max_len else None)
     T = 2 * n
     wide = ref.queries(T, 12, 128, "bf16", 15).cuda()
     q = wide[:, 2:10]
@@ -319,7 +340,7 @@ def test_attention_strides_and_repeats(n, max_len):
 @pytest.mark.parametrize("n,max_len", [(2, 0), (60, 0), (60, LONG)])
 def test_attention_bad_cache(n, max_len):
     """Pages that are none hold no keys; lengths past the table end with it."""
-    cache = ref.Cache([64, 50], 2, 64, 16, seed=16)
+    cache = ref.Cache([64, 50], 2, 64, 16, seed=16, W=WIDE if max_len else None)
     q = ref.queries(2 * n, 4, 64, "bf16", 17)
     keep = cache.table.clone()
     cache.table[0, 1] = cache.pages
@@ -337,6 +358,8 @@ def test_attention_bad_cache(n, max_len):
     cache.lens[0] = 64
     out, lse, _ = attend(cache, q, [n, n], max_len=max_len)
     assert (out[:n] == 0).all() and (lse[:n] == -math.inf).all()
+    if max_len:
+        return
     # lengths outside [0, W P]
     cache.table = keep
     cache.lens = [10 ** 6, -5]
@@ -350,7 +373,7 @@ def test_attention_bad_cache(n, max_len):
 
 @pytest.mark.parametrize("n,max_len", [(4, 0), (100, 0), (100, LONG)])
 def test_attention_bad_offsets(n, max_len):
-    cache = ref.Cache([64, 50], 2, 64, 16, seed=16)
+    cache = ref.Cache([64, 50], 2, 64, 16, seed=16, W=WIDE if max_len else None)
     k, v, table, lens = cache.on_device()
     q = ref.queries(n, 4, 64, "bf16", 17).cuda()
     for offs in ([n - 1, n - 2], [2, n + 5], [-1, n]):
@@ -624,7 +647,7 @@ def test_captured_decode_step():
 def test_cache_past_32_bits():
     """Pages behind more than 2^32 bytes of codes: the same bits as in a small pool."""
     H, P, D, pages = 16, 64, 128, 70000
-    cache = ref.Cache([300, 129], H, D, P, seed=21)
+    cache = ref.Cache([300, 129], H, D, P, seed=21, W=256)
     small = cache.on_device()
     up = pages - cache.pages
     far = []
@@ -644,6 +667,8 @@ def test_cache_past_32_bits():
         got = []
         for n, max_len in ((1, 0), (60, LONG)):
             q = ref.queries(2 * n, 2 * H, D, "bf16", 23).cuda()
+            if n > 1:
+                assert_tiles(cache, q)
             out, lse = fos.fos_kv_attention(q, ends([n, n]), kc, vc, table, lens, max_len=max_len)
             acc = torch.zeros(2, H, cache.W * P, device="cuda")
             got += [out, lse, fos.fos_kv_weights(q, ends([n, n]), kc, table, lens, lse, acc)]
@@ -657,10 +682,12 @@ def test_cache_past_32_bits():
 @pytest.mark.parametrize("n", [1, 60])
 def test_calls_on_two_streams(n):
     """The same calls on two streams at once, each with workspaces of its own."""
-    cache = ref.Cache([700, 333], 2, 128, 64, seed=24)
+    cache = ref.Cache([700, 333], 2, 128, 64, seed=24, W=128)
     kc, vc, table, lens = cache.on_device()
     q = ref.queries(2 * n, 8, 128, "bf16", 25).cuda()
     offs = ends([n, n])
+    if n > 1:
+        assert_tiles(cache, q)
 
     def calls():
         k, v = (tuple(t.clone() for t in side) for side in (kc, vc))
