@@ -349,6 +349,8 @@ template <int NC> struct Mover {
 
 // The digit at `shift` of the wanted weight: counts are from the largest down.
 // Leaves how many of the digit's own are wanted in `want`, and how many there are.
+// `share` has a word for each wave, as many again that this leaves alone, and four for
+// the result: waves that have read it go on while others still have to.
 struct Digit {
   uint32_t digit;
   int want, of;
@@ -368,7 +370,7 @@ __device__ Digit find_digit(const int* hist, int* share, int want) {
   int before = 0;
   for (int w = 0; w < (t >> 6); w++) before += share[w];
   const int above = before + sum - c0 - c1;  // weights in the bins above this thread's
-  int* out = share + kWaves;
+  int* out = share + 2 * kWaves;
   if (2 * t < BINS && above < want && above + c0 + c1 >= want) {
     const bool first = above + c0 >= want;
     out[0] = BINS - 1 - 2 * t - (first ? 0 : 1);
