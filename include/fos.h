@@ -548,7 +548,9 @@ int fos_kv_append(const void* k, const void* v, int dtype, int64_t T, int64_t k_
  *   s_j = scale q . k_j,  j < lens[b] - n + i + 1 if causal, else j < lens[b],
  *   out = sum_j softmax_j(s) v_j in q's type,  lse = log sum_j exp(s_j).
  * A query that sees no key, or whose every score is -infinity, and rows at or past
- * offs[B-1], have out = 0 and lse = -infinity.
+ * offs[B-1], have out = 0 and lse = -infinity. A row of the cache that is no number (a block
+ * scale that is a NaN, S_dec a NaN or infinite, which the append writes none of) makes no
+ * numbers of the results of the queries that see it, and is nothing to the others.
  *   max_len: what the caller knows lens to be at most (0: W P). It shapes the
  *            launch; results are right for longer ones too.
  *   lse:     nullable float [T, Hq].

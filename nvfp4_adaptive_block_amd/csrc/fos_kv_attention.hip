@@ -34,6 +34,7 @@ namespace {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -73,9 +74,10 @@ __device__ __forceinline__ float col_sum(float v) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-// Exponent of S (its floor's log2) for the running maximum; kLeast for 0.
+// Exponent of S (its floor's log2) for the running maximum; kLeast for 0, and for an infinity
+// or a NaN, whose exponent is one more than any and so wraps to none.
 __device__ __forceinline__ float log2_of(float S) {
-  return __builtin_fmaxf((float)(__float_as_uint(S) >> 23) - 127.0f, kLeast);
+  return __builtin_fmaxf((float)(((__float_as_uint(S) << 1) + 0x01000000u) >> 24) - 128.0f, kLeast);
 }
 
 // Two weights in fp16. For fp16 results what the rounding leaves out is kept too, and
@@ -101,6 +103,12 @@ __device__ __forceinline__ void decode8(uint32_t codes, h2 s, uint32_t* out) {
   out[3] = bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3) * s);
 }
 
+// E4M3 NaN among four block scales: 0x80 in the byte of each; and all bits of such bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t scales) {
+  return ((scales & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+__device__ __forceinline__ uint32_t whole_bytes(uint32_t tops) { return (tops << 1) - (tops >> 7); }
+
 // A quarter of a row of D = 32 NC values: 8 NC neighbouring values, NC dwords of
 // codes, and the scales of the blocks that they lie in.
 template <int NC> struct Quarter {
@@ -110,6 +118,15 @@ template <int NC> struct Quarter {
 
   // the first block of quarter g
   static __device__ __forceinline__ int block(int g) { return (g * NC) >> 1; }
+  // the row's blocks, a bit each, that nan_bytes() names in this lane's quarter and in those of
+  // the three lanes that have the rest of the row
+  static __device__ __forceinline__ uint32_t blocks_of(int g, uint32_t tops) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kScales; i++) m |= ((tops >> (8 * i + 7)) & 1u) << (block(g) + i);
+    m |= __shfl_xor(m, 1, 64);
+    return m | __shfl_xor(m, 2, 64);
+  }
 
   __device__ __forceinline__ void load_scales(const uint8_t* row, int g) {
     const uint8_t* p = row + block(g);
@@ -154,13 +171,20 @@ template <int NC> struct Quarter {
       for (int i = 0; i < NC; i++) reinterpret_cast<uint32_t*>(p)[i] = codes[i];
     }
   }
-  // fp16 values; f[c] holds values 8c .. 8c + 7 of the quarter g
-  __device__ __forceinline__ void decode(int g, Frag* f) const {
+  // fp16 values; f[c] holds values 8c .. 8c + 7 of the quarter g. NUMBERS: a scale that is a NaN
+  // becomes a number, and `most` collects the scales' bits, above an infinity's after a NaN (or a
+  // negative scale).
+  template <bool NUMBERS = false>
+  __device__ __forceinline__ void decode(int g, Frag* f, us2* most = nullptr) const {
     h2 s[(kScales + 1) / 2 * 2];
 #pragma unroll
     for (int i = 0; i < kScales; i += 2) {
-      const h2 p = i < 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales, 1.0f, false)
-                         : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales, 1.0f, true);
+      h2 p = i < 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales, 1.0f, false)
+                   : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales, 1.0f, true);
+      if constexpr (NUMBERS) {
+        *most = __builtin_elementwise_max(*most, __builtin_bit_cast(us2, p));
+        p = __builtin_elementwise_min(p, h2{(_Float16)448.0f, (_Float16)448.0f});
+      }
       s[i] = __builtin_shufflevector(p, p, 0, 0);
       s[i + 1] = __builtin_shufflevector(p, p, 1, 1);
     }
@@ -402,6 +426,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 #pragma unroll
   for (int t = 0; t < DT16; t++) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = kLowest, l = 0.0f;
+  int nan_blocks = 0;  // of o, a bit each, that a NaN belongs in
   uint8_t* keys = lds + wave * L::kWave;
   uint8_t* vals = keys + L::kKeys;
   float* sizes = reinterpret_cast<float*>(keys + L::kSizes);
@@ -422,13 +447,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
     find(32 * (s + WAVES));
   }
   while (s < to) {
-    const Step<NC> st = next;
+    Step<NC> st = next;
     const int first = 32 * s;
     s += WAVES;
     next.load(a.c, pg, page, 32 * s);
     find(32 * (s + WAVES));
 
     const bool missing = first + 32 > len || !st.there[0] || !st.there[1];
+    const bool edge = first + 32 > least || missing;  // not all rows see all of these keys
     wave_lds_order();
 #pragma unroll
     for (int u = 0; u < 2; u++) st.k[u].store_codes(keys + u * 256 * NC + 4 * NC * piece(lane >> 2, lane & 3));
@@ -446,13 +472,29 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 #pragma unroll
       for (int c = 0; c < NC; c++) sc[u] = mfma16(kf[c], q[c], sc[u]);
     }
-    // value rows to fp16, zero where there is no key: a stale scale may be a NaN
+    // Value rows to fp16, zero where there is no key: a stale scale may be a NaN. A NaN in a row
+    // that is there reaches the queries that see it by itself, and here no others: 0 times it is
+    // a NaN too.
+    if (edge) {
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        uint32_t& scales = st.v[u].scales;
+        if (!st.there[u] || first + 16 * u + (lane >> 2) >= len) scales = 0;
+        const uint32_t nans = nan_bytes(scales);
+        if (!__any(nans != 0)) continue;
+        scales &= ~whole_bytes(nans);
+        const int rows = (int)Quarter<NC>::blocks_of(lane & 3, nans);
+#pragma unroll 1
+        for (int r = 0; r < 16; r++) {
+          const int of_row = __builtin_amdgcn_readlane(rows, 4 * r);
+          nan_blocks |= first + 16 * u + r < limit ? of_row : 0;
+        }
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      Quarter<NC> t = st.v[u];
-      if (missing && (!st.there[u] || first + 16 * u + (lane >> 2) >= len)) t.scales = 0;
       Frag vf[NC];
-      t.decode(lane & 3, vf);
+      st.v[u].decode(lane & 3, vf);
 #pragma unroll
       for (int c = 0; c < NC; c++)
         *reinterpret_cast<u32x4*>(vals + L::value(16 * u + (lane >> 2), (lane & 3) * NC + c)) =
@@ -468,7 +510,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 #pragma unroll
       for (int i = 0; i < 4; i++) z[4 * u + i] = sc[u][i] * (ks[i] * qf);
     }
-    if (first + 32 > least || missing) {
+    if (edge) {
 #pragma unroll
       for (int u = 0; u < 2; u++)
 #pragma unroll
@@ -517,6 +559,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
     }
   }
 
+  if (__any(nan_blocks != 0)) {
+#pragma unroll
+    for (int t = 0; t < DT16; t++)
+      if ((nan_blocks >> t) & 1) o[t] += __builtin_nanf("");
+  }
   // join the waves
   l = col_sum(l);
   __syncthreads();
@@ -640,6 +687,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   __shared__ __attribute__((aligned(16))) float sizes[2][3 * L::kKeys + 8];
   __shared__ __attribute__((aligned(16))) float ones[L::kKeys];
   __shared__ int ends[8];  // largest and least exponent of a wave's rows of q
+  __shared__ int found[4];  // whether a wave's value rows had a NaN
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
   check_cache(a);
@@ -697,6 +745,9 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   const Pages pg{a.c.table + (int64_t)(gt.g < a.c.B ? gt.g : 0) * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
 
   TileStep<NC> st;
+  // of this wave's value rows: the scales' bits, and the lanes whose S_dec was no number or infinite
+  us2 scale_bits = {0, 0};
+  unsigned long long odd_sizes = 0;
   int page = 0;  // of this wave's rows of the step that is loaded next
   const int my_key = 16 * wave + (lane >> 2), my_size = 16 * wave + (lane & 15);
   const int to_size = lane < 16 ? my_size : lane < 32 ? kValues + my_size : kNowhere;
@@ -706,6 +757,10 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   const float size_by = lane < 16 ? a.scale_log2 : 1.0f, size_undo = lane < 16 ? undo_all : 1.0f;
   // This wave's rows of a step, decoded, to the step's side of the LDS, without a branch, so that
   // it can run beside matrix instructions. Zeros where there is no key: a stale scale may be a NaN.
+  // One in a value row that is there must reach the queries that see it and no others, but 0 times
+  // it is a NaN too: it becomes a number here, and is seen to after the last step. (8192 new tokens,
+  // 32 heads: 698 us for 692 without this at D 128, 2038 for 2026 at D 256; by a branch in the loop
+  // for steps with masked keys 699 and 2560.)
   auto put = [&](int step) {
     const int side = step & 1, first = step * L::kKeys;
     if (!st.there || first + my_key >= len) st.k.scales = st.v.scales = 0;
@@ -716,12 +771,15 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
     for (int c = 0; c < NC; c++)
       *reinterpret_cast<u32x4*>(base + my_key * L::kK + 16 * ((lane & 3) * NC + c)) =
           u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
-    st.v.decode(lane & 3, f);
+    st.v.template decode<true>(lane & 3, f, &scale_bits);
 #pragma unroll
     for (int c = 0; c < NC; c++)
       *reinterpret_cast<u32x4*>(base + L::kKeys * L::kK + L::value(my_key, (lane & 3) * NC + c)) =
           u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
-    const float S = !st.there || first + my_size >= len ? 0.0f : st.sdec;
+    float S = !st.there || first + my_size >= len ? 0.0f : st.sdec;
+    const bool odd = lane >= 16 && !(__builtin_fabsf(S) < __builtin_huge_valf());
+    odd_sizes |= __ballot(odd);
+    S = odd ? 0.0f : S;
     sizes[side][to_size] = S * size_by * size_undo;
     sizes[side][to_log2] = log2_of(S);
     sizes[side][to_gone] = st.there ? 0.0f : 1.0f;
@@ -868,6 +926,34 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
     __syncthreads();
   }
 
+  // NaN where a row sees one: the value rows' scales and sizes once more, by every wave
+  const int any = odd_sizes || __any(max(scale_bits.x, scale_bits.y) > 0x7C00);
+  if (lane == 0) found[wave] = any;
+  __syncthreads();
+  if (found[0] | found[1] | found[2] | found[3]) {
+    int blocks = 0;  // of the row's result, a bit each
+#pragma unroll 1
+    for (int first = from * L::kKeys; first < min(to * L::kKeys, most); first += 16) {
+      bool there;
+      const int64_t at = pg.row(pg.page(first, len), first, there);
+      if (!there) continue;
+      Quarter<NC> v;
+      v.load_scales(a.c.v.scales + (at + (lane >> 2)) * (2 * NC), lane & 3);
+      uint32_t tops = nan_bytes(v.scales);
+      if (!(__builtin_fabsf(a.c.v.sdec[at + (lane >> 2)]) < __builtin_huge_valf())) tops = 0x80808080u;
+      const int of_lane = (int)Quarter<NC>::blocks_of(lane & 3, tops);
+#pragma unroll 1
+      for (int r = 0; r < 16; r++) {
+        const int of_row = __builtin_amdgcn_readlane(of_lane, 4 * r);
+        blocks |= first + r < limit ? of_row : 0;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NC; t++)
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        if ((blocks >> (2 * t + (i >> 3))) & 1) o[t][i] += __builtin_nanf("");
+  }
   const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
   l = __uint_as_float(both[0]) + __uint_as_float(both[1]);
   const int64_t at = row.token * ((int64_t)a.c.H * a.G) + row.head;

@@ -1,10 +1,13 @@
 """The key/value cache's calls where they can go wrong: what the plain tests of
 test_gpu_kv.py do not reach. GPU only."""
+import math
+
 import pytest
 import torch
 
-from operator_reference import gen
-from test_gpu_kv import check_evict
+import kv_reference as ref
+from operator_reference import assert_within, gen
+from test_gpu_kv import DIMS, LONG, WIDE, attend, check_evict
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +25,70 @@ def test_evict_short_middles(middle):
     n, sinks, recent = middle + 24, 4, 20
     for budget in sorted({sinks + recent, n - 1, sinks + recent + middle // 2}):
         check_evict([n, n + 1], 64, 64, 16, budget, sinks, recent, seed=middle, acc=distinct)
+
+
+# --------------------------------------------------------------- attention
+
+
+def poison(cache, side, pos, what, block):
+    """A row of the first head of the first sequence with a NaN block scale or an S_dec of `what`."""
+    page, slot = int(cache.table[0, pos // cache.P]), pos % cache.P
+    if what == "scale":
+        cache.sides[side][1][page, 0, slot, block] = 0xFF if block % 2 else 0x7F
+    else:
+        cache.sides[side][2][page, 0, slot] = float(what)
+
+
+@pytest.mark.parametrize("what", ["scale", "nan", "-nan", "inf"])
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("dtype,n,max_len", [("bf16", 7, 0), ("fp16", 24, 2000), ("bf16", 60, LONG), ("fp16", 60, LONG)])
+def test_attention_rows_that_are_not_numbers(dtype, n, max_len, D, what):
+    """A value row with a NaN reaches the queries that see it, in the block that it is in, and
+    no others; the same for keys, whose queries are NaN as a whole."""
+    G, L = 3, 150
+    bad = [(L - 1, 0), (L - 5, D // 16 - 1), (L - n + 2, 1)]  # (place, block) of three of the new tokens
+    cache = ref.Cache([L, 40], 2, D, 16, seed=D + n, W=WIDE if max_len == LONG else None)
+    for pos, block in bad:  # whatever random rows hold there, a size that counts
+        page, slot = int(cache.table[0, pos // 16]), pos % 16
+        for _, scales, sdec in cache.sides:
+            scales[page, 0, slot], sdec[page, 0, slot] = 0x38, 0.02
+    q, new = ref.queries(2 * n, 2 * G, D, dtype, D + 1), [n, n]
+    want, bound, want_lse, lse_bound = ref.attention(cache, q, new)
+    keep = [tuple(t.clone() for t in side) for side in cache.sides]
+    for side in (1, 0):
+        cache.sides = [tuple(t.clone() for t in s) for s in keep]
+        hit = torch.zeros(2 * n, 2 * G, D, dtype=torch.bool)
+        for pos, block in bad:
+            poison(cache, side, pos, what, block)
+            where = slice(16 * block, 16 * block + 16) if what == "scale" and side == 1 else slice(None)
+            hit[pos - (L - n):n, :G, where] = True
+        out, lse, status = attend(cache, q, new, max_len=max_len)
+        out, lse = out.cpu(), lse.cpu()
+        assert status == 0
+        whole, none = hit.all(-1), want_lse == -math.inf
+        assert_within(out[~hit], want[~hit], bound[~hit], "out")
+        assert torch.equal(lse == -math.inf, none)
+        rest = ~whole & ~none
+        assert_within(lse[rest], want_lse[rest], lse_bound[rest], "lse")
+        if what != "inf":
+            assert torch.isnan(out[hit]).all()
+        elif side == 1:
+            assert not torch.isfinite(out[hit]).any()
+        if side == 0 and what != "inf":
+            assert torch.isnan(lse[whole]).all()
+
+
+@pytest.mark.parametrize("n,max_len", [(3, 0), (60, LONG)])
+def test_attention_a_nan_that_all_see(n, max_len):
+    """In an early row, in a page's last place, and where some keys of the step are not there."""
+    L, D = 130, 128
+    cache = ref.Cache([L], 2, D, 16, seed=5, W=WIDE if max_len else None)
+    for pos in (0, 47, L - n - 1):
+        poison(cache, 1, pos, "scale", 2)
+    cache.table[0, 1] = -1  # keys 16 to 31
+    q = ref.queries(n, 4, D, "bf16", 6)
+    for causal in (True, False):
+        out, lse, _ = attend(cache, q, [n], causal=causal, max_len=max_len)
+        nan = torch.isnan(out.cpu())
+        assert nan[:, :2, 32:48].all() and not nan[:, 2:].any()
+        assert not nan[:, :2, :32].any() and not nan[:, :2, 48:].any() and torch.isfinite(lse).all()
