@@ -534,13 +534,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
       for (int t = 0; t < DT16; t++) o[t] *= f;
     }
     Frag p, rest;
-    float w[8];
+    float w[8], sum = 0.0f;  // of the step's weights first: small ones are not lost beside l one by one
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       const float e = __builtin_amdgcn_exp2f(z[i] - m);
-      l += e;
+      sum += e;
       w[i] = e * vs[i / 4][i % 4];
     }
+    l += sum;
 #pragma unroll
     for (int i = 0; i < 4; i++) p.u[i] = round_pair<DT>(w[2 * i], w[2 * i + 1], rest.u[i]);
     wave_lds_order();
@@ -881,6 +882,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
             vf[c][t].u[2 * u + 1] = y.y;
           }
       };
+      float sum = 0.0f;  // of the step's weights first: small ones are not lost beside l one by one
       auto weigh = [&](int kb) {
 #pragma unroll
         for (int b = 0; b < 4; b++) {
@@ -889,7 +891,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[kb][4 * b + i], ks[i], -m));
-            l += e;
+            sum += e;
             w[i] = e * vs[i];
           }
 #pragma unroll
@@ -913,6 +915,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
       add(0);
       add(1);
       weigh(1);
+      l += sum;
       read_values(2);
       FOS_INTERLEAVE(2 * NC, 72 / (2 * NC), 2)
       __builtin_amdgcn_sched_barrier(0);

@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import kv_reference as ref
-from operator_reference import assert_within, gen
-from test_gpu_kv import DIMS, LONG, WIDE, attend, check_evict
+import nvfp4_adaptive_block_amd as fos
+from operator_reference import DTYPES, assert_within, gen, half_step
+from test_gpu_kv import DIMS, LONG, WIDE, attend, check_evict, ends
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +93,49 @@ def test_attention_a_nan_that_all_see(n, max_len):
         nan = torch.isnan(out.cpu())
         assert nan[:, :2, 32:48].all() and not nan[:, 2:].any()
         assert not nan[:, :2, :32].any() and not nan[:, :2, 48:].any() and torch.isfinite(lse).all()
+
+
+def one_row(sides, page, slot, values):
+    """A row of block scales and S_dec of 1: values 0 and 1."""
+    codes = (2 * values[0::2] + 32 * values[1::2]).to(torch.uint8)
+    sides[0][page, 0, slot], sides[1][page, 0, slot], sides[2][page, 0, slot] = codes, 0x38, 1.0
+
+
+def many_small_weights(B, G, N, dtype):
+    """(out, lse, its value without rounding, the few keys' part of it, their values) of a few keys far
+    ahead of very many. All sequences share one's pages, so that each workgroup walks over all keys."""
+    D, P, a = 32, 2 ** 16, 18.5  # a query gives the few keys a weight e^a times the others'
+    half = torch.arange(D) < D // 2
+    k, v = (fos.fos_kv_cache(N // P, 1, P, D, device="cpu") for _ in range(2))
+    one_row(k, slice(None), slice(None), torch.zeros(D, dtype=torch.int32))
+    one_row(v, slice(None), slice(None), (~half).int())
+    few = [0, 32, 64, 96]  # in the first step of each wave
+    for pos in few:
+        one_row(k, 0, pos, (torch.arange(D) < 1).int())
+        one_row(v, 0, pos, half.int())
+    k, v = (tuple(t.cuda() for t in side) for side in (k, v))
+    table = torch.arange(N // P, dtype=torch.int32).expand(B, -1).contiguous().cuda()
+    lens = torch.full((B,), N, dtype=torch.int32).cuda()
+    q = torch.zeros(B, G, D, dtype=DTYPES[dtype])
+    q[..., 0] = a
+    if B > 1:
+        assert fos.fos_kv_attention_workspace(B, G, B, N // P, 1, P, D) == 0  # one part
+    out, lse = fos.fos_kv_attention(q.cuda(), ends([1] * B), k, v, table, lens, scale=1.0, causal=False)
+    small = (N - len(few)) * math.exp(-a)
+    part = len(few) / (len(few) + small)
+    score = 6 * ref.E24 * a + 3 * 2.0 ** -23  # six roundings of a score of at most a log2 e, the exponential
+    return out, lse, a + math.log(len(few) + small), part, half, score
+
+
+MANY = [(2304, 1, 2 ** 20), (512, 64, 2 ** 18), (1, 4, 2 ** 20)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("B,G,N", MANY)
+def test_attention_sum_of_many_small_weights(B, G, N, dtype):
+    """A step's weights are added up before they meet what a lane has: a wave of four has
+    N / 128 steps of 32 keys, one of 32 rows N / 64 of 64, and each addition is off by half a step
+    of binary32 at most, 2^-24 of the sum."""
+    _, lse, want, _, _, score = many_small_weights(B, G, N, dtype)
+    err = score + (N / (64 if G > 48 else 128) + 64) * ref.E24
+    assert ((lse.cpu().double() - want).abs() < err).all()
