@@ -11,11 +11,13 @@
 //    2^-32 of the row's largest, and what is smaller is off by 2^-40 of it.
 //  - S_dec of a key multiplies the sum, in binary32.
 //  - S_dec of a value row multiplies the softmax's weight: p_rj = 2^(z_rj - m) S_j is
-//    rounded to fp16 (at most 2^-11 of its size, an eighth of what bf16 rounds), and m
-//    runs along with the largest z_rj + log2 S_j, so the products that matter lie
-//    between 1/2 and 2^7 whatever the rows' sizes are. m only has to be near that maximum:
-//    log2 S is taken from the exponent bits, and m follows when it is left behind by
-//    more than kLag.
+//    rounded to fp16, and m runs along with the largest z_rj + log2 S_j, kAbove below it,
+//    so the largest p of a query lies between 2^8 and 2^15 whatever the rows' sizes are. What is
+//    2^-22 of it or more is rounded by at most 2^-11 of its own size, an eighth of what bf16
+//    rounds; what is smaller by at most 2^-33 of the largest. (Where no S is 2^-82, p shrinks with
+//    them, kLeast being what m goes down to: whole to S of 2^-104, gone at 2^-115.) m only has to be
+//    near its maximum: log2 S is taken from the exponent bits, and m follows when it is left behind
+//    by more than kLag.
 // Sums, m and the softmax's denominator are binary32.
 //
 // Scores are computed as K Q^T: the matrix instruction leaves a query per lane and
@@ -45,7 +47,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLowest = -kFltMax;  // m before any key
 constexpr float kLag = 6.0f;
-constexpr float kLeast = -90.0f;     // log2 S of rows without a size: 2^96 a key sums up to 2^127
+constexpr float kAbove = 8.0f;       // so that p is below 2^(kAbove + kLag + 1), and fp16 ends at 2^16
+constexpr float kLeast = -90.0f;     // log2_of rows without a size: 2^96 a key sums up to 2^127
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMaxParts = 256;
 
@@ -74,10 +77,10 @@ __device__ __forceinline__ float col_sum(float v) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-// Exponent of S (its floor's log2) for the running maximum; kLeast for 0, and for an infinity
-// or a NaN, whose exponent is one more than any and so wraps to none.
+// Exponent of S (its floor's log2) less kAbove, for the running maximum; kLeast for 0, and for an
+// infinity or a NaN, whose exponent is one more than any and so wraps to none.
 __device__ __forceinline__ float log2_of(float S) {
-  return __builtin_fmaxf((float)(((__float_as_uint(S) << 1) + 0x01000000u) >> 24) - 128.0f, kLeast);
+  return __builtin_fmaxf((float)(((__float_as_uint(S) << 1) + 0x01000000u) >> 24) - (128.0f + kAbove), kLeast);
 }
 
 // Two weights in fp16. For fp16 results what the rounding leaves out is kept too, and

@@ -139,3 +139,18 @@ def test_attention_sum_of_many_small_weights(B, G, N, dtype):
     _, lse, want, _, _, score = many_small_weights(B, G, N, dtype)
     err = score + (N / (64 if G > 48 else 128) + 64) * ref.E24
     assert ((lse.cpu().double() - want).abs() < err).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("B,G,N", MANY)
+def test_attention_values_of_many_small_weights(B, G, N, dtype):
+    """What very many small weights have together counts beside a few large ones."""
+    out, _, _, part, half, score = many_small_weights(B, G, N, dtype)
+    want = torch.where(half, part, 1 - part).double().expand(B, G, -1)
+    # a weight in fp16: half a step, 2^-11, or below fp16's normal range 2^-25 where the few keys'
+    # are 2^8 or more; then the sums of both, an addition a step as above and up to two for the
+    # products; the result
+    steps = N / (64 if G > 48 else 128) + 64
+    bound = want * (2 * score + 2.0 ** -11 + 3 * steps * ref.E24) + (1 - part) / math.exp(-18.5) * 2.0 ** -33
+    bound = bound + half_step(out.dtype) * (want + bound)
+    assert_within(out, want, bound, "out")
