@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -939,7 +940,11 @@ int kv_attend_args(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride
   a.T = (int)T;
   a.G = Hq / cache->H;
   a.by_group = fos::fast_div((uint32_t)a.G);
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  int e;
+  const double mant = frexp((double)scale * 1.4426950408889634, &e);  // in [1/2, 1)
+  const int power = e - 1 > 127 ? 127 : e - 1;
+  a.scale_mant = (float)ldexp(mant, e - power);
+  a.scale_pow = ldexpf(1.0f, power);
   a.causal = causal != 0;
   a.max_len = max_len == 0 || max_len > places ? places : max_len;
   a.splits = fos::kv_splits(T, cache->B, cache->H, a.G, cache->D, a.max_len);

@@ -9,7 +9,9 @@
 //  - q in fp16 as it is; in bf16 times a power of two that brings the row's (or the tile's) largest
 //    value to [2^14, 2^15). The 8 bits of a bf16 value are exact there down to
 //    2^-32 of the row's largest, and what is smaller is off by 2^-40 of it.
-//  - S_dec of a key multiplies the sum, in binary32.
+//  - S_dec of a key multiplies the sum, in binary32: with the scale's mantissa first, then with
+//    its power of two and what undoes q's, which are exact, so that nothing between leaves
+//    binary32's range where the score does not.
 //  - S_dec of a value row multiplies the softmax's weight: p_rj = 2^(z_rj - m) S_j is
 //    rounded to fp16, and m runs along with the largest z_rj + log2 S_j, kAbove below it,
 //    so the largest p of a query lies between 2^8 and 2^15 whatever the rows' sizes are. What is
@@ -424,7 +426,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 
   Frag q[NC];
   const float undo = load_q<DT, NC, true>(a.q, row.token * a.stride + (int64_t)row.head * D + g * 8 * NC, 8, row.have, q);
-  const float qf = a.scale_log2 * undo;
+  const float qf = a.scale_pow * undo;
   f32x4 o[DT16];
 #pragma unroll
   for (int t = 0; t < DT16; t++) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -435,6 +437,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
   float* sizes = reinterpret_cast<float*>(keys + L::kSizes);
   const Pages pg{a.c.table + (int64_t)(gt.g < a.c.B ? gt.g : 0) * a.c.W, a.c.pages, a.c.H, h, a.c.P, a.c.by_page};
 
+  const float size_by = lane < 32 ? a.scale_mant : 1.0f;  // the keys' S_dec have the scale's mantissa
   // pages a step ahead of the loads, loads a step ahead of their use; past the last step
   // the cache's first rows, unused
   Step<NC> next;
@@ -461,7 +464,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
     wave_lds_order();
 #pragma unroll
     for (int u = 0; u < 2; u++) st.k[u].store_codes(keys + u * 256 * NC + 4 * NC * piece(lane >> 2, lane & 3));
-    sizes[lane] = st.sdec;
+    sizes[lane] = st.sdec * size_by;
     wave_lds_order();
     f32x4 sc[2];
 #pragma unroll
@@ -738,8 +741,9 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
     lo = min(min(ends[4], ends[5]), min(ends[6], ends[7]));
     common = __builtin_amdgcn_readfirstlane(hi - lo <= 8 && hi <= 141 && hi >= 77);
     undo = scale_q<2 * NC>(q, common ? hi : e);
-    if (common) undo_all = undo, undo = 1.0f;
   }
+  undo *= a.scale_pow;
+  if (common) undo_all = undo, undo = 1.0f;
   f32x16 o[NC];
 #pragma unroll
   for (int t = 0; t < NC; t++)
@@ -758,7 +762,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   const int to_log2 = lane >= 16 && lane < 32 ? kLog2 + my_size : kNowhere + 1;
   const int to_gone = lane == 0 ? kGone + wave : kNowhere + 2;
   // the keys' scale goes with their S_dec, so that what is left for a query is its power of two
-  const float size_by = lane < 16 ? a.scale_log2 : 1.0f, size_undo = lane < 16 ? undo_all : 1.0f;
+  const float size_by = lane < 16 ? a.scale_mant : 1.0f, size_undo = lane < 16 ? undo_all : 1.0f;
   // This wave's rows of a step, decoded, to the step's side of the LDS, without a branch, so that
   // it can run beside matrix instructions. Zeros where there is no key: a stale scale may be a NaN.
   // One in a value row that is there must reach the queries that see it and no others, but 0 times
@@ -846,7 +850,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
             const int past = absent[j >> 4] != 0.0f ? 0 : limit - first - j - 4 * half;  // keys from here on are not seen
 #pragma unroll
             for (int i = 0; i < 4; i++)
-              x[kb][4 * b + i] = i < past ? x[kb][4 * b + i] * ks[i] * undo : -__builtin_huge_valf();
+              x[kb][4 * b + i] = i < past ? x[kb][4 * b + i] * (ks[i] * undo) : -__builtin_huge_valf();
           }
       }
       auto size_of = [&](int kb, int b) { return *reinterpret_cast<const f32x4*>(by + 32 * kb + 8 * b + 4 * half); };
@@ -1186,7 +1190,7 @@ __global__ __launch_bounds__(256, kRows == 32 && NC <= 4 ? 4 : 2) void k_kv_weig
         float lse = row.have ? a.lse[row.token * ((int64_t)a.c.H * a.G) + row.head] : 0.0f;
         // a row that sees nothing has no weights: 2^-infinity
         if (!row.have || lse == -__builtin_huge_valf()) lse = __builtin_huge_valf();
-        factor[r0 + col] = a.scale_log2 * undo;
+        factor[r0 + col] = a.scale_pow * undo;
         ref[r0 + col] = lse * 1.44269504088896341f;
         limits[r0 + col] = a.causal ? min(len, len - n + row.place + 1) : len;
       }
@@ -1206,6 +1210,7 @@ __global__ __launch_bounds__(256, kRows == 32 && NC <= 4 ? 4 : 2) void k_kv_weig
       for (int i = 0; i < 2; i++)
         codes[i].load_codes(mine + (col >> 4) * 256 * NC + 4 * NC * piece(col & 15, 2 * half + i));
       st.half.decode(codes, kf);
+      const float key = st.sdec * a.scale_mant;
       float sum = 0.0f;
       auto product = [&](int rt) {
         f32x16 x;
@@ -1226,7 +1231,7 @@ __global__ __launch_bounds__(256, kRows == 32 && NC <= 4 ? 4 : 2) void k_kv_weig
         const f32x4 f = *reinterpret_cast<const f32x4*>(factor + r), z = *reinterpret_cast<const f32x4*>(ref + r);
         float e[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[4 * i + j] * st.sdec, f[j], -z[j]));
+        for (int j = 0; j < 4; j++) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[4 * i + j], key * f[j], -z[j]));
         if (partly) {
           const int4 lim = *reinterpret_cast<const int4*>(limits + r);
           const int l4[4] = {lim.x, lim.y, lim.z, lim.w};

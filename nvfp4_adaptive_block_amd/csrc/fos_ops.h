@@ -141,7 +141,7 @@ struct KvAttendArgs {
   const int32_t* offs;
   int T, G;
   FastDiv by_group;      // / G
-  float scale_log2;      // scale log2(e)
+  float scale_mant, scale_pow;  // scale log2(e) as m 2^k: m of 0 or 1 <= |m| < 4, and 2^k
   bool causal;
   void* out;             // [T, H G, D]
   float* lse;            // [T, H G]; nullable for attention, an input for weights

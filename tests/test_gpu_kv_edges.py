@@ -8,7 +8,7 @@ import torch
 import kv_reference as ref
 import nvfp4_adaptive_block_amd as fos
 from operator_reference import DTYPES, assert_within, gen, half_step
-from test_gpu_kv import DIMS, LONG, WIDE, attend, check_evict, ends
+from test_gpu_kv import DIMS, LONG, WIDE, attend, check_attention, check_evict, check_weights, ends
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,30 @@ def test_attention_values_of_many_small_weights(B, G, N, dtype):
     bound = want * (2 * score + 2.0 ** -11 + 3 * steps * ref.E24) + (1 - part) / math.exp(-18.5) * 2.0 ** -33
     bound = bound + half_step(out.dtype) * (want + bound)
     assert_within(out, want, bound, "out")
+
+
+@pytest.mark.parametrize("size_q,size_k,scale", [(2.0 ** -108, 2.0 ** 106, 0.125), (2.0 ** -115, 2.0 ** 112, 0.125),
+                                                 (2.0 ** 110, 2.0 ** -112, 0.125), (1.0, 2.0 ** 110, 2.0 ** -115),
+                                                 (2.0 ** -100, 1.0, 2.0 ** 96), (1.0, 0.02, 0.125)])
+def test_scores_between_rows_of_opposite_sizes(size_q, size_k, scale):
+    """Scores of ordinary size from queries, keys and scales that are not: no product on the way
+    leaves binary32's range. Attention of few rows and of many, whose queries have a power of two
+    each or one for all; weights of 32 rows and of 256."""
+    for G, n, max_len in ((3, 2, 0), (4, 25, LONG), (2, 200, 0)):
+        cache = ref.Cache([230, 210], 2, 64, 16, seed=31, sizes=(size_k, 0.01), W=WIDE if max_len else None)
+        q = ref.queries(2 * n, 2 * G, 64, "bf16", 32)
+        for spread in (1.0, 2.0 ** -11):  # rows of one size and of two
+            q[::3] *= spread
+            x = (q.double() * size_q).bfloat16()
+            check_attention(cache, x, [n, n], scale=scale, max_len=max_len)
+            if not max_len:
+                check_weights(cache, x, [n, n], scale=scale)
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.0 ** -140, 1e-45])
+def test_scales_at_the_end_of_the_range(scale):
+    """The largest and the smallest scale that float32 has."""
+    cache = ref.Cache([50, 9], 2, 64, 16, seed=33, sizes=(0.02, 0.01))
+    size = 1 / abs(scale) if abs(scale) > 1 else 2.0 ** 120
+    q = (ref.queries(4, 4, 64, "bf16", 34).double() * size).bfloat16()
+    check_attention(cache, q, [2, 2], scale=scale)
