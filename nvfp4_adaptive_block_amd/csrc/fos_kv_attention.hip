@@ -7,8 +7,8 @@
 // float32 S_dec. c b has at most 6 significant bits and lies in [2^-10, 2688], so it
 // is exact in fp16, which is what the matrix instructions take on both sides:
 //  - q in fp16 as it is; in bf16 times a power of two that brings the row's (or the tile's) largest
-//    value to [2^14, 2^15). The 8 bits of a bf16 value are exact there down to
-//    2^-32 of the row's largest, and what is smaller is off by 2^-40 of it.
+//    value to [2^15, 2^16), where fp16 still has all 8 bits. They are exact down to 2^-32 of
+//    the row's largest, and what is smaller is off by 2^-40 of it (2^-32 where a tile has one).
 //  - S_dec of a key multiplies the sum, in binary32: with the scale's mantissa first, then with
 //    its power of two and what undoes q's, which are exact, so that nothing between leaves
 //    binary32's range where the score does not.
@@ -292,10 +292,10 @@ __device__ __forceinline__ int q_exponent(const Frag* f) {
   return (int)(__float_as_uint(row_max<QUARTERS>(__uint_as_float(top << 16))) >> 23);
 }
 
-// bf16 to fp16, times the power of two that brings exponent e to 2^14; returns what undoes it.
+// bf16 to fp16, times the power of two that brings exponent e to 2^15; returns what undoes it.
 template <int N>
 __device__ __forceinline__ float scale_q(Frag* f, int e) {
-  int up = 141 - e;
+  int up = 142 - e;
   up = up > 126 ? 126 : up;
   const float by = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll

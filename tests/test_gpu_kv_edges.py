@@ -181,3 +181,37 @@ def test_scales_at_the_end_of_the_range(scale):
     size = 1 / abs(scale) if abs(scale) > 1 else 2.0 ** 120
     q = (ref.queries(4, 4, 64, "bf16", 34).double() * size).bfloat16()
     check_attention(cache, q, [2, 2], scale=scale)
+
+
+@pytest.mark.parametrize("n,max_len", [(1, 0), (60, LONG)])
+def test_small_values_beside_a_large_one(n, max_len):
+    """bf16 queries go through fp16 times a power of two: a value of eight bits down to 2^-32 of the
+    row's largest is exact, and where rows of 2^-8 of the tile's largest share theirs, too, as long
+    as it is 2^-32 of the tile's. A key that has only the small value's place shows it."""
+    D, small = 64, (1 + 2.0 ** -7) * 2.0 ** -32
+    L = max(n, 40)
+    cache = ref.Cache([L], 1, D, 16, seed=41, W=WIDE if max_len else None)
+    for t in cache.sides[0]:
+        t.zero_()
+    cache.sides[0][2].fill_(1.0)
+    cache.sides[0][1].fill_(0x38)
+    at = int(cache.table[0, 0])
+    cache.sides[0][0][at, 0, 0, 0] = 0x20  # the first key: 1 in the second place
+    q = torch.zeros(n, 2, D, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    q[:, 1, 0] = 2.0 ** -8
+    q[..., 1] = small
+    assert (q[..., 1].double() == small).all()
+    scale = 2.0 ** 34
+    want, bound, want_lse, _ = ref.attention(cache, q, [n], scale=scale)
+    out, lse, _ = attend(cache, q, [n], scale=scale, max_len=max_len)
+    # exact queries: the score's and the sums' roundings alone (a score of 4, L weights)
+    err = (6 * 4 + 4 * math.sqrt(L) + 40) * ref.E24
+    assert ((lse.cpu().double() - want_lse).abs() < err).all()
+    assert_within(out, want, bound, "out")
+    if not max_len:
+        acc = torch.zeros(1, 1, cache.W * 16, device="cuda")
+        k, v, table, lens = cache.on_device()
+        fos.fos_kv_weights(q.cuda(), ends([n]), k, table, lens, lse, acc, scale=scale)
+        sums, _ = ref.weights(cache, q, [n], lse.cpu(), scale=scale)
+        assert ((acc.cpu().double() - sums).abs() <= 2 * n * err * sums).all()
