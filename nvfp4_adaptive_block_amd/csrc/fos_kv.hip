@@ -169,8 +169,9 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
   const int64_t rows = (int64_t)a.T * a.c.H;
   if (a.status && blockIdx.x == 0 && side == 0) {
     for (int g = threadIdx.x; g < a.c.B; g += 256) {
-      const int e = a.offs[g], p = g ? a.offs[g - 1] : 0;
+      const int e = a.offs[g], p = g ? a.offs[g - 1] : 0, n = a.c.lens[g];
       if (e < p || e > a.T) atomicOr(a.status, kStatusBadOffs);
+      if (n < 0 || n > a.c.W * a.c.P) atomicOr(a.status, kStatusBadCache);
     }
   }
   if (first >= rows) return;
@@ -218,9 +219,9 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
   int start = b ? a.offs[b - 1] : 0, end = a.offs[b];
   if (start < 0) start = 0;
   if (end > a.T) end = a.T;
-  const int len = a.c.lens[b];
+  const int len = min(a.c.lens[b], a.c.W * a.c.P);
   const int64_t pos = (int64_t)len - (end - start) + (t - start);
-  const bool inside = pos >= 0 && pos < (int64_t)a.c.W * a.c.P;
+  const bool inside = pos >= 0;
   int64_t page = -1;
   int slot = 0;
   if (inside) {

@@ -8,7 +8,7 @@ import torch
 import kv_reference as ref
 import nvfp4_adaptive_block_amd as fos
 from operator_reference import DTYPES, assert_within, gen, half_step
-from test_gpu_kv import DIMS, LONG, WIDE, attend, check_attention, check_evict, check_weights, ends
+from test_gpu_kv import DIMS, LONG, WIDE, attend, check_attention, check_evict, check_weights, ends, oracle_rows, rows_like, same
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +26,43 @@ def test_evict_short_middles(middle):
     n, sinks, recent = middle + 24, 4, 20
     for budget in sorted({sinks + recent, n - 1, sinks + recent + middle // 2}):
         check_evict([n, n + 1], 64, 64, 16, budget, sinks, recent, seed=middle, acc=distinct)
+
+
+# ------------------------------------------------------------------ append
+
+
+def test_append_to_lengths_past_the_table(orc):
+    """They are taken as the table's end, as the attention takes them: the new rows are its last."""
+    H, D, P = 2, 64, 16
+    x = rows_like((9, H, D), "bf16", 7).cuda()
+    offs = torch.tensor([4, 4, 9], dtype=torch.int32).cuda()
+    table = torch.tensor([[2, 0], [1, 3], [4, 5]], dtype=torch.int32).cuda()
+    codes, scales, sdec, _ = oracle_rows(orc, x.cpu())
+    for lens in ([32, 0, 32], [33, 0, 10 ** 9], [2 ** 31 - 1, 0, 40]):
+        kc, vc = (fos.fos_kv_cache(6, H, P, D) for _ in range(2))
+        status = torch.zeros(1, dtype=torch.int32).cuda()
+        fos.fos_kv_append(x, x, offs, kc, vc, table, torch.tensor(lens, dtype=torch.int32).cuda(), status=status)
+        assert int(status.item()) == (0 if max(lens) == 32 else fos.STATUS_BAD_CACHE)
+        want = [torch.zeros_like(t).cpu() for t in kc]
+        for b, start, n, page in ((0, 0, 4, 0), (2, 4, 5, 5)):
+            for i in range(n):
+                r = (start + i) * H
+                for w, o in zip(want, (codes, scales, sdec)):
+                    w[page, :, P - n + i] = torch.from_numpy(o[r:r + H])
+        for side in (kc, vc):
+            assert all(same(t, w) for t, w in zip(side, want))
+
+
+@pytest.mark.parametrize("length", [33, -1, -2 ** 31])
+def test_append_reports_lengths_of_sequences_without_new_rows(length):
+    kc, vc = (fos.fos_kv_cache(4, 2, 16, 64) for _ in range(2))
+    table = torch.arange(4, dtype=torch.int32).view(2, 2).cuda()
+    x = torch.ones(3, 2, 64, device="cuda")
+    for bad in (False, True):
+        status = torch.zeros(1, dtype=torch.int32).cuda()
+        lens = torch.tensor([3, length if bad else 32], dtype=torch.int32).cuda()
+        fos.fos_kv_append(x, x, torch.tensor([3, 3], dtype=torch.int32).cuda(), kc, vc, table, lens, status=status)
+        assert int(status.item()) == (fos.STATUS_BAD_CACHE if bad else 0)
 
 
 # --------------------------------------------------------------- attention
