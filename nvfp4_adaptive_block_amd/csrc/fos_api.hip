@@ -975,7 +975,7 @@ int fos_kv_append(const void* k, const void* v, int dtype, int64_t T, int64_t k_
     return fail(FOS_ERR_ALIGN, "a tensor is not 16-byte aligned");
   if (!aligned(offs, 4) || !aligned(d_status, 4)) return fail(FOS_ERR_ALIGN, "offs/status misaligned");
   if ((rc = check_device())) return rc;
-  if (T == 0) return FOS_OK;
+  if (T == 0) return launch_status(fos::launch_kv_check(a.c, offs, d_status, static_cast<hipStream_t>(stream)));
   a.x[0] = k;
   a.x[1] = v;
   a.stride[0] = k_stride;
@@ -1014,7 +1014,7 @@ int fos_kv_attention(const void* q, int dtype, int64_t T, int Hq, int64_t q_stri
     return fail(FOS_ERR_INVALID_ARG, "the workspace holds %lld bytes, %lld needed", (long long)(work ? work_bytes : 0), (long long)need);
   if (need > 0 && !aligned(work, 16)) return fail(FOS_ERR_ALIGN, "workspace not 16-byte aligned");
   if ((rc = check_device())) return rc;
-  if (T == 0) return FOS_OK;
+  if (T == 0) return launch_status(fos::launch_kv_check(a.c, offs, d_status, static_cast<hipStream_t>(stream)));
   a.out = out;
   a.lse = lse;
   a.work = work;
@@ -1030,7 +1030,7 @@ int fos_kv_weights(const void* q, int dtype, int64_t T, int Hq, int64_t q_stride
   if ((T > 0 && !lse) || !acc) return fail(FOS_ERR_INVALID_ARG, "lse and acc must be non-NULL");
   if (!aligned(lse, 4) || !aligned(acc, 4)) return fail(FOS_ERR_ALIGN, "lse/acc misaligned");
   if ((rc = check_device())) return rc;
-  if (T == 0) return FOS_OK;
+  if (T == 0) return launch_status(fos::launch_kv_check(a.c, offs, d_status, static_cast<hipStream_t>(stream)));
   a.lse = const_cast<float*>(lse);
   a.acc = acc;
   return launch_status(fos::launch_kv_weights(dtype, a, static_cast<hipStream_t>(stream)));

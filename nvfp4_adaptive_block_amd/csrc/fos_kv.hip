@@ -15,6 +15,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 
+// Of a call without tokens, which has nothing else to do.
+__global__ __launch_bounds__(256) void k_kv_check(KvCache c, const int32_t* offs, int32_t* status) {
+  check_kv(c, offs, 0, status);
+}
+
 // ---------------------------------------------------------------- append
 //
 // One lane has one block of 16 values, and the D/16 blocks of a row are
@@ -167,13 +172,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
   const int sh = blocks <= 2 ? 1 : blocks <= 4 ? 2 : blocks <= 8 ? 3 : 4;  // log2 of the lanes per row
   const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * (64 >> sh);
   const int64_t rows = (int64_t)a.T * a.c.H;
-  if (a.status && blockIdx.x == 0 && side == 0) {
-    for (int g = threadIdx.x; g < a.c.B; g += 256) {
-      const int e = a.offs[g], p = g ? a.offs[g - 1] : 0, n = a.c.lens[g];
-      if (e < p || e > a.T) atomicOr(a.status, kStatusBadOffs);
-      if (n < 0 || n > a.c.W * a.c.P) atomicOr(a.status, kStatusBadCache);
-    }
-  }
+  if (side == 0) check_kv(a.c, a.offs, a.T, a.status);
   if (first >= rows) return;
   // the sequence of the wave's first token: the first whose end lies behind it
   const int t0 = a.by_head.div((int)first);
@@ -682,6 +681,12 @@ void evict(const KvEvictArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_kv_check(const KvCache& c, const int32_t* offs, int32_t* status, hipStream_t s) {
+  if (!status) return hipSuccess;
+  k_kv_check<<<1, 256, 0, s>>>(c, offs, status);
+  return hipGetLastError();
+}
 
 hipError_t launch_kv_append(int dt, const KvAppendArgs& a, hipStream_t s) {
   const int blocks = a.c.D / 16;

@@ -120,6 +120,9 @@ struct KvCache {
   FastDiv by_page;       // / P
 };
 
+// Reports offsets and lengths out of their range to the nullable status, for a call without tokens.
+hipError_t launch_kv_check(const KvCache& c, const int32_t* offs, int32_t* status, hipStream_t s);
+
 struct KvAppendArgs {
   KvCache c;
   const void* x[2];      // k, v: rows of H D values

@@ -6,7 +6,19 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "fos_ops.h"
+
 namespace fos {
+
+// Offsets and lengths out of their range, reported by the first workgroups of a launch along x.
+__device__ __forceinline__ void check_kv(const KvCache& c, const int32_t* offs, int T, int32_t* status) {
+  if (!status || blockIdx.x != 0) return;
+  for (int b = threadIdx.x; b < c.B; b += blockDim.x) {
+    const int e = offs[b], p = b ? offs[b - 1] : 0, n = c.lens[b];
+    if (e < p || e > T) atomicOr(status, kStatusBadOffs);
+    if (n < 0 || n > c.W * c.P) atomicOr(status, kStatusBadCache);
+  }
+}
 
 // Between LDS accesses of one wave that different lanes make to the same place.
 // The hardware runs a wave's LDS operations in order; the compiler, which sees

@@ -252,3 +252,33 @@ def test_small_values_beside_a_large_one(n, max_len):
         fos.fos_kv_weights(q.cuda(), ends([n]), k, table, lens, lse, acc, scale=scale)
         sums, _ = ref.weights(cache, q, [n], lse.cpu(), scale=scale)
         assert ((acc.cpu().double() - sums).abs() <= 2 * n * err * sums).all()
+
+
+# ---------------------------------------------------------------- together
+
+
+@pytest.mark.parametrize("B", [2, 300])
+def test_calls_without_tokens_report_what_is_bad(B):
+    cache = ref.Cache([33] * B, 2, 64, 16, seed=51)
+    k, v, table, lens = cache.on_device()
+    none = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    acc = torch.zeros(B, 2, cache.W * 16, device="cuda")
+
+    def calls(offs, lens):
+        yield lambda **kw: fos.fos_kv_append(none, none, offs, k, v, table, lens, **kw)
+        yield lambda **kw: fos.fos_kv_attention(none, offs, k, v, table, lens, **kw)
+        yield lambda **kw: fos.fos_kv_weights(none, offs, k, table, lens, none[..., 0].float(), acc, **kw)
+
+    zeros = [0] * B
+    late = lambda t, x: t[:-1] + [x]
+    for offs, lengths, want in ((zeros, [33] * B, 0), (late(zeros, 1), [33] * B, fos.STATUS_BAD_OFFS),
+                                (late(zeros, -1), [33] * B, fos.STATUS_BAD_OFFS),
+                                (zeros, late([33] * B, 49), fos.STATUS_BAD_CACHE),
+                                (late(zeros, 3), late([33] * B, -1), fos.STATUS_BAD_OFFS | fos.STATUS_BAD_CACHE)):
+        o, n = (torch.tensor(t, dtype=torch.int32).cuda() for t in (offs, lengths))
+        for call in calls(o, n):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            call(status=status)
+            call()
+            assert int(status.item()) == want
+    assert not acc.any()
