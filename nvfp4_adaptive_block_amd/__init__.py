@@ -901,6 +901,13 @@ def _kv_room(workspace, need, index):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+def _kv_ints(**values):
+    """Sizes that the library takes in 32 bits, of which ctypes would drop the others."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name}={v} is out of range")
+
+
 def _kv_status(status, index):
     return None if status is None else _status_pointer(status, _kv_device(index))
 
@@ -989,6 +996,7 @@ def fos_kv_attention(q: torch.Tensor, offs: torch.Tensor, k_cache, v_cache, tabl
 def fos_kv_attention_workspace(T: int, Hq: int, B: int, W: int, H: int, P: int, D: int, max_len: int = 0) -> int:
     """Bytes of workspace of fos_kv_attention for T tokens of Hq query heads on a
     cache of H heads, with a table [B, W] of pages of P rows of D values."""
+    _kv_ints(Hq=Hq, H=H, P=P, D=D)
     need = load_library().fos_kv_attention_workspace(T, Hq, B, W, H, P, D, max_len)
     if need < 0:
         raise ValueError(f"unsupported sizes T={T} Hq={Hq} B={B} W={W} H={H} P={P} D={D}")
@@ -1020,6 +1028,7 @@ def fos_kv_evict(acc: torch.Tensor, k_cache, v_cache, table: torch.Tensor, lens:
     with the largest acc float32[B, H, W * P] stay. Kept rows, and their acc, move
     into the places that others gave up; the last rows end at the new length in
     their order. Returns new_lens int32[B], min(lens, budget); lens itself is left."""
+    _kv_ints(budget=budget, sinks=sinks, recent=recent)
     cache, index, B, W, H, P, _ = _kv_cache(k_cache, v_cache, table, lens)
     lib = load_library()
     if new_lens is None:
@@ -1036,6 +1045,7 @@ def fos_kv_evict(acc: torch.Tensor, k_cache, v_cache, table: torch.Tensor, lens:
 
 def fos_kv_evict_workspace(B: int, H: int, budget: int, recent: int = 0) -> int:
     """Bytes of workspace of fos_kv_evict."""
+    _kv_ints(H=H, budget=budget, recent=recent)
     need = load_library().fos_kv_evict_workspace(B, H, budget, recent)
     if need < 0:
         raise ValueError(f"unsupported sizes B={B} H={H} budget={budget} recent={recent}")
