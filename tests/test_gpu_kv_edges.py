@@ -8,7 +8,8 @@ import torch
 import kv_reference as ref
 import nvfp4_adaptive_block_amd as fos
 from operator_reference import DTYPES, assert_within, gen, half_step
-from test_gpu_kv import DIMS, LONG, WIDE, attend, check_attention, check_evict, check_weights, ends, oracle_rows, rows_like, same
+from test_gpu_kv import (DIMS, LONG, WIDE, assert_guard, attend, check_attention, check_evict, check_weights, ends, guarded,
+                         oracle_rows, rows_like, same)
 
 pytestmark = pytest.mark.gpu
 
@@ -252,6 +253,73 @@ def test_small_values_beside_a_large_one(n, max_len):
         fos.fos_kv_weights(q.cuda(), ends([n]), k, table, lens, lse, acc, scale=scale)
         sums, _ = ref.weights(cache, q, [n], lse.cpu(), scale=scale)
         assert ((acc.cpu().double() - sums).abs() <= 2 * n * err * sums).all()
+
+
+# ----------------------------------------------------------------- weights
+
+
+def add_weights(cache, q, offs, lse, causal=True):
+    """(acc after the call, acc before it, status)."""
+    k, v, table, lens = cache.on_device()
+    start = torch.rand(cache.B, cache.H, cache.W * cache.P, generator=gen(1)).cuda()
+    acc, raw = guarded(start.shape, torch.float32)
+    acc.copy_(start)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fos.fos_kv_weights(q.cuda(), torch.tensor(offs, dtype=torch.int32).cuda(), k, table, lens, lse.cuda(), acc,
+                       causal=causal, status=status)
+    assert_guard(raw)
+    return acc.cpu(), start.cpu(), int(status.item())
+
+
+def check_sums(acc, want, bound):
+    """What is past float32's range has become an infinity."""
+    over = want > 3.5e38
+    assert (acc[over] == math.inf).all()
+    assert_within(acc[~over], want[~over], bound[~over], "acc")
+
+
+@pytest.mark.parametrize("n,G", [(2, 3), (16, 2), (17, 2), (100, 4)])
+def test_weights_bad_cache(n, G):
+    """32 rows staged and 256. Pages that are none add nothing to their keys; lengths past the
+    table end with it, negative ones have no keys."""
+    cache = ref.Cache([64, 50], 2, 64, 16, seed=61)
+    q = ref.queries(2 * n, 2 * G, 64, "bf16", 62)
+    lse = 3 + torch.rand(2 * n, 2 * G, generator=gen(63))  # any: the sums are of exp(s - lse)
+    keep = cache.table.clone()
+    want, bound = ref.weights(cache, q, [n, n], lse, causal=False)
+    parts = -(-n * G // 32)
+    for bad in (cache.pages, -1, -2 ** 31, 2 ** 31 - 1):
+        cache.table = keep.clone()
+        cache.table[0, 1], cache.table[1, 3] = bad, -1  # keys 16 to 31, and 48 and 49
+        acc, start, status = add_weights(cache, q, [n, 2 * n], lse, causal=False)
+        assert status == 0
+        gone = torch.zeros_like(acc, dtype=torch.bool)
+        gone[0, :, 16:32] = gone[1, :, 48:] = True
+        assert same(acc[gone], start[gone])
+        total = want + start.double()
+        check_sums(acc[~gone], total[~gone], (bound + ref.E24 * parts * total.abs())[~gone])
+    cache.table = keep
+    for lens, taken in (([64, -5], [64, 0]), ([10 ** 6, 50], [64, 50]), ([2 ** 31 - 1, -2 ** 31], [64, 0])):
+        cache.lens = lens
+        acc, start, status = add_weights(cache, q, [n, 2 * n], lse)
+        assert status == fos.STATUS_BAD_CACHE
+        cache.lens = taken
+        sums, bound = ref.weights(cache, q, [n, n], lse)
+        total = sums + start.double()
+        check_sums(acc, total, bound + ref.E24 * parts * total.abs())
+        for b, length in enumerate(taken):
+            assert same(acc[b, :, length:], start[b, :, length:])
+
+
+@pytest.mark.parametrize("n,G", [(4, 2), (60, 3)])
+def test_weights_bad_offsets(n, G):
+    cache = ref.Cache([64, 50], 2, 64, 16, seed=64)
+    q = ref.queries(n, 2 * G, 64, "bf16", 65)
+    lse = 3 + torch.rand(n, 2 * G, generator=gen(66))
+    for offs in ([n - 1, n - 2], [2, n + 5], [-1, n], [2 ** 31 - 1, -2 ** 31]):
+        acc, start, status = add_weights(cache, q, offs, lse)
+        assert status == fos.STATUS_BAD_OFFS
+        assert same(acc[1, :, 50:], start[1, :, 50:])
 
 
 # ---------------------------------------------------------------- together
