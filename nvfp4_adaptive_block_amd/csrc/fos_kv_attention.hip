@@ -1339,12 +1339,17 @@ hipError_t run(bool attention, const KvAttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// A short cache of few sequences is left whole, by twelve waves to a workgroup (eight for
-// D 192: what LDS holds), with one launch and no workspace. One token on 8 heads of 128, 1000
-// keys: 11.7 us instead of 9.0 in parts, but the call 14.0 instead of 21.3; 16 such sequences
-// 13.6 instead of 16.2. (Eight waves: 12.4.)
+// A short cache is left whole, by twelve waves to a workgroup (eight for D 192: what LDS holds),
+// with one launch and no workspace, where there are no more tiles than CUs. Whole and in parts, us,
+// a token to a sequence on 4 query heads to each of the cache's: calls one after another, and
+// captured in a graph in brackets. One sequence, 8 heads of 128: 256 keys 14.9 (8.3) and 19.4 (8.5),
+// 1024 15.2 (12.9) and 19.8 (8.4), 1536 16.5 (16.6) and 19.2 (8.8), 2048 19.4 (19.8) and 20.1 (8.8):
+// a call gains up to 2048 keys, a captured step loses from 512 on, and 1024 is between. 1000 keys:
+// 64 tiles 15.2 (13.0) and 19.7 (10.2), 120 15.2 (13.0) and 19.7 (14.2), 256 15.1 (15.6) and 24.9
+// (25.3), 264 25.7 (26.3) and 26.6 (27.1); heads of 64, 256 tiles 14.5 (10.7) and 18.9 (16.4), 264
+// 18.1 (18.3) and 19.4 (17.9); of 192, 256 tiles 19.1 (19.5) and 36.4 (37.3).
 bool kv_wide(int64_t T, int B, int H, int G, int D, int64_t max_len) {
-  return !kv_tiled(T, B, H, G, max_len) && D <= 192 && max_len <= 1024 && kv_tiles(T, B, H, G, 16) < 128;
+  return !kv_tiled(T, B, H, G, max_len) && D <= 192 && max_len <= 1024 && kv_tiles(T, B, H, G, 16) <= 256;
 }
 
 // Parts of the keys. Few rows: where the tiles alone fill the chip's 256 CUs, workgroups enough

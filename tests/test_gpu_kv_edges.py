@@ -255,6 +255,19 @@ def test_small_values_beside_a_large_one(n, max_len):
         assert ((acc.cpu().double() - sums).abs() <= 2 * n * err * sums).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", DIMS)
+def test_attention_short_caches_of_many_sequences(D, dtype):
+    """As many tiles as CUs, each walking over a whole cache, and more."""
+    for B, whole in ((32, D <= 192), (33, False)):
+        lens = torch.randint(0, 290, (B,), generator=gen(D)).tolist()
+        lens[3], lens[4], lens[5] = 290, 1, 0
+        cache = ref.Cache(lens, 8, D, 16, seed=D)
+        need = fos.fos_kv_attention_workspace(B, 16, B, cache.W, 8, 16, D)
+        assert need == 0 if whole else need > 0
+        check_attention(cache, ref.queries(B, 16, D, dtype, D + 1), [1] * B)
+
+
 # ----------------------------------------------------------------- weights
 
 
