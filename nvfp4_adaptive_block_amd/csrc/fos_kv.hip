@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
   const int sh = blocks <= 2 ? 1 : blocks <= 4 ? 2 : blocks <= 8 ? 3 : 4;  // log2 of the lanes per row
   const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * (64 >> sh);
   const int64_t rows = (int64_t)a.T * a.c.H;
-  if (side == 0) check_kv(a.c, a.offs, a.T, a.status);
+  check_kv(a.c, a.offs, a.T, a.status);
   if (first >= rows) return;
   // the sequence of the wave's first token: the first whose end lies behind it
   const int t0 = a.by_head.div((int)first);

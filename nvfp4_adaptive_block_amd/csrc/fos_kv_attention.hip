@@ -393,7 +393,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
   __shared__ __attribute__((aligned(16))) uint8_t lds[L::kAll];
   constexpr int D = 32 * NC, DT16 = 2 * NC;  // tiles of 16 values
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
-  if (blockIdx.y == 0) check_kv(a.c, a.offs, a.T, a.status);
+  check_kv(a.c, a.offs, a.T, a.status);
   const Place at_ = place_of(a);
   const int h = at_.h, tile = at_.tile, part = at_.part;
   const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 16, tile, a.G, a.c.lens);
@@ -687,7 +687,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   __shared__ int found[4];  // whether a wave's value rows had a NaN
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  if (blockIdx.y == 0) check_kv(a.c, a.offs, a.T, a.status);
+  check_kv(a.c, a.offs, a.T, a.status);
   // the last tiles of a sequence see the most keys: they start first
   const Place at_ = place_of(a);
   const int h = at_.h, tile = (int)gridDim.x / (a.c.H * a.splits) - 1 - at_.tile, part = at_.part;
@@ -1133,7 +1133,7 @@ __global__ __launch_bounds__(256, kRows == 32 && NC <= 4 ? 4 : 2) void k_kv_weig
   __shared__ __attribute__((aligned(16))) int limits[kRows];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  if (blockIdx.y == 0) check_kv(a.c, a.offs, a.T, a.status);
+  check_kv(a.c, a.offs, a.T, a.status);
   const int h = blockIdx.x % a.c.H, b = blockIdx.x / a.c.H;
   GroupTile gt;
   gt.g = b;
