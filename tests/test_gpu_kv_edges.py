@@ -29,6 +29,26 @@ def test_evict_short_middles(middle):
         check_evict([n, n + 1], 64, 64, 16, budget, sinks, recent, seed=middle, acc=distinct)
 
 
+@pytest.mark.parametrize("budget", [40, 1200])
+def test_evict_bad_lengths(budget):
+    """In one launch and in three: lengths past the table are cut to it, negative ones are empty."""
+    H, D, P, W = 2, 32, 64, 60
+    cache = ref.Cache([W * P, 30, W * P], H, D, P, seed=9)
+    acc = torch.rand(3, H, W * P, generator=gen(10))
+    results = []
+    for lens in ([W * P, 0, W * P], [2 ** 31 - 1, -1, W * P + 1], [W * P + 7, -2 ** 31, W * P]):
+        kc, vc, table, _ = cache.on_device()
+        acc_d = acc.cuda()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        n = torch.tensor(lens, dtype=torch.int32).cuda()
+        new = fos.fos_kv_evict(acc_d, kc, vc, table, n, budget, sinks=2, recent=30, status=status)
+        assert int(status.item()) == (fos.STATUS_BAD_CACHE if results else 0)
+        assert new.tolist() == [budget, 0, budget]
+        results.append([acc_d, *kc, *vc])
+    for got in results[1:]:
+        assert all(same(a, b) for a, b in zip(got, results[0]))
+
+
 # ------------------------------------------------------------------ append
 
 
@@ -64,6 +84,27 @@ def test_append_reports_lengths_of_sequences_without_new_rows(length):
         lens = torch.tensor([3, length if bad else 32], dtype=torch.int32).cuda()
         fos.fos_kv_append(x, x, torch.tensor([3, 3], dtype=torch.int32).cuda(), kc, vc, table, lens, status=status)
         assert int(status.item()) == (fos.STATUS_BAD_CACHE if bad else 0)
+
+
+def test_append_bad_offsets():
+    """Reported; no row goes outside the pages that the table names, or the outputs."""
+    H, D, P, T = 2, 64, 16, 70
+    x = rows_like((T, H, D), "fp16", 8).cuda()
+    table = torch.tensor([[1, 2, 5], [3, 6, 7]], dtype=torch.int32).cuda()
+    lens = torch.tensor([48, 40], dtype=torch.int32).cuda()
+    for offs in ([T - 1, T - 2], [2, T + 5], [-1, T], [2 ** 31 - 1, -2 ** 31], [-2 ** 31, 2 ** 31 - 1], [T, 0]):
+        kc, vc = (fos.fos_kv_cache(9, H, P, D) for _ in range(2))
+        for side in (kc, vc):
+            for t in side:
+                t.fill_(77)
+        ko, raw = guarded((T, H, D), x.dtype)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        fos.fos_kv_append(x, x, torch.tensor(offs, dtype=torch.int32).cuda(), kc, vc, table, lens, k_out=ko, status=status)
+        assert int(status.item()) & fos.STATUS_BAD_OFFS
+        assert_guard(raw)
+        for side in (kc, vc):
+            for t in side:
+                assert (t[[0, 4, 8]] == 77).all()
 
 
 # --------------------------------------------------------------- attention
