@@ -176,20 +176,19 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
   if (first >= rows) return;
   // the sequence of the wave's first token: the first whose end lies behind it
   const int t0 = a.by_head.div((int)first);
-  int b = a.c.B;
-  for (int base = 0; base < a.c.B; base += 64) {
-    const int e = base + lane < a.c.B ? a.offs[base + lane] : INT32_MAX;
-    const unsigned long long hit = __ballot(e > t0);
-    if (hit) {
-      b = base + __ffsll(hit) - 1;
-      break;
-    }
-  }
+  int b = first_end_behind(a.offs, a.c.B, t0);
   const int64_t r = first + (lane >> sh);
   const int j = lane & ((1 << sh) - 1);
   const bool have = r < rows && j < blocks;
   const int t = a.by_head.div((int)(r < rows ? r : rows - 1)), h = (int)(r < rows ? r : rows - 1) - t * a.c.H;
-  while (b < a.c.B && a.offs[b] <= t) b++;
+  // a later token's, by steps that double and then halve again
+  if (b < a.c.B && a.offs[b] <= t) {
+    int step = 1;
+    while (b + step < a.c.B && a.offs[b + step] <= t) b += step, step *= 2;
+    for (; step > 0; step >>= 1)
+      if (b + step < a.c.B && a.offs[b + step] <= t) b += step;
+    b++;
+  }
   const bool tail = b >= a.c.B;
 
   float x[16];
@@ -215,12 +214,10 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
     store_block<DT>(a.y[side], r * a.c.D + 16 * j, y);
   }
   if (!have || tail) return;
-  int start = b ? a.offs[b - 1] : 0, end = a.offs[b];
-  if (start < 0) start = 0;
-  if (end > a.T) end = a.T;
+  // so many before the end of the sequence's new rows, and of its cache
   const int len = min(a.c.lens[b], a.c.W * a.c.P);
-  const int64_t pos = (int64_t)len - (end - start) + (t - start);
-  const bool inside = pos >= 0;
+  const int64_t pos = (int64_t)len - min(a.offs[b], a.T) + t;
+  const bool inside = pos >= 0 && pos < len;
   int64_t page = -1;
   int slot = 0;
   if (inside) {

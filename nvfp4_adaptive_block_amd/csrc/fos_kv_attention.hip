@@ -346,6 +346,16 @@ __device__ __forceinline__ Place place_of(const KvAttendArgs& a) {
   return Place{(int)(blockIdx.x - r * a.c.H), (int)(r % (uint32_t)a.splits), (int)(r / (uint32_t)a.splits)};
 }
 
+// The rows of a tile of 2^ROWS: by the tile's number among those that there are, a pass over all
+// sequences, or from 257 on by search, whose numbers have gaps (a token each on 128 keys, 8 heads of
+// 128, passes and searches: 256 sequences 29 and 30 us, 1024 124 and 87, 16384 11961 and 1437; 17
+// sequences of three tokens, 2999 keys, 12 heads of 64: 20.2 and 20.9).
+template <int ROWS>
+__device__ __forceinline__ GroupTile find_rows(const KvAttendArgs& a, int tile) {
+  return a.c.B <= 256 ? find_group_tile(a.offs, a.c.B, a.T, 1 << ROWS, tile, a.G, a.c.lens)
+                      : search_group_tile<ROWS>(a.offs, a.c.B, a.T, tile, a.G, a.c.lens);
+}
+
 // ---------------------------------------------------------------- few rows
 //
 // A workgroup has 16 rows and a part of their keys; its four waves (twelve for a short
@@ -396,7 +406,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
   check_kv(a.c, a.offs, a.T, a.status);
   const Place at_ = place_of(a);
   const int h = at_.h, tile = at_.tile, part = at_.part;
-  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 16, tile, a.G, a.c.lens);
+  const GroupTile gt = find_rows<4>(a, tile);
   if (gt.g < 0) return;
   const int n = gt.end - gt.start;
   const int len = length_of(a.c, gt.value);  // of the tail 0
@@ -691,7 +701,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   // the last tiles of a sequence see the most keys: they start first
   const Place at_ = place_of(a);
   const int h = at_.h, tile = (int)gridDim.x / (a.c.H * a.splits) - 1 - at_.tile, part = at_.part;
-  const GroupTile gt = find_group_tile(a.offs, a.c.B, a.T, 128, tile, a.G, a.c.lens);
+  const GroupTile gt = find_rows<7>(a, tile);
   if (gt.g < 0) return;
   const int n = gt.end - gt.start;
   const int len = length_of(a.c, gt.value);  // of the tail 0

@@ -107,6 +107,55 @@ __device__ __forceinline__ GroupTile find_group_tile(const int32_t* offs, int G,
   return GroupTile{0, 0, -1, 0, 0};
 }
 
+// Tile `t` of the rows of many groups, where each row of a group stands for `per` rows of its tiles of
+// 2^ROWS. Group g's tiles start at number (offs[g-1] per >> ROWS) + g: no two groups share a number, every
+// tile has one, some numbers have no tile (g < 0), and a number's group is found by search, 64 groups a
+// round. There are (M per >> ROWS) + G + 1 numbers. Offsets are clamped, as above; M per is below 2^31.
+template <int ROWS>
+__device__ __forceinline__ GroupTile search_group_tile(const int32_t* offs, int G, int M, int t, int per, const int32_t* values) {
+  const int lane = threadIdx.x & 63;
+  GroupTile r{0, M, G, 0, 0};
+  int lo = 0, hi = G;  // the group is one of [lo, hi]
+  for (;;) {
+    const int step = (hi - lo + 63) / 64, g = lo + step * (lane + 1) - 1;
+    const bool have = g < G;
+    const int start = have && g ? min(max(offs[g - 1], 0), M) : 0, end = have ? min(max(offs[g], 0), M) : M;
+    const int value = have ? values[g] : 0;
+    const unsigned long long behind = __ballot(g >= hi || (end * per >> ROWS) + g + 1 > t);
+    const int l = behind ? __ffsll(behind) - 1 : 64;
+    if (step == 1 && lo + l < G && l < 64) {
+      r.g = lo + l;
+      r.start = __builtin_amdgcn_readlane(start, l);
+      r.end = __builtin_amdgcn_readlane(end, l);
+      r.value = __builtin_amdgcn_readlane(value, l);
+      break;
+    }
+    lo = min(hi, lo + step * l);
+    if (behind) hi = min(hi, lo + step - 1);
+    if (lo < hi) continue;
+    r.g = lo;
+    if (lo > 0) r.start = min(max(offs[lo - 1], 0), M);
+    if (lo < G) r.end = min(max(offs[lo], 0), M), r.value = values[lo];
+    break;
+  }
+  r.tile = t - ((r.start * per >> ROWS) + r.g);
+  if (r.tile < 0 || ((int64_t)r.tile << ROWS) >= (int64_t)(r.end - r.start) * per) r.g = -1;
+  return r;
+}
+
+// The first of n ascending ends that lies behind t, n if none does, by a wave: 64 places a round.
+__device__ __forceinline__ int first_end_behind(const int32_t* ends, int n, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int step = (hi - lo + 63) / 64, i = lo + step * (lane + 1) - 1;
+    const unsigned long long behind = __ballot(i >= hi || ends[i] > t);
+    lo = min(hi, lo + step * (behind ? __ffsll(behind) - 1 : 64));
+    if (behind) hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
 __device__ inline RowTile find_tile(const int32_t* offs, int G, int M, int rows, int t) {
   const GroupTile r = find_group_tile(offs, G, M, rows, t, 1);
   return RowTile{(int64_t)r.start + (int64_t)r.tile * rows, r.end, r.g};

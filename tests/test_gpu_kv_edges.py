@@ -8,8 +8,8 @@ import torch
 import kv_reference as ref
 import nvfp4_adaptive_block_amd as fos
 from operator_reference import DTYPES, assert_within, gen, half_step
-from test_gpu_kv import (DIMS, LONG, WIDE, assert_guard, attend, check_attention, check_evict, check_weights, ends, guarded,
-                         oracle_rows, rows_like, same)
+from test_gpu_kv import (DIMS, LONG, WIDE, assert_guard, attend, check_append, check_attention, check_evict, check_weights,
+                         ends, guarded, oracle_rows, rows_like, same)
 
 pytestmark = pytest.mark.gpu
 
@@ -105,6 +105,15 @@ def test_append_bad_offsets():
         for side in (kc, vc):
             for t in side:
                 assert (t[[0, 4, 8]] == 77).all()
+
+
+@pytest.mark.parametrize("B,most", [(300, 2), (5000, 2), (5000, 5)])
+def test_append_to_many_sequences(orc, B, most):
+    """A token here and there: sequences far apart in one wave."""
+    g = gen(B)
+    new = torch.where(torch.rand(B, generator=g) < 0.1, torch.randint(1, most, (B,), generator=g), 0)
+    lens = (new + torch.randint(0, 5, (B,), generator=g)).tolist()
+    check_append(orc, lens, new.tolist(), 1, 32, 16, "bf16", seed=B, tail=2)
 
 
 # --------------------------------------------------------------- attention
@@ -307,6 +316,32 @@ def test_attention_short_caches_of_many_sequences(D, dtype):
         need = fos.fos_kv_attention_workspace(B, 16, B, cache.W, 8, 16, D)
         assert need == 0 if whole else need > 0
         check_attention(cache, ref.queries(B, 16, D, dtype, D + 1), [1] * B)
+
+
+@pytest.mark.parametrize("B,G,most", [(257, 3, 3), (700, 2, 2), (700, 16, 9), (4200, 1, 2)])
+def test_attention_batches_of_many_sequences(B, G, most):
+    """Their sequences are found by search: ragged ones, a long run without new tokens, and a tail.
+    Tiles of 16 rows and, with sixteen query heads and up to eight tokens each, of 128."""
+    g = gen(B + G)
+    new = torch.randint(0, most, (B,), generator=g)
+    new[B // 2:B // 2 + 90] = 0
+    lens = new + torch.randint(0, 40, (B,), generator=g)
+    cache = ref.Cache(lens.tolist(), 1, 32, 16, seed=B)
+    T = int(new.sum())
+    q = ref.queries(T + 3, G, 32, "bf16", B)
+    if G == 16:
+        assert T * G > 48 * B
+    check_attention(cache, q, new.tolist())
+    k, v, table, lens_d = cache.on_device()
+    good = new.cumsum(0).int()
+    for at, bad in ((B // 3, -1), (B - 1, T + 9), (0, 2 ** 31 - 1), (B - 2, -2 ** 31)):
+        offs = good.clone()
+        offs[at] = bad
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, raw = guarded(q.shape, q.dtype)
+        fos.fos_kv_attention(q.cuda(), offs.cuda(), k, v, table, lens_d, out=out, status=status)
+        assert int(status.item()) == fos.STATUS_BAD_OFFS
+        assert_guard(raw)
 
 
 # ----------------------------------------------------------------- weights
