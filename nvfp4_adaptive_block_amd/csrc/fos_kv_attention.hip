@@ -88,7 +88,9 @@ __device__ __forceinline__ float log2_of(float S) {
 // Two weights in fp16. For fp16 results what the rounding leaves out is kept too, and
 // multiplied in a second product: alone it would cost as much precision as the result's
 // own rounding (at most 2^-11 each; measured 2.1e-4 of a result's norm with it, 2.7e-4
-// to 3.3e-4 without). A bf16 result's rounding is eight times as large.
+// to 3.3e-4 without). A bf16 result's rounding is eight times as large, errors grow by 1 % of
+// it (1.61e-3 for 1.60e-3), and the second product would take 28 % of a prompt's time (8192 new
+// tokens, 32 heads of 128: 907 us for 709) and 3 to 8 % of a decode step's: left out.
 template <int DT>
 __device__ __forceinline__ uint32_t round_pair(float a, float b, uint32_t& rest) {
   const f32x2 two = {a, b};
@@ -366,8 +368,8 @@ __device__ __forceinline__ GroupTile find_rows(const KvAttendArgs& a, int tile) 
 //
 // A key and its value of D are 9 D / 8 + 8 bytes, from 4 to 16 rows use them, so memory is the
 // bound where there is work enough: 64 sequences of 2500 to 8192 tokens, 8 heads of 128, 416 MB
-// in 91 us and a join of 5, 4.3 TB/s. One sequence of 131072 tokens on 4 heads, 80 MB, takes 23 us
-// (3.4 TB/s): each of 1024 workgroups has eight steps, and its start and end weigh. Two steps ahead
+// in 90 to 93 us and a join of 5, 4.3 TB/s. One sequence of 131072 tokens on 4 heads, 80 MB, takes 24 us
+// (3.3 TB/s): each of 1024 workgroups has eight steps, and its start and end weigh. Two steps ahead
 // lost (17 x 12 heads of 64: 21.5 us for 19.4), and so did branches around the loads. Three waves
 // to a SIMD where registers allow it (D up to 128).
 
@@ -635,12 +637,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 1 : NC <= 4 ? 3 : 2) void k
 //
 // 4 D operations for each row and key are the bound, but the vector units' part (decode, scale,
 // maximum, exponential, conversion) nearly fills the time beside them: 8192 new tokens, 32 query
-// heads of 128, 0.56 PFLOP in 679 us, 817 TFLOP/s; matrix units busy 30 % of the cycles, vector
-// units 50 to 57 %, LDS 45 % (a little before the last step). Decode goes beside the first product and exponentials beside the
+// heads of 128, 0.555 TFLOP in 690 to 735 us from card to card, 755 to 805 TFLOP/s; matrix units
+// busy 35 % of the cycles, vector units 56 %. Decode goes beside the first product and exponentials beside the
 // second, which the scheduler is told. Two workgroups to a CU for D 96 and 128 (three of 32 keys:
-// 730 us; bounded to three with spills: 947). Not kept: the next step's first product beside this
+// 730 us for 695 then; bounded to three with spills: 947). Not kept: the next step's first product beside this
 // one's softmax (816 us), a wave's priority raised in its products (738 for 722 then), raw codes
-// two steps ahead. D 256 fills 256 registers and spills 53, one workgroup to a CU: 506 TFLOP/s.
+// two steps ahead. D 256 fills 256 registers and spills 59, one workgroup to a CU: 540 TFLOP/s.
 
 template <int NC> struct TileLds {
   static constexpr int kKeys = 64;
@@ -724,8 +726,8 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
   read_q<2 * NC>(a.q, row.token * a.stride + (int64_t)row.head * D + 8 * half, 16, row.have, q);
   if (threadIdx.x < L::kKeys) ones[threadIdx.x] = 1.0f;
   // bf16 rows of about one size have one power of two, which then goes with the keys' sizes: a
-  // multiplication less for each score (8192 new tokens, 32 heads of 128: 675 us for 708). The
-  // smallest row's values are then good to 2^-32 of its largest, and sizes grow no larger.
+  // multiplication less for each score (8192 new tokens, 32 heads of 128: 713 us for 806, of 64 451
+  // for 526). The smallest row's values are then good to 2^-32 of its largest, and sizes grow no larger.
   bool common = true;
   float undo = 1.0f, undo_all = 1.0f;
   if constexpr (DT == kBF16) {
@@ -1085,8 +1087,8 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_kv_join(KvAtt
 // added to what is there without atomics, in an order that is always the same.
 //
 // Keys alone are read, 9 D / 16 + 4 bytes each, and 4 bytes of sums read and written. 16 sequences
-// of up to 4096 tokens on 8 heads of 128, a token each, 28 MB: 12.4 us, the chain of a workgroup's
-// start and three or four steps. 64 new tokens of 32 query heads over 32768 keys, 17.4 GFLOP: 33 us,
+// of up to 4096 tokens on 8 heads of 128, a token each, 28 MB: 12.5 us, the chain of a workgroup's
+// start and three or four steps. 64 new tokens of 32 query heads over 32768 keys, 17.4 GFLOP: 34 us,
 // bound by the exponentials of 256 rows for each key beside the products (128 rows staged: 44 us
 // for 40 then).
 
