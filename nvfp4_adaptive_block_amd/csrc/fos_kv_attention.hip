@@ -8,7 +8,8 @@
 // is exact in fp16, which is what the matrix instructions take on both sides:
 //  - q in fp16 as it is; in bf16 times a power of two that brings the row's (or the tile's) largest
 //    value to [2^15, 2^16), where fp16 still has all 8 bits. They are exact down to 2^-32 of
-//    the row's largest, and what is smaller is off by 2^-40 of it (2^-32 where a tile has one).
+//    the row's largest, and what is smaller is off by 2^-40 of it (where a tile's rows share a
+//    power of two, by 2^-40 of the tile's largest, which is 2^-32 of any row's).
 //  - S_dec of a key multiplies the sum, in binary32: with the scale's mantissa first, then with
 //    its power of two and what undoes q's, which are exact, so that nothing between leaves
 //    binary32's range where the score does not.
@@ -787,7 +788,7 @@ __global__ __launch_bounds__(256, NC <= 2 ? 3 : NC <= 4 ? 2 : 1) void k_kv_tile(
       *reinterpret_cast<u32x4*>(base + L::kKeys * L::kK + L::value(my_key, (lane & 3) * NC + c)) =
           u32x4{f[c].u[0], f[c].u[1], f[c].u[2], f[c].u[3]};
     float S = !st.there || first + my_size >= len ? 0.0f : st.sdec;
-    const bool odd = lane >= 16 && !(__builtin_fabsf(S) < __builtin_huge_valf());
+    const bool odd = (lane & 16) && !(__builtin_fabsf(S) < __builtin_huge_valf());
     odd_sizes |= __ballot(odd);
     S = odd ? 0.0f : S;
     sizes[side][to_size] = S * size_by * size_undo;

@@ -167,6 +167,27 @@ def test_attention_rows_that_are_not_numbers(dtype, n, max_len, D, what):
             assert torch.isnan(lse[whole]).all()
 
 
+@pytest.mark.parametrize("what", ["scale", "nan"])
+@pytest.mark.parametrize("H,lens,new", [(30, [150, 33, 5], [80, 30, 5]), (2, [2500, 700], [60, 90])])
+def test_attention_rows_that_are_not_numbers_in_tiles_of_many_heads_and_in_parts(H, lens, new, what):
+    """Tiles whose keys are in one part, and in several, of which the last has the rows."""
+    D = 64
+    cache = ref.Cache(lens, H, D, 16, seed=H, W=None if H == 30 else WIDE)
+    q = ref.queries(sum(new) + 3, H * 8 if H == 30 else 8, D, "bf16", H + 1)
+    want, bound, want_lse, lse_bound = ref.attention(cache, q, new)
+    G, L, n = q.shape[1] // H, lens[0], new[0]
+    hit = torch.zeros(q.shape, dtype=torch.bool)
+    for pos, block in ((L - 1, 0), (L - 33, 3)):
+        poison(cache, 1, pos, what, block)
+        hit[pos - (L - n):n, :G, slice(16 * block, 16 * block + 16) if what == "scale" else slice(None)] = True
+    out, lse, _ = attend(cache, q, new, max_len=0 if H == 30 else LONG)
+    out, lse = out.cpu(), lse.cpu()
+    assert torch.isnan(out[hit]).all()
+    assert_within(out[~hit], want[~hit], bound[~hit], "out")
+    some = want_lse > -math.inf
+    assert_within(lse[some], want_lse[some], lse_bound[some], "lse")
+
+
 @pytest.mark.parametrize("n,max_len", [(3, 0), (60, LONG)])
 def test_attention_a_nan_that_all_see(n, max_len):
     """In an early row, in a page's last place, and where some keys of the step are not there."""
